@@ -69,6 +69,9 @@ enum {
  * d and d_ff to be multiples of 8 and 16-byte aligned data pointers. */
 #define MOE_MAX_EXPERTS 256
 #define MOE_MAX_TOPK 16
+#define MOE_FEW_MAX_TOKENS 64      /* tokens of moe_forward_few */
+#define MOE_NORM_MAX_WIDTH 16384   /* row width of moe_layer_norm */
+#define MOE_LINEAR_MAX_EXTENT (1 << 30)  /* rows and widths of moe_linear */
 
 /* A tensor view: data (device), element type, rank and extents (row-major,
  * contiguous). A 3-D activation [B, T, d] is read as [B*T, d]. */
@@ -172,7 +175,7 @@ int moe_forward(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *no
  *   with the same seed and offset draws the same mask, so moe_backward_ex
  *   differentiates exactly the forward's dropped-out layer.
  * Zero-initialise the struct and set the fields used. */
-enum { MOE_ACT_RELU = 0, MOE_ACT_GELU = 1 };
+enum { MOE_ACT_RELU = 0, MOE_ACT_GELU = 1, MOE_ACT_NONE = 2 /* moe_linear only */ };
 typedef struct {
     int32_t activation;
     const moe_tensor *b_up;
@@ -442,6 +445,117 @@ int moe_backward_after_forward(const moe_tensor *x, const moe_tensor *W_g,
  * other than MOE_BF16). */
 size_t moe_backward_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k,
                                    float capacity_factor, int32_t dtype);
+
+/* ---------------------------------------------------------------------------
+ * The rest of a transformer block's feed-forward half: the layer for a few
+ * tokens, the linear product of a shared or dense expert, the norm in front.
+ * Same conventions as above.
+ * ------------------------------------------------------------------------- */
+
+/* moe_forward_ex for at most MOE_FEW_MAX_TOKENS tokens (MOE_ERR_UNSUPPORTED
+ * beyond), the form of a decoding step: the same arguments, routing (bit for
+ * bit), capacity drops, options and exports, on kernels that stream each hit
+ * expert's weights once instead of computing row tiles. Training-mode dropout
+ * is refused (MOE_ERR_UNSUPPORTED). Numerics: as moe_forward's, except that a
+ * bf16 layer keeps the hidden activation to 16 significant bits (two bf16
+ * terms) and the experts' output rows in fp32, so that out carries only its
+ * own rounding; the sum over a token's choices runs in ascending expert id.
+ * stats->workspace holds moe_few_workspace_size() bytes (256-byte aligned;
+ * a size for more tokens serves fewer). Bias data 16-byte aligned, as there. */
+int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
+                    const moe_tensor *W_up, const moe_tensor *W_down,
+                    const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
+                    moe_stats *stats);
+
+/* Bytes of workspace moe_forward_few needs (0 on invalid sizes, or beyond
+ * MOE_FEW_MAX_TOKENS). */
+size_t moe_few_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k,
+                              float capacity_factor, int32_t dtype);
+
+/* Linear product with its epilogue, the dense feed-forward layer or shared
+ * expert beside the routed ones:
+ *   z = x W^T + bias,  out = act(z) + residual
+ *   x        [N, K] (or [B, T, K])  MOE_BF16 (MOE_ERR_UNSUPPORTED for fp32)
+ *   W        [M, K]                 MOE_BF16 (row m: output neuron m)
+ *   bias     [M] MOE_F32 or NULL
+ *   activation  MOE_ACT_NONE, MOE_ACT_RELU or MOE_ACT_GELU (as
+ *            moe_expert_opts); MOE_ERR_ARG otherwise
+ *   residual [N, M] MOE_BF16 or NULL; may be the buffer of out
+ *   out      [N, M] MOE_BF16, every row written
+ *   z        [N, M] MOE_BF16 or NULL: the pre-activations, for the backward
+ *            (a buffer of its own: MOE_ERR_ARG)
+ * fp32 accumulation, bias, activation and residual; out and z are each rounded
+ * once. out must not overlap x or W. K and M are multiples of 8 and N, K, M at
+ * most MOE_LINEAR_MAX_EXTENT (MOE_ERR_UNSUPPORTED); data 16-byte aligned
+ * (MOE_ERR_ALIGN). workspace: device scratch of moe_linear_workspace_size()
+ * bytes, 256-byte aligned (may be NULL when that is 0): fp32 partial products
+ * of a product too small to fill the GPU. N = 0 is valid. */
+int moe_linear(const moe_tensor *x, const moe_tensor *W, const moe_tensor *bias,
+               int32_t activation, const moe_tensor *residual, moe_tensor *out, moe_tensor *z,
+               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of scratch of moe_linear (0 when it needs none, or for invalid sizes). */
+size_t moe_linear_workspace_size(int64_t N, int64_t K, int64_t M);
+
+/* Its backward, for dout [N, M] MOE_BF16 the gradient of out:
+ *   dz = dout act'(z),  dx = dz W,  dW = dz^T x,  dbias = sum of the dz rows
+ * (the residual's gradient is dout itself). z: the forward's, required with an
+ * activation, NULL without one (MOE_ERR_ARG). dx [N, K] and dW [M, K] are
+ * MOE_BF16 or MOE_F32, dbias [M] MOE_F32; each may be NULL and is then not
+ * computed (all three NULL: MOE_ERR_NULL). The products read dz rounded once
+ * to bf16 (the dz of MOE_ACT_NONE is dout, exactly); dbias sums the fp32
+ * values. dx must not be the buffer of x, z or dout (MOE_ERR_ARG). Widths and
+ * alignment as moe_linear's. workspace:
+ * moe_linear_backward_workspace_size() bytes, 256-byte aligned. N = 0: dW and
+ * dbias are zero. */
+int moe_linear_backward(const moe_tensor *x, const moe_tensor *W, const moe_tensor *z,
+                        int32_t activation, const moe_tensor *dout, moe_tensor *dx,
+                        moe_tensor *dW, moe_tensor *dbias, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Bytes of scratch of moe_linear_backward (0 for N = 0 or invalid sizes). */
+size_t moe_linear_backward_workspace_size(int64_t N, int64_t K, int64_t M, int32_t activation);
+
+/* Layer norm over the last dimension, the norm in front of the router:
+ *   h = x + residual, rounded to the type of x (h = x without a residual)
+ *   out = (h - mean) rstd weight + bias,
+ *   mean = sum h / d, rstd = 1 / sqrt(sum (h - mean)^2 / d + eps)
+ *   x        [N, d] (or [B, T, d])  MOE_F32 or MOE_BF16
+ *   residual same shape and dtype as x, or NULL
+ *   weight   [d] MOE_F32; bias [d] MOE_F32 or NULL
+ *   eps      > 0, finite
+ *   h        as x; required with a residual, NULL without one (MOE_ERR_ARG)
+ *   out      as x, every row written
+ *   mean, rstd  [N] MOE_F32 or NULL: what the backward needs
+ * Statistics are fp32, of the values h holds after its rounding. out or h may
+ * be the buffer of x or of residual (each element is read before it is
+ * written), not both the same buffer (MOE_ERR_ARG). d <= MOE_NORM_MAX_WIDTH;
+ * bf16 rows need d % 8 == 0 (MOE_ERR_UNSUPPORTED) and 16-byte aligned x,
+ * residual, h, out, weight and bias (MOE_ERR_ALIGN); fp32 rows any d. */
+int moe_layer_norm(const moe_tensor *x, const moe_tensor *residual, const moe_tensor *weight,
+                   const moe_tensor *bias, float eps, moe_tensor *h, moe_tensor *out,
+                   moe_tensor *mean, moe_tensor *rstd, void *stream);
+
+/* Its backward, for dout the gradient of out and dres (or NULL) the gradient
+ * that reaches h along the residual path:
+ *   g = dout weight, xh = (x - mean) rstd,
+ *   dx = rstd (g - sum g / d - xh (sum g xh) / d) + dres
+ *   dweight = sum over rows of dout xh, dbias = sum over rows of dout
+ * x is the h of the forward (or its x without a residual); with a residual
+ * dx is the gradient of both summands. dx, dout and dres have x's shape and
+ * dtype (dx may be the buffer of dout or dres, not of x: MOE_ERR_ARG);
+ * weight, dweight and dbias [d], mean and rstd [N] MOE_F32; dbias may be
+ * NULL. Sums are fp32 in a fixed order. workspace: device scratch of
+ * moe_layer_norm_backward_workspace_size() bytes, 256-byte aligned. Widths
+ * and alignment as moe_layer_norm's. N = 0: the sums are zero. */
+int moe_layer_norm_backward(const moe_tensor *x, const moe_tensor *weight, const moe_tensor *mean,
+                            const moe_tensor *rstd, const moe_tensor *dout,
+                            const moe_tensor *dres, moe_tensor *dx, moe_tensor *dweight,
+                            moe_tensor *dbias, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Bytes of scratch of moe_layer_norm_backward (0 for N = 0 or invalid sizes). */
+size_t moe_layer_norm_backward_workspace_size(int64_t N, int64_t d);
 
 #ifdef __cplusplus
 }

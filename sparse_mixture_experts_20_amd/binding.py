@@ -27,10 +27,15 @@ EXPORTS = ("moe_forward", "moe_workspace_size", "moe_capacity", "moe_error_strin
            "moe_backward", "moe_backward_ex", "moe_backward_workspace_size",
            "moe_forward_train", "moe_backward_after_forward", "moe_dispatch_workspace_size",
            "moe_expert_kernel_name", "moe_dispatch_noalloc", "moe_expert_down_compact",
-           "moe_combine_compact")
+           "moe_combine_compact", "moe_forward_few", "moe_few_workspace_size", "moe_linear",
+           "moe_linear_workspace_size", "moe_linear_backward",
+           "moe_linear_backward_workspace_size", "moe_layer_norm", "moe_layer_norm_backward",
+           "moe_layer_norm_backward_workspace_size")
 
-MOE_ACT_RELU, MOE_ACT_GELU = 0, 1
+MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_NONE = 0, 1, 2
 ACTS = {"relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU}
+LINEAR_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU}
+MOE_FEW_MAX_TOKENS, MOE_NORM_MAX_WIDTH = 64, 16384
 
 
 class MoeTensor(ctypes.Structure):
@@ -148,6 +153,27 @@ def lib():
         L.moe_combine.restype = ctypes.c_int
         L.moe_combine_compact.argtypes = [_i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp, _T, _vp]
         L.moe_combine_compact.restype = ctypes.c_int
+        L.moe_forward_few.argtypes = L.moe_forward_ex.argtypes
+        L.moe_forward_few.restype = ctypes.c_int
+        L.moe_few_workspace_size.argtypes = L.moe_workspace_size.argtypes
+        L.moe_few_workspace_size.restype = ctypes.c_size_t
+        L.moe_linear.argtypes = [_T, _T, _T, ctypes.c_int32, _T, _T, _T, _vp, ctypes.c_size_t,
+                                 _vp]
+        L.moe_linear.restype = ctypes.c_int
+        L.moe_linear_workspace_size.argtypes = [_i64, _i64, _i64]
+        L.moe_linear_workspace_size.restype = ctypes.c_size_t
+        L.moe_linear_backward.argtypes = [_T, _T, _T, ctypes.c_int32, _T, _T, _T, _T, _vp,
+                                          ctypes.c_size_t, _vp]
+        L.moe_linear_backward.restype = ctypes.c_int
+        L.moe_linear_backward_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int32]
+        L.moe_linear_backward_workspace_size.restype = ctypes.c_size_t
+        L.moe_layer_norm.argtypes = [_T, _T, _T, _T, ctypes.c_float, _T, _T, _T, _T, _vp]
+        L.moe_layer_norm.restype = ctypes.c_int
+        L.moe_layer_norm_backward.argtypes = [_T, _T, _T, _T, _T, _T, _T, _T, _T, _vp,
+                                              ctypes.c_size_t, _vp]
+        L.moe_layer_norm_backward.restype = ctypes.c_int
+        L.moe_layer_norm_backward_workspace_size.argtypes = [_i64, _i64]
+        L.moe_layer_norm_backward_workspace_size.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -707,3 +733,236 @@ def combine(Y, gate, slot, out, stream=None):
     _check(lib().moe_combine(N, d, k, _ref(dy), _ptr(gate), _ptr(slot), _ref(do),
                              _stream(stream)), "moe_combine")
     return out
+
+
+# --------------------------------------------------------------------------
+# The rest of the feed-forward half: the layer for a few tokens, the linear
+# product, the layer norm
+# --------------------------------------------------------------------------
+def _place(device, tensors):
+    """The tensors' common device; each must be on it (the library takes
+    device pointers of one GPU)."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a HIP device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+
+
+def _run(device, where, fn, *args):
+    """Call ``fn(*args)`` with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != 0:
+        raise MoeError(rc, where)
+
+
+def _stream_of(device, stream):
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def few_workspace_size(N: int, d: int, E: int, d_ff: int, k: int, capacity_factor: float,
+                       dtype: torch.dtype) -> int:
+    code = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+    return int(lib().moe_few_workspace_size(N, d, E, d_ff, k, capacity_factor, code))
+
+
+def forward_few(x: torch.Tensor, W_g: torch.Tensor, noise: Optional[torch.Tensor],
+                W_up: torch.Tensor, W_down: torch.Tensor, k: int, capacity_factor: float,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                export: bool = True, stream=None, act: str = "relu",
+                b_up: Optional[torch.Tensor] = None, b_down: Optional[torch.Tensor] = None,
+                router_stats: bool = False):
+    """Run ``moe_forward_few`` (at most ``MOE_FEW_MAX_TOKENS`` tokens): the
+    arguments and results of :func:`forward`, without dropout."""
+    N, d = x.numel() // x.shape[-1], x.shape[-1]
+    E, d_ff = W_up.shape[0], W_up.shape[1]
+    dev = x.device
+    if out is None:
+        out = torch.empty_like(x)
+    _place(dev, (W_g, noise, W_up, W_down, out, b_up, b_down, workspace))
+    if workspace is None:
+        workspace = alloc_workspace(few_workspace_size(N, d, E, d_ff, k, capacity_factor, x.dtype),
+                                    dev)
+    idx = gate = slot = used = None
+    if export:
+        idx = torch.empty((N, k), dtype=torch.int32, device=dev)
+        gate = torch.empty((N, k), dtype=torch.float32, device=dev)
+        slot = torch.empty((N, k), dtype=torch.int32, device=dev)
+        used = torch.empty((E,), dtype=torch.int32, device=dev)
+    dem, drp, gsum = _router_stats(E, dev, router_stats)
+    st = MoeStats(_stream_of(dev, stream), ctypes.c_void_p(workspace.data_ptr()),
+                  workspace.numel(), _ptr(idx), _ptr(gate), _ptr(slot), _ptr(used), -1, _ptr(dem),
+                  _ptr(drp), _ptr(gsum), None)
+    ds = [desc(t) for t in (x, W_g, noise, W_up, W_down, out)]
+    r = [_ref(t) for t in ds]
+    o = _opts(act, b_up, b_down)
+    _run(dev, "moe_forward_few", lib().moe_forward_few, r[0], r[1], r[2], r[3], r[4],
+         None if o is None else o.ref(), k, capacity_factor, r[5], ctypes.byref(st))
+    return out, Stats(idx, gate, slot, used, int(st.capacity), dem, drp, gsum)
+
+
+class FewLayer:
+    """A layer kept for decoding: the weights' descriptors, the workspace and
+    (with ``export``) the routing buffers are built once, for up to
+    ``max_tokens`` tokens; ``layer(x, noise=None, out=None)`` runs
+    ``moe_forward_few`` on the current stream and returns ``(out, Stats)``.
+    Calls share the workspace and the routing buffers, so they must be ordered
+    on one stream; ``out`` is a new tensor unless given."""
+
+    def __init__(self, W_g, W_up, W_down, k, capacity_factor, act="relu", b_up=None, b_down=None,
+                 max_tokens=MOE_FEW_MAX_TOKENS, export=False, router_stats=False):
+        E, d_ff, d = W_up.shape
+        dev = W_up.device
+        self.tensors = (W_g, W_up, W_down, b_up, b_down)
+        self.k, self.cf, self.d, self.max_tokens = k, capacity_factor, d, max_tokens
+        self.device = dev
+        _place(dev, (W_g, W_down, b_up, b_down))
+        n = few_workspace_size(max_tokens, d, E, d_ff, k, capacity_factor, W_up.dtype)
+        if n == 0:
+            raise ValueError("sizes outside moe_forward_few's limits")
+        self.workspace = alloc_workspace(n, dev)
+        self._w = [desc(t) for t in (W_g, W_up, W_down)]
+        self._r = [_ref(t) for t in self._w]
+        self._opts = _opts(act, b_up, b_down)
+        self._o = None if self._opts is None else self._opts.ref()
+        idx = gate = slot = used = None
+        if export:
+            idx = torch.empty((max_tokens, k), dtype=torch.int32, device=dev)
+            gate = torch.empty((max_tokens, k), dtype=torch.float32, device=dev)
+            slot = torch.empty((max_tokens, k), dtype=torch.int32, device=dev)
+            used = torch.empty((E,), dtype=torch.int32, device=dev)
+        self._routing = (idx, gate, slot, used)
+        self._counts = _router_stats(E, dev, router_stats)
+        dem, drp, gsum = self._counts
+        self.stats = MoeStats(None, ctypes.c_void_p(self.workspace.data_ptr()),
+                              self.workspace.numel(), _ptr(idx), _ptr(gate), _ptr(slot),
+                              _ptr(used), -1, _ptr(dem), _ptr(drp), _ptr(gsum), None)
+        self._sref = ctypes.byref(self.stats)
+        self._fn = lib().moe_forward_few
+
+    def __call__(self, x, noise=None, out=None, stream=None):
+        N = x.numel() // x.shape[-1]
+        if N > self.max_tokens:
+            raise ValueError(f"{N} tokens: this layer was built for {self.max_tokens}")
+        if out is None:
+            out = torch.empty_like(x)
+        _place(self.device, (x, noise, out))
+        st = self.stats
+        st.stream = _stream_of(self.device, stream)
+        dx, dn, do = desc(x), desc(noise), desc(out)
+        r = self._r
+        _run(self.device, "moe_forward_few", self._fn, _ref(dx), r[0], _ref(dn), r[1], r[2],
+             self._o, self.k, self.cf, _ref(do), self._sref)
+        idx, gate, slot, used = self._routing
+        if idx is not None and N != self.max_tokens:
+            idx, gate, slot = idx[:N], gate[:N], slot[:N]
+        return out, Stats(idx, gate, slot, used, int(st.capacity), *self._counts)
+
+
+def _linear_act(act):
+    if act not in LINEAR_ACTS:
+        raise ValueError("act must be 'none', 'relu' or 'gelu'")
+    return LINEAR_ACTS[act]
+
+
+def linear_workspace_size(N: int, K: int, M: int) -> int:
+    return int(lib().moe_linear_workspace_size(N, K, M))
+
+
+def linear(x, W, bias=None, act: str = "none", residual=None, out=None, keep_z: bool = False,
+           workspace=None, stream=None):
+    """``act(x W^T + bias) + residual`` (bf16; x [..., K], W [M, K]): returns
+    ``(out, z)``, z the bf16 pre-activations with ``keep_z``, else None."""
+    N, K, M = x.numel() // x.shape[-1], x.shape[-1], W.shape[0]
+    if out is None:
+        out = torch.empty((*x.shape[:-1], M), dtype=x.dtype, device=x.device)
+    z = torch.empty_like(out) if keep_z else None
+    _place(x.device, (W, bias, residual, out, workspace))
+    if workspace is None:
+        n = linear_workspace_size(N, K, M)
+        workspace = alloc_workspace(n, x.device) if n else None
+    wp, wn = _ws_args(workspace)
+    ds = [desc(t) for t in (x, W, bias, residual, out, z)]
+    r = [_ref(t) for t in ds]
+    _run(x.device, "moe_linear", lib().moe_linear, r[0], r[1], r[2], _linear_act(act), r[3], r[4],
+         r[5], wp, wn, _stream_of(x.device, stream))
+    return out, z
+
+
+def linear_backward_workspace_size(N: int, K: int, M: int, act: str = "none") -> int:
+    return int(lib().moe_linear_backward_workspace_size(N, K, M, _linear_act(act)))
+
+
+def linear_backward(x, W, z, dout, act: str = "none", bias: bool = True, need_dx: bool = True,
+                    need_dW: bool = True, dx_dtype=torch.float32, dW_dtype=torch.float32,
+                    workspace=None, stream=None):
+    """Gradients of :func:`linear` for ``dout``: ``(dx, dW, dbias)``, None for
+    the ones not asked for; z is the forward's (None without an activation)."""
+    N, K, M = x.numel() // x.shape[-1], x.shape[-1], W.shape[0]
+    dev = x.device
+    _place(dev, (W, z, dout, workspace))
+    dx = torch.empty(x.shape, dtype=dx_dtype, device=dev) if need_dx else None
+    dW = torch.empty((M, K), dtype=dW_dtype, device=dev) if need_dW else None
+    db = torch.empty((M,), dtype=torch.float32, device=dev) if bias else None
+    if workspace is None:
+        n = linear_backward_workspace_size(N, K, M, act)
+        workspace = alloc_workspace(n, dev) if n else None
+    wp, wn = _ws_args(workspace)
+    ds = [desc(t) for t in (x, W, z, dout, dx, dW, db)]
+    r = [_ref(t) for t in ds]
+    _run(dev, "moe_linear_backward", lib().moe_linear_backward, r[0], r[1], r[2],
+         _linear_act(act), r[3], r[4], r[5], r[6], wp, wn, _stream_of(dev, stream))
+    return dx, dW, db
+
+
+def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, h=None, out=None,
+               stats: bool = False, stream=None):
+    """Layer norm of ``x`` (of ``h = x + residual`` when given, h returned):
+    ``(out, h, mean, rstd)``; h is x without a residual, mean and rstd (fp32,
+    one per row: what the backward needs) are None unless ``stats``."""
+    N = x.numel() // x.shape[-1]
+    if out is None:
+        out = torch.empty_like(x)
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    _place(x.device, (weight, bias, residual, h, out))
+    mean = rstd = None
+    if stats:
+        mean = torch.empty((N,), dtype=torch.float32, device=x.device)
+        rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
+    ds = [desc(t) for t in (x, residual, weight, bias, h, out, mean, rstd)]
+    r = [_ref(t) for t in ds]
+    _run(x.device, "moe_layer_norm", lib().moe_layer_norm, r[0], r[1], r[2], r[3], eps, r[4],
+         r[5], r[6], r[7], _stream_of(x.device, stream))
+    return out, (x if h is None else h), mean, rstd
+
+
+def layer_norm_backward_workspace_size(N: int, d: int) -> int:
+    return int(lib().moe_layer_norm_backward_workspace_size(N, d))
+
+
+def layer_norm_backward(h, weight, mean, rstd, dout, dres=None, bias: bool = True, dx=None,
+                        workspace=None, stream=None):
+    """Gradients of :func:`layer_norm` for ``dout`` (and ``dres``, what reaches
+    h along the residual path): ``(dx, dweight, dbias)``, dbias None without
+    ``bias``. h, mean and rstd are the forward's."""
+    N, d = h.numel() // h.shape[-1], h.shape[-1]
+    if dx is None:
+        dx = torch.empty_like(h)
+    _place(h.device, (weight, mean, rstd, dout, dres, dx, workspace))
+    dw = torch.empty((d,), dtype=torch.float32, device=h.device)
+    db = torch.empty((d,), dtype=torch.float32, device=h.device) if bias else None
+    if workspace is None:
+        n = layer_norm_backward_workspace_size(N, d)
+        workspace = alloc_workspace(n, h.device) if n else None
+    wp, wn = _ws_args(workspace)
+    ds = [desc(t) for t in (h, weight, mean, rstd, dout, dres, dx, dw, db)]
+    r = [_ref(t) for t in ds]
+    _run(h.device, "moe_layer_norm_backward", lib().moe_layer_norm_backward, r[0], r[1], r[2],
+         r[3], r[4], r[5], r[6], r[7], r[8], wp, wn, _stream_of(h.device, stream))
+    return dx, dw, db

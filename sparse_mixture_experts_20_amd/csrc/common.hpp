@@ -296,3 +296,51 @@ hipError_t launch_combine_compact(const void *Y, const signed char *ysh, const f
                                   int out_dtype, hipStream_t s);
 
 }  // namespace moe
+
+// ---------------------------------------------------------------------------
+// The rest of the feed-forward half: few-token layer, linear product, norm.
+// ---------------------------------------------------------------------------
+namespace moe {
+
+// The layer for N <= kFewMaxTokens tokens after its router: H is
+// [2][N k][d_ff] bf16 (two terms) or [N k][d_ff] fp32, plan few_plan_bytes().
+// slot, used, demand, drops, gate_sum may each be NULL.
+constexpr int kFewMaxTokens = 64;
+size_t few_plan_bytes();
+hipError_t launch_few(bool bf16, const void *x, const void *w_up, const void *w_down,
+                      const float *b_up, const float *b_down, const int32_t *idx,
+                      const float *gate, int64_t N, int64_t d, int E, int64_t d_ff, int k,
+                      int64_t ceff, int act, void *H, void *plan, void *out, int32_t *slot,
+                      int32_t *used, int32_t *demand, int32_t *drops, float *gate_sum,
+                      hipStream_t s);
+
+// Layer norm of N rows of d (h = x + res kept when res is given) and its
+// backward. vec (fp32 rows): d % 4 == 0 and 16-byte aligned data.
+size_t layer_norm_backward_bytes(int64_t N, int64_t d);
+hipError_t launch_layer_norm(bool bf16, bool vec, const void *x, const void *res, const float *w,
+                             const float *b, float eps, int64_t N, int64_t d, void *h, void *out,
+                             float *mean, float *rstd, hipStream_t s);
+hipError_t launch_layer_norm_backward(bool bf16, bool vec, const void *x, const float *w,
+                                      const float *mean, const float *rstd, const void *dout,
+                                      const void *dres, int64_t N, int64_t d, void *dx, float *dw,
+                                      float *db, float *part, hipStream_t s);
+
+// Linear product out = act(x W^T + bias) + residual (bf16, x [N, K], W [M, K];
+// K, M multiples of 8) and its backward; act: kActRelu, kActGelu or kActNone
+// (activation.hpp). z: the pre-activations, or NULL.
+size_t linear_bytes(int64_t N, int64_t K, int64_t M);
+hipError_t launch_linear(const void *x, const void *W, const float *bias, int act,
+                         const void *residual, int64_t N, int64_t K, int64_t M, void *out, void *z,
+                         void *ws, hipStream_t s);
+// Workspace regions of the backward (byte offsets): bf16 dz (with an
+// activation), partial column sums, fp32 partial products.
+struct LinearBackwardLayout {
+    size_t dz, sums, part, total;
+};
+LinearBackwardLayout linear_backward_layout(int64_t N, int64_t K, int64_t M, bool act);
+hipError_t launch_linear_backward(const void *x, const void *W, const void *z, int act,
+                                  const void *dout, int64_t N, int64_t K, int64_t M, void *dx,
+                                  bool dx32, void *dW, bool dW32, float *db, void *ws,
+                                  hipStream_t s);
+
+}  // namespace moe

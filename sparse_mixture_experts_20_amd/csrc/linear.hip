@@ -1,0 +1,616 @@
+// Linear product with bias, activation and residual in its epilogue, and its
+// backward: the dense feed-forward layer or shared expert that stands beside
+// the routed experts (nanoMoE slide 32's expert without the routing).
+//
+//   z = x W^T + b,  out = act(z) + r                     x [N, K], W [M, K]
+//   backward: dz = dout act'(z),  dx = dz W,  dW = dz^T x,  db = sum of dz rows
+//
+// bf16 operands, fp32 accumulation. dz is rounded to bf16 once, as the operand
+// of the two matrix products (they run on the bf16 matrix cores); db sums the
+// fp32 values before that rounding. Without an activation dz is dout itself.
+//
+// Few rows (N <= 64): bound by the stream of W, run on the skinny core
+// (skinny.hpp): one workgroup per 16 output columns, its waves splitting K.
+//
+// More rows: one kernel for the three products, BM x BN output tiles, K-step
+// 64 in a two-stage LDS ring filled by direct global-to-LDS loads (16 bytes a
+// lane); waves of (FM 16) x 64 on 16x16x32 MFMAs. An operand whose rows run
+// along the reduction (x, W of the forward, dz of dx) is staged row by row; one
+// stored the other way (W of dx, both of dW) is staged as it lies and turned
+// into fragments by the transposing LDS read. The output's columns are the
+// MFMA's rows, and the 64 columns of a wave are dealt to its four fragments so
+// that a lane ends with 16 adjacent columns of one row: the epilogue stores
+// whole 128-byte lines from registers, with no pass through LDS. When the tiles
+// leave CUs idle, the reduction is cut into ranges whose fp32 partials go to
+// the workspace and a second kernel adds them in order (no atomics).
+#include <algorithm>
+#include <type_traits>
+
+#include "activation.hpp"
+#include "common.hpp"
+#include "skinny.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kXcdCount = 8;
+constexpr int kStep = 64;   // K-step of the tiled product
+
+__device__ __forceinline__ void barrier_lds() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Direct copy of 16 bytes per lane to LDS: lane l's bytes land at base + 16 l.
+// In asm so that the compiler does not wait for it before every LDS read; the
+// waits are explicit.
+__device__ __forceinline__ void copy_to_lds(unsigned base, const void *g) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 ::"s"(base), "v"(g)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ unsigned lds_address(const void *p) {
+    return (unsigned)(uintptr_t)((__attribute__((address_space(3))) const void *)p);
+}
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+// Transposing LDS read: within 16 lanes, lane l gets element l % 4 of the 8
+// bytes that lane 4 q + l / 4 addresses, as its element q.
+__device__ __forceinline__ s16x4 read_transposed(const void *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
+}
+
+struct Epilogue {
+    unsigned short *out16;          // bf16 output, or NULL
+    float *out32;                   // fp32 output, or NULL
+    const float *bias;              // [columns] or NULL
+    const unsigned short *res;      // bf16 like the output, or NULL
+    unsigned short *z16;            // bf16 pre-activations, or NULL
+    int act;
+};
+
+// Epilogue of G adjacent columns (a multiple of 8) of one row at element
+// offset o; b: their biases (0 without one).
+template <int G>
+__device__ __forceinline__ void store_columns(const Epilogue &ep, int64_t o, float (&v)[G],
+                                              const float (&b)[G], int valid) {
+#pragma unroll
+    for (int h = 0; h < G / 8; ++h) {
+        if (8 * h >= valid)
+            continue;
+        float *p = &v[8 * h];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[i] += b[8 * h + i];
+        if (ep.z16)
+            *reinterpret_cast<u32x4 *>(ep.z16 + o + 8 * h) =
+                u32x4{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
+                      pack_bf16x2(p[6], p[7])};
+        if (ep.act != kActNone)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                p[i] = activate(p[i], ep.act);
+        if (ep.res) {
+            const u32x4 r = *reinterpret_cast<const u32x4 *>(ep.res + o + 8 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[2 * i] += __uint_as_float(r[i] << 16);
+                p[2 * i + 1] += __uint_as_float(r[i] & 0xffff0000u);
+            }
+        }
+        if (ep.out16) {
+            *reinterpret_cast<u32x4 *>(ep.out16 + o + 8 * h) =
+                u32x4{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
+                      pack_bf16x2(p[6], p[7])};
+        } else {
+            *reinterpret_cast<f32x4 *>(ep.out32 + o + 8 * h) = f32x4{p[0], p[1], p[2], p[3]};
+            *reinterpret_cast<f32x4 *>(ep.out32 + o + 8 * h + 4) = f32x4{p[4], p[5], p[6], p[7]};
+        }
+    }
+}
+
+// out [rows, cols] = A B over K. AT: A is [K][rows] (else [rows][K]); BT: B is
+// [K][cols] (else [cols][K]). grid: (tiles rounded up to the XCD count,
+// K-ranges); with more than one range, range s writes its fp32 partial tile
+// rows to part + s rows cols and the epilogue is left to the second kernel.
+template <int BM, int BN, int WM, int WN, bool AT, bool BT>
+__global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
+    const unsigned short *__restrict__ A, const unsigned short *__restrict__ B, int rows,
+    int cols, int K, Epilogue ep, float *__restrict__ part) {
+    constexpr int NW = WM * WN;
+    constexpr int FM = BM / WM / 16, FN = 4;
+    static_assert(BN / WN == 64, "a wave holds 64 columns");
+    constexpr int ABYTES = BM * kStep * 2, BBYTES = BN * kStep * 2, STAGE = ABYTES + BBYTES;
+    constexpr int IA = ABYTES / (NW * 1024), IB = BBYTES / (NW * 1024);
+    static_assert(IA * NW * 1024 == ABYTES && IB * NW * 1024 == BBYTES, "whole wave copies");
+    __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+
+    // Tile of this workgroup: block b runs on XCD b mod 8 and takes index
+    // (b mod 8) T8/8 + b/8, one contiguous range per XCD; within it, column
+    // blocks of 8 row tiles, rows fastest, so that the tiles in flight on an
+    // XCD share operand panels in its L2.
+    const int tm = (rows + BM - 1) / BM, tn = (cols + BN - 1) / BN, T = tm * tn;
+    const int T8 = (T + kXcdCount - 1) / kXcdCount;
+    const int L = (int)(blockIdx.x % kXcdCount) * T8 + (int)(blockIdx.x / kXcdCount);
+    if (L >= T)
+        return;
+    constexpr int GM = 8;
+    const int band = L / (GM * tn), bm = min(GM, tm - band * GM), in = L - band * GM * tn;
+    const int m0 = (band * GM + in % bm) * BM, n0 = (in / bm) * BN;
+    const int KT = (K + kStep - 1) / kStep;
+    const int kb = (int)((int64_t)blockIdx.y * KT / gridDim.y);
+    const int ke = (int)((int64_t)(blockIdx.y + 1) * KT / gridDim.y);
+
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wv / WN, wn = wv % WN;
+
+    // Copy sources: per wave copy one 16-byte chunk per lane. Row-major tile:
+    // row r of 8 chunks, chunk c kept at position c ^ f(r); tile stored the
+    // other way: row k of BM/8 (BN/8) chunks, chunk c at c ^ g(k). Rows and
+    // columns past the edge read a valid place (their products are not stored).
+    auto fa = [](int r) { return (r >> 1) & 7; };                       // 16 adjacent rows
+    auto fb = [](int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); };    // rows 16 i + 4 j + 0..3
+    auto ga = [](int k) { return 2 * ((k & 3) | ((k >> 1) & 4)); };
+    auto gb = [](int k) { return (k & 1) | ((k & 2) << 2); };
+    const unsigned short *pa[IA], *pb[IB];
+    int ka[IA], kbb[IB];   // K offset (elements) of the lane's chunk within the step
+#pragma unroll
+    for (int i = 0; i < IA; ++i) {
+        const int q = (wv * IA + i) * 64 + lane;
+        if constexpr (AT) {
+            const int r = q / (BM / 8), c = (q % (BM / 8)) ^ ga(r);
+            ka[i] = r;
+            pa[i] = A + min(m0 + 8 * c, rows - 8);
+        } else {
+            const int r = q / 8, c = (q % 8) ^ fa(r);
+            ka[i] = 8 * c;
+            pa[i] = A + (int64_t)min(m0 + r, rows - 1) * K;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+        const int q = (wv * IB + i) * 64 + lane;
+        if constexpr (BT) {
+            const int r = q / (BN / 8), c = (q % (BN / 8)) ^ gb(r);
+            kbb[i] = r;
+            pb[i] = B + min(n0 + 8 * c, cols - 8);
+        } else {
+            const int r = q / 8, c = (q % 8) ^ fb(r);
+            kbb[i] = 8 * c;
+            pb[i] = B + (int64_t)min(n0 + r, cols - 1) * K;
+        }
+    }
+    const unsigned base = lds_address(smem);
+    auto issue = [&](int kt) {
+        const unsigned st = base + (unsigned)(kt & 1) * STAGE;
+#pragma unroll
+        for (int i = 0; i < IA; ++i) {
+            const unsigned dst = st + (unsigned)(wv * IA + i) * 1024;
+            if constexpr (AT)
+                copy_to_lds(dst, pa[i] + (int64_t)min(kt * kStep + ka[i], K - 1) * rows);
+            else
+                copy_to_lds(dst, pa[i] + min(kt * kStep + ka[i], K - 8));
+        }
+#pragma unroll
+        for (int i = 0; i < IB; ++i) {
+            const unsigned dst = st + ABYTES + (unsigned)(wv * IB + i) * 1024;
+            if constexpr (BT)
+                copy_to_lds(dst, pb[i] + (int64_t)min(kt * kStep + kbb[i], K - 1) * cols);
+            else
+                copy_to_lds(dst, pb[i] + min(kt * kStep + kbb[i], K - 8));
+        }
+    };
+    // chunks of the last step that lie past K, in both operands
+    auto zero_tail = [&](int kt) {
+        char *st = smem + (kt & 1) * STAGE;
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        for (int q = threadIdx.x; q < ABYTES / 16; q += NW * 64) {
+            const int k = AT ? q / (BM / 8) : 8 * ((q % 8) ^ fa(q / 8));
+            if (kt * kStep + k >= K)
+                *reinterpret_cast<u32x4 *>(st + q * 16) = zero;
+        }
+        for (int q = threadIdx.x; q < BBYTES / 16; q += NW * 64) {
+            const int k = BT ? q / (BN / 8) : 8 * ((q % 8) ^ fb(q / 8));
+            if (kt * kStep + k >= K)
+                *reinterpret_cast<u32x4 *>(st + ABYTES + q * 16) = zero;
+        }
+    };
+    const int l16 = lane & 15, g = lane >> 4;
+    auto frag_a = [&](const char *st, int ks, int i) {
+        if constexpr (AT) {
+            const int col = wm * FM * 16 + i * 16 + 4 * (l16 & 3);
+            s16x4 q[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = ks * 32 + 8 * g + 4 * h + (l16 >> 2);
+                q[h] = read_transposed(st + k * BM * 2 + (((col >> 3) ^ ga(k)) << 4) +
+                                       (col & 7) * 2);
+            }
+            return __builtin_bit_cast(bf16x8,
+                                      __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int r = wm * FM * 16 + i * 16 + l16;
+            return *reinterpret_cast<const bf16x8 *>(st + r * 128 + (((ks * 4 + g) ^ fa(r)) << 4));
+        }
+    };
+    // fragment j of the wave's 64 columns: its index i is column 16 (i / 4) + 4 j + i % 4
+    auto frag_b = [&](const char *st, int ks, int j) {
+        st += ABYTES;
+        if constexpr (BT) {
+            const int col = wn * 64 + 16 * (l16 & 3) + 4 * j;
+            s16x4 q[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = ks * 32 + 8 * g + 4 * h + (l16 >> 2);
+                q[h] = read_transposed(st + k * BN * 2 + (((col >> 3) ^ gb(k)) << 4) +
+                                       (col & 7) * 2);
+            }
+            return __builtin_bit_cast(bf16x8,
+                                      __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int r = wn * 64 + 16 * (l16 >> 2) + 4 * j + (l16 & 3);
+            return *reinterpret_cast<const bf16x8 *>(st + r * 128 + (((ks * 4 + g) ^ fb(r)) << 4));
+        }
+    };
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (kb < ke)
+        issue(kb);
+    for (int kt = kb; kt < ke; ++kt) {
+        wait_loads();
+        barrier_lds();
+        if (kt + 1 < ke)
+            issue(kt + 1);
+        if (kt == KT - 1 && K % kStep != 0) {
+            zero_tail(kt);
+            barrier_lds();
+        }
+        const char *st = smem + (kt & 1) * STAGE;
+        bf16x8 fA[2][FM], fB[2][FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            fB[0][j] = frag_b(st, 0, j);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            fA[0][i] = frag_a(st, 0, i);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            if (ks == 0) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    fB[1][j] = frag_b(st, 1, j);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    fA[1][i] = frag_a(st, 1, i);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fB[ks][j], fA[ks][i],
+                                                                         acc[i][j], 0, 0, 0);
+        }
+    }
+    // lane: row l16 of each 16-row strip, 16 adjacent columns
+    const int n = n0 + wn * 64 + 16 * g, valid = min(16, cols - n);
+    if (valid <= 0)
+        return;
+    float bias[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+        bias[c] = 0.f;
+    if (ep.bias && !part) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            if (4 * h < valid) {
+                const f32x4 t = *reinterpret_cast<const f32x4 *>(ep.bias + n + 4 * h);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    bias[4 * h + c] = t[c];
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int m = m0 + wm * FM * 16 + i * 16 + l16;
+        if (m >= rows)
+            continue;
+        const int64_t o = (int64_t)m * cols + n;
+        if (part) {
+            float *dst = part + (int64_t)blockIdx.y * rows * cols + o;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                if (4 * j < valid)
+                    *reinterpret_cast<f32x4 *>(dst + 4 * j) = acc[i][j];
+            continue;
+        }
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[4 * j + q] = acc[i][j][q];
+        store_columns<16>(ep, o, v, bias, valid);
+    }
+}
+
+// The sum of S partials in order, then the epilogue; 8 columns per thread.
+__global__ __launch_bounds__(256) void linear_join_kernel(const float *__restrict__ part, int S,
+                                                          int64_t rows, int cols, Epilogue ep) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int64_t n = rows * cols;
+    if (i >= n)
+        return;
+    f32x4 a = *reinterpret_cast<const f32x4 *>(part + i);
+    f32x4 c = *reinterpret_cast<const f32x4 *>(part + i + 4);
+    for (int s = 1; s < S; ++s) {
+        a += *reinterpret_cast<const f32x4 *>(part + s * n + i);
+        c += *reinterpret_cast<const f32x4 *>(part + s * n + i + 4);
+    }
+    float v[8], b[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[q] = a[q];
+        v[4 + q] = c[q];
+    }
+    const int col = (int)(i % cols);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        b[q] = ep.bias ? ep.bias[col + q] : 0.f;
+    store_columns<8>(ep, i, v, b, 8);
+}
+
+// Few rows: 16 output columns per workgroup, kFewWaves waves over K.
+constexpr int kFewWaves = 16;
+template <int TT>
+__global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(
+    const unsigned short *__restrict__ x, const unsigned short *__restrict__ W, int N, int M,
+    int K, Epilogue ep) {
+    __shared__ f32x4 part[kFewWaves][TT][64];
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c0 = blockIdx.x * 16;
+    const unsigned short *w = W + (int64_t)min(c0 + (lane & 15), M - 1) * K;
+    const unsigned short *xt[TT];
+    f32x4 acc[TT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        xt[i] = x + (int64_t)min(i * 16 + (lane & 15), N - 1) * K;
+        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const int steps = (K + 31) / 32;
+    const int kb = (int)((int64_t)wv * steps / kFewWaves) * 32;
+    const int ke = (int)((int64_t)(wv + 1) * steps / kFewWaves) * 32;
+    skinny_mma<TT, 1, TT == 1 ? 4 : TT == 2 ? 3 : 2>(w, xt, 0, kb, ke, K, acc);
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+        part[wv][i][lane] = acc[i];
+    __syncthreads();
+    // thread -> (row, 8 columns): lanes l and l + 16 of a tile hold columns
+    // 4 (l / 16) + 0..3 and the next four of row l % 16
+    for (int q = threadIdx.x; q < TT * 32; q += kFewWaves * 64) {
+        const int i = q >> 5, l = (q & 15) + 32 * ((q >> 4) & 1);
+        const int r = i * 16 + (l & 15), c = c0 + 4 * (l >> 4);
+        if (r >= N || c >= M)
+            continue;
+        f32x4 a = part[0][i][l], b4 = part[0][i][l + 16];
+#pragma unroll
+        for (int s = 1; s < kFewWaves; ++s) {
+            a += part[s][i][l];
+            b4 += part[s][i][l + 16];
+        }
+        float v[8], b[8];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            v[s] = a[s];
+            v[4 + s] = b4[s];
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            b[s] = ep.bias ? ep.bias[c + s] : 0.f;
+        store_columns<8>(ep, (int64_t)r * M + c, v, b, 8);
+    }
+}
+
+// dz = dout act'(z) in bf16 (not written without an activation) and, with
+// part, the fp32 column sums of this workgroup's rows before the rounding
+// (part [gridDim.y][M]). 8 columns per thread: 32 threads across 256
+// columns, 8 rows at a time.
+__global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__restrict__ dout,
+                                                        const unsigned short *__restrict__ z,
+                                                        int N, int M, int act, int rows_per_wg,
+                                                        unsigned short *__restrict__ dz,
+                                                        float *__restrict__ part) {
+    __shared__ float red[8][256 + 8];
+    const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+    const int c = blockIdx.x * 256 + cx * 8;
+    const int r0 = blockIdx.y * rows_per_wg, r1 = min(N, r0 + rows_per_wg);
+    float s[8] = {};
+    if (c < M) {
+#pragma unroll 2
+        for (int r = r0 + ry; r < r1; r += 8) {
+            const int64_t o = (int64_t)r * M + c;
+            const u32x4 gr = *reinterpret_cast<const u32x4 *>(dout + o);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(gr[i] << 16);
+                v[2 * i + 1] = __uint_as_float(gr[i] & 0xffff0000u);
+            }
+            if (act != kActNone) {
+                const u32x4 zr = *reinterpret_cast<const u32x4 *>(z + o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float zl = __uint_as_float(zr[i] << 16);
+                    const float zh = __uint_as_float(zr[i] & 0xffff0000u);
+                    if (act == kActRelu) {   // a choice, so that a masked infinity gives 0
+                        v[2 * i] = zl > 0.f ? v[2 * i] : 0.f;
+                        v[2 * i + 1] = zh > 0.f ? v[2 * i + 1] : 0.f;
+                    } else {
+                        v[2 * i] *= act_gelu_grad(zl);
+                        v[2 * i + 1] *= act_gelu_grad(zh);
+                    }
+                }
+                *reinterpret_cast<u32x4 *>(dz + o) =
+                    u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s[i] += v[i];
+        }
+    }
+    if (!part)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        red[ry][cx * 8 + i] = s[i];
+    __syncthreads();
+    const int cc = blockIdx.x * 256 + threadIdx.x;
+    if (cc < M) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t += red[i][threadIdx.x];
+        part[(int64_t)blockIdx.y * M + cc] = t;
+    }
+}
+
+// Tile and K-ranges of a product of rows x cols over K. 256x256 tiles (one
+// workgroup of 8 waves per CU) when they fill the 256 CUs about once, else
+// 128x128 (two workgroups per CU) with the reduction cut so that about 512
+// workgroups run, each with at least 4 K-steps.
+struct Shape {
+    bool big;
+    int splits;
+};
+Shape shape_of(int64_t rows, int64_t cols, int64_t K) {
+    const int64_t big = ((rows + 255) / 256) * ((cols + 255) / 256);
+    if (big >= 192)
+        return {true, 1};
+    const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
+    const int64_t KT = (K + kStep - 1) / kStep;
+    int64_t s = std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), KT / 4);
+    s = std::min<int64_t>(std::max<int64_t>(s, 1), 16);
+    return {false, (int)s};
+}
+size_t part_bytes(int64_t rows, int64_t cols, int64_t K) {
+    const Shape sh = shape_of(rows, cols, K);
+    return sh.splits > 1 ? (size_t)(sh.splits * rows * cols) * sizeof(float) : 0;
+}
+
+template <bool AT, bool BT>
+hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t cols, int64_t K,
+                          const Epilogue &ep, float *part, hipStream_t s) {
+    const Shape sh = shape_of(rows, cols, K);
+    const auto *a = static_cast<const unsigned short *>(A);
+    const auto *b = static_cast<const unsigned short *>(B);
+    if (sh.big) {
+        const int64_t T = ((rows + 255) / 256) * ((cols + 255) / 256);
+        const int64_t grid = (T + kXcdCount - 1) / kXcdCount * kXcdCount;
+        hipLaunchKernelGGL((linear_kernel<256, 256, 2, 4, AT, BT>), dim3((unsigned)grid), dim3(512),
+                           0, s, a, b, (int)rows, (int)cols, (int)K, ep, (float *)nullptr);
+        return hipGetLastError();
+    }
+    const int64_t T = ((rows + 127) / 128) * ((cols + 127) / 128);
+    const int64_t grid = (T + kXcdCount - 1) / kXcdCount * kXcdCount;
+    hipLaunchKernelGGL((linear_kernel<128, 128, 2, 2, AT, BT>),
+                       dim3((unsigned)grid, (unsigned)sh.splits), dim3(256), 0, s, a, b, (int)rows,
+                       (int)cols, (int)K, ep, sh.splits > 1 ? part : (float *)nullptr);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || sh.splits == 1)
+        return err;
+    hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)((rows * cols / 8 + 255) / 256)),
+                       dim3(256), 0, s, (const float *)part, sh.splits, rows, (int)cols, ep);
+    return hipGetLastError();
+}
+
+// Rows of the column-sum partials of the dz pass: workgroups along N.
+int dz_groups(int64_t N, int64_t M) {
+    const int64_t across = (M + 255) / 256;
+    const int64_t want = std::max<int64_t>(1, 2048 / across);
+    return (int)std::min<int64_t>(want, (N + 31) / 32);
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t linear_bytes(int64_t N, int64_t K, int64_t M) {
+    return N <= kFewMaxTokens ? 0 : part_bytes(N, M, K);
+}
+
+hipError_t launch_linear(const void *x, const void *W, const float *bias, int act,
+                         const void *residual, int64_t N, int64_t K, int64_t M, void *out, void *z,
+                         void *ws, hipStream_t s) {
+    const Epilogue ep{static_cast<unsigned short *>(out), nullptr, bias,
+                      static_cast<const unsigned short *>(residual),
+                      static_cast<unsigned short *>(z), act};
+    if (N <= kFewMaxTokens) {
+        auto go = [&](auto tiles) {
+            hipLaunchKernelGGL(linear_few_kernel<decltype(tiles)::value>,
+                               dim3((unsigned)((M + 15) / 16)), dim3(kFewWaves * 64), 0, s,
+                               static_cast<const unsigned short *>(x),
+                               static_cast<const unsigned short *>(W), (int)N, (int)M, (int)K, ep);
+            return hipGetLastError();
+        };
+        return N <= 16   ? go(std::integral_constant<int, 1>{})
+               : N <= 32 ? go(std::integral_constant<int, 2>{})
+                         : go(std::integral_constant<int, 4>{});
+    }
+    return launch_product<false, false>(x, W, N, M, K, ep, static_cast<float *>(ws), s);
+}
+
+LinearBackwardLayout linear_backward_layout(int64_t N, int64_t K, int64_t M, bool act) {
+    LinearBackwardLayout L;
+    size_t o = 0;
+    L.dz = o;   o += act ? up256((size_t)(N * M) * 2) : 0;
+    L.sums = o; o += up256((size_t)dz_groups(N, M) * M * sizeof(float));
+    L.part = o; o += up256(std::max(part_bytes(N, K, M), part_bytes(M, K, N)));
+    L.total = o;
+    return L;
+}
+
+hipError_t launch_linear_backward(const void *x, const void *W, const void *z, int act,
+                                  const void *dout, int64_t N, int64_t K, int64_t M, void *dx,
+                                  bool dx32, void *dW, bool dW32, float *db, void *ws,
+                                  hipStream_t s) {
+    const LinearBackwardLayout L = linear_backward_layout(N, K, M, act != kActNone);
+    char *w = static_cast<char *>(ws);
+    const void *dz = dout;
+    if (act != kActNone || db) {
+        const int P = dz_groups(N, M);
+        const int per = (int)((N + P - 1) / P);
+        float *sums = reinterpret_cast<float *>(w + L.sums);
+        hipLaunchKernelGGL(linear_dz_kernel, dim3((unsigned)((M + 255) / 256), (unsigned)P),
+                           dim3(256), 0, s, static_cast<const unsigned short *>(dout),
+                           static_cast<const unsigned short *>(z), (int)N, (int)M, act, per,
+                           reinterpret_cast<unsigned short *>(w + L.dz), db ? sums : nullptr);
+        hipError_t err = hipGetLastError();
+        if (err == hipSuccess && db)
+            err = launch_chunk_sum(sums, P, M, db, s);
+        if (err != hipSuccess)
+            return err;
+        if (act != kActNone)
+            dz = w + L.dz;
+    }
+    float *part = reinterpret_cast<float *>(w + L.part);
+    auto plain = [](void *o, bool f32) {
+        return Epilogue{f32 ? nullptr : static_cast<unsigned short *>(o),
+                        f32 ? static_cast<float *>(o) : nullptr, nullptr, nullptr, nullptr,
+                        kActNone};
+    };
+    if (dx) {
+        hipError_t err = launch_product<false, true>(dz, W, N, K, M, plain(dx, dx32), part, s);
+        if (err != hipSuccess)
+            return err;
+    }
+    if (dW)
+        return launch_product<true, true>(dz, x, M, K, N, plain(dW, dW32), part, s);
+    return hipSuccess;
+}
+
+}  // namespace moe

@@ -1232,3 +1232,411 @@ static int forward_state(const BwdLayout &L, char *ws, const moe_tensor *x,
                                     o.drop, reinterpret_cast<signed char *>(ws + L.Ysh)));
     return MOE_OK;
 }
+
+// ---------------------------------------------------------------------------
+// The layer for a few tokens
+// ---------------------------------------------------------------------------
+namespace {
+
+// Workspace of moe_forward_few: routing, the down product's plan, H (two bf16
+// terms per value, or fp32) and the router's scratch.
+struct FewLayout {
+    size_t idx, gate, plan, H, router, total;
+};
+FewLayout few_layout_of(const Dims &m) {
+    FewLayout L;
+    size_t o = 0;
+    const size_t nk = (size_t)m.N * m.k;
+    L.idx = o;    o += align_up(nk * 4);
+    L.gate = o;   o += align_up(nk * 4);
+    L.plan = o;   o += align_up(moe::few_plan_bytes());
+    L.H = o;      o += align_up(nk * (size_t)m.d_ff * 4);
+    L.router = o; o += router_bytes(m.N, m.d, m.E, m.dtype);
+    L.total = o;
+    return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_few_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k,
+                              float capacity_factor, int32_t dtype) {
+    if (!valid_dtype(dtype) || !cf_ok(capacity_factor))
+        return 0;
+    if (N < 0 || N > MOE_FEW_MAX_TOKENS || E <= 0 || k < 1 || k > E)
+        return 0;
+    Dims m{N, d, E, d_ff, k, 0, 0, dtype};
+    m.C = capacity_of(N, E, k, capacity_factor);
+    m.ceff = m.C < N ? m.C : N;
+    if (check_sizes(m) != MOE_OK)
+        return 0;
+    return few_layout_of(m).total;
+}
+
+int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
+                    const moe_tensor *W_up, const moe_tensor *W_down,
+                    const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
+                    moe_stats *stats) {
+    if (!stats || !W_up || !W_down || !out)
+        return MOE_ERR_NULL;
+    int64_t N, d, E;
+    int rc = check_router_args(x, W_g, noise, k, N, d, E);
+    if (rc != MOE_OK)
+        return rc;
+    if (!cf_ok(capacity_factor))
+        return MOE_ERR_ARG;
+    if (W_up->dtype != x->dtype || W_down->dtype != x->dtype || out->dtype != x->dtype)
+        return MOE_ERR_DTYPE;
+    if (W_up->ndim != 3 || W_down->ndim != 3)
+        return MOE_ERR_SHAPE;
+    const int64_t d_ff = W_up->shape[1];
+    if (W_up->shape[0] != E || W_up->shape[2] != d || W_down->shape[0] != E ||
+        W_down->shape[1] != d || W_down->shape[2] != d_ff)
+        return MOE_ERR_SHAPE;
+    ExpertOpts o;
+    rc = check_opts(opts, E, d, d_ff, o);
+    if (rc != MOE_OK)
+        return rc;
+    if (o.drop.on)
+        return MOE_ERR_UNSUPPORTED;   // dropout belongs to training: moe_forward_ex
+    int64_t oN, od;
+    if (!act_rows(out, oN, od) || oN != N || od != d)
+        return MOE_ERR_SHAPE;
+    if (N > MOE_FEW_MAX_TOKENS)
+        return MOE_ERR_UNSUPPORTED;
+    Dims m{N, d, E, d_ff, k, 0, 0, x->dtype};
+    m.C = capacity_of(N, E, k, capacity_factor);
+    m.ceff = m.C < N ? m.C : N;
+    rc = check_sizes(m);
+    if (rc != MOE_OK)
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stats->stream);
+    if (N == 0) {
+        stats->capacity = 0;
+        if (stats->used_capacity)
+            MOE_TRY(moe::launch_fill_i32(stats->used_capacity, E, 0, s));
+        return zero_router_stats(E, stats->expert_demand, stats->expert_drops,
+                                 stats->expert_gate_sum, s);
+    }
+    if (!W_up->data || !W_down->data || !out->data || !stats->workspace)
+        return MOE_ERR_NULL;
+    if (!aligned(stats->workspace, kAlign))
+        return MOE_ERR_ALIGN;
+    if (x->dtype == MOE_BF16 &&
+        (!aligned(W_up->data, 16) || !aligned(W_down->data, 16) || !aligned(out->data, 16)))
+        return MOE_ERR_ALIGN;
+    const FewLayout L = few_layout_of(m);
+    if (stats->workspace_bytes < L.total)
+        return MOE_ERR_WORKSPACE;
+    stats->capacity = m.C;
+    char *ws = static_cast<char *>(stats->workspace);
+    int32_t *idx = stats->topk_idx ? stats->topk_idx : reinterpret_cast<int32_t *>(ws + L.idx);
+    float *gate = stats->topk_gate ? stats->topk_gate : reinterpret_cast<float *>(ws + L.gate);
+    rc = router_checked(x, W_g, noise, N, d, E, k, idx, gate, ws + L.router, s);
+    if (rc != MOE_OK)
+        return rc;
+    return hip_status(moe::launch_few(x->dtype == MOE_BF16, x->data, W_up->data, W_down->data,
+                                      o.b_up, o.b_down, idx, gate, N, d, (int)E, d_ff, k, m.ceff,
+                                      o.act, ws + L.H, ws + L.plan, out->data, stats->slot,
+                                      stats->used_capacity, stats->expert_demand,
+                                      stats->expert_drops, stats->expert_gate_sum, s));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Layer norm
+// ---------------------------------------------------------------------------
+namespace {
+
+// A [n] fp32 vector (optional: NULL stays NULL).
+int check_vec(const moe_tensor *v, int64_t n, bool required, const float *&p) {
+    p = nullptr;
+    if (!v)
+        return required ? MOE_ERR_NULL : MOE_OK;
+    if (v->dtype != MOE_F32)
+        return MOE_ERR_DTYPE;
+    if (v->ndim != 1 || v->shape[0] != n)
+        return MOE_ERR_SHAPE;
+    if (n > 0 && !v->data)
+        return MOE_ERR_NULL;
+    p = static_cast<const float *>(v->data);
+    return MOE_OK;
+}
+
+// Rows [N, d] of the type of x (optional: NULL stays NULL).
+int check_rows(const moe_tensor *t, int64_t N, int64_t d, int32_t dtype, bool required,
+               void *&p) {
+    p = nullptr;
+    if (!t)
+        return required ? MOE_ERR_NULL : MOE_OK;
+    if (t->dtype != dtype)
+        return MOE_ERR_DTYPE;
+    int64_t tN, td;
+    if (!act_rows(t, tN, td) || tN != N || td != d)
+        return MOE_ERR_SHAPE;
+    if (N > 0 && !t->data)
+        return MOE_ERR_NULL;
+    p = t->data;
+    return MOE_OK;
+}
+
+// x of a norm: extents, type and limits.
+int check_norm_x(const moe_tensor *x, int64_t &N, int64_t &d) {
+    if (!x)
+        return MOE_ERR_NULL;
+    if (!act_rows(x, N, d))
+        return MOE_ERR_SHAPE;
+    if (!valid_dtype(x->dtype))
+        return MOE_ERR_DTYPE;
+    if (N > 0 && !x->data)
+        return MOE_ERR_NULL;
+    if (d > MOE_NORM_MAX_WIDTH || N >= ((int64_t)1 << 40) ||
+        (x->dtype == MOE_BF16 && d % 8 != 0))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+template <typename... P>
+bool all_aligned16(P... p) { return (aligned(p, 16) && ...); }
+
+}  // namespace
+
+extern "C" {
+
+int moe_layer_norm(const moe_tensor *x, const moe_tensor *residual, const moe_tensor *weight,
+                   const moe_tensor *bias, float eps, moe_tensor *h, moe_tensor *out,
+                   moe_tensor *mean, moe_tensor *rstd, void *stream) {
+    int64_t N, d;
+    int rc = check_norm_x(x, N, d);
+    if (rc != MOE_OK)
+        return rc;
+    if (!(eps > 0.f) || !isfinite(eps))
+        return MOE_ERR_ARG;
+    const float *w, *b, *mp, *rp;
+    void *r, *hp, *op;
+    if ((rc = check_vec(weight, d, true, w)) != MOE_OK ||
+        (rc = check_vec(bias, d, false, b)) != MOE_OK ||
+        (rc = check_vec(mean, N, false, mp)) != MOE_OK ||
+        (rc = check_vec(rstd, N, false, rp)) != MOE_OK ||
+        (rc = check_rows(residual, N, d, x->dtype, false, r)) != MOE_OK ||
+        (rc = check_rows(h, N, d, x->dtype, residual != nullptr, hp)) != MOE_OK ||
+        (rc = check_rows(out, N, d, x->dtype, true, op)) != MOE_OK)
+        return rc;
+    if (h && !residual)
+        return MOE_ERR_ARG;   // without a residual, h is x itself
+    if (N == 0)
+        return MOE_OK;
+    if (hp && hp == op)
+        return MOE_ERR_ARG;
+    const bool al = all_aligned16((const void *)x->data, r, hp, op, w, b);
+    const bool bf16 = x->dtype == MOE_BF16;
+    if (bf16 && !al)
+        return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_layer_norm(bf16, bf16 || (al && d % 4 == 0), x->data, r, w, b,
+                                             eps, N, d, hp, op, const_cast<float *>(mp),
+                                             const_cast<float *>(rp),
+                                             static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_layer_norm_backward_workspace_size(int64_t N, int64_t d) {
+    if (N < 0 || d <= 0 || d > MOE_NORM_MAX_WIDTH)
+        return 0;
+    return align_up(moe::layer_norm_backward_bytes(N, d));
+}
+
+int moe_layer_norm_backward(const moe_tensor *x, const moe_tensor *weight, const moe_tensor *mean,
+                            const moe_tensor *rstd, const moe_tensor *dout,
+                            const moe_tensor *dres, moe_tensor *dx, moe_tensor *dweight,
+                            moe_tensor *dbias, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+    int64_t N, d;
+    int rc = check_norm_x(x, N, d);
+    if (rc != MOE_OK)
+        return rc;
+    const float *w, *m, *rs, *dw, *db;
+    void *g, *r, *dxp;
+    if ((rc = check_vec(weight, d, true, w)) != MOE_OK ||
+        (rc = check_vec(mean, N, true, m)) != MOE_OK ||
+        (rc = check_vec(rstd, N, true, rs)) != MOE_OK ||
+        (rc = check_vec(dweight, d, true, dw)) != MOE_OK ||
+        (rc = check_vec(dbias, d, false, db)) != MOE_OK ||
+        (rc = check_rows(dout, N, d, x->dtype, true, g)) != MOE_OK ||
+        (rc = check_rows(dres, N, d, x->dtype, false, r)) != MOE_OK ||
+        (rc = check_rows(dx, N, d, x->dtype, true, dxp)) != MOE_OK)
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (N == 0) {
+        // no rows: the sums over them are zero (fill kernels: the call may be captured)
+        MOE_TRY(moe::launch_fill_i32(reinterpret_cast<int32_t *>(const_cast<float *>(dw)), d, 0,
+                                     s));
+        if (db)
+            MOE_TRY(moe::launch_fill_i32(reinterpret_cast<int32_t *>(const_cast<float *>(db)), d,
+                                         0, s));
+        return MOE_OK;
+    }
+    if (dxp == x->data)
+        return MOE_ERR_ARG;
+    const bool al = all_aligned16((const void *)x->data, g, r, dxp, w);
+    const bool bf16 = x->dtype == MOE_BF16;
+    if (bf16 && !al)
+        return MOE_ERR_ALIGN;
+    if (!workspace)
+        return MOE_ERR_NULL;
+    if (!aligned(workspace, kAlign))
+        return MOE_ERR_ALIGN;
+    if (workspace_bytes < moe::layer_norm_backward_bytes(N, d))
+        return MOE_ERR_WORKSPACE;
+    return hip_status(moe::launch_layer_norm_backward(
+        bf16, bf16 || (al && d % 4 == 0), x->data, w, m, rs, g, r, N, d, dxp,
+        const_cast<float *>(dw), const_cast<float *>(db), static_cast<float *>(workspace), s));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Linear product
+// ---------------------------------------------------------------------------
+namespace {
+
+// x [N, K] and W [M, K] of a linear product (bf16), the activation.
+int check_linear(const moe_tensor *x, const moe_tensor *W, int32_t act, int64_t &N, int64_t &K,
+                 int64_t &M) {
+    if (!x || !W)
+        return MOE_ERR_NULL;
+    if (!act_rows(x, N, K))
+        return MOE_ERR_SHAPE;
+    if (!valid_dtype(x->dtype) || W->dtype != x->dtype)
+        return MOE_ERR_DTYPE;
+    if (W->ndim != 2 || W->shape[1] != K || W->shape[0] <= 0)
+        return MOE_ERR_SHAPE;
+    M = W->shape[0];
+    if (act != MOE_ACT_NONE && act != MOE_ACT_RELU && act != MOE_ACT_GELU)
+        return MOE_ERR_ARG;
+    if (x->dtype != MOE_BF16)
+        return MOE_ERR_UNSUPPORTED;   // bf16 only
+    if (K % 8 != 0 || M % 8 != 0 || N > MOE_LINEAR_MAX_EXTENT || K > MOE_LINEAR_MAX_EXTENT ||
+        M > MOE_LINEAR_MAX_EXTENT)
+        return MOE_ERR_UNSUPPORTED;
+    if (!W->data || (N > 0 && !x->data))
+        return MOE_ERR_NULL;
+    if (!aligned(x->data, 16) || !aligned(W->data, 16))
+        return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+
+int check_scratch(const void *ws, size_t have, size_t need) {
+    if (need == 0)
+        return MOE_OK;
+    if (!ws)
+        return MOE_ERR_NULL;
+    if (!aligned(ws, kAlign))
+        return MOE_ERR_ALIGN;
+    return have < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+bool linear_sizes_ok(int64_t N, int64_t K, int64_t M) {
+    return N > 0 && K > 0 && M > 0 && K % 8 == 0 && M % 8 == 0 && N <= MOE_LINEAR_MAX_EXTENT &&
+           K <= MOE_LINEAR_MAX_EXTENT && M <= MOE_LINEAR_MAX_EXTENT;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_linear_workspace_size(int64_t N, int64_t K, int64_t M) {
+    return linear_sizes_ok(N, K, M) ? align_up(moe::linear_bytes(N, K, M)) : 0;
+}
+
+int moe_linear(const moe_tensor *x, const moe_tensor *W, const moe_tensor *bias,
+               int32_t activation, const moe_tensor *residual, moe_tensor *out, moe_tensor *z,
+               void *workspace, size_t workspace_bytes, void *stream) {
+    int64_t N, K, M;
+    int rc = check_linear(x, W, activation, N, K, M);
+    if (rc != MOE_OK)
+        return rc;
+    const float *b;
+    void *r, *o, *zp;
+    if ((rc = check_vec(bias, M, false, b)) != MOE_OK ||
+        (rc = check_rows(residual, N, M, MOE_BF16, false, r)) != MOE_OK ||
+        (rc = check_rows(out, N, M, MOE_BF16, true, o)) != MOE_OK ||
+        (rc = check_rows(z, N, M, MOE_BF16, false, zp)) != MOE_OK)
+        return rc;
+    if (N == 0)
+        return MOE_OK;
+    if (!all_aligned16(b, r, o, zp))
+        return MOE_ERR_ALIGN;
+    if (zp && (zp == o || zp == r))
+        return MOE_ERR_ARG;
+    rc = check_scratch(workspace, workspace_bytes, moe::linear_bytes(N, K, M));
+    if (rc != MOE_OK)
+        return rc;
+    return hip_status(moe::launch_linear(x->data, W->data, b, activation, r, N, K, M, o, zp,
+                                         workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_linear_backward_workspace_size(int64_t N, int64_t K, int64_t M, int32_t activation) {
+    if (!linear_sizes_ok(N, K, M) || activation < 0 || activation > MOE_ACT_NONE)
+        return 0;
+    return moe::linear_backward_layout(N, K, M, activation != MOE_ACT_NONE).total;
+}
+
+int moe_linear_backward(const moe_tensor *x, const moe_tensor *W, const moe_tensor *z,
+                        int32_t activation, const moe_tensor *dout, moe_tensor *dx,
+                        moe_tensor *dW, moe_tensor *dbias, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    int64_t N, K, M;
+    int rc = check_linear(x, W, activation, N, K, M);
+    if (rc != MOE_OK)
+        return rc;
+    const float *db;
+    void *zp, *g, *dxp = nullptr, *dWp = nullptr;
+    if ((rc = check_rows(z, N, M, MOE_BF16, activation != MOE_ACT_NONE, zp)) != MOE_OK ||
+        (rc = check_rows(dout, N, M, MOE_BF16, true, g)) != MOE_OK ||
+        (rc = check_vec(dbias, M, false, db)) != MOE_OK)
+        return rc;
+    if (activation == MOE_ACT_NONE && z)
+        return MOE_ERR_ARG;   // without an activation nothing reads z
+    if (dx) {
+        if (!valid_dtype(dx->dtype))
+            return MOE_ERR_DTYPE;
+        if ((rc = check_rows(dx, N, K, dx->dtype, true, dxp)) != MOE_OK)
+            return rc;
+    }
+    if (dW) {
+        if (!valid_dtype(dW->dtype))
+            return MOE_ERR_DTYPE;
+        if (dW->ndim != 2 || dW->shape[0] != M || dW->shape[1] != K)
+            return MOE_ERR_SHAPE;
+        if (!dW->data)
+            return MOE_ERR_NULL;
+        dWp = dW->data;
+    }
+    if (!dx && !dW && !db)
+        return MOE_ERR_NULL;   // nothing to compute
+    if (!all_aligned16(zp, g, dxp, dWp))
+        return MOE_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (N == 0) {
+        // no rows: the sums over them are zero (fill kernels: the call may be captured)
+        if (dWp)
+            MOE_TRY(moe::launch_fill_i32(static_cast<int32_t *>(dWp),
+                                         M * K / (dW->dtype == MOE_BF16 ? 2 : 1), 0, s));
+        if (db)
+            MOE_TRY(moe::launch_fill_i32(reinterpret_cast<int32_t *>(const_cast<float *>(db)), M,
+                                         0, s));
+        return MOE_OK;
+    }
+    if ((dxp && (dxp == x->data || dxp == g || dxp == zp)))
+        return MOE_ERR_ARG;   // the weight gradient reads them after dx is written
+    rc = check_scratch(workspace, workspace_bytes,
+                       moe::linear_backward_layout(N, K, M, activation != MOE_ACT_NONE).total);
+    if (rc != MOE_OK)
+        return rc;
+    return hip_status(moe::launch_linear_backward(
+        x->data, W->data, zp, activation, g, N, K, M, dxp, dx && dx->dtype == MOE_F32, dWp,
+        dW && dW->dtype == MOE_F32, const_cast<float *>(db), workspace, s));
+}
+
+}  // extern "C"
