@@ -70,6 +70,7 @@ enum {
 #define MOE_MAX_EXPERTS 256
 #define MOE_MAX_TOPK 16
 #define MOE_FEW_MAX_TOKENS 64      /* tokens of moe_forward_few */
+#define MOE_FEW_MAX_WIDTH (1 << 20)  /* d and d_ff of moe_forward_few */
 #define MOE_NORM_MAX_WIDTH 16384   /* row width of moe_layer_norm */
 #define MOE_LINEAR_MAX_EXTENT (1 << 30)  /* rows and widths of moe_linear */
 
@@ -452,16 +453,18 @@ size_t moe_backward_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff
  * Same conventions as above.
  * ------------------------------------------------------------------------- */
 
-/* moe_forward_ex for at most MOE_FEW_MAX_TOKENS tokens (MOE_ERR_UNSUPPORTED
- * beyond), the form of a decoding step: the same arguments, routing (bit for
- * bit), capacity drops, options and exports, on kernels that stream each hit
- * expert's weights once instead of computing row tiles. Training-mode dropout
- * is refused (MOE_ERR_UNSUPPORTED). Numerics: as moe_forward's, except that a
- * bf16 layer keeps the hidden activation to 16 significant bits (two bf16
- * terms) and the experts' output rows in fp32, so that out carries only its
- * own rounding; the sum over a token's choices runs in ascending expert id.
+/* moe_forward_ex for at most MOE_FEW_MAX_TOKENS tokens and widths d, d_ff up
+ * to MOE_FEW_MAX_WIDTH (MOE_ERR_UNSUPPORTED beyond), the form of a decoding
+ * step: the same arguments, routing, capacity drops, options and exports, on
+ * kernels that stream each hit expert's weights once instead of computing row
+ * tiles. Training-mode dropout is refused (MOE_ERR_UNSUPPORTED). Numerics: as
+ * moe_forward's (scores differ from its only in fp32 summation order), except
+ * that a bf16 layer keeps the hidden activation to 16 significant bits (two
+ * bf16 terms) and the experts' output rows in fp32, so that out carries only
+ * its own rounding; a token's choices are added in ascending expert id.
  * stats->workspace holds moe_few_workspace_size() bytes (256-byte aligned;
- * a size for more tokens serves fewer). Bias data 16-byte aligned, as there. */
+ * a size for more tokens serves fewer). Bias data 16-byte aligned, as there.
+ * out must not overlap x. */
 int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
                     const moe_tensor *W_up, const moe_tensor *W_down,
                     const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,

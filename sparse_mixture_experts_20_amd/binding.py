@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -67,6 +68,7 @@ class MoeError(RuntimeError):
 
 _lib = None
 _T = ctypes.POINTER(MoeTensor)
+_D = ctypes.c_char_p
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 
@@ -153,23 +155,25 @@ def lib():
         L.moe_combine.restype = ctypes.c_int
         L.moe_combine_compact.argtypes = [_i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp, _T, _vp]
         L.moe_combine_compact.restype = ctypes.c_int
-        L.moe_forward_few.argtypes = L.moe_forward_ex.argtypes
+        # (tensor descriptors of these calls are packed bytes, see _pack)
+        L.moe_forward_few.argtypes = [_D, _D, _D, _D, _D, ctypes.POINTER(MoeExpertOpts),
+                                      ctypes.c_int, ctypes.c_float, _D, ctypes.POINTER(MoeStats)]
         L.moe_forward_few.restype = ctypes.c_int
         L.moe_few_workspace_size.argtypes = L.moe_workspace_size.argtypes
         L.moe_few_workspace_size.restype = ctypes.c_size_t
-        L.moe_linear.argtypes = [_T, _T, _T, ctypes.c_int32, _T, _T, _T, _vp, ctypes.c_size_t,
+        L.moe_linear.argtypes = [_D, _D, _D, ctypes.c_int32, _D, _D, _D, _vp, ctypes.c_size_t,
                                  _vp]
         L.moe_linear.restype = ctypes.c_int
         L.moe_linear_workspace_size.argtypes = [_i64, _i64, _i64]
         L.moe_linear_workspace_size.restype = ctypes.c_size_t
-        L.moe_linear_backward.argtypes = [_T, _T, _T, ctypes.c_int32, _T, _T, _T, _T, _vp,
+        L.moe_linear_backward.argtypes = [_D, _D, _D, ctypes.c_int32, _D, _D, _D, _D, _vp,
                                           ctypes.c_size_t, _vp]
         L.moe_linear_backward.restype = ctypes.c_int
         L.moe_linear_backward_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int32]
         L.moe_linear_backward_workspace_size.restype = ctypes.c_size_t
-        L.moe_layer_norm.argtypes = [_T, _T, _T, _T, ctypes.c_float, _T, _T, _T, _T, _vp]
+        L.moe_layer_norm.argtypes = [_D, _D, _D, _D, ctypes.c_float, _D, _D, _D, _D, _vp]
         L.moe_layer_norm.restype = ctypes.c_int
-        L.moe_layer_norm_backward.argtypes = [_T, _T, _T, _T, _T, _T, _T, _T, _T, _vp,
+        L.moe_layer_norm_backward.argtypes = [_D, _D, _D, _D, _D, _D, _D, _D, _D, _vp,
                                               ctypes.c_size_t, _vp]
         L.moe_layer_norm_backward.restype = ctypes.c_int
         L.moe_layer_norm_backward_workspace_size.argtypes = [_i64, _i64]
@@ -739,30 +743,64 @@ def combine(Y, gate, slot, out, stream=None):
 # The rest of the feed-forward half: the layer for a few tokens, the linear
 # product, the layer norm
 # --------------------------------------------------------------------------
-def _place(device, tensors):
-    """The tensors' common device; each must be on it (the library takes
-    device pointers of one GPU)."""
-    if device.type != "cuda":
+# A call of these takes a few microseconds on the GPU, so its arguments are
+# marshalled with little Python: a descriptor is the 48 bytes of a moe_tensor
+# (pointer, dtype, rank, extents), handed over as a bytes object.
+_PACK = [struct.Struct("=Qii%dq%dx" % (n, 8 * (4 - n))).pack for n in range(5)]
+_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _pack(t: Optional[torch.Tensor], index: int):
+    """The ``moe_tensor`` of a contiguous tensor on device ``index`` as bytes
+    (None -> NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        raise ValueError(f"a tensor on {t.device}, others on cuda:{index}: the library takes "
+                         "device pointers of one GPU")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    shape = t.shape
+    n = len(shape)
+    if n > 4:
+        raise ValueError("at most 4 dimensions")
+    return _PACK[n](t.data_ptr(), code, n, *shape)
+
+
+def _device_of(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a HIP device")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
+    return index
 
 
-def _run(device, where, fn, *args):
+def _scratch(workspace, index: int):
+    """(pointer, bytes) of a workspace tensor, or (None, 0)."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != index:
+        raise ValueError("the workspace is on another device")
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _stream_of(index: int, stream):
+    return (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
+
+
+def _run(index: int, where: str, fn, *args):
     """Call ``fn(*args)`` with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
+    if index == torch.cuda.current_device():
         rc = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args)
     if rc != 0:
         raise MoeError(rc, where)
-
-
-def _stream_of(device, stream):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
 
 
 def few_workspace_size(N: int, d: int, E: int, d_ff: int, k: int, capacity_factor: float,
@@ -781,10 +819,9 @@ def forward_few(x: torch.Tensor, W_g: torch.Tensor, noise: Optional[torch.Tensor
     arguments and results of :func:`forward`, without dropout."""
     N, d = x.numel() // x.shape[-1], x.shape[-1]
     E, d_ff = W_up.shape[0], W_up.shape[1]
-    dev = x.device
+    dev, index = x.device, _device_of(x)
     if out is None:
         out = torch.empty_like(x)
-    _place(dev, (W_g, noise, W_up, W_down, out, b_up, b_down, workspace))
     if workspace is None:
         workspace = alloc_workspace(few_workspace_size(N, d, E, d_ff, k, capacity_factor, x.dtype),
                                     dev)
@@ -795,14 +832,14 @@ def forward_few(x: torch.Tensor, W_g: torch.Tensor, noise: Optional[torch.Tensor
         slot = torch.empty((N, k), dtype=torch.int32, device=dev)
         used = torch.empty((E,), dtype=torch.int32, device=dev)
     dem, drp, gsum = _router_stats(E, dev, router_stats)
-    st = MoeStats(_stream_of(dev, stream), ctypes.c_void_p(workspace.data_ptr()),
-                  workspace.numel(), _ptr(idx), _ptr(gate), _ptr(slot), _ptr(used), -1, _ptr(dem),
-                  _ptr(drp), _ptr(gsum), None)
-    ds = [desc(t) for t in (x, W_g, noise, W_up, W_down, out)]
-    r = [_ref(t) for t in ds]
+    ws, wn = _scratch(workspace, index)
+    st = MoeStats(_stream_of(index, stream), ws, wn, _ptr(idx), _ptr(gate), _ptr(slot),
+                  _ptr(used), -1, _ptr(dem), _ptr(drp), _ptr(gsum), None)
+    _pack(b_up, index), _pack(b_down, index)   # (same checks as every tensor)
     o = _opts(act, b_up, b_down)
-    _run(dev, "moe_forward_few", lib().moe_forward_few, r[0], r[1], r[2], r[3], r[4],
-         None if o is None else o.ref(), k, capacity_factor, r[5], ctypes.byref(st))
+    _run(index, "moe_forward_few", lib().moe_forward_few, _pack(x, index), _pack(W_g, index),
+         _pack(noise, index), _pack(W_up, index), _pack(W_down, index),
+         None if o is None else o.ref(), k, capacity_factor, _pack(out, index), ctypes.byref(st))
     return out, Stats(idx, gate, slot, used, int(st.capacity), dem, drp, gsum)
 
 
@@ -817,17 +854,15 @@ class FewLayer:
     def __init__(self, W_g, W_up, W_down, k, capacity_factor, act="relu", b_up=None, b_down=None,
                  max_tokens=MOE_FEW_MAX_TOKENS, export=False, router_stats=False):
         E, d_ff, d = W_up.shape
-        dev = W_up.device
+        dev, index = W_up.device, _device_of(W_up)
         self.tensors = (W_g, W_up, W_down, b_up, b_down)
-        self.k, self.cf, self.d, self.max_tokens = k, capacity_factor, d, max_tokens
-        self.device = dev
-        _place(dev, (W_g, W_down, b_up, b_down))
+        self.k, self.cf, self.max_tokens, self.index = k, capacity_factor, max_tokens, index
         n = few_workspace_size(max_tokens, d, E, d_ff, k, capacity_factor, W_up.dtype)
         if n == 0:
             raise ValueError("sizes outside moe_forward_few's limits")
         self.workspace = alloc_workspace(n, dev)
-        self._w = [desc(t) for t in (W_g, W_up, W_down)]
-        self._r = [_ref(t) for t in self._w]
+        self._w = [_pack(t, index) for t in (W_g, W_up, W_down)]
+        _pack(b_up, index), _pack(b_down, index)   # (same checks as every tensor)
         self._opts = _opts(act, b_up, b_down)
         self._o = None if self._opts is None else self._opts.ref()
         idx = gate = slot = used = None
@@ -839,9 +874,9 @@ class FewLayer:
         self._routing = (idx, gate, slot, used)
         self._counts = _router_stats(E, dev, router_stats)
         dem, drp, gsum = self._counts
-        self.stats = MoeStats(None, ctypes.c_void_p(self.workspace.data_ptr()),
-                              self.workspace.numel(), _ptr(idx), _ptr(gate), _ptr(slot),
-                              _ptr(used), -1, _ptr(dem), _ptr(drp), _ptr(gsum), None)
+        self.stats = MoeStats(None, self.workspace.data_ptr(), self.workspace.numel(), _ptr(idx),
+                              _ptr(gate), _ptr(slot), _ptr(used), -1, _ptr(dem), _ptr(drp),
+                              _ptr(gsum), None)
         self._sref = ctypes.byref(self.stats)
         self._fn = lib().moe_forward_few
 
@@ -851,17 +886,14 @@ class FewLayer:
             raise ValueError(f"{N} tokens: this layer was built for {self.max_tokens}")
         if out is None:
             out = torch.empty_like(x)
-        _place(self.device, (x, noise, out))
-        st = self.stats
-        st.stream = _stream_of(self.device, stream)
-        dx, dn, do = desc(x), desc(noise), desc(out)
-        r = self._r
-        _run(self.device, "moe_forward_few", self._fn, _ref(dx), r[0], _ref(dn), r[1], r[2],
-             self._o, self.k, self.cf, _ref(do), self._sref)
+        index, w, st = self.index, self._w, self.stats
+        st.stream = _stream_of(index, stream)
+        _run(index, "moe_forward_few", self._fn, _pack(x, index), w[0], _pack(noise, index), w[1],
+             w[2], self._o, self.k, self.cf, _pack(out, index), self._sref)
         idx, gate, slot, used = self._routing
         if idx is not None and N != self.max_tokens:
             idx, gate, slot = idx[:N], gate[:N], slot[:N]
-        return out, Stats(idx, gate, slot, used, int(st.capacity), *self._counts)
+        return out, Stats(idx, gate, slot, used, st.capacity, *self._counts)
 
 
 def _linear_act(act):
@@ -878,19 +910,18 @@ def linear(x, W, bias=None, act: str = "none", residual=None, out=None, keep_z: 
            workspace=None, stream=None):
     """``act(x W^T + bias) + residual`` (bf16; x [..., K], W [M, K]): returns
     ``(out, z)``, z the bf16 pre-activations with ``keep_z``, else None."""
-    N, K, M = x.numel() // x.shape[-1], x.shape[-1], W.shape[0]
+    K, M = x.shape[-1], W.shape[0]
+    index = _device_of(x)
     if out is None:
         out = torch.empty((*x.shape[:-1], M), dtype=x.dtype, device=x.device)
     z = torch.empty_like(out) if keep_z else None
-    _place(x.device, (W, bias, residual, out, workspace))
     if workspace is None:
-        n = linear_workspace_size(N, K, M)
+        n = linear_workspace_size(x.numel() // K, K, M)
         workspace = alloc_workspace(n, x.device) if n else None
-    wp, wn = _ws_args(workspace)
-    ds = [desc(t) for t in (x, W, bias, residual, out, z)]
-    r = [_ref(t) for t in ds]
-    _run(x.device, "moe_linear", lib().moe_linear, r[0], r[1], r[2], _linear_act(act), r[3], r[4],
-         r[5], wp, wn, _stream_of(x.device, stream))
+    ws, wn = _scratch(workspace, index)
+    _run(index, "moe_linear", lib().moe_linear, _pack(x, index), _pack(W, index),
+         _pack(bias, index), _linear_act(act), _pack(residual, index), _pack(out, index),
+         _pack(z, index), ws, wn, _stream_of(index, stream))
     return out, z
 
 
@@ -904,19 +935,17 @@ def linear_backward(x, W, z, dout, act: str = "none", bias: bool = True, need_dx
     """Gradients of :func:`linear` for ``dout``: ``(dx, dW, dbias)``, None for
     the ones not asked for; z is the forward's (None without an activation)."""
     N, K, M = x.numel() // x.shape[-1], x.shape[-1], W.shape[0]
-    dev = x.device
-    _place(dev, (W, z, dout, workspace))
+    dev, index = x.device, _device_of(x)
     dx = torch.empty(x.shape, dtype=dx_dtype, device=dev) if need_dx else None
     dW = torch.empty((M, K), dtype=dW_dtype, device=dev) if need_dW else None
     db = torch.empty((M,), dtype=torch.float32, device=dev) if bias else None
     if workspace is None:
         n = linear_backward_workspace_size(N, K, M, act)
         workspace = alloc_workspace(n, dev) if n else None
-    wp, wn = _ws_args(workspace)
-    ds = [desc(t) for t in (x, W, z, dout, dx, dW, db)]
-    r = [_ref(t) for t in ds]
-    _run(dev, "moe_linear_backward", lib().moe_linear_backward, r[0], r[1], r[2],
-         _linear_act(act), r[3], r[4], r[5], r[6], wp, wn, _stream_of(dev, stream))
+    ws, wn = _scratch(workspace, index)
+    _run(index, "moe_linear_backward", lib().moe_linear_backward, _pack(x, index),
+         _pack(W, index), _pack(z, index), _linear_act(act), _pack(dout, index),
+         _pack(dx, index), _pack(dW, index), _pack(db, index), ws, wn, _stream_of(index, stream))
     return dx, dW, db
 
 
@@ -925,20 +954,19 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, h=None, o
     """Layer norm of ``x`` (of ``h = x + residual`` when given, h returned):
     ``(out, h, mean, rstd)``; h is x without a residual, mean and rstd (fp32,
     one per row: what the backward needs) are None unless ``stats``."""
-    N = x.numel() // x.shape[-1]
+    index = _device_of(x)
     if out is None:
         out = torch.empty_like(x)
     if residual is not None and h is None:
         h = torch.empty_like(x)
-    _place(x.device, (weight, bias, residual, h, out))
     mean = rstd = None
     if stats:
-        mean = torch.empty((N,), dtype=torch.float32, device=x.device)
-        rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
-    ds = [desc(t) for t in (x, residual, weight, bias, h, out, mean, rstd)]
-    r = [_ref(t) for t in ds]
-    _run(x.device, "moe_layer_norm", lib().moe_layer_norm, r[0], r[1], r[2], r[3], eps, r[4],
-         r[5], r[6], r[7], _stream_of(x.device, stream))
+        N = x.numel() // x.shape[-1]
+        mean = torch.empty(N, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    _run(index, "moe_layer_norm", lib().moe_layer_norm, _pack(x, index), _pack(residual, index),
+         _pack(weight, index), _pack(bias, index), eps, _pack(h, index), _pack(out, index),
+         _pack(mean, index), _pack(rstd, index), _stream_of(index, stream))
     return out, (x if h is None else h), mean, rstd
 
 
@@ -951,18 +979,18 @@ def layer_norm_backward(h, weight, mean, rstd, dout, dres=None, bias: bool = Tru
     """Gradients of :func:`layer_norm` for ``dout`` (and ``dres``, what reaches
     h along the residual path): ``(dx, dweight, dbias)``, dbias None without
     ``bias``. h, mean and rstd are the forward's."""
-    N, d = h.numel() // h.shape[-1], h.shape[-1]
+    d = h.shape[-1]
+    index = _device_of(h)
     if dx is None:
         dx = torch.empty_like(h)
-    _place(h.device, (weight, mean, rstd, dout, dres, dx, workspace))
-    dw = torch.empty((d,), dtype=torch.float32, device=h.device)
-    db = torch.empty((d,), dtype=torch.float32, device=h.device) if bias else None
+    dw = torch.empty(d, dtype=torch.float32, device=h.device)
+    db = torch.empty_like(dw) if bias else None
     if workspace is None:
-        n = layer_norm_backward_workspace_size(N, d)
+        n = layer_norm_backward_workspace_size(h.numel() // d, d)
         workspace = alloc_workspace(n, h.device) if n else None
-    wp, wn = _ws_args(workspace)
-    ds = [desc(t) for t in (h, weight, mean, rstd, dout, dres, dx, dw, db)]
-    r = [_ref(t) for t in ds]
-    _run(h.device, "moe_layer_norm_backward", lib().moe_layer_norm_backward, r[0], r[1], r[2],
-         r[3], r[4], r[5], r[6], r[7], r[8], wp, wn, _stream_of(h.device, stream))
+    ws, wn = _scratch(workspace, index)
+    _run(index, "moe_layer_norm_backward", lib().moe_layer_norm_backward, _pack(h, index),
+         _pack(weight, index), _pack(mean, index), _pack(rstd, index), _pack(dout, index),
+         _pack(dres, index), _pack(dx, index), _pack(dw, index), _pack(db, index), ws, wn,
+         _stream_of(index, stream))
     return dx, dw, db

@@ -302,16 +302,20 @@ hipError_t launch_combine_compact(const void *Y, const signed char *ysh, const f
 // ---------------------------------------------------------------------------
 namespace moe {
 
-// The layer for N <= kFewMaxTokens tokens after its router: H is
-// [2][N k][d_ff] bf16 (two terms) or [N k][d_ff] fp32, plan few_plan_bytes().
-// slot, used, demand, drops, gate_sum may each be NULL.
+// The layer for N <= kFewMaxTokens tokens. Workspace regions (byte offsets):
+// routing, plan, partial scores, H, partial outputs. idx, gate, slot, used,
+// demand, drops, gate_sum may each be NULL. aligned: 16-byte aligned data
+// (fp32 layers; bf16 layers need it).
 constexpr int kFewMaxTokens = 64;
-size_t few_plan_bytes();
-hipError_t launch_few(bool bf16, const void *x, const void *w_up, const void *w_down,
-                      const float *b_up, const float *b_down, const int32_t *idx,
-                      const float *gate, int64_t N, int64_t d, int E, int64_t d_ff, int k,
-                      int64_t ceff, int act, void *H, void *plan, void *out, int32_t *slot,
-                      int32_t *used, int32_t *demand, int32_t *drops, float *gate_sum,
+struct FewLayout {
+    size_t idx, gate, plan, done, scores, H, part, total;
+};
+FewLayout few_layout(bool bf16, int64_t N, int64_t d, int64_t E, int64_t d_ff, int k);
+hipError_t launch_few(bool bf16, bool aligned, const void *x, const float *wg, const float *noise,
+                      const void *w_up, const void *w_down, const float *b_up,
+                      const float *b_down, int64_t N, int64_t d, int E, int64_t d_ff, int k,
+                      int64_t ceff, int act, void *ws, int32_t *idx, float *gate, int32_t *slot,
+                      int32_t *used, int32_t *demand, int32_t *drops, float *gate_sum, void *out,
                       hipStream_t s);
 
 // Layer norm of N rows of d (h = x + res kept when res is given) and its

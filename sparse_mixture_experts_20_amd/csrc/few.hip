@@ -5,27 +5,35 @@
 //
 // With a few tokens every expert that is hit serves a handful of rows, so the
 // call is bound by the stream of the hit experts' weights (2 d d_ff elements
-// each) and, for the smallest layers, by launch latency. After the router:
+// each) and, for the smallest layers, by launch latency:
 //
-//   up:   one workgroup per (hit expert, 16 hidden neurons). Each workgroup
-//         derives what it needs of the dispatch plan from the expert ids
-//         itself (at most 1024 of them): the set of hit experts, its own
-//         expert and that expert's rows in (choice, token) order. No scan
-//         launch, and the grid is sized by min(E, N k) without a host sync.
-//         Four waves split K and add through LDS.
-//   down: one workgroup per 16 output columns walks every hit expert's rows
-//         of those columns, its waves taking contiguous ranges of the
-//         (expert, K-chunk) sequence, and keeps the gate-weighted sums of all
-//         tokens in LDS, one copy per wave, added in wave order: the combine
-//         costs no pass of its own and the result does not depend on timing.
+//   scores: one workgroup per (16 experts, range of d), partial scores to the
+//         workspace (the bf16 layer's fp32 router weights as three exact bf16
+//         terms on the matrix cores, the fp32 layer on fp32 MFMAs).
+//   plan: one workgroup ranks the tokens (top-k and gates of a token per wave,
+//         its partial scores added in range order) and lists the hit experts
+//         and their kept rows in (choice, token) order. With many tokens and
+//         experts the ranking is a launch of its own, a wave per token.
+//   up:   one workgroup per (hit expert, 16 hidden neurons), four waves over K
+//         that add through LDS. The grid is sized by min(E, N k), without a
+//         host sync; workgroups past the last hit expert end at once.
+//   down: one workgroup per (16 output columns, range of the hit experts'
+//         K-chunks); its four waves take contiguous parts of the range and
+//         keep the gate-weighted sums of all tokens in LDS, one copy per wave,
+//         added in wave order. The workgroup of a column block that finishes
+//         last adds the ranges' partial sums in range order and writes the
+//         output: the combine costs no launch and the result does not depend
+//         on which workgroup that is.
 //
-// The hidden row is kept as two bf16 terms (hi + lo, 16 significant bits):
-// the product that reads it is bound by its weights, so the second MFMA is
-// free, and the layer's output then carries only its own final rounding.
+// A bf16 layer's hidden row is kept as two bf16 terms (hi + lo, 16 significant
+// bits): the product that reads it is bound by its weights, so the second MFMA
+// is free, and the layer's output then carries only its own final rounding.
+#include <algorithm>
 #include <type_traits>
 
 #include "activation.hpp"
 #include "common.hpp"
+#include "ranking.hpp"
 #include "skinny.hpp"
 
 namespace moe {
@@ -34,9 +42,12 @@ namespace {
 constexpr int kFewTokens = kFewMaxTokens;
 constexpr int kFewAssign = kFewTokens * kMaxTopK;   // assignments of a call
 constexpr int kChunk = 256;                         // K elements of one down unit
+constexpr int kScoreRange = 512;                    // columns of d per score range
+constexpr int kWaves = 4;                           // waves of a workgroup
+constexpr int kThreads = kWaves * 64;
+constexpr int kPlanWaves = 16;                      // waves of the plan's workgroup
 
-// Dispatch plan of the call, written by the up product, read by the down
-// product (device, in the workspace).
+// Dispatch plan of the call (device, in the workspace).
 struct FewPlan {
     int nhit;                              // experts with a kept row
     int expert[kMaxExperts];               // their ids, ascending
@@ -44,162 +55,397 @@ struct FewPlan {
     int row[kMaxExperts][kFewTokens];      // their assignments, slot order
 };
 
-// What a workgroup of the up product derives from the ids: the a-th hit expert
-// and its kept rows. All threads of the workgroup (a multiple of 64, at least
-// 64) call it; ends with a barrier. Returns the number of hit experts.
-struct PlanShared {
-    unsigned mask[kMaxExperts / 32];
-    unsigned char id[kFewAssign];      // expert of assignment (j, t) at j N + t
-    int row[kFewTokens];
-    int expert, count, kept;
+// Where the layer's types differ: the hidden row's storage and its terms.
+template <typename S>
+struct Kind {
+    static constexpr bool bf16 = std::is_same<S, SkinnyBf16>::value;
+    typedef typename S::type type;
+    static constexpr int terms = bf16 ? 2 : 1;   // operand terms of a hidden row
 };
-__device__ __forceinline__ int few_plan(const int32_t *__restrict__ idx, int N, int k, int cap,
-                                        int a, int nthr, PlanShared &p) {
-    const int tid = threadIdx.x, A = N * k;
-    if (tid < kMaxExperts / 32)
-        p.mask[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < A; i += nthr) {
-        const int e = idx[i], t = i / k, j = i - t * k;
-        p.id[j * N + t] = (unsigned char)e;
-        atomicOr(&p.mask[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    int nhit = 0, e = -1;
+
+// Four adjacent fp32 values at p[0..3] of which n exist.
+template <bool ALIGNED>
+__device__ __forceinline__ f32x4 load4(const float *p, int n) {
+    if (ALIGNED)
+        return n > 0 ? *reinterpret_cast<const f32x4 *>(p) : f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 v;
 #pragma unroll
-    for (int w = 0; w < kMaxExperts / 32; ++w) {
-        unsigned m = p.mask[w];
-        const int c = __popc(m);
-        if (a >= nhit && a < nhit + c) {
-            for (int i = nhit; i < a; ++i)
-                m &= m - 1;
-            e = w * 32 + __ffs(m) - 1;
-        }
-        nhit += c;
-    }
-    if (tid < 64) {
-        int base = 0;
-        if (e >= 0) {
-            for (int c = 0; c < A; c += 64) {
-                const int o = c + tid;
-                const bool mine = o < A && p.id[o] == e;
-                const uint64_t m = __ballot(mine);
-                const int r = base + __popcll(m & lanemask_lt());
-                if (mine && r < cap) {
-                    const int j = o / N, t = o - j * N;
-                    p.row[r] = t * k + j;
-                }
-                base += __popcll(m);
-            }
-        }
-        if (tid == 0) {
-            p.expert = e;
-            p.count = base;
-            p.kept = min(base, cap);
-        }
-    }
-    __syncthreads();
-    return nhit;
+    for (int i = 0; i < 4; ++i)
+        v[i] = i < n ? p[i] : 0.f;
+    return v;
 }
 
-// Exports of the workgroup that owns expert e (its first column tile): the
-// plan of the down product, slots, counts and gate sums.
-struct FewExports {
-    int32_t *slot, *used, *demand, *drops;
-    float *gate_sum;
-};
-__device__ __forceinline__ void few_exports(const PlanShared &p, const float *__restrict__ gate,
-                                            int N, int k, int E, int a, int nhit, int nthr,
-                                            FewPlan *__restrict__ plan, const FewExports &x) {
-    const int tid = threadIdx.x, e = p.expert, A = N * k;
-    if (a == 0) {
-        if (tid == 0)
-            plan->nhit = nhit;
-        // experts nobody took
-        for (int i = tid; i < E; i += nthr)
-            if (!((p.mask[i >> 5] >> (i & 31)) & 1u)) {
-                if (x.used) x.used[i] = 0;
-                if (x.demand) x.demand[i] = 0;
-                if (x.drops) x.drops[i] = 0;
-                if (x.gate_sum) x.gate_sum[i] = 0.f;
-            }
-    }
-    if (tid == 0) {
-        plan->expert[a] = e;
-        plan->rows[a] = p.kept;
-        if (x.used) x.used[e] = p.kept;
-        if (x.demand) x.demand[e] = p.count;
-        if (x.drops) x.drops[e] = p.count - p.kept;
-        if (x.gate_sum) {
-            float s = 0.f;   // (choice, token) order
-            for (int o = 0; o < A; ++o)
-                if (p.id[o] == e)
-                    s += gate[(o % N) * k + o / N];
-            x.gate_sum[e] = s;
-        }
-    }
-    if (tid < p.kept)
-        plan->row[a][tid] = p.row[tid];
-    if (x.slot && tid < 64) {
-        int base = 0;
-        for (int c = 0; c < A; c += 64) {
-            const int o = c + tid;
-            const bool mine = o < A && p.id[o] == e;
-            const uint64_t m = __ballot(mine);
-            if (mine) {
-                const int r = base + __popcll(m & lanemask_lt());
-                x.slot[(o % N) * k + o / N] = r < p.kept ? r : -1;
-            }
-            base += __popcll(m);
-        }
-    }
+// ---- scores ------------------------------------------------------------
+
+// Score columns: experts a ranking lane holds (e, e + 64, ...) side by side.
+__device__ __host__ __forceinline__ int score_lanes(int E) {
+    return E <= 64 ? 1 : E <= 128 ? 2 : 4;
 }
 
-// H (two bf16 terms, [2][N k][d_ff]) = act(W_up[e] x + b_up[e]) for the rows of
-// the hit experts. grid: (column tiles of 16, min(E, N k)); TT token tiles.
-constexpr int kUpWaves = 4;
-template <int TT>
-__global__ __launch_bounds__(kUpWaves * 64) void few_up_kernel(
-    const unsigned short *__restrict__ x, const unsigned short *__restrict__ w_up,
-    const float *__restrict__ b_up, const int32_t *__restrict__ idx,
-    const float *__restrict__ gate, int N, int d, int E, int d_ff, int k, int cap, int act,
-    unsigned short *__restrict__ H, FewPlan *__restrict__ plan, FewExports ex) {
-    __shared__ PlanShared p;
-    __shared__ f32x4 part[kUpWaves][TT][64];
-    const int nthr = kUpWaves * 64;
-    const int a = blockIdx.y, f0 = blockIdx.x * 16;
-    const int nhit = few_plan(idx, N, k, cap, a, nthr, p);
-    if (a >= nhit)
-        return;
-    if (blockIdx.x == 0)
-        few_exports(p, gate, N, k, E, a, nhit, nthr, plan, ex);
-    const int rows = p.kept, e = p.expert;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int ntile = (rows + 15) / 16;
-    const unsigned short *w =
-        w_up + ((int64_t)e * d_ff + min(f0 + (lane & 15), d_ff - 1)) * d;
-    // this wave's K range, in steps of 32
-    const int steps = (d + 31) / 32;
-    const int kb = (int)((int64_t)wv * steps / kUpWaves) * 32;
-    const int ke = (int)((int64_t)(wv + 1) * steps / kUpWaves) * 32;
-    f32x4 acc[TT];
+// Scores of a lane's expert row w and TT token rows over U K-steps from column
+// kb on (none where kb is past d), all loads issued before the MFMAs.
+template <typename S, int TT, int U>
+__device__ __forceinline__ void score_tile(const float *w, const typename S::type *const (&xt)[TT],
+                                           int kb, int d, f32x4 (&acc)[TT]) {
+    const int ko = 8 * (int)(__lane_id() >> 4);
 #pragma unroll
     for (int i = 0; i < TT; ++i)
         acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (Kind<S>::bf16) {
+        f32x4 w0[U], w1[U];
+        u32x4 b[U][TT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = kb + 32 * u + ko;
+            w0[u] = w1[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+                b[u][i] = u32x4{0u, 0u, 0u, 0u};
+            if (k < d) {   // (d % 8 == 0)
+                w0[u] = *reinterpret_cast<const f32x4 *>(w + k);
+                w1[u] = *reinterpret_cast<const f32x4 *>(w + k + 4);
+#pragma unroll
+                for (int i = 0; i < TT; ++i)
+                    b[u][i] = *reinterpret_cast<const u32x4 *>(xt[i] + k);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            u32x4 term[3];
+            split8(w0[u], w1[u], term[0], term[1], term[2]);
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    acc[i] = SkinnyBf16::mma(term[m], b[u][i], acc[i]);
+        }
+    } else {
+        const float *wr[1] = {w};
+        f32x4 c[1][TT];
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            c[0][i] = acc[i];
+        const int ke = min(kb + 32 * U, (d + 31) / 32 * 32);
+        if (kb < ke)
+            skinny_mma<S, 1, TT, 1, 1>(wr, xt, 0, kb, ke, d, c);
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            acc[i] = c[0][i];
+    }
+}
+
+// P[s][t][64 Q]: partial scores of the s-th range of d, expert e at column
+// (e mod 64) Q + e / 64. grid: (tiles of 16 experts, ranges); the waves take
+// quarters of the range.
+template <typename S, int TT>
+__global__ __launch_bounds__(kThreads) void few_scores_kernel(
+    const typename S::type *__restrict__ x, const float *__restrict__ wg, int N, int d, int E,
+    float *__restrict__ P) {
+    __shared__ f32x4 part[kWaves][TT][64];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int e0 = blockIdx.x * 16;
+    const float *w = wg + (int64_t)min(e0 + (lane & 15), E - 1) * d;
+    const typename S::type *xt[TT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+        xt[i] = x + (int64_t)min(i * 16 + (lane & 15), N - 1) * d;
+    const int kb = blockIdx.y * kScoreRange + wv * (kScoreRange / kWaves);
+    f32x4 acc[TT];
+    score_tile<S, TT, kScoreRange / kWaves / 32>(w, xt, kb, d, acc);
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+        part[wv][i][lane] = acc[i];
+    __syncthreads();
+    const int Q = score_lanes(E);
+    for (int q = threadIdx.x; q < TT * 64; q += kThreads) {
+        const int i = q >> 6, l = q & 63;
+        const int t = i * 16 + (l & 15), e = e0 + 4 * (l >> 4);
+        f32x4 v = part[0][i][l];
+#pragma unroll
+        for (int s = 1; s < kWaves; ++s)
+            v += part[s][i][l];
+        if (t < N)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (e + c < E)
+                    P[((int64_t)blockIdx.y * N + t) * (64 * Q) + (e + c) % 64 * Q + (e + c) / 64] =
+                        v[c];
+    }
+}
+
+// One wave ranks token t: partial scores added in range order, noise, top-k
+// and softmax of the kept scores into idx[t k ..] and gate[t k ..].
+template <int Q>
+__device__ __forceinline__ void few_rank(const float *__restrict__ P, int ns,
+                                         const float *__restrict__ noise, int N, int E, int k,
+                                         int t, int32_t *idx, float *gate) {
+    typedef float vec __attribute__((ext_vector_type(Q == 1 ? 2 : Q)));   // (Q == 1: v[0])
+    const int lane = __lane_id();
+    const float *p = P + ((int64_t)t * 64 + lane) * Q;
+    const int64_t step = (int64_t)N * 64 * Q;
+    auto load = [&](int r) {
+        vec o = {};
+        if constexpr (Q == 1)
+            o[0] = p[r * step];
+        else
+            o = *reinterpret_cast<const vec *>(p + r * step);
+        return o;
+    };
+    constexpr int B = 8;   // loads in flight
+    vec s = load(0);
+    for (int r = 1; r < ns; r += B) {
+        vec u[B];
+#pragma unroll
+        for (int c = 0; c < B; ++c)
+            u[c] = load(min(r + c, ns - 1));
+#pragma unroll
+        for (int c = 0; c < B; ++c)
+            if (r + c < ns)
+                s += u[c];
+    }
+    float v[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int e = lane + 64 * q;
+        v[q] = -INFINITY;
+        if (e < E)   // (columns past E hold no score)
+            v[q] = noise ? s[q] + noise[(int64_t)t * E + e] : s[q];
+    }
+    topk_softmax_wave<Q>(v, E, k, t, true, idx, gate);
+}
+
+template <int Q>
+__global__ __launch_bounds__(kThreads) void few_rank_kernel(const float *__restrict__ P, int ns,
+                                                            const float *__restrict__ noise, int N,
+                                                            int E, int k, int32_t *idx,
+                                                            float *gate) {
+    const int t = blockIdx.x * kWaves + (threadIdx.x >> 6);
+    if (t < N)
+        few_rank<Q>(P, ns, noise, N, E, k, t, idx, gate);
+}
+
+// ---- plan --------------------------------------------------------------
+
+struct FewRoute {
+    const float *P, *noise;   // partial scores to rank, or P NULL: ranked already
+    int ns;
+    int32_t *idx;             // [N, k]
+    float *gate;
+    int32_t *slot, *used, *demand, *drops;   // exports, or NULL
+    float *gate_sum;
+    FewPlan *plan;
+    int *done;                // finished ranges per column block of the down product
+    int blocks;               // column blocks
+};
+
+// Layers whose scores the plan's workgroup computes itself, wave w taking
+// K-steps w, w + 16, ...: up to 16 tokens and experts, rows of up to 1024.
+constexpr int kPlanScoreWidth = 2 * kPlanWaves * 32;
+bool scores_in_plan(int64_t N, int64_t d, int64_t E) {
+    return N <= 16 && E <= 16 && d <= kPlanScoreWidth;
+}
+
+// One workgroup: scores (SCORE, see above), idx and gates (with SCORE, or when
+// P is given), then the plan: the hit
+// experts in ascending order, the rows each keeps (the first `cap` of its
+// assignments in (choice, token) order) and the exports.
+template <typename S, int Q, bool SCORE>
+__global__ __launch_bounds__(kPlanWaves * 64) void few_plan_kernel(
+    const typename S::type *__restrict__ x, const float *__restrict__ wg, FewRoute r, int N, int d,
+    int E, int k, int cap) {
+    constexpr int nthr = kPlanWaves * 64;
+    static_assert(kFewAssign <= nthr && kMaxExperts <= nthr, "a thread per assignment and expert");
+    __shared__ __attribute__((aligned(16))) unsigned char id[kFewAssign];   // see below
+    __shared__ int32_t s_idx[kFewAssign];      // [N, k]
+    __shared__ float s_gate[kFewAssign];
+    __shared__ float by_expert[kFewAssign];    // gates, expert by expert
+    __shared__ int count[kMaxExperts], hit_of[kMaxExperts], first[kMaxExperts];
+    __shared__ int hits_w[kMaxExperts / 64], count_w[kMaxExperts / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, A = N * k;
+    if (tid < kMaxExperts)
+        count[tid] = 0;
+    for (int i = tid; i < r.blocks; i += nthr)
+        r.done[i] = 0;
+    const bool rank_here = SCORE || r.P;
+    if constexpr (SCORE) {
+        __shared__ f32x4 part[kPlanWaves][64];
+        __shared__ float score[16][64];   // [token][expert]
+        const float *w = wg + (int64_t)min(lane & 15, E - 1) * d;
+        const typename S::type *xt[1] = {x + (int64_t)min(lane & 15, N - 1) * d};
+        f32x4 a, b, c[1];
+        score_tile<S, 1, 1>(w, xt, wv * 32, d, c);
+        a = c[0];
+        score_tile<S, 1, 1>(w, xt, (kPlanWaves + wv) * 32, d, c);
+        b = c[0];
+        part[wv][lane] = a + b;
+        __syncthreads();
+        if (wv < 4) {
+            // lane: expert 4 wv + q of token l % 16 ... one value per thread
+            const int l = (lane >> 2) + 16 * wv, q = lane & 3;
+            float v = part[0][l][q];
+#pragma unroll
+            for (int u = 1; u < kPlanWaves; ++u)
+                v += part[u][l][q];
+            score[l & 15][4 * (l >> 4) + q] = v;
+        }
+        __syncthreads();
+        if (wv < N)
+            few_rank<1>(&score[0][0], 1, r.noise, N, E, k, wv, s_idx, s_gate);
+    } else if (r.P) {
+        for (int t = wv; t < N; t += kPlanWaves)
+            few_rank<Q>(r.P, r.ns, r.noise, N, E, k, t, s_idx, s_gate);
+    }
+    __syncthreads();
+    // thread o: assignment (j, t), o = j N + t, so that threads follow the
+    // order in which capacity is given; id[o] is its expert
+    const int o = tid, j = o / N, i = (o - j * N) * k + j;
+    int e = 0;
+    float g = 0.f;
+    if (o < A) {
+        if (rank_here) {
+            e = s_idx[i];
+            g = s_gate[i];
+            r.idx[i] = e;
+            r.gate[i] = g;
+        } else {
+            e = r.idx[i];
+            g = r.gate[i];
+        }
+        id[o] = (unsigned char)e;
+        atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    // rank: assignments before o to the same expert, the bytes equal to e in
+    // id[0 .. o), four at a time (v has a zero byte for each; the bit trick
+    // leaves bit 7 of exactly the zero bytes)
+    int rank = 0;
+    if (o < A) {
+        const unsigned ee = (unsigned)e * 0x01010101u;
+        auto equal = [&](unsigned v) {
+            v ^= ee;
+            return ~(((v & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v | 0x7f7f7f7fu);
+        };
+        const u32x4 *quad = reinterpret_cast<const u32x4 *>(id);
+        for (int c = 0; c < o / 16; ++c) {
+            const u32x4 v = quad[c];
+            rank += __popc(equal(v[0])) + __popc(equal(v[1])) + __popc(equal(v[2])) +
+                    __popc(equal(v[3]));
+        }
+        const unsigned *word = reinterpret_cast<const unsigned *>(id);
+        for (int c = o / 16 * 4; c < o / 4; ++c)
+            rank += __popc(equal(word[c]));
+        if (o % 4)
+            rank += __popc(equal(word[o / 4]) & ((1u << (8 * (o % 4))) - 1u));
+    }
+    // hit experts in ascending order, and the assignments before each expert
+    int n = 0, before = 0;
+    uint64_t hits = 0;
+    if (tid < kMaxExperts) {
+        n = count[tid];
+        hits = __ballot(n > 0);
+        before = n;
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const int u = __shfl_up(before, s);
+            if (lane >= s)
+                before += u;
+        }
+        if (lane == 63) {
+            hits_w[wv] = __popcll(hits);
+            count_w[wv] = before;
+        }
+        before -= n;
+    }
+    __syncthreads();
+    if (tid < kMaxExperts) {
+        int a = __popcll(hits & lanemask_lt());
+        for (int w = 0; w < wv; ++w) {
+            a += hits_w[w];
+            before += count_w[w];
+        }
+        hit_of[tid] = a;
+        first[tid] = before;
+        if (n > 0) {
+            r.plan->expert[a] = tid;
+            r.plan->rows[a] = min(n, cap);
+        }
+        if (tid < E) {
+            if (r.used) r.used[tid] = min(n, cap);
+            if (r.demand) r.demand[tid] = n;
+            if (r.drops) r.drops[tid] = n - min(n, cap);
+        }
+        if (tid == 0) {
+            int c = 0;
+            for (int w = 0; w < kMaxExperts / 64; ++w)
+                c += hits_w[w];
+            r.plan->nhit = c;
+        }
+    }
+    __syncthreads();
+    if (o < A) {
+        if (rank < cap)
+            r.plan->row[hit_of[e]][rank] = i;
+        if (r.slot)
+            r.slot[i] = rank < cap ? rank : -1;
+        by_expert[first[e] + rank] = g;
+    }
+    if (r.gate_sum) {   // (the same for the whole workgroup)
+        __syncthreads();
+        if (tid < E) {
+            float s = 0.f;   // in (choice, token) order
+            for (int c = 0; c < n; ++c)
+                s += by_expert[first[tid] + c];
+            r.gate_sum[tid] = s;
+        }
+    }
+}
+
+// ---- up ----------------------------------------------------------------
+
+// H (bf16: two terms, [2][N k][d_ff]; fp32: [N k][d_ff]) = act(W_up[e] x +
+// b_up[e]) for the rows of the hit experts. grid: (tiles of 16 FM neurons,
+// min(E, N k)); TT token tiles at most.
+template <typename S, int FM, int TT>
+__global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
+    const typename S::type *__restrict__ x, const typename S::type *__restrict__ w_up,
+    const float *__restrict__ b_up, const FewPlan *__restrict__ plan, int N, int d, int d_ff,
+    int k, int act, typename S::type *__restrict__ H) {
+    __shared__ f32x4 part[kWaves][FM * TT][64];
+    const int a = blockIdx.y, f0 = blockIdx.x * (16 * FM);
+    if (a >= plan->nhit)
+        return;
+    const int rows = plan->rows[a], e = plan->expert[a];
+    const int *row = plan->row[a];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int ntile = (rows + 15) / 16;
+    const typename S::type *w[FM];
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+        w[m] = w_up + ((int64_t)e * d_ff + min(f0 + 16 * m + (lane & 15), d_ff - 1)) * d;
+    // this wave's K range, in steps of 32
+    const int steps = (d + 31) / 32;
+    const int kb = (int)((int64_t)wv * steps / kWaves) * 32;
+    const int ke = (int)((int64_t)(wv + 1) * steps / kWaves) * 32;
     auto run = [&](auto tiles) {
         constexpr int T = decltype(tiles)::value;
-        const unsigned short *xt[T];
-        f32x4 c[T];
+        const typename S::type *xt[T];
+        f32x4 c[FM][T];
 #pragma unroll
         for (int i = 0; i < T; ++i) {
             const int r = i * 16 + (lane & 15);
-            xt[i] = x + (int64_t)(p.row[r < rows ? r : 0] / k) * d;
-            c[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-        skinny_mma<T, 1, T == 1 ? 8 : T == 2 ? 4 : 2>(w, xt, 0, kb, ke, d, c);
+            xt[i] = x + (int64_t)(row[r < rows ? r : 0] / k) * d;
 #pragma unroll
-        for (int i = 0; i < T; ++i)
-            acc[i] = c[i];
+            for (int m = 0; m < FM; ++m)
+                c[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        // operand registers of a batch: U (FM + T) fragments, twice
+        constexpr int U = (FM + T <= 2 ? 8 : FM + T <= 4 ? 4 : 2) / (Kind<S>::bf16 ? 1 : 2);
+        skinny_mma<S, FM, T, 1, U>(w, xt, 0, kb, ke, d, c);
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+                part[wv][m * TT + i][lane] = c[m][i];
     };
     if (TT == 1 || ntile <= 1)
         run(std::integral_constant<int, 1>{});
@@ -207,300 +453,373 @@ __global__ __launch_bounds__(kUpWaves * 64) void few_up_kernel(
         run(std::integral_constant<int, TT < 2 ? TT : 2>{});
     else
         run(std::integral_constant<int, TT>{});
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-        if (i < ntile)
-            part[wv][i][lane] = acc[i];
     __syncthreads();
     // thread -> (row, 4 neurons): tile i's lane l holds neurons 4 (l / 16) + q
     // of row l % 16
-    for (int q = threadIdx.x; q < ntile * 64; q += nthr) {
-        const int i = q >> 6, l = q & 63;
-        const int r = i * 16 + (l & 15), f = f0 + 4 * (l >> 4);
+    for (int q = threadIdx.x; q < ntile * FM * 64; q += kThreads) {
+        const int m = (q >> 6) % FM, i = (q >> 6) / FM, l = q & 63;
+        const int r = i * 16 + (l & 15), f = f0 + 16 * m + 4 * (l >> 4);
         if (r >= rows || f >= d_ff)
             continue;
-        f32x4 z = part[0][i][l];
+        f32x4 z = part[0][m * TT + i][l];
 #pragma unroll
-        for (int s = 1; s < kUpWaves; ++s)
-            z += part[s][i][l];
+        for (int s = 1; s < kWaves; ++s)
+            z += part[s][m * TT + i][l];
         if (b_up)
-            z += *reinterpret_cast<const f32x4 *>(b_up + (int64_t)e * d_ff + f);
-        float h[4], lo[4];
+            z += load4<Kind<S>::bf16>(b_up + (int64_t)e * d_ff + f, d_ff - f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            h[c] = activate(z[c], act);
-            // the rest of an infinity or a NaN would be NaN: it has none
-            const float rest = h[c] - bf16_bits_to_f32(f32_to_bf16_bits(h[c]));
-            lo[c] = fabsf(rest) < __builtin_inff() ? rest : 0.f;
+        for (int c = 0; c < 4; ++c)
+            z[c] = activate(z[c], act);
+        typename S::type *dst = H + (int64_t)row[r] * d_ff + f;
+        if constexpr (Kind<S>::bf16) {
+            float lo[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // the rest of an infinity or a NaN would be NaN: it has none
+                const float rest = z[c] - bf16_bits_to_f32(f32_to_bf16_bits(z[c]));
+                lo[c] = fabsf(rest) < __builtin_inff() ? rest : 0.f;
+            }
+            *reinterpret_cast<u32x2 *>(dst) =
+                u32x2{pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3])};
+            *reinterpret_cast<u32x2 *>(dst + (int64_t)N * k * d_ff) =
+                u32x2{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (f + c < d_ff)
+                    dst[c] = z[c];
         }
-        unsigned short *dst = H + (int64_t)p.row[r] * d_ff + f;
-        *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
-        *reinterpret_cast<u32x2 *>(dst + (int64_t)N * k * d_ff) =
-            u32x2{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
     }
 }
 
-// out[t] = sum over kept choices of gate (W_down[e] h + b_down[e]), 16 columns
-// per workgroup. LDS: one [N][16] copy of the sums per wave.
-constexpr int kDownWaves = 16;
-template <int TT>
-__global__ __launch_bounds__(kDownWaves * 64) void few_down_kernel(
-    const unsigned short *__restrict__ H, const unsigned short *__restrict__ w_down,
+// ---- down --------------------------------------------------------------
+
+// out[t] = sum over kept choices of gate (W_down[e] h + b_down[e]). grid:
+// (blocks of 16 FM columns, ranges); part [ranges][N][16 FM blocks] when there is
+// more than one range. The partial sums and the counter are written and read
+// past the XCD's own L2 (agent scope), which other XCDs do not see.
+template <typename S, int FM, int TT>
+__global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
+    const typename S::type *__restrict__ H, const typename S::type *__restrict__ w_down,
     const float *__restrict__ b_down, const float *__restrict__ gate,
-    const FewPlan *__restrict__ plan, int N, int d, int d_ff, int k,
-    unsigned short *__restrict__ out) {
+    const FewPlan *__restrict__ plan, int N, int d, int d_ff, int k, int *__restrict__ done,
+    float *__restrict__ part, typename S::type *__restrict__ out) {
     constexpr int NT = TT * 16;
-    __shared__ float sum[kDownWaves][NT][16 + 1];
-    const int c0 = blockIdx.x * 16;
+    constexpr int NB = Kind<S>::terms;
+    constexpr int CB = 16 * FM;
+    __shared__ float sum[kWaves][NT][CB + 1];
+    __shared__ int last;
+    const int c0 = blockIdx.x * CB;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int i = lane; i < NT * 17; i += 64)
+    for (int i = lane; i < NT * (CB + 1); i += 64)
         (&sum[wv][0][0])[i] = 0.f;
     const int chunks = (d_ff + kChunk - 1) / kChunk;
     const int units = plan->nhit * chunks;
-    const int ub = (int)((int64_t)wv * units / kDownWaves);
-    const int ue = (int)((int64_t)(wv + 1) * units / kDownWaves);
+    const int parts = (int)gridDim.y * kWaves, me = (int)blockIdx.y * kWaves + wv;
+    const int ub = (int)((int64_t)me * units / parts);
+    const int ue = (int)((int64_t)(me + 1) * units / parts);
     const int64_t lo = (int64_t)N * k * d_ff;
-    const int col = min(c0 + (lane & 15), d - 1);
     for (int u = ub; u < ue;) {
         const int a = u / chunks, uc = u - a * chunks;
         const int un = min(ue - u, chunks - uc);   // chunks of this expert
         const int e = plan->expert[a], rows = plan->rows[a];
-        const unsigned short *w = w_down + ((int64_t)e * d + col) * d_ff;
+        const typename S::type *w[FM];
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+            w[m] = w_down + ((int64_t)e * d + min(c0 + 16 * m + (lane & 15), d - 1)) * d_ff;
         const int kb = uc * kChunk, ke = min((uc + un) * kChunk, (d_ff + 31) / 32 * 32);
         u += un;
+        f32x4 bias[FM];
+#pragma unroll
+        for (int m = 0; m < FM; ++m) {
+            const int cc = c0 + 16 * m + 4 * (lane >> 4);
+            bias[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (b_down && uc == 0)
+                bias[m] = load4<Kind<S>::bf16>(b_down + (int64_t)e * d + cc, d - cc);
+        }
         auto run = [&](auto tiles) {
             constexpr int T = decltype(tiles)::value;
-            const unsigned short *ht[T];
-            f32x4 acc[T];
+            const typename S::type *ht[T];
+            f32x4 acc[FM][T];
             int as[T];
-            f32x4 bias = {0.f, 0.f, 0.f, 0.f};
-            if (b_down && uc == 0 && c0 + 4 * (lane >> 4) < d)
-                bias = *reinterpret_cast<const f32x4 *>(b_down + (int64_t)e * d + c0 +
-                                                        4 * (lane >> 4));
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 const int r = i * 16 + (lane & 15);
                 as[i] = plan->row[a][r < rows ? r : 0];
                 ht[i] = H + (int64_t)as[i] * d_ff;
-                acc[i] = bias;
+#pragma unroll
+                for (int m = 0; m < FM; ++m)
+                    acc[m][i] = bias[m];
             }
-            skinny_mma<T, 2, T == 1 ? 4 : T == 2 ? 2 : 1>(w, ht, lo, kb, ke, d_ff, acc);
+            constexpr int U = FM + NB * T <= 4 ? 4 : FM + NB * T <= 6 ? 2 : 1;
+            skinny_mma<S, FM, T, NB, U>(w, ht, lo, kb, ke, d_ff, acc);
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 if (i * 16 + (lane & 15) < rows) {
                     const float g = gate[as[i]];
-                    float *s = &sum[wv][as[i] / k][4 * (lane >> 4)];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        s[q] = fmaf(g, acc[i][q], s[q]);
+                    for (int m = 0; m < FM; ++m) {
+                        float *s = &sum[wv][as[i] / k][16 * m + 4 * (lane >> 4)];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            s[q] = fmaf(g, acc[m][i][q], s[q]);
+                    }
                 }
             }
         };
-        if (TT == 1 || rows <= 16)
+        if (NB == 2 && rows <= 8) {
+            // both terms of up to 8 rows fill one tile: columns 0-7 the hi
+            // terms, columns 8-15 the lo terms of the same rows, added at the
+            // end (half the loads and MFMAs of two operand terms)
+            const int r = lane & 7;
+            const int as = plan->row[a][r < rows ? r : 0];
+            const typename S::type *ht[1] = {H + (int64_t)as * d_ff + (lane & 8 ? lo : 0)};
+            f32x4 acc[FM][1];
+#pragma unroll
+            for (int m = 0; m < FM; ++m)
+                acc[m][0] = lane & 8 ? f32x4{0.f, 0.f, 0.f, 0.f} : bias[m];
+            skinny_mma<S, FM, 1, 1, FM == 1 ? 8 : 4>(w, ht, 0, kb, ke, d_ff, acc);
+            const float g = gate[as];
+#pragma unroll
+            for (int m = 0; m < FM; ++m) {
+                float *s = &sum[wv][as / k][16 * m + 4 * (lane >> 4)];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float y = acc[m][0][q] + __shfl_xor(acc[m][0][q], 8);
+                    if ((lane & 15) < rows)
+                        s[q] = fmaf(g, y, s[q]);
+                }
+            }
+        } else if (TT == 1 || rows <= 16) {
             run(std::integral_constant<int, 1>{});
-        else if (TT == 2 || rows <= 32)
+        } else if (TT == 2 || rows <= 32) {
             run(std::integral_constant<int, TT < 2 ? TT : 2>{});
-        else
+        } else {
             run(std::integral_constant<int, TT>{});
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < N * 2; i += kDownWaves * 64) {
-        const int t = i >> 1, c = (i & 1) * 8;
-        if (c0 + c >= d)
-            continue;
-        float v[8];
+    auto wave_sums = [&](int t, int c) {
+        float v = sum[0][t][c];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            v[q] = sum[0][t][c + q];
-#pragma unroll
-            for (int w = 1; w < kDownWaves; ++w)
-                v[q] += sum[w][t][c + q];
+        for (int w = 1; w < kWaves; ++w)
+            v += sum[w][t][c];
+        return v;
+    };
+    auto store = [&](int t, int c, float lo_v, float hi_v) {
+        // columns c and c + 1 of token t
+        if constexpr (Kind<S>::bf16) {
+            if (c0 + c < d)   // (d % 8 == 0)
+                *reinterpret_cast<unsigned *>(out + (int64_t)t * d + c0 + c) =
+                    pack_bf16x2(lo_v, hi_v);
+        } else {
+            if (c0 + c < d)
+                out[(int64_t)t * d + c0 + c] = lo_v;
+            if (c0 + c + 1 < d)
+                out[(int64_t)t * d + c0 + c + 1] = hi_v;
         }
-        *reinterpret_cast<u32x4 *>(out + (int64_t)t * d + c0 + c) =
-            u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                  pack_bf16x2(v[6], v[7])};
-    }
-}
-
-// fp32 layers (any widths): a wave takes four weight rows at a time against
-// eight token rows, lanes along K, and adds across its lanes at the end.
-constexpr int kF32Rows = 4, kF32Toks = 8;
-__device__ __forceinline__ float wave_add(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        v += __shfl_xor(v, o);
-    return v;
-}
-__device__ __forceinline__ void dots_f32(const float *const (&w)[kF32Rows],
-                                         const float *const (&x)[kF32Toks], int K,
-                                         float (&acc)[kF32Rows][kF32Toks]) {
-#pragma unroll
-    for (int i = 0; i < kF32Rows; ++i)
-#pragma unroll
-        for (int j = 0; j < kF32Toks; ++j)
-            acc[i][j] = 0.f;
-    for (int c = (int)__lane_id(); c < K; c += 64) {
-        float wv[kF32Rows], xv[kF32Toks];
-#pragma unroll
-        for (int i = 0; i < kF32Rows; ++i)
-            wv[i] = w[i][c];
-#pragma unroll
-        for (int j = 0; j < kF32Toks; ++j)
-            xv[j] = x[j][c];
-#pragma unroll
-        for (int i = 0; i < kF32Rows; ++i)
-#pragma unroll
-            for (int j = 0; j < kF32Toks; ++j)
-                acc[i][j] = fmaf(wv[i], xv[j], acc[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < kF32Rows; ++i)
-#pragma unroll
-        for (int j = 0; j < kF32Toks; ++j)
-            acc[i][j] = wave_add(acc[i][j]);
-}
-
-__global__ __launch_bounds__(256) void few_up_f32_kernel(
-    const float *__restrict__ x, const float *__restrict__ w_up, const float *__restrict__ b_up,
-    const int32_t *__restrict__ idx, const float *__restrict__ gate, int N, int d, int E, int d_ff,
-    int k, int cap, int act, float *__restrict__ H, FewPlan *__restrict__ plan, FewExports ex) {
-    __shared__ PlanShared p;
-    const int a = blockIdx.y;
-    const int nhit = few_plan(idx, N, k, cap, a, 256, p);
-    if (a >= nhit)
-        return;
-    if (blockIdx.x == 0)
-        few_exports(p, gate, N, k, E, a, nhit, 256, plan, ex);
-    const int rows = p.kept, e = p.expert;
-    const int lane = threadIdx.x & 63;
-    const int f0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kF32Rows;
-    if (f0 >= d_ff)
-        return;
-    const float *w[kF32Rows];
-#pragma unroll
-    for (int i = 0; i < kF32Rows; ++i)
-        w[i] = w_up + ((int64_t)e * d_ff + min(f0 + i, d_ff - 1)) * d;
-    for (int r0 = 0; r0 < rows; r0 += kF32Toks) {
-        const float *xr[kF32Toks];
-#pragma unroll
-        for (int j = 0; j < kF32Toks; ++j)
-            xr[j] = x + (int64_t)(p.row[min(r0 + j, rows - 1)] / k) * d;
-        float acc[kF32Rows][kF32Toks];
-        dots_f32(w, xr, d, acc);
-#pragma unroll
-        for (int i = 0; i < kF32Rows; ++i)
-#pragma unroll
-            for (int j = 0; j < kF32Toks; ++j)
-                if (lane == i * kF32Toks + j && f0 + i < d_ff && r0 + j < rows) {
-                    const float z =
-                        b_up ? acc[i][j] + b_up[(int64_t)e * d_ff + f0 + i] : acc[i][j];
-                    H[(int64_t)p.row[r0 + j] * d_ff + f0 + i] = activate(z, act);
-                }
-    }
-}
-
-__global__ __launch_bounds__(256) void few_down_f32_kernel(
-    const float *__restrict__ H, const float *__restrict__ w_down,
-    const float *__restrict__ b_down, const float *__restrict__ gate,
-    const FewPlan *__restrict__ plan, int N, int d, int d_ff, int k, float *__restrict__ out) {
-    __shared__ float sum[4][kFewTokens][kF32Rows];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int c0 = (blockIdx.x * 4 + wv) * kF32Rows;
-    if (c0 >= d)
-        return;   // (no barrier follows: each wave keeps to its own sums)
-    for (int i = lane; i < kFewTokens * kF32Rows; i += 64)
-        (&sum[wv][0][0])[i] = 0.f;
-    const int nhit = plan->nhit;
-    for (int a = 0; a < nhit; ++a) {
-        const int e = plan->expert[a], rows = plan->rows[a];
-        const float *w[kF32Rows];
-#pragma unroll
-        for (int i = 0; i < kF32Rows; ++i)
-            w[i] = w_down + ((int64_t)e * d + min(c0 + i, d - 1)) * d_ff;
-        for (int r0 = 0; r0 < rows; r0 += kF32Toks) {
-            const float *hr[kF32Toks];
-            int as[kF32Toks];
-#pragma unroll
-            for (int j = 0; j < kF32Toks; ++j) {
-                as[j] = plan->row[a][min(r0 + j, rows - 1)];
-                hr[j] = H + (int64_t)as[j] * d_ff;
-            }
-            float acc[kF32Rows][kF32Toks];
-            dots_f32(w, hr, d_ff, acc);
-#pragma unroll
-            for (int i = 0; i < kF32Rows; ++i)
-#pragma unroll
-                for (int j = 0; j < kF32Toks; ++j)
-                    if (lane == i * kF32Toks + j && c0 + i < d && r0 + j < rows) {
-                        const float y = b_down ? acc[i][j] + b_down[(int64_t)e * d + c0 + i]
-                                               : acc[i][j];
-                        float *s = &sum[wv][as[j] / k][i];
-                        *s = fmaf(gate[as[j]], y, *s);
-                    }
+    };
+    const int ranges = gridDim.y;
+    if (ranges == 1) {
+        for (int i = threadIdx.x; i < N * (CB / 2); i += kThreads) {
+            const int t = i / (CB / 2), c = 2 * (i % (CB / 2));
+            store(t, c, wave_sums(t, c), wave_sums(t, c + 1));
         }
+        return;
     }
-    __builtin_amdgcn_wave_barrier();
-    for (int i = lane; i < N * kF32Rows; i += 64) {
-        const int t = i / kF32Rows, c = c0 + i % kF32Rows;
-        if (c < d)
-            out[(int64_t)t * d + c] = sum[wv][t][i % kF32Rows];
+    const int64_t ld = (int64_t)gridDim.x * CB;   // columns of a partial row
+    float *mine = part + (int64_t)blockIdx.y * N * ld + c0;
+    for (int i = threadIdx.x; i < N * CB; i += kThreads) {
+        const int t = i / CB, c = i % CB;
+        __hip_atomic_store(mine + t * ld + c, wave_sums(t, c), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // Every partial sum of the workgroup has reached memory before it counts
+    // (agent-scope stores write through; the wait is for their completion). A
+    // release fence instead would write back, and an acquire drop, the whole
+    // L2 for every workgroup: 222 against 47 us at the Mixtral-shaped layer.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(done + blockIdx.x, 1, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT) == ranges - 1;
+    __syncthreads();
+    if (!last)
+        return;
+    for (int i = threadIdx.x; i < N * (CB / 2); i += kThreads) {
+        const int t = i / (CB / 2), c = 2 * (i % (CB / 2));
+        const float *p = part + t * ld + c0 + c;
+        float v0 = 0.f, v1 = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < ranges; ++s) {
+            v0 += __hip_atomic_load(p + s * N * ld, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v1 += __hip_atomic_load(p + s * N * ld + 1, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
+        }
+        store(t, c, v0, v1);
     }
 }
+
+// Weight rows per lane: two where an expert has more than about 8 rows, whose
+// two operand terms no longer share a tile (Mixtral-shaped layer, 64 tokens:
+// 500 against 620 us; at 2 rows per expert one is faster: fine-grained layer,
+// 61 tokens, 2192 against 2322 us).
+// (fp32 rows are one term, and their layers small: always one.)
+int rows_per_lane(bool bf16, int64_t N, int64_t E, int k) { return bf16 && N * k > 8 * E ? 2 : 1; }
+
+// Column blocks and ranges of the down product: about 4096 workgroups, each
+// wave with at least two chunks when every possible expert is hit.
+struct DownGrid {
+    int fm, blocks, ranges;
+};
+DownGrid down_grid(bool bf16, int64_t N, int64_t d, int64_t E, int64_t d_ff, int k) {
+    const int64_t hits = std::min<int64_t>(E, N * k);
+    DownGrid g;
+    g.fm = rows_per_lane(bf16, N, E, k);
+    g.blocks = (int)((d + 16 * g.fm - 1) / (16 * g.fm));
+    const int64_t units = hits * ((d_ff + kChunk - 1) / kChunk);
+    const int64_t r = std::min<int64_t>((4096 + g.blocks - 1) / g.blocks, units / (2 * kWaves));
+    g.ranges = (int)std::min<int64_t>(std::max<int64_t>(r, 1), 64);
+    return g;
+}
+int score_ranges(int64_t d) { return (int)((d + kScoreRange - 1) / kScoreRange); }
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t few_plan_bytes() { return sizeof(FewPlan); }
+FewLayout few_layout(bool bf16, int64_t N, int64_t d, int64_t E, int64_t d_ff, int k) {
+    FewLayout L;
+    size_t o = 0;
+    const size_t nk = (size_t)(N * k);
+    L.idx = o;    o += up256(nk * 4);
+    L.gate = o;   o += up256(nk * 4);
+    L.plan = o;   o += up256(sizeof(FewPlan));
+    L.done = o;   o += up256((size_t)((d + 15) / 16) * 4);
+    L.scores = o; o += up256((size_t)score_ranges(d) * N * 64 * score_lanes((int)E) * 4);
+    L.H = o;      o += up256(nk * d_ff * 4);   // fp32, or two bf16 terms
+    const DownGrid g = down_grid(bf16, N, d, E, d_ff, k);
+    L.part = o;   o += up256((size_t)g.ranges * N * g.blocks * (16 * g.fm) * 4);
+    L.total = o;
+    return L;
+}
 
-hipError_t launch_few(bool bf16, const void *x, const void *w_up, const void *w_down,
-                      const float *b_up, const float *b_down, const int32_t *idx,
-                      const float *gate, int64_t N, int64_t d, int E, int64_t d_ff, int k,
-                      int64_t ceff, int act, void *H, void *plan, void *out, int32_t *slot,
-                      int32_t *used, int32_t *demand, int32_t *drops, float *gate_sum,
-                      hipStream_t s) {
-    FewPlan *pl = static_cast<FewPlan *>(plan);
-    const FewExports ex{slot, used, demand, drops, gate_sum};
-    const int n = (int)N, A = n * k;
-    const unsigned hits = (unsigned)(E < A ? E : A);
-    if (!bf16) {
-        hipLaunchKernelGGL(few_up_f32_kernel,
-                           dim3((unsigned)((d_ff + 4 * kF32Rows - 1) / (4 * kF32Rows)), hits),
-                           dim3(256), 0, s, static_cast<const float *>(x),
-                           static_cast<const float *>(w_up), b_up, idx, gate, n, (int)d, E,
-                           (int)d_ff, k, (int)ceff, act, static_cast<float *>(H), pl, ex);
-        hipError_t err = hipGetLastError();
+template <typename S, int TT>
+static hipError_t few_call(const void *xv, const float *wg, const float *noise, const void *wu,
+                           const void *wd, const float *b_up, const float *b_down, int N, int d,
+                           int E, int d_ff, int k, int cap, int act, char *ws, FewRoute r,
+                           void *out, hipStream_t s) {
+    typedef typename S::type T;
+    const FewLayout L = few_layout(Kind<S>::bf16, N, d, E, d_ff, k);
+    const T *x = static_cast<const T *>(xv);
+    float *P = reinterpret_cast<float *>(ws + L.scores);
+    T *H = reinterpret_cast<T *>(ws + L.H);
+    const int ns = score_ranges(d);
+    const DownGrid g = down_grid(Kind<S>::bf16, N, d, E, d_ff, k);
+    const unsigned hits = (unsigned)std::min(E, N * k);
+    r.plan = reinterpret_cast<FewPlan *>(ws + L.plan);
+    r.done = reinterpret_cast<int *>(ws + L.done);
+    r.blocks = g.blocks;
+    r.noise = noise;
+    r.ns = ns;
+    hipError_t err = hipSuccess;
+    const bool score = scores_in_plan(N, d, E);
+    if (!score) {
+        hipLaunchKernelGGL((few_scores_kernel<S, TT>),
+                           dim3((unsigned)((E + 15) / 16), (unsigned)ns), dim3(kThreads), 0, s, x,
+                           wg, N, d, E, P);
+        err = hipGetLastError();
         if (err != hipSuccess)
             return err;
-        hipLaunchKernelGGL(few_down_f32_kernel,
-                           dim3((unsigned)((d + 4 * kF32Rows - 1) / (4 * kF32Rows))), dim3(256), 0,
-                           s, static_cast<const float *>(H), static_cast<const float *>(w_down),
-                           b_down, gate, (const FewPlan *)pl, n, (int)d, (int)d_ff, k,
-                           static_cast<float *>(out));
-        return hipGetLastError();
     }
-    // token tiles an expert can need: min(N, C) rows
-    auto go = [&](auto tiles) {
-        constexpr int TT = decltype(tiles)::value;
-        hipLaunchKernelGGL(few_up_kernel<TT>, dim3((unsigned)((d_ff + 15) / 16), hits),
-                           dim3(kUpWaves * 64), 0, s, static_cast<const unsigned short *>(x),
-                           static_cast<const unsigned short *>(w_up), b_up, idx, gate, n, (int)d,
-                           E, (int)d_ff, k, (int)ceff, act, static_cast<unsigned short *>(H), pl,
-                           ex);
-        hipError_t err = hipGetLastError();
-        if (err != hipSuccess)
-            return err;
-        hipLaunchKernelGGL(few_down_kernel<TT>, dim3((unsigned)((d + 15) / 16)),
-                           dim3(kDownWaves * 64), 0, s, static_cast<const unsigned short *>(H),
-                           static_cast<const unsigned short *>(w_down), b_down, gate,
-                           (const FewPlan *)pl, n, (int)d, (int)d_ff, k,
-                           static_cast<unsigned short *>(out));
+    // The plan's one workgroup ranks a token per wave in about 2 us, four rounds
+    // of them at 64 tokens; with many experts the partial scores of a round are
+    // 64 times Q ns words a token, more than one CU reads quickly.
+    const int Q = score_lanes(E);
+    const bool inside = N <= kPlanWaves || Q == 1;
+    r.P = inside ? P : nullptr;
+    auto rank_and_plan = [&](auto lanes) {
+        constexpr int QQ = decltype(lanes)::value;
+        if (!inside) {
+            hipLaunchKernelGGL(few_rank_kernel<QQ>, dim3((unsigned)((N + kWaves - 1) / kWaves)),
+                               dim3(kThreads), 0, s, (const float *)P, ns, noise, N, E, k, r.idx,
+                               r.gate);
+            const hipError_t rc = hipGetLastError();
+            if (rc != hipSuccess)
+                return rc;
+        }
+        if (QQ == 1 && TT == 1 && score)
+            hipLaunchKernelGGL((few_plan_kernel<S, 1, true>), dim3(1), dim3(kPlanWaves * 64), 0, s,
+                               x, wg, r, N, d, E, k, cap);
+        else
+            hipLaunchKernelGGL((few_plan_kernel<S, QQ, false>), dim3(1), dim3(kPlanWaves * 64), 0,
+                               s, x, wg, r, N, d, E, k, cap);
         return hipGetLastError();
     };
-    if (n <= 16)
-        return go(std::integral_constant<int, 1>{});
-    if (n <= 32)
-        return go(std::integral_constant<int, 2>{});
-    return go(std::integral_constant<int, 4>{});
+    err = Q == 1   ? rank_and_plan(std::integral_constant<int, 1>{})
+          : Q == 2 ? rank_and_plan(std::integral_constant<int, 2>{})
+                   : rank_and_plan(std::integral_constant<int, 4>{});
+    if (err != hipSuccess)
+        return err;
+    auto up = [&](auto fm) {
+        constexpr int FM = decltype(fm)::value;
+        hipLaunchKernelGGL((few_up_kernel<S, FM, TT>),
+                           dim3((unsigned)((d_ff + 16 * FM - 1) / (16 * FM)), hits),
+                           dim3(kThreads), 0, s, x, static_cast<const T *>(wu), b_up,
+                           (const FewPlan *)r.plan, N, d, d_ff, k, act, H);
+        return hipGetLastError();
+    };
+    auto down = [&](auto fm) {
+        constexpr int FM = decltype(fm)::value;
+        hipLaunchKernelGGL((few_down_kernel<S, FM, TT>), dim3((unsigned)g.blocks, (unsigned)g.ranges),
+                           dim3(kThreads), 0, s, (const T *)H, static_cast<const T *>(wd), b_down,
+                           (const float *)r.gate, (const FewPlan *)r.plan, N, d, d_ff, k, r.done,
+                           reinterpret_cast<float *>(ws + L.part), static_cast<T *>(out));
+        return hipGetLastError();
+    };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    err = rows_per_lane(Kind<S>::bf16, N, E, k) == 2 ? up(two) : up(one);
+    if (err != hipSuccess)
+        return err;
+    return g.fm == 2 ? down(two) : down(one);
+}
+
+hipError_t launch_few(bool bf16, bool aligned, const void *x, const float *wg, const float *noise,
+                      const void *w_up, const void *w_down, const float *b_up,
+                      const float *b_down, int64_t N, int64_t d, int E, int64_t d_ff, int k,
+                      int64_t ceff, int act, void *ws, int32_t *idx, float *gate, int32_t *slot,
+                      int32_t *used, int32_t *demand, int32_t *drops, float *gate_sum, void *out,
+                      hipStream_t s) {
+    char *w = static_cast<char *>(ws);
+    const FewLayout L = few_layout(bf16, N, d, E, d_ff, k);
+    FewRoute r{};
+    r.idx = idx ? idx : reinterpret_cast<int32_t *>(w + L.idx);
+    r.gate = gate ? gate : reinterpret_cast<float *>(w + L.gate);
+    r.slot = slot;
+    r.used = used;
+    r.demand = demand;
+    r.drops = drops;
+    r.gate_sum = gate_sum;
+    auto go = [&](auto kind, auto tiles) {
+        return few_call<decltype(kind), decltype(tiles)::value>(
+            x, wg, noise, w_up, w_down, b_up, b_down, (int)N, (int)d, E, (int)d_ff, k, (int)ceff,
+            act, w, r, out, s);
+    };
+    auto with_tiles = [&](auto kind) {
+        if (N <= 16)
+            return go(kind, std::integral_constant<int, 1>{});
+        if (N <= 32)
+            return go(kind, std::integral_constant<int, 2>{});
+        return go(kind, std::integral_constant<int, 4>{});
+    };
+    if (bf16)
+        return with_tiles(SkinnyBf16{});
+    // fp32 rows are read 16 bytes at a time where every row starts aligned
+    if (aligned && d % 4 == 0 && d_ff % 4 == 0)
+        return with_tiles(SkinnyF32<true>{});
+    return with_tiles(SkinnyF32<false>{});
 }
 
 }  // namespace moe

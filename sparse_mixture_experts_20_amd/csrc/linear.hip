@@ -373,21 +373,21 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c0 = blockIdx.x * 16;
-    const unsigned short *w = W + (int64_t)min(c0 + (lane & 15), M - 1) * K;
+    const unsigned short *w[1] = {W + (int64_t)min(c0 + (lane & 15), M - 1) * K};
     const unsigned short *xt[TT];
-    f32x4 acc[TT];
+    f32x4 acc[1][TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         xt[i] = x + (int64_t)min(i * 16 + (lane & 15), N - 1) * K;
-        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     const int steps = (K + 31) / 32;
     const int kb = (int)((int64_t)wv * steps / kFewWaves) * 32;
     const int ke = (int)((int64_t)(wv + 1) * steps / kFewWaves) * 32;
-    skinny_mma<TT, 1, TT == 1 ? 4 : TT == 2 ? 3 : 2>(w, xt, 0, kb, ke, K, acc);
+    skinny_mma<SkinnyBf16, 1, TT, 1, TT == 1 ? 4 : TT == 2 ? 3 : 2>(w, xt, 0, kb, ke, K, acc);
 #pragma unroll
     for (int i = 0; i < TT; ++i)
-        part[wv][i][lane] = acc[i];
+        part[wv][i][lane] = acc[0][i];
     __syncthreads();
     // thread -> (row, 8 columns): lanes l and l + 16 of a tile hold columns
     // 4 (l / 16) + 0..3 and the next four of row l % 16

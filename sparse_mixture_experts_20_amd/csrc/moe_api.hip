@@ -1238,22 +1238,9 @@ static int forward_state(const BwdLayout &L, char *ws, const moe_tensor *x,
 // ---------------------------------------------------------------------------
 namespace {
 
-// Workspace of moe_forward_few: routing, the down product's plan, H (two bf16
-// terms per value, or fp32) and the router's scratch.
-struct FewLayout {
-    size_t idx, gate, plan, H, router, total;
-};
-FewLayout few_layout_of(const Dims &m) {
-    FewLayout L;
-    size_t o = 0;
-    const size_t nk = (size_t)m.N * m.k;
-    L.idx = o;    o += align_up(nk * 4);
-    L.gate = o;   o += align_up(nk * 4);
-    L.plan = o;   o += align_up(moe::few_plan_bytes());
-    L.H = o;      o += align_up(nk * (size_t)m.d_ff * 4);
-    L.router = o; o += router_bytes(m.N, m.d, m.E, m.dtype);
-    L.total = o;
-    return L;
+// Widths whose tiles fit the grid's second dimension and 32-bit counts.
+bool few_fits(const Dims &m) {
+    return m.d <= MOE_FEW_MAX_WIDTH && m.d_ff <= MOE_FEW_MAX_WIDTH;
 }
 
 }  // namespace
@@ -1269,9 +1256,9 @@ size_t moe_few_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int
     Dims m{N, d, E, d_ff, k, 0, 0, dtype};
     m.C = capacity_of(N, E, k, capacity_factor);
     m.ceff = m.C < N ? m.C : N;
-    if (check_sizes(m) != MOE_OK)
+    if (check_sizes(m) != MOE_OK || !few_fits(m))
         return 0;
-    return few_layout_of(m).total;
+    return N == 0 ? 0 : moe::few_layout(dtype == MOE_BF16, N, d, E, d_ff, k).total;
 }
 
 int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
@@ -1311,6 +1298,8 @@ int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor
     rc = check_sizes(m);
     if (rc != MOE_OK)
         return rc;
+    if (!few_fits(m))
+        return MOE_ERR_UNSUPPORTED;
     hipStream_t s = static_cast<hipStream_t>(stats->stream);
     if (N == 0) {
         stats->capacity = 0;
@@ -1326,21 +1315,18 @@ int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor
     if (x->dtype == MOE_BF16 &&
         (!aligned(W_up->data, 16) || !aligned(W_down->data, 16) || !aligned(out->data, 16)))
         return MOE_ERR_ALIGN;
-    const FewLayout L = few_layout_of(m);
-    if (stats->workspace_bytes < L.total)
+    const bool bf16 = x->dtype == MOE_BF16;
+    if (stats->workspace_bytes < moe::few_layout(bf16, N, d, E, d_ff, k).total)
         return MOE_ERR_WORKSPACE;
     stats->capacity = m.C;
-    char *ws = static_cast<char *>(stats->workspace);
-    int32_t *idx = stats->topk_idx ? stats->topk_idx : reinterpret_cast<int32_t *>(ws + L.idx);
-    float *gate = stats->topk_gate ? stats->topk_gate : reinterpret_cast<float *>(ws + L.gate);
-    rc = router_checked(x, W_g, noise, N, d, E, k, idx, gate, ws + L.router, s);
-    if (rc != MOE_OK)
-        return rc;
-    return hip_status(moe::launch_few(x->dtype == MOE_BF16, x->data, W_up->data, W_down->data,
-                                      o.b_up, o.b_down, idx, gate, N, d, (int)E, d_ff, k, m.ceff,
-                                      o.act, ws + L.H, ws + L.plan, out->data, stats->slot,
-                                      stats->used_capacity, stats->expert_demand,
-                                      stats->expert_drops, stats->expert_gate_sum, s));
+    const bool al = aligned(x->data, 16) && aligned(W_g->data, 16) && aligned(W_up->data, 16) &&
+                    aligned(W_down->data, 16);
+    return hip_status(moe::launch_few(
+        bf16, al, x->data, static_cast<const float *>(W_g->data),
+        noise ? static_cast<const float *>(noise->data) : nullptr, W_up->data, W_down->data,
+        o.b_up, o.b_down, N, d, (int)E, d_ff, k, m.ceff, o.act, stats->workspace, stats->topk_idx,
+        stats->topk_gate, stats->slot, stats->used_capacity, stats->expert_demand,
+        stats->expert_drops, stats->expert_gate_sum, out->data, s));
 }
 
 }  // extern "C"

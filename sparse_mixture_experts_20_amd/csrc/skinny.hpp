@@ -3,95 +3,139 @@
 // of the linear product for a few rows.
 //
 // Such a product is bound by the stream of its weights, so the weights go from
-// global memory straight into MFMA operand registers (no LDS): lane l of a
-// 16x16x32 bf16 MFMA holds 8 consecutive elements of weight row l % 16 at
-// K offset 8 (l / 16), i.e. one 16-byte load, and a wave's load covers 64
-// contiguous bytes of 16 rows. The token rows are the other operand, TT tiles
-// of 16, read the same way from L2. A batch of U K-steps is loaded while the
-// previous one is multiplied, which keeps U KB of weights per wave in flight.
-// Columns of the product are independent of each other, so a lane whose token
-// does not exist may hold any row's values: its column is never read.
+// global memory straight into MFMA operand registers (no LDS): lane l holds 8
+// consecutive elements of weight row l % 16 at K offset 8 (l / 16). bf16: one
+// 16-byte load and one 16x16x32 MFMA per K-step of 32; a wave's load covers 64
+// contiguous bytes of 16 rows. fp32: two 16-byte loads (single words where the
+// rows are not 16-byte aligned) and eight 16x16x4 fp32 MFMAs, the j-th taking
+// element j of every lane. The token rows are the other operand, TT tiles of
+// 16, read the same way from L2. A batch of U K-steps is loaded while the
+// previous one is multiplied. Columns of the product are independent of each
+// other, so a lane whose token does not exist may hold any row's values: its
+// column is never read.
 #pragma once
 
 #include "common.hpp"
 
 namespace moe {
 
-// Product of K columns [kbeg, kend) (multiples of 32, kend possibly past K)
-// of a weight row and TT token rows into acc (row 4 (l / 16) + q of the weight
-// rows, column l % 16 of the tokens). w and xt[i] point at this lane's row
-// (column 0); NB operand terms per token row, `lo` elements apart, are added
-// (2: a row kept as the sum of two bf16 terms). K % 8 == 0: the last step's
-// chunks past K are taken as zeros.
-template <int TT, int NB, int U>
-__device__ __forceinline__ void skinny_mma(const unsigned short *w,
-                                           const unsigned short *const (&xt)[TT], int64_t lo,
-                                           int kbeg, int kend, int K, f32x4 (&acc)[TT]) {
-    const int ko = 8 * (int)(__lane_id() >> 4);
-    const unsigned short *wp = w + ko;
-    const int full = min(kend, K / 32 * 32);   // steps that need no mask
-    u32x4 a[U], b[U][TT][NB];
-    auto load = [&](int k) {
+// Eight consecutive elements of a row.
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+struct SkinnyBf16 {
+    typedef unsigned short type;
+    typedef u32x4 frag;
+    static __device__ __forceinline__ frag load(const type *p) {
+        return *reinterpret_cast<const frag *>(p);
+    }
+    // n: elements of the row left at p (a multiple of 8)
+    static __device__ __forceinline__ frag load_tail(const type *p, int n) {
+        return n > 0 ? load(p) : frag{0u, 0u, 0u, 0u};
+    }
+    static __device__ __forceinline__ f32x4 mma(const frag &a, const frag &b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+template <bool ALIGNED>
+struct SkinnyF32 {
+    typedef float type;
+    typedef f32x8 frag;
+    static __device__ __forceinline__ frag load(const type *p) {
+        if constexpr (ALIGNED) {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 4);
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return frag{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+        }
+    }
+    static __device__ __forceinline__ frag load_tail(const type *p, int n) {
+        frag r;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            a[u] = *reinterpret_cast<const u32x4 *>(wp + k + 32 * u);
+        for (int i = 0; i < 8; ++i)
+            r[i] = i < n ? p[i] : 0.f;
+        return r;
+    }
+    static __device__ __forceinline__ f32x4 mma(const frag &a, const frag &b, f32x4 c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Product of K columns [kbeg, kend) (multiples of 32, kend possibly past K)
+// of FM weight rows and TT token rows per lane into acc (row 4 (l / 16) + q of
+// the weight rows, column l % 16 of the tokens). w[m] and xt[i] point at this
+// lane's rows (column 0); NB operand terms per token row, `lo` elements apart,
+// are added (2: a row kept as the sum of two bf16 terms). Columns past K are
+// zeros. Two weight rows per lane (FM = 2) halve the token rows' loads.
+template <typename S, int FM, int TT, int NB, int U>
+__device__ __forceinline__ void skinny_mma(const typename S::type *const (&w)[FM],
+                                           const typename S::type *const (&xt)[TT], int64_t lo,
+                                           int kbeg, int kend, int K, f32x4 (&acc)[FM][TT]) {
+    typedef typename S::frag frag;
+    struct Step {
+        frag a[FM], b[TT][NB];
+    };
+    const int ko = 8 * (int)(__lane_id() >> 4);
+    const int full = min(kend, K / 32 * 32);   // steps that need no mask
+    // the weights of a batch first: their addresses are known before the token
+    // rows', which come from the dispatch plan
+    auto load = [&](int k, Step (&s)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < FM; ++m)
+                s[u].a[m] = S::load(w[m] + ko + k + 32 * u);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < TT; ++i)
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
-                    b[u][i][n] =
-                        *reinterpret_cast<const u32x4 *>(xt[i] + n * lo + ko + k + 32 * u);
-        }
+                    s[u].b[i][n] = S::load(xt[i] + n * lo + ko + k + 32 * u);
     };
-    auto mma = [&](const u32x4 &av, const u32x4 (&bv)[TT][NB]) {
+    auto mma = [&](const Step &s) {
 #pragma unroll
-        for (int i = 0; i < TT; ++i)
+        for (int m = 0; m < FM; ++m)
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, av), __builtin_bit_cast(bf16x8, bv[i][n]), acc[i],
-                    0, 0, 0);
+            for (int i = 0; i < TT; ++i)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    acc[m][i] = S::mma(s.a[m], s.b[i][n], acc[m][i]);
     };
+    Step next[U];
     int k = kbeg;
     if (k + 32 * U <= full) {
-        load(k);
+        load(k, next);
         for (k += 32 * U; k + 32 * U <= full; k += 32 * U) {
-            u32x4 ac[U], bc[U][TT][NB];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                ac[u] = a[u];
-#pragma unroll
-                for (int i = 0; i < TT; ++i)
-#pragma unroll
-                    for (int n = 0; n < NB; ++n)
-                        bc[u][i][n] = b[u][i][n];
-            }
-            load(k);
+            Step cur[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                mma(ac[u], bc[u]);
+                cur[u] = next[u];
+            load(k, next);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                mma(cur[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            mma(a[u], b[u]);
+            mma(next[u]);
     }
     for (; k < kend; k += 32) {
         // single steps, masked where they reach past K
-        u32x4 av = {0u, 0u, 0u, 0u}, bv[TT][NB];
+        const int left = K - k - ko;
+        Step s;
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+            s.a[m] = S::load_tail(w[m] + ko + k, left);
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
             for (int n = 0; n < NB; ++n)
-                bv[i][n] = u32x4{0u, 0u, 0u, 0u};
-        if (k + ko < K) {
-            av = *reinterpret_cast<const u32x4 *>(wp + k);
-#pragma unroll
-            for (int i = 0; i < TT; ++i)
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    bv[i][n] = *reinterpret_cast<const u32x4 *>(xt[i] + n * lo + ko + k);
-        }
-        mma(av, bv);
+                s.b[i][n] = S::load_tail(xt[i] + n * lo + ko + k, left);
+        mma(s);
     }
 }
 

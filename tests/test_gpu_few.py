@@ -1,5 +1,5 @@
 """moe_forward_few against its float64 form and against moe_forward's routing
-(ids, gates, slots and counts bit for bit): one token to the limit, both types,
+(ids, slots and counts equal, gates to the router's tolerance): one token to the limit, both types,
 few and many experts, drops, biases, both activations, widths that end inside
 a tile or a K-step."""
 import numpy as np
@@ -89,10 +89,11 @@ def test_against_float64(torch_mod, case):
     want = torch.zeros(c.E, dtype=torch.float64).index_add_(
         0, idx.flatten().cpu(), st.gate.double().flatten().cpu())
     assert float((st.gate_sum.double().cpu() - want).abs().max()) <= 1e-5 * (1 + c.N)
-    # moe_forward routes the same tokens the same way, bit for bit
+    # moe_forward routes the same tokens the same way
     _, ref = B.forward(*args, router_stats=True, **kw)
-    for name in ("idx", "gate", "slot", "used", "demand", "drops"):
+    for name in ("idx", "slot", "used", "demand", "drops"):
         assert torch.equal(getattr(st, name), getattr(ref, name)), name
+    assert float((st.gate - ref.gate).abs().max()) <= 2 * G.GATE_TOL
     # again, without exports, and through the kept layer: the same bits
     assert torch.equal(B.forward_few(*args, export=False, **kw)[0], out)
     layer = B.FewLayer(dev["W_g"], dev["W_up"], dev["W_down"], c.k, c.cf, export=True, **kw)
