@@ -789,7 +789,8 @@ def _scratch(workspace, index: int):
 
 
 def _stream_of(index: int, stream):
-    return (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
+    # (the handle of torch's current stream without building a Stream object)
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _run(index: int, where: str, fn, *args):

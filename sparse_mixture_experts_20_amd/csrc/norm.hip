@@ -86,6 +86,11 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return v;
 }
 
+// Whether a row's loads are issued a row ahead: 16 waves of 16 elements a
+// thread have no registers for it (they would spill).
+template <int TPR, int ELEMS>
+constexpr bool kLoadAhead = TPR < 1024 || ELEMS < 16;
+
 template <typename T, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_kernel(
     const T *x, const T *res, const float *__restrict__ w, const float *__restrict__ b, float eps,
@@ -135,13 +140,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_kernel(
     };
     const int64_t step = (int64_t)gridDim.x * GROUPS;
     int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR;
+    constexpr bool AHEAD = kLoadAhead<TPR, NV * VEC>;
     Raw xr[NV], rr[NV];
-    if (row < N) {
-        load(x, row, xr);
+    auto fetch = [&](int64_t r) {
+        load(x, r, xr);
         if (res)
-            load(res, row, rr);
-    }
+            load(res, r, rr);
+    };
+    if (AHEAD && row < N)
+        fetch(row);
     for (; row < N; row += step) {
+        if constexpr (!AHEAD)
+            fetch(row);
         float v[NV][VEC];
         float s = 0.f;
 #pragma unroll
@@ -165,11 +175,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_kernel(
             for (int i = 0; i < VEC; ++i)
                 s += v[j][i];
         }
-        if (row + step < N) {
-            load(x, row + step, xr);
-            if (res)
-                load(res, row + step, rr);
-        }
+        if (AHEAD && row + step < N)
+            fetch(row + step);
         const float mean = row_sum<TPR>(s, red[0]) * inv_d;
         float q = 0.f;
 #pragma unroll
@@ -264,17 +271,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_backward_ker
     int parity = 0;
     Raw xr[NV], gr[NV], rr[NV];
     float mean = 0.f, rstd = 0.f;
+    constexpr bool AHEAD = kLoadAhead<TPR, NV * VEC>;
     auto fetch = [&](int64_t r) {
         load(x, r, xr);
         load(dout, r, gr);
-        if (dres)
+        if (AHEAD && dres)
             load(dres, r, rr);
         mean = mean_in[r];
         rstd = rstd_in[r];
     };
-    if (row < N)
+    if (AHEAD && row < N)
         fetch(row);
     for (; row < N; row += step) {
+        if constexpr (!AHEAD)
+            fetch(row);
         // xh and g = dy w; the column sums of this row are added at once
         float xh[NV][VEC], g[NV][VEC];
         Raw rc[NV];
@@ -287,7 +297,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_backward_ker
             weight(j, wv);
             R::unpack(xr[j], xh[j]);
             R::unpack(gr[j], g[j]);
-            rc[j] = rr[j];
+            if constexpr (AHEAD)
+                rc[j] = rr[j];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 xh[j][i] = in ? (xh[j][i] - mean) * rs : 0.f;
@@ -298,7 +309,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_backward_ker
                 s2 = fmaf(g[j][i], xh[j][i], s2);
             }
         }
-        if (row + step < N)
+        if (AHEAD && row + step < N)
             fetch(row + step);
         s1 = wave_sum(s1);
         s2 = wave_sum(s2);
@@ -327,6 +338,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_backward_ker
                     o[i] = rs * (g[j][i] - m1 - xh[j][i] * m2);
                 if (dres) {
                     float rv[VEC];
+                    if constexpr (!AHEAD)
+                        rc[j] = *reinterpret_cast<const Raw *>(dres + row * d + (int64_t)vi * VEC);
                     R::unpack(rc[j], rv);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
@@ -369,33 +382,39 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_backward_ker
     }
 }
 
-// dw[c] and db[c] = sum over the P partial rows, in order within each of four
-// interleaved sets that are then added in order. 64 columns per workgroup.
-__global__ __launch_bounds__(256) void norm_column_sums_kernel(const float *__restrict__ part,
-                                                               int P, int d, float *__restrict__ dw,
-                                                               float *__restrict__ db) {
-    __shared__ float red[4][64];
+// dw[c] and db[c] = sum over the P partial rows, each of kSumGroups interleaved
+// sets in order and then the sets in order: a chain of P / 16 loads (the
+// latency of a chain of P / 4 was most of this kernel's time). 64 columns per
+// workgroup.
+constexpr int kSumGroups = 16;
+__global__ __launch_bounds__(kSumGroups * 64) void norm_column_sums_kernel(
+    const float *__restrict__ part, int P, int d, float *__restrict__ dw, float *__restrict__ db) {
+    __shared__ float red[kSumGroups][64];
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
     const float *p = part + (int64_t)blockIdx.y * d + c;
     float s = 0.f;
     if (c < d) {
 #pragma unroll 8
-        for (int r = q; r < P; r += 4)
+        for (int r = q; r < P; r += kSumGroups)
             s += p[(int64_t)r * 2 * d];
     }
     red[q][lane] = s;
     __syncthreads();
     if (q == 0 && c < d) {
-        const float t = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
-        float *o = blockIdx.y == 0 ? dw : db;
-        o[c] = t;
+        float t = red[0][lane];
+#pragma unroll
+        for (int g = 1; g < kSumGroups; ++g)
+            t += red[g][lane];
+        (blockIdx.y == 0 ? dw : db)[c] = t;
     }
 }
 
-// Workgroups of the backward (rows of the partial sums): enough to fill the
-// 256 CUs, few enough that the partial rows stay a small share of the traffic.
-constexpr int kNormBackwardGroups = 512;
+// Workgroups of the backward (rows of the partial sums): about one round of
+// the 256 CUs. More hide more latency but write and add more partial rows
+// (8192x7168 bf16: 97 us at 256, 113 at 512, 136 at 1024).
+constexpr int kNormBackwardMax = 512;
+constexpr int backward_groups(int threads) { return threads >= 512 ? 256 : kNormBackwardMax; }
 
 // Calls f(<T, VEC, TPR, NV> tag) for the variant that holds a row of d
 // elements: waves for narrow rows, a workgroup for wide ones.
@@ -404,13 +423,16 @@ struct NormCfg {
     typedef T type;
     static constexpr int vec = VEC, tpr = TPR, nv = NV;
 };
-template <typename F>
+template <bool BACKWARD, typename F>
 hipError_t with_norm(bool bf16, bool vec, int d, F f) {
     if (bf16) {
         typedef unsigned short u16;
         if (d <= 512) return f(NormCfg<u16, 8, 64, 1>{});
         if (d <= 1024) return f(NormCfg<u16, 8, 64, 2>{});
-        if (d <= 4096) return f(NormCfg<u16, 8, 256, 2>{});
+        // (the backward's column sums take registers: more threads per row;
+        // 4096x4096: 34.7 against 37.8 us, the forward 15.8 against 17.4)
+        if (BACKWARD && d <= 2048) return f(NormCfg<u16, 8, 256, 1>{});
+        if (d <= 4096) return f(NormCfg<u16, 8, BACKWARD ? 512 : 256, BACKWARD ? 1 : 2>{});
         if (d <= 8192) return f(NormCfg<u16, 8, 512, 2>{});
         return f(NormCfg<u16, 8, 1024, 2>{});
     }
@@ -430,14 +452,14 @@ hipError_t with_norm(bool bf16, bool vec, int d, F f) {
 }  // namespace
 
 size_t layer_norm_backward_bytes(int64_t N, int64_t d) {
-    const int64_t P = N < kNormBackwardGroups ? N : kNormBackwardGroups;
+    const int64_t P = N < kNormBackwardMax ? N : kNormBackwardMax;
     return (size_t)(P * 2 * d) * sizeof(float);
 }
 
 hipError_t launch_layer_norm(bool bf16, bool vec, const void *x, const void *res, const float *w,
                              const float *b, float eps, int64_t N, int64_t d, void *h, void *out,
                              float *mean, float *rstd, hipStream_t s) {
-    return with_norm(bf16, vec, (int)d, [&](auto c) {
+    return with_norm<false>(bf16, vec, (int)d, [&](auto c) {
         typedef decltype(c) C;
         typedef typename C::type T;
         constexpr int groups = C::tpr < 256 ? 256 / C::tpr : 1;
@@ -458,12 +480,13 @@ hipError_t launch_layer_norm_backward(bool bf16, bool vec, const void *x, const 
                                       const void *dres, int64_t N, int64_t d, void *dx, float *dw,
                                       float *db, float *part, hipStream_t s) {
     int P = 0;
-    hipError_t err = with_norm(bf16, vec, (int)d, [&](auto c) {
+    hipError_t err = with_norm<true>(bf16, vec, (int)d, [&](auto c) {
         typedef decltype(c) C;
         typedef typename C::type T;
         constexpr int groups = C::tpr < 256 ? 256 / C::tpr : 1;
         const int64_t blocks = (N + groups - 1) / groups;
-        P = (int)(blocks < kNormBackwardGroups ? blocks : kNormBackwardGroups);
+        const int64_t most = backward_groups(C::tpr);
+        P = (int)(blocks < most ? blocks : most);
         hipLaunchKernelGGL((layer_norm_backward_kernel<T, C::vec, C::tpr, C::nv>),
                            dim3((unsigned)P), dim3(C::tpr < 256 ? 256 : C::tpr), 0, s,
                            static_cast<const T *>(x), w, mean, rstd, static_cast<const T *>(dout),
@@ -473,7 +496,7 @@ hipError_t launch_layer_norm_backward(bool bf16, bool vec, const void *x, const 
     if (err != hipSuccess)
         return err;
     hipLaunchKernelGGL(norm_column_sums_kernel, dim3((unsigned)((d + 63) / 64), db ? 2u : 1u),
-                       dim3(256), 0, s, (const float *)part, P, (int)d, dw, db);
+                       dim3(kSumGroups * 64), 0, s, (const float *)part, P, (int)d, dw, db);
     return hipGetLastError();
 }
 
