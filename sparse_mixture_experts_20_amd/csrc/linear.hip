@@ -270,29 +270,21 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
             barrier_lds();
         }
         const char *st = smem + (kt & 1) * STAGE;
-        bf16x8 fA[2][FM], fB[2][FN];
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-            fB[0][j] = frag_b(st, 0, j);
+        for (int ks = 0; ks < kStep / 32; ++ks) {
+            bf16x8 fA[FM], fB[FN];
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-            fA[0][i] = frag_a(st, 0, i);
+            for (int j = 0; j < FN; ++j)
+                fB[j] = frag_b(st, ks, j);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            if (ks == 0) {
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    fB[1][j] = frag_b(st, 1, j);
-#pragma unroll
-                for (int i = 0; i < FM; ++i)
-                    fA[1][i] = frag_a(st, 1, i);
-            }
+            for (int i = 0; i < FM; ++i)
+                fA[i] = frag_a(st, ks, i);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fB[ks][j], fA[ks][i],
-                                                                         acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fB[j], fA[i], acc[i][j], 0,
+                                                                         0, 0);
         }
     }
     // lane: row l16 of each 16-row strip, 16 adjacent columns
@@ -480,7 +472,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
 }
 
 // Tile and K-ranges of a product of rows x cols over K. 256x256 tiles (one
-// workgroup of 8 waves per CU) when they fill the 256 CUs about once, else
+// workgroup of 16 waves of 64x64 per CU: four per SIMD hide more LDS latency
+// than the 8 waves of 128x64 save in LDS reads, 1061 against 1018 TFLOP/s at
+// 4096x4096x14336) when they fill the 256 CUs about once, else
 // 128x128 (two workgroups per CU) with the reduction cut so that about 512
 // workgroups run, each with at least 4 K-steps.
 struct Shape {
@@ -511,7 +505,7 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
     if (sh.big) {
         const int64_t T = ((rows + 255) / 256) * ((cols + 255) / 256);
         const int64_t grid = (T + kXcdCount - 1) / kXcdCount * kXcdCount;
-        hipLaunchKernelGGL((linear_kernel<256, 256, 2, 4, AT, BT>), dim3((unsigned)grid), dim3(512),
+        hipLaunchKernelGGL((linear_kernel<256, 256, 4, 4, AT, BT>), dim3((unsigned)grid), dim3(1024),
                            0, s, a, b, (int)rows, (int)cols, (int)K, ep, (float *)nullptr);
         return hipGetLastError();
     }
