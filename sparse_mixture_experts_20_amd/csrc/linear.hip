@@ -13,7 +13,7 @@
 // (skinny.hpp): one workgroup per 16 output columns, its waves splitting K.
 //
 // More rows: one kernel for the three products, BM x BN output tiles, K-step
-// 64 in a two-stage LDS ring filled by direct global-to-LDS loads (16 bytes a
+// 64 in an LDS ring of S stages filled by direct global-to-LDS loads (16 bytes a
 // lane); waves of (FM 16) x 64 on 16x16x32 MFMAs. An operand whose rows run
 // along the reduction (x, W of the forward, dz of dx) is staged row by row; one
 // stored the other way (W of dx, both of dW) is staged as it lies and turned
@@ -39,7 +39,10 @@ constexpr int kStep = 64;   // K-step of the tiled product
 __device__ __forceinline__ void barrier_lds() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_loads() {   // until at most N are in flight
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 // Direct copy of 16 bytes per lane to LDS: lane l's bytes land at base + 16 l.
 // In asm so that the compiler does not wait for it before every LDS read; the
@@ -112,7 +115,7 @@ __device__ __forceinline__ void store_columns(const Epilogue &ep, int64_t o, flo
 // [K][cols] (else [cols][K]). grid: (tiles rounded up to the XCD count,
 // K-ranges); with more than one range, range s writes its fp32 partial tile
 // rows to part + s rows cols and the epilogue is left to the second kernel.
-template <int BM, int BN, int WM, int WN, bool AT, bool BT>
+template <int BM, int BN, int WM, int WN, int S, bool AT, bool BT>
 __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     const unsigned short *__restrict__ A, const unsigned short *__restrict__ B, int rows,
     int cols, int K, Epilogue ep, float *__restrict__ part) {
@@ -121,8 +124,9 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     static_assert(BN / WN == 64, "a wave holds 64 columns");
     constexpr int ABYTES = BM * kStep * 2, BBYTES = BN * kStep * 2, STAGE = ABYTES + BBYTES;
     constexpr int IA = ABYTES / (NW * 1024), IB = BBYTES / (NW * 1024);
+    static_assert(S >= 2 && S <= 4, "waits below");
     static_assert(IA * NW * 1024 == ABYTES && IB * NW * 1024 == BBYTES, "whole wave copies");
-    __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) char smem[S * STAGE];
 
     // Tile of this workgroup: block b runs on XCD b mod 8 and takes index
     // (b mod 8) T8/8 + b/8, one contiguous range per XCD; within it, column
@@ -182,7 +186,7 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     }
     const unsigned base = lds_address(smem);
     auto issue = [&](int kt) {
-        const unsigned st = base + (unsigned)(kt & 1) * STAGE;
+        const unsigned st = base + (unsigned)(kt % S) * STAGE;
 #pragma unroll
         for (int i = 0; i < IA; ++i) {
             const unsigned dst = st + (unsigned)(wv * IA + i) * 1024;
@@ -202,7 +206,7 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     };
     // chunks of the last step that lie past K, in both operands
     auto zero_tail = [&](int kt) {
-        char *st = smem + (kt & 1) * STAGE;
+        char *st = smem + (kt % S) * STAGE;
         const u32x4 zero = {0u, 0u, 0u, 0u};
         for (int q = threadIdx.x; q < ABYTES / 16; q += NW * 64) {
             const int k = AT ? q / (BM / 8) : 8 * ((q % 8) ^ fa(q / 8));
@@ -258,18 +262,27 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (kb < ke)
-        issue(kb);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+        if (kb + s < ke)
+            issue(kb + s);
     for (int kt = kb; kt < ke; ++kt) {
-        wait_loads();
+        // step kt has landed; the later ones issued so far may stay in flight
+        const int later = min(S - 2, ke - 1 - kt);
+        if (later >= 2)
+            wait_loads<2 * (IA + IB)>();
+        else if (later == 1)
+            wait_loads<IA + IB>();
+        else
+            wait_loads<0>();
         barrier_lds();
-        if (kt + 1 < ke)
-            issue(kt + 1);
+        if (kt + S - 1 < ke)
+            issue(kt + S - 1);
         if (kt == KT - 1 && K % kStep != 0) {
             zero_tail(kt);
             barrier_lds();
         }
-        const char *st = smem + (kt & 1) * STAGE;
+        const char *st = smem + (kt % S) * STAGE;
 #pragma unroll
         for (int ks = 0; ks < kStep / 32; ++ks) {
             bf16x8 fA[FM], fB[FN];
@@ -471,25 +484,41 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
     }
 }
 
-// Tile and K-ranges of a product of rows x cols over K. 256x256 tiles (one
-// workgroup of 16 waves of 64x64 per CU: four per SIMD hide more LDS latency
-// than the 8 waves of 128x64 save in LDS reads, 1061 against 1018 TFLOP/s at
-// 4096x4096x14336) when they fill the 256 CUs about once, else
-// 128x128 (two workgroups per CU) with the reduction cut so that about 512
-// workgroups run, each with at least 4 K-steps.
+// Tile and K-ranges of a product of rows x cols over K.
+//  - 256x256 tiles, one workgroup of 16 waves of 64x64 per CU (four per SIMD
+//    hide more LDS latency than the 8 waves of 128x64 save in LDS reads, 1061
+//    against 1018 TFLOP/s at 4096x4096x14336), when they fill the 256 CUs about
+//    once;
+//  - 128x128 tiles, two workgroups of 4 waves per CU, for more than 256 of them
+//    (2048x768x3072: 25 us, against 28 with the next form);
+//  - 128x128 tiles, one workgroup of 8 waves per CU and a ring of four stages,
+//    for up to 256 of them: alone on its CU a workgroup waits for the latency
+//    of its loads, and three K-steps in flight instead of one take a K-step from
+//    0.83 to 0.6 us. The reduction is cut where the model below, in us, gains
+//    from it: K-steps, and for the joining pass its launch and the partials
+//    written and read at 4 TB/s (2048x3072x768: 29 us in 2 ranges, 32 in one;
+//    512x768x3072: 15 us in one, 21 in 2).
+enum class Tile { k256, k128x2, k128 };
 struct Shape {
-    bool big;
+    Tile tile;
     int splits;
 };
 Shape shape_of(int64_t rows, int64_t cols, int64_t K) {
-    const int64_t big = ((rows + 255) / 256) * ((cols + 255) / 256);
-    if (big >= 192)
-        return {true, 1};
+    if (((rows + 255) / 256) * ((cols + 255) / 256) >= 192)
+        return {Tile::k256, 1};
     const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
+    if (tiles > 256)
+        return {Tile::k128x2, 1};
     const int64_t KT = (K + kStep - 1) / kStep;
-    int64_t s = std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), KT / 4);
-    s = std::min<int64_t>(std::max<int64_t>(s, 1), 16);
-    return {false, (int)s};
+    auto cost = [&](int64_t s) {
+        const double join = 4.5 + (double)(s + 1) * (double)(rows * cols) * 4.0 / 4e6;
+        return 0.6 * (double)((KT + s - 1) / s) + (s > 1 ? join : 0.0);
+    };
+    int64_t best = 1;
+    for (int64_t s = 2; s <= 16 && s * tiles <= 256 && 4 * s <= KT; ++s)
+        if (cost(s) < cost(best))
+            best = s;
+    return {Tile::k128, (int)best};
 }
 size_t part_bytes(int64_t rows, int64_t cols, int64_t K) {
     const Shape sh = shape_of(rows, cols, K);
@@ -502,18 +531,19 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
     const Shape sh = shape_of(rows, cols, K);
     const auto *a = static_cast<const unsigned short *>(A);
     const auto *b = static_cast<const unsigned short *>(B);
-    if (sh.big) {
-        const int64_t T = ((rows + 255) / 256) * ((cols + 255) / 256);
+    auto go = [&](auto kernel, int bm, int bn, int threads) {
+        const int64_t T = ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
         const int64_t grid = (T + kXcdCount - 1) / kXcdCount * kXcdCount;
-        hipLaunchKernelGGL((linear_kernel<256, 256, 4, 4, AT, BT>), dim3((unsigned)grid), dim3(1024),
-                           0, s, a, b, (int)rows, (int)cols, (int)K, ep, (float *)nullptr);
-        return hipGetLastError();
-    }
-    const int64_t T = ((rows + 127) / 128) * ((cols + 127) / 128);
-    const int64_t grid = (T + kXcdCount - 1) / kXcdCount * kXcdCount;
-    hipLaunchKernelGGL((linear_kernel<128, 128, 2, 2, AT, BT>),
-                       dim3((unsigned)grid, (unsigned)sh.splits), dim3(256), 0, s, a, b, (int)rows,
-                       (int)cols, (int)K, ep, sh.splits > 1 ? part : (float *)nullptr);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid, (unsigned)sh.splits), dim3(threads), 0, s,
+                           a, b, (int)rows, (int)cols, (int)K, ep,
+                           sh.splits > 1 ? part : (float *)nullptr);
+    };
+    if (sh.tile == Tile::k256)
+        go(linear_kernel<256, 256, 4, 4, 2, AT, BT>, 256, 256, 1024);
+    else if (sh.tile == Tile::k128x2)
+        go(linear_kernel<128, 128, 2, 2, 2, AT, BT>, 128, 128, 256);
+    else
+        go(linear_kernel<128, 128, 4, 2, 4, AT, BT>, 128, 128, 512);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || sh.splits == 1)
         return err;
