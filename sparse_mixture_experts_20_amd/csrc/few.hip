@@ -127,7 +127,7 @@ __device__ __forceinline__ void score_tile(const float *w, const typename S::typ
             c[0][i] = acc[i];
         const int ke = min(kb + 32 * U, (d + 31) / 32 * 32);
         if (kb < ke)
-            skinny_mma<S, 1, TT, 1, 1>(wr, xt, 0, kb, ke, d, c);
+            skinny_mma<S, 1, TT, 1, 1>(wr, xt, 0, kb, ke, d, d, c);
 #pragma unroll
         for (int i = 0; i < TT; ++i)
             acc[i] = c[0][i];
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
         }
         // operand registers of a batch: U (FM + T) fragments, twice
         constexpr int U = (FM + T <= 2 ? 8 : FM + T <= 4 ? 4 : 2) / (Kind<S>::bf16 ? 1 : 2);
-        skinny_mma<S, FM, T, 1, U>(w, xt, 0, kb, ke, d, c);
+        skinny_mma<S, FM, T, 1, U>(w, xt, 0, kb, ke, d, d, c);
 #pragma unroll
         for (int m = 0; m < FM; ++m)
 #pragma unroll
@@ -553,7 +553,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
                     acc[m][i] = bias[m];
             }
             constexpr int U = FM + NB * T <= 4 ? 4 : FM + NB * T <= 6 ? 2 : 1;
-            skinny_mma<S, FM, T, NB, U>(w, ht, lo, kb, ke, d_ff, acc);
+            skinny_mma<S, FM, T, NB, U>(w, ht, lo, kb, ke, d_ff, d_ff, acc);
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 if (i * 16 + (lane & 15) < rows) {
@@ -579,7 +579,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
 #pragma unroll
             for (int m = 0; m < FM; ++m)
                 acc[m][0] = lane & 8 ? f32x4{0.f, 0.f, 0.f, 0.f} : bias[m];
-            skinny_mma<S, FM, 1, 1, FM == 1 ? 8 : 4>(w, ht, 0, kb, ke, d_ff, acc);
+            skinny_mma<S, FM, 1, 1, FM == 1 ? 8 : 4>(w, ht, 0, kb, ke, d_ff, d_ff, acc);
             const float g = gate[as];
 #pragma unroll
             for (int m = 0; m < FM; ++m) {

@@ -9,10 +9,11 @@
 // of the two matrix products (they run on the bf16 matrix cores); db sums the
 // fp32 values before that rounding. Without an activation dz is dout itself.
 //
-// Few rows (N <= 64): bound by the stream of W, run on the skinny core
-// (skinny.hpp): one workgroup per 16 output columns, its waves splitting K.
+// Few rows and a small W: bound by latency, run on the skinny core
+// (skinny.hpp): one workgroup per 16 (or 8) output columns, its waves splitting
+// K.
 //
-// More rows: one kernel for the three products, BM x BN output tiles, K-step
+// Otherwise one kernel for the three products, BM x BN output tiles, K-step
 // 64 in an LDS ring of S stages filled by direct global-to-LDS loads (16 bytes a
 // lane); waves of (FM 16) x 64 on 16x16x32 MFMAs. An operand whose rows run
 // along the reduction (x, W of the forward, dz of dx) is staged row by row; one
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     static_assert(BN / WN == 64, "a wave holds 64 columns");
     constexpr int ABYTES = BM * kStep * 2, BBYTES = BN * kStep * 2, STAGE = ABYTES + BBYTES;
     constexpr int IA = ABYTES / (NW * 1024), IB = BBYTES / (NW * 1024);
-    static_assert(S >= 2 && S <= 4, "waits below");
+    static_assert(S >= 2 && (S - 2) * (IA + IB) < 64, "a wait counts to 63");
     static_assert(IA * NW * 1024 == ABYTES && IB * NW * 1024 == BBYTES, "whole wave copies");
     __shared__ __attribute__((aligned(1024))) char smem[S * STAGE];
 
@@ -154,7 +155,9 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     // columns past the edge read a valid place (their products are not stored).
     auto fa = [](int r) { return (r >> 1) & 7; };                       // 16 adjacent rows
     auto fb = [](int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); };    // rows 16 i + 4 j + 0..3
-    auto ga = [](int k) { return 2 * ((k & 3) | ((k >> 1) & 4)); };
+    auto ga = [](int k) {                                          // rows 8 i + 4 j + 0..3
+        return BM == 64 ? (k & 2) | ((k >> 1) & 4) : 2 * ((k & 3) | ((k >> 1) & 4));
+    };
     auto gb = [](int k) { return (k & 1) | ((k & 2) << 2); };
     const unsigned short *pa[IA], *pb[IB];
     int ka[IA], kbb[IB];   // K offset (elements) of the lane's chunk within the step
@@ -268,11 +271,9 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
             issue(kb + s);
     for (int kt = kb; kt < ke; ++kt) {
         // step kt has landed; the later ones issued so far may stay in flight
-        const int later = min(S - 2, ke - 1 - kt);
-        if (later >= 2)
-            wait_loads<2 * (IA + IB)>();
-        else if (later == 1)
-            wait_loads<IA + IB>();
+        // (the last S - 2 steps wait for all that is in flight)
+        if (kt + S - 2 < ke)
+            wait_loads<(S - 2) * (IA + IB)>();
         else
             wait_loads<0>();
         barrier_lds();
@@ -349,11 +350,22 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float *__restric
     const int64_t n = rows * cols;
     if (i >= n)
         return;
-    f32x4 a = *reinterpret_cast<const f32x4 *>(part + i);
-    f32x4 c = *reinterpret_cast<const f32x4 *>(part + i + 4);
-    for (int s = 1; s < S; ++s) {
-        a += *reinterpret_cast<const f32x4 *>(part + s * n + i);
-        c += *reinterpret_cast<const f32x4 *>(part + s * n + i + 4);
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, c = a;
+    constexpr int B = 4;   // ranges in flight
+    for (int s = 0; s < S; s += B) {
+        f32x4 u[B][2];
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+            const float *p = part + min(s + q, S - 1) * n + i;
+            u[q][0] = *reinterpret_cast<const f32x4 *>(p);
+            u[q][1] = *reinterpret_cast<const f32x4 *>(p + 4);
+        }
+#pragma unroll
+        for (int q = 0; q < B; ++q)
+            if (s + q < S) {
+                a += u[q][0];
+                c += u[q][1];
+            }
     }
     float v[8], b[8];
 #pragma unroll
@@ -368,44 +380,57 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float *__restric
     store_columns<8>(ep, i, v, b, 8);
 }
 
-// Few rows: 16 output columns per workgroup, kFewWaves waves over K.
-constexpr int kFewWaves = 16;
-template <int TT>
+// Few rows: 16 output columns per workgroup, kFewWaves waves over K. HALF (at
+// most 8 rows): 8 columns per workgroup, so that a narrow product still fills
+// the CUs; the MFMA's rows 0-7 and columns 0-7 take the first half of K, rows
+// and columns 8-15 the second half of the same weight and token rows, and the
+// two diagonal blocks of the result are added.
+constexpr int kFewWaves = 8;
+template <int TT, bool HALF>
 __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(
     const unsigned short *__restrict__ x, const unsigned short *__restrict__ W, int N, int M,
     int K, Epilogue ep) {
+    static_assert(!HALF || TT == 1, "one tile of tokens");
     __shared__ f32x4 part[kFewWaves][TT][64];
-    const int lane = threadIdx.x & 63;
+    constexpr int CB = HALF ? 8 : 16;
+    const int lane = threadIdx.x & 63, l16 = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c0 = blockIdx.x * 16;
-    const unsigned short *w[1] = {W + (int64_t)min(c0 + (lane & 15), M - 1) * K};
+    const int c0 = blockIdx.x * CB;
+    // columns a wave's lanes walk together, and where this lane's start
+    const int steps = HALF ? (K + 63) / 64 : (K + 31) / 32;
+    const int shift = HALF && l16 >= 8 ? steps * 32 : 0;
+    const unsigned short *w[1] = {W + (int64_t)min(c0 + l16 % CB, M - 1) * K + shift};
     const unsigned short *xt[TT];
     f32x4 acc[1][TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-        xt[i] = x + (int64_t)min(i * 16 + (lane & 15), N - 1) * K;
+        xt[i] = x + (int64_t)min(i * 16 + l16 % CB, N - 1) * K + shift;
         acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    const int steps = (K + 31) / 32;
     const int kb = (int)((int64_t)wv * steps / kFewWaves) * 32;
     const int ke = (int)((int64_t)(wv + 1) * steps / kFewWaves) * 32;
-    skinny_mma<SkinnyBf16, 1, TT, 1, TT == 1 ? 4 : TT == 2 ? 3 : 2>(w, xt, 0, kb, ke, K, acc);
+    skinny_mma<SkinnyBf16, 1, TT, 1, TT == 1 ? 4 : TT == 2 ? 3 : 2>(
+        w, xt, 0, kb, ke, K - shift, HALF ? K - steps * 32 : K, acc);
 #pragma unroll
     for (int i = 0; i < TT; ++i)
         part[wv][i][lane] = acc[0][i];
     __syncthreads();
     // thread -> (row, 8 columns): lanes l and l + 16 of a tile hold columns
     // 4 (l / 16) + 0..3 and the next four of row l % 16
-    for (int q = threadIdx.x; q < TT * 32; q += kFewWaves * 64) {
-        const int i = q >> 5, l = (q & 15) + 32 * ((q >> 4) & 1);
+    for (int q = threadIdx.x; q < TT * 16 * (CB / 8); q += kFewWaves * 64) {
+        const int i = q / (2 * CB), l = (q & 15) + 32 * (q / 16 % (CB / 8));
         const int r = i * 16 + (l & 15), c = c0 + 4 * (l >> 4);
         if (r >= N || c >= M)
             continue;
-        f32x4 a = part[0][i][l], b4 = part[0][i][l + 16];
+        f32x4 a = {0.f, 0.f, 0.f, 0.f}, b4 = a;
 #pragma unroll
-        for (int s = 1; s < kFewWaves; ++s) {
+        for (int s = 0; s < kFewWaves; ++s) {
             a += part[s][i][l];
             b4 += part[s][i][l + 16];
+            if constexpr (HALF) {   // rows and columns 8 further
+                a += part[s][i][l + 40];
+                b4 += part[s][i][l + 56];
+            }
         }
         float v[8], b[8];
 #pragma unroll
@@ -485,6 +510,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
 }
 
 // Tile and K-ranges of a product of rows x cols over K.
+//  - up to 64 rows: 64x128 tiles (8 waves, five stages), the reduction cut for
+//    256 workgroups: a stream of W through LDS with 96 KB in flight per CU;
 //  - 256x256 tiles, one workgroup of 16 waves of 64x64 per CU (four per SIMD
 //    hide more LDS latency than the 8 waves of 128x64 save in LDS reads, 1061
 //    against 1018 TFLOP/s at 4096x4096x14336), when they fill the 256 CUs about
@@ -498,18 +525,22 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
 //    from it: K-steps, and for the joining pass its launch and the partials
 //    written and read at 4 TB/s (2048x3072x768: 29 us in 2 ranges, 32 in one;
 //    512x768x3072: 15 us in one, 21 in 2).
-enum class Tile { k256, k128x2, k128 };
+enum class Tile { k64, k256, k128x2, k128 };
 struct Shape {
     Tile tile;
     int splits;
 };
 Shape shape_of(int64_t rows, int64_t cols, int64_t K) {
+    const int64_t KT = (K + kStep - 1) / kStep;
+    if (rows <= 64) {
+        const int64_t s = std::min<int64_t>(256 / std::max<int64_t>((cols + 127) / 128, 1), KT / 4);
+        return {Tile::k64, (int)std::min<int64_t>(std::max<int64_t>(s, 1), 16)};
+    }
     if (((rows + 255) / 256) * ((cols + 255) / 256) >= 192)
         return {Tile::k256, 1};
     const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
     if (tiles > 256)
         return {Tile::k128x2, 1};
-    const int64_t KT = (K + kStep - 1) / kStep;
     auto cost = [&](int64_t s) {
         const double join = 4.5 + (double)(s + 1) * (double)(rows * cols) * 4.0 / 4e6;
         return 0.6 * (double)((KT + s - 1) / s) + (s > 1 ? join : 0.0);
@@ -538,7 +569,9 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
                            a, b, (int)rows, (int)cols, (int)K, ep,
                            sh.splits > 1 ? part : (float *)nullptr);
     };
-    if (sh.tile == Tile::k256)
+    if (sh.tile == Tile::k64)
+        go(linear_kernel<64, 128, 4, 2, AT ? 4 : 5, AT, BT>, 64, 128, 512);
+    else if (sh.tile == Tile::k256)
         go(linear_kernel<256, 256, 4, 4, 2, AT, BT>, 256, 256, 1024);
     else if (sh.tile == Tile::k128x2)
         go(linear_kernel<128, 128, 2, 2, 2, AT, BT>, 128, 128, 256);
@@ -552,19 +585,28 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
     return hipGetLastError();
 }
 
-// Rows of the column-sum partials of the dz pass: workgroups along N.
+// Workgroups of the dz pass along N (rows of its column-sum partials): about
+// 2048 in all, each with at least one row per thread.
 int dz_groups(int64_t N, int64_t M) {
     const int64_t across = (M + 255) / 256;
     const int64_t want = std::max<int64_t>(1, 2048 / across);
-    return (int)std::min<int64_t>(want, (N + 31) / 32);
+    return (int)std::min<int64_t>(want, (N + 7) / 8);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
+// Whether a forward product runs on the skinny kernel: up to 16 rows and 32 MB
+// of weights, or up to 64 rows and 4 MB. Beyond, the tiled kernel's stream is
+// faster (1x4096x14336: 24 against 34 us; 64x7168x2048: 19 against 35 us), below
+// its joining launch costs more (16x1024x1024: 6 against 9 us).
+static bool skinny(int64_t N, int64_t K, int64_t M) {
+    return N <= kFewMaxTokens && K * M <= ((int64_t)(N <= 16 ? 16 : 2) << 20);
+}
+
 size_t linear_bytes(int64_t N, int64_t K, int64_t M) {
-    return N <= kFewMaxTokens ? 0 : part_bytes(N, M, K);
+    return skinny(N, K, M) ? 0 : part_bytes(N, M, K);
 }
 
 hipError_t launch_linear(const void *x, const void *W, const float *bias, int act,
@@ -573,17 +615,22 @@ hipError_t launch_linear(const void *x, const void *W, const float *bias, int ac
     const Epilogue ep{static_cast<unsigned short *>(out), nullptr, bias,
                       static_cast<const unsigned short *>(residual),
                       static_cast<unsigned short *>(z), act};
-    if (N <= kFewMaxTokens) {
-        auto go = [&](auto tiles) {
-            hipLaunchKernelGGL(linear_few_kernel<decltype(tiles)::value>,
-                               dim3((unsigned)((M + 15) / 16)), dim3(kFewWaves * 64), 0, s,
-                               static_cast<const unsigned short *>(x),
+    if (skinny(N, K, M)) {
+        auto go = [&](auto tiles, auto half) {
+            constexpr int TT = decltype(tiles)::value;
+            constexpr bool HALF = decltype(half)::value;
+            constexpr int CB = HALF ? 8 : 16;
+            hipLaunchKernelGGL((linear_few_kernel<TT, HALF>), dim3((unsigned)((M + CB - 1) / CB)),
+                               dim3(kFewWaves * 64), 0, s, static_cast<const unsigned short *>(x),
                                static_cast<const unsigned short *>(W), (int)N, (int)M, (int)K, ep);
             return hipGetLastError();
         };
-        return N <= 16   ? go(std::integral_constant<int, 1>{})
-               : N <= 32 ? go(std::integral_constant<int, 2>{})
-                         : go(std::integral_constant<int, 4>{});
+        const std::false_type whole;
+        if (N <= 8 && M < 16 * 256)
+            return go(std::integral_constant<int, 1>{}, std::true_type{});
+        return N <= 16   ? go(std::integral_constant<int, 1>{}, whole)
+               : N <= 32 ? go(std::integral_constant<int, 2>{}, whole)
+                         : go(std::integral_constant<int, 4>{}, whole);
     }
     return launch_product<false, false>(x, W, N, M, K, ep, static_cast<float *>(ws), s);
 }

@@ -68,18 +68,21 @@ struct SkinnyF32 {
 // of FM weight rows and TT token rows per lane into acc (row 4 (l / 16) + q of
 // the weight rows, column l % 16 of the tokens). w[m] and xt[i] point at this
 // lane's rows (column 0); NB operand terms per token row, `lo` elements apart,
-// are added (2: a row kept as the sum of two bf16 terms). Columns past K are
-// zeros. Two weight rows per lane (FM = 2) halve the token rows' loads.
+// are added (2: a row kept as the sum of two bf16 terms). K: columns the rows
+// have from w[m] and xt[i] on, which may differ between lanes (those past it
+// are zeros); all: the smallest K of the wave. Two weight rows per lane (FM =
+// 2) halve the token rows' loads.
 template <typename S, int FM, int TT, int NB, int U>
 __device__ __forceinline__ void skinny_mma(const typename S::type *const (&w)[FM],
                                            const typename S::type *const (&xt)[TT], int64_t lo,
-                                           int kbeg, int kend, int K, f32x4 (&acc)[FM][TT]) {
+                                           int kbeg, int kend, int K, int all,
+                                           f32x4 (&acc)[FM][TT]) {
     typedef typename S::frag frag;
     struct Step {
         frag a[FM], b[TT][NB];
     };
     const int ko = 8 * (int)(__lane_id() >> 4);
-    const int full = min(kend, K / 32 * 32);   // steps that need no mask
+    const int full = min(kend, all / 32 * 32);   // steps that need no mask
     // the weights of a batch first: their addresses are known before the token
     // rows', which come from the dispatch plan
     auto load = [&](int k, Step (&s)[U]) {

@@ -35,6 +35,11 @@ SHAPES = [
     (127, 64, 128, "relu", False, True), (130, 2056, 136, "gelu", True, False),
     (257, 1544, 776, "none", True, True), (1000, 200, 3000, "gelu", True, True),
     (3500, 136, 3592, "relu", True, True), (4097, 520, 3080, "none", False, False),
+    # few rows past what the skinny kernel takes, and its half tiles' limits
+    (1, 4104, 4360, "gelu", True, True), (9, 4104, 4360, "none", True, False),
+    (40, 2056, 1544, "relu", True, True), (64, 4104, 1032, "gelu", False, True),
+    (8, 264, 4088, "gelu", True, True), (8, 264, 4096, "relu", True, False),
+    (5, 8, 40, "none", False, True), (8, 72, 16, "gelu", True, False),
 ]
 
 
@@ -70,6 +75,8 @@ BACKWARD = [
     (64, 1032, 72, "gelu"), (65, 72, 264, "none"), (127, 136, 1000, "relu"),
     (200, 712, 520, "gelu"), (1031, 264, 2056, "gelu"), (2047, 1000, 136, "none"),
     (3600, 3592, 136, "relu"), (3333, 3080, 3336, "gelu"),
+    # weight gradients of at most 64 rows, over several K-steps
+    (129, 8, 8, "none"), (300, 264, 56, "gelu"), (2000, 72, 64, "relu"), (640, 1000, 40, "none"),
 ]
 
 
