@@ -8,6 +8,7 @@ There is no fallback: if the library is missing, :func:`lib` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional
@@ -788,9 +789,27 @@ def _scratch(workspace, index: int):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _stream_of(index: int, stream):
+def _stream_of(index: int):
     # (the handle of torch's current stream without building a Stream object)
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_stream(fn):
+    """``stream=``: the call and everything it allocates belong to that stream
+    (memory allocated for one stream and used on another could be handed out
+    again while the call still runs)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                if t.get_device() != stream.device.index:
+                    raise ValueError(f"a tensor on {t.device}, the stream on {stream.device}")
+                break
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _run(index: int, where: str, fn, *args):
@@ -810,10 +829,11 @@ def few_workspace_size(N: int, d: int, E: int, d_ff: int, k: int, capacity_facto
     return int(lib().moe_few_workspace_size(N, d, E, d_ff, k, capacity_factor, code))
 
 
+@_on_stream
 def forward_few(x: torch.Tensor, W_g: torch.Tensor, noise: Optional[torch.Tensor],
                 W_up: torch.Tensor, W_down: torch.Tensor, k: int, capacity_factor: float,
                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                export: bool = True, stream=None, act: str = "relu",
+                export: bool = True, act: str = "relu",
                 b_up: Optional[torch.Tensor] = None, b_down: Optional[torch.Tensor] = None,
                 router_stats: bool = False):
     """Run ``moe_forward_few`` (at most ``MOE_FEW_MAX_TOKENS`` tokens): the
@@ -834,7 +854,7 @@ def forward_few(x: torch.Tensor, W_g: torch.Tensor, noise: Optional[torch.Tensor
         used = torch.empty((E,), dtype=torch.int32, device=dev)
     dem, drp, gsum = _router_stats(E, dev, router_stats)
     ws, wn = _scratch(workspace, index)
-    st = MoeStats(_stream_of(index, stream), ws, wn, _ptr(idx), _ptr(gate), _ptr(slot),
+    st = MoeStats(_stream_of(index), ws, wn, _ptr(idx), _ptr(gate), _ptr(slot),
                   _ptr(used), -1, _ptr(dem), _ptr(drp), _ptr(gsum), None)
     _pack(b_up, index), _pack(b_down, index)   # (same checks as every tensor)
     o = _opts(act, b_up, b_down)
@@ -849,8 +869,9 @@ class FewLayer:
     (with ``export``) the routing buffers are built once, for up to
     ``max_tokens`` tokens; ``layer(x, noise=None, out=None)`` runs
     ``moe_forward_few`` on the current stream and returns ``(out, Stats)``.
-    Calls share the workspace and the routing buffers, so they must be ordered
-    on one stream; ``out`` is a new tensor unless given."""
+    Calls share the workspace and the routing buffers, so they must not overlap
+    (calls on one stream do not; between streams, order them with events);
+    ``out`` is a new tensor unless given."""
 
     def __init__(self, W_g, W_up, W_down, k, capacity_factor, act="relu", b_up=None, b_down=None,
                  max_tokens=MOE_FEW_MAX_TOKENS, export=False, router_stats=False):
@@ -880,15 +901,25 @@ class FewLayer:
                               _ptr(gsum), None)
         self._sref = ctypes.byref(self.stats)
         self._fn = lib().moe_forward_few
+        self._home = _stream_of(index)   # the stream the buffers were allocated for
 
     def __call__(self, x, noise=None, out=None, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self(x, noise, out)
         N = x.numel() // x.shape[-1]
         if N > self.max_tokens:
             raise ValueError(f"{N} tokens: this layer was built for {self.max_tokens}")
         if out is None:
             out = torch.empty_like(x)
         index, w, st = self.index, self._w, self.stats
-        st.stream = _stream_of(index, stream)
+        st.stream = _stream_of(index)
+        if st.stream != self._home:
+            # keep the buffers until that stream is done, should the layer go first
+            s = torch.cuda.current_stream(index)
+            for b in (self.workspace, *self._routing, *self._counts):
+                if b is not None:
+                    b.record_stream(s)
         _run(index, "moe_forward_few", self._fn, _pack(x, index), w[0], _pack(noise, index), w[1],
              w[2], self._o, self.k, self.cf, _pack(out, index), self._sref)
         idx, gate, slot, used = self._routing
@@ -907,8 +938,9 @@ def linear_workspace_size(N: int, K: int, M: int) -> int:
     return int(lib().moe_linear_workspace_size(N, K, M))
 
 
+@_on_stream
 def linear(x, W, bias=None, act: str = "none", residual=None, out=None, keep_z: bool = False,
-           workspace=None, stream=None):
+           workspace=None):
     """``act(x W^T + bias) + residual`` (bf16; x [..., K], W [M, K]): returns
     ``(out, z)``, z the bf16 pre-activations with ``keep_z``, else None."""
     K, M = x.shape[-1], W.shape[0]
@@ -922,7 +954,7 @@ def linear(x, W, bias=None, act: str = "none", residual=None, out=None, keep_z: 
     ws, wn = _scratch(workspace, index)
     _run(index, "moe_linear", lib().moe_linear, _pack(x, index), _pack(W, index),
          _pack(bias, index), _linear_act(act), _pack(residual, index), _pack(out, index),
-         _pack(z, index), ws, wn, _stream_of(index, stream))
+         _pack(z, index), ws, wn, _stream_of(index))
     return out, z
 
 
@@ -930,9 +962,10 @@ def linear_backward_workspace_size(N: int, K: int, M: int, act: str = "none") ->
     return int(lib().moe_linear_backward_workspace_size(N, K, M, _linear_act(act)))
 
 
+@_on_stream
 def linear_backward(x, W, z, dout, act: str = "none", bias: bool = True, need_dx: bool = True,
                     need_dW: bool = True, dx_dtype=torch.float32, dW_dtype=torch.float32,
-                    workspace=None, stream=None):
+                    workspace=None):
     """Gradients of :func:`linear` for ``dout``: ``(dx, dW, dbias)``, None for
     the ones not asked for; z is the forward's (None without an activation)."""
     N, K, M = x.numel() // x.shape[-1], x.shape[-1], W.shape[0]
@@ -946,12 +979,13 @@ def linear_backward(x, W, z, dout, act: str = "none", bias: bool = True, need_dx
     ws, wn = _scratch(workspace, index)
     _run(index, "moe_linear_backward", lib().moe_linear_backward, _pack(x, index),
          _pack(W, index), _pack(z, index), _linear_act(act), _pack(dout, index),
-         _pack(dx, index), _pack(dW, index), _pack(db, index), ws, wn, _stream_of(index, stream))
+         _pack(dx, index), _pack(dW, index), _pack(db, index), ws, wn, _stream_of(index))
     return dx, dW, db
 
 
+@_on_stream
 def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, h=None, out=None,
-               stats: bool = False, stream=None):
+               stats: bool = False):
     """Layer norm of ``x`` (of ``h = x + residual`` when given, h returned):
     ``(out, h, mean, rstd)``; h is x without a residual, mean and rstd (fp32,
     one per row: what the backward needs) are None unless ``stats``."""
@@ -967,7 +1001,7 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, residual=None, h=None, o
         rstd = torch.empty_like(mean)
     _run(index, "moe_layer_norm", lib().moe_layer_norm, _pack(x, index), _pack(residual, index),
          _pack(weight, index), _pack(bias, index), eps, _pack(h, index), _pack(out, index),
-         _pack(mean, index), _pack(rstd, index), _stream_of(index, stream))
+         _pack(mean, index), _pack(rstd, index), _stream_of(index))
     return out, (x if h is None else h), mean, rstd
 
 
@@ -975,8 +1009,9 @@ def layer_norm_backward_workspace_size(N: int, d: int) -> int:
     return int(lib().moe_layer_norm_backward_workspace_size(N, d))
 
 
+@_on_stream
 def layer_norm_backward(h, weight, mean, rstd, dout, dres=None, bias: bool = True, dx=None,
-                        workspace=None, stream=None):
+                        workspace=None):
     """Gradients of :func:`layer_norm` for ``dout`` (and ``dres``, what reaches
     h along the residual path): ``(dx, dweight, dbias)``, dbias None without
     ``bias``. h, mean and rstd are the forward's."""
@@ -993,5 +1028,5 @@ def layer_norm_backward(h, weight, mean, rstd, dout, dres=None, bias: bool = Tru
     _run(index, "moe_layer_norm_backward", lib().moe_layer_norm_backward, _pack(h, index),
          _pack(weight, index), _pack(mean, index), _pack(rstd, index), _pack(dout, index),
          _pack(dres, index), _pack(dx, index), _pack(dw, index), _pack(db, index), ws, wn,
-         _stream_of(index, stream))
+         _stream_of(index))
     return dx, dw, db
