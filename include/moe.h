@@ -461,7 +461,7 @@ size_t moe_backward_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff
  * moe_forward's (scores differ from its only in fp32 summation order), except
  * that a bf16 layer keeps the hidden activation to 16 significant bits (two
  * bf16 terms) and the experts' output rows in fp32, so that out carries only
- * its own rounding; a token's choices are added in ascending expert id.
+ * its own rounding; each token's choices are added in a fixed order.
  * stats->workspace holds moe_few_workspace_size() bytes (256-byte aligned;
  * a size for more tokens serves fewer). Bias data 16-byte aligned, as there.
  * out must not overlap x. */

@@ -308,7 +308,7 @@ namespace moe {
 // (fp32 layers; bf16 layers need it).
 constexpr int kFewMaxTokens = 64;
 struct FewLayout {
-    size_t idx, gate, plan, done, scores, H, part, total;
+    size_t idx, gate, slot, plan, done, scores, H, part, total;
 };
 FewLayout few_layout(bool bf16, int64_t N, int64_t d, int64_t E, int64_t d_ff, int k);
 hipError_t launch_few(bool bf16, bool aligned, const void *x, const float *wg, const float *noise,

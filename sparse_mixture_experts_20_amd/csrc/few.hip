@@ -12,8 +12,8 @@
 //         terms on the matrix cores, the fp32 layer on fp32 MFMAs).
 //   plan: one workgroup ranks the tokens (top-k and gates of a token per wave,
 //         its partial scores added in range order) and lists the hit experts
-//         and their kept rows in (choice, token) order. With many tokens and
-//         experts the ranking is a launch of its own, a wave per token.
+//         and their kept rows in (choice, token) order. More than 16 tokens are
+//         ranked by a launch of their own, a wave per token.
 //   up:   one workgroup per (hit expert, 16 hidden neurons), four waves over K
 //         that add through LDS. The grid is sized by min(E, N k), without a
 //         host sync; workgroups past the last hit expert end at once.
@@ -25,6 +25,12 @@
 //         output: the combine costs no launch and the result does not depend
 //         on which workgroup that is.
 //
+// Where a bf16 layer's experts have more than a few rows each, their tokens'
+// operand loads would outnumber the weights': up and down then run on the tiled
+// product (tile.hpp) instead, 64 rows (all an expert can have) by 128 columns a
+// workgroup, the down product writing each assignment's fp32 row for a combine
+// pass.
+//
 // A bf16 layer's hidden row is kept as two bf16 terms (hi + lo, 16 significant
 // bits): the product that reads it is bound by its weights, so the second MFMA
 // is free, and the layer's output then carries only its own final rounding.
@@ -35,6 +41,7 @@
 #include "common.hpp"
 #include "ranking.hpp"
 #include "skinny.hpp"
+#include "tile.hpp"
 
 namespace moe {
 namespace {
@@ -73,6 +80,13 @@ __device__ __forceinline__ f32x4 load4(const float *p, int n) {
     for (int i = 0; i < 4; ++i)
         v[i] = i < n ? p[i] : 0.f;
     return v;
+}
+
+// What rounding z to bf16 leaves, the second term of a hidden value (an
+// infinity or a NaN leaves nothing, not the NaN of its difference).
+__device__ __forceinline__ float second_term(float z) {
+    const float rest = z - bf16_bits_to_f32(f32_to_bf16_bits(z));
+    return fabsf(rest) < __builtin_inff() ? rest : 0.f;
 }
 
 // ---- scores ------------------------------------------------------------
@@ -120,17 +134,9 @@ __device__ __forceinline__ void score_tile(const float *w, const typename S::typ
                     acc[i] = SkinnyBf16::mma(term[m], b[u][i], acc[i]);
         }
     } else {
-        const float *wr[1] = {w};
-        f32x4 c[1][TT];
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-            c[0][i] = acc[i];
         const int ke = min(kb + 32 * U, (d + 31) / 32 * 32);
         if (kb < ke)
-            skinny_mma<S, 1, TT, 1, 1>(wr, xt, 0, kb, ke, d, d, c);
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-            acc[i] = c[0][i];
+            skinny_mma<S, TT, 1, 1>(w, xt, 0, kb, ke, d, d, acc);
     }
 }
 
@@ -231,7 +237,8 @@ struct FewRoute {
     int ns;
     int32_t *idx;             // [N, k]
     float *gate;
-    int32_t *slot, *used, *demand, *drops;   // exports, or NULL
+    int32_t *slot;            // [N, k]
+    int32_t *used, *demand, *drops;   // exports, or NULL
     float *gate_sum;
     FewPlan *plan;
     int *done;                // finished ranges per column block of the down product
@@ -385,8 +392,7 @@ __global__ __launch_bounds__(kPlanWaves * 64) void few_plan_kernel(
     if (o < A) {
         if (rank < cap)
             r.plan->row[hit_of[e]][rank] = i;
-        if (r.slot)
-            r.slot[i] = rank < cap ? rank : -1;
+        r.slot[i] = rank < cap ? rank : -1;
         by_expert[first[e] + rank] = g;
     }
     if (r.gate_sum) {   // (the same for the whole workgroup)
@@ -403,25 +409,22 @@ __global__ __launch_bounds__(kPlanWaves * 64) void few_plan_kernel(
 // ---- up ----------------------------------------------------------------
 
 // H (bf16: two terms, [2][N k][d_ff]; fp32: [N k][d_ff]) = act(W_up[e] x +
-// b_up[e]) for the rows of the hit experts. grid: (tiles of 16 FM neurons,
+// b_up[e]) for the rows of the hit experts. grid: (tiles of 16 neurons,
 // min(E, N k)); TT token tiles at most.
-template <typename S, int FM, int TT>
+template <typename S, int TT>
 __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const typename S::type *__restrict__ x, const typename S::type *__restrict__ w_up,
     const float *__restrict__ b_up, const FewPlan *__restrict__ plan, int N, int d, int d_ff,
     int k, int act, typename S::type *__restrict__ H) {
-    __shared__ f32x4 part[kWaves][FM * TT][64];
-    const int a = blockIdx.y, f0 = blockIdx.x * (16 * FM);
+    __shared__ f32x4 part[kWaves][TT][64];
+    const int a = blockIdx.y, f0 = blockIdx.x * 16;
     if (a >= plan->nhit)
         return;
     const int rows = plan->rows[a], e = plan->expert[a];
     const int *row = plan->row[a];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int ntile = (rows + 15) / 16;
-    const typename S::type *w[FM];
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
-        w[m] = w_up + ((int64_t)e * d_ff + min(f0 + 16 * m + (lane & 15), d_ff - 1)) * d;
+    const typename S::type *w = w_up + ((int64_t)e * d_ff + min(f0 + (lane & 15), d_ff - 1)) * d;
     // this wave's K range, in steps of 32
     const int steps = (d + 31) / 32;
     const int kb = (int)((int64_t)wv * steps / kWaves) * 32;
@@ -429,23 +432,19 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     auto run = [&](auto tiles) {
         constexpr int T = decltype(tiles)::value;
         const typename S::type *xt[T];
-        f32x4 c[FM][T];
+        f32x4 c[T];
 #pragma unroll
         for (int i = 0; i < T; ++i) {
             const int r = i * 16 + (lane & 15);
             xt[i] = x + (int64_t)(row[r < rows ? r : 0] / k) * d;
-#pragma unroll
-            for (int m = 0; m < FM; ++m)
-                c[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            c[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        // operand registers of a batch: U (FM + T) fragments, twice
-        constexpr int U = (FM + T <= 2 ? 8 : FM + T <= 4 ? 4 : 2) / (Kind<S>::bf16 ? 1 : 2);
-        skinny_mma<S, FM, T, 1, U>(w, xt, 0, kb, ke, d, d, c);
+        // operand registers of a batch: U (1 + T) fragments, twice
+        constexpr int U = (T == 1 ? 8 : T == 2 ? 4 : 2) / (Kind<S>::bf16 ? 1 : 2);
+        skinny_mma<S, T, 1, U>(w, xt, 0, kb, ke, d, d, c);
 #pragma unroll
-        for (int m = 0; m < FM; ++m)
-#pragma unroll
-            for (int i = 0; i < T; ++i)
-                part[wv][m * TT + i][lane] = c[m][i];
+        for (int i = 0; i < T; ++i)
+            part[wv][i][lane] = c[i];
     };
     if (TT == 1 || ntile <= 1)
         run(std::integral_constant<int, 1>{});
@@ -456,15 +455,15 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     __syncthreads();
     // thread -> (row, 4 neurons): tile i's lane l holds neurons 4 (l / 16) + q
     // of row l % 16
-    for (int q = threadIdx.x; q < ntile * FM * 64; q += kThreads) {
-        const int m = (q >> 6) % FM, i = (q >> 6) / FM, l = q & 63;
-        const int r = i * 16 + (l & 15), f = f0 + 16 * m + 4 * (l >> 4);
+    for (int q = threadIdx.x; q < ntile * 64; q += kThreads) {
+        const int i = q >> 6, l = q & 63;
+        const int r = i * 16 + (l & 15), f = f0 + 4 * (l >> 4);
         if (r >= rows || f >= d_ff)
             continue;
-        f32x4 z = part[0][m * TT + i][l];
+        f32x4 z = part[0][i][l];
 #pragma unroll
         for (int s = 1; s < kWaves; ++s)
-            z += part[s][m * TT + i][l];
+            z += part[s][i][l];
         if (b_up)
             z += load4<Kind<S>::bf16>(b_up + (int64_t)e * d_ff + f, d_ff - f);
 #pragma unroll
@@ -474,11 +473,8 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
         if constexpr (Kind<S>::bf16) {
             float lo[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                // the rest of an infinity or a NaN would be NaN: it has none
-                const float rest = z[c] - bf16_bits_to_f32(f32_to_bf16_bits(z[c]));
-                lo[c] = fabsf(rest) < __builtin_inff() ? rest : 0.f;
-            }
+            for (int c = 0; c < 4; ++c)
+                lo[c] = second_term(z[c]);
             *reinterpret_cast<u32x2 *>(dst) =
                 u32x2{pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3])};
             *reinterpret_cast<u32x2 *>(dst + (int64_t)N * k * d_ff) =
@@ -495,10 +491,10 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
 // ---- down --------------------------------------------------------------
 
 // out[t] = sum over kept choices of gate (W_down[e] h + b_down[e]). grid:
-// (blocks of 16 FM columns, ranges); part [ranges][N][16 FM blocks] when there is
+// (blocks of 16 columns, ranges); part [ranges][N][16 blocks] when there is
 // more than one range. The partial sums and the counter are written and read
 // past the XCD's own L2 (agent scope), which other XCDs do not see.
-template <typename S, int FM, int TT>
+template <typename S, int TT>
 __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
     const typename S::type *__restrict__ H, const typename S::type *__restrict__ w_down,
     const float *__restrict__ b_down, const float *__restrict__ gate,
@@ -506,7 +502,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
     float *__restrict__ part, typename S::type *__restrict__ out) {
     constexpr int NT = TT * 16;
     constexpr int NB = Kind<S>::terms;
-    constexpr int CB = 16 * FM;
+    constexpr int CB = 16;
     __shared__ float sum[kWaves][NT][CB + 1];
     __shared__ int last;
     const int c0 = blockIdx.x * CB;
@@ -524,47 +520,36 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
         const int a = u / chunks, uc = u - a * chunks;
         const int un = min(ue - u, chunks - uc);   // chunks of this expert
         const int e = plan->expert[a], rows = plan->rows[a];
-        const typename S::type *w[FM];
-#pragma unroll
-        for (int m = 0; m < FM; ++m)
-            w[m] = w_down + ((int64_t)e * d + min(c0 + 16 * m + (lane & 15), d - 1)) * d_ff;
+        const typename S::type *w =
+            w_down + ((int64_t)e * d + min(c0 + (lane & 15), d - 1)) * d_ff;
         const int kb = uc * kChunk, ke = min((uc + un) * kChunk, (d_ff + 31) / 32 * 32);
         u += un;
-        f32x4 bias[FM];
-#pragma unroll
-        for (int m = 0; m < FM; ++m) {
-            const int cc = c0 + 16 * m + 4 * (lane >> 4);
-            bias[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (b_down && uc == 0)
-                bias[m] = load4<Kind<S>::bf16>(b_down + (int64_t)e * d + cc, d - cc);
-        }
+        const int cc = c0 + 4 * (lane >> 4);
+        f32x4 bias = {0.f, 0.f, 0.f, 0.f};
+        if (b_down && uc == 0)
+            bias = load4<Kind<S>::bf16>(b_down + (int64_t)e * d + cc, d - cc);
         auto run = [&](auto tiles) {
             constexpr int T = decltype(tiles)::value;
             const typename S::type *ht[T];
-            f32x4 acc[FM][T];
+            f32x4 acc[T];
             int as[T];
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 const int r = i * 16 + (lane & 15);
                 as[i] = plan->row[a][r < rows ? r : 0];
                 ht[i] = H + (int64_t)as[i] * d_ff;
-#pragma unroll
-                for (int m = 0; m < FM; ++m)
-                    acc[m][i] = bias[m];
+                acc[i] = bias;
             }
-            constexpr int U = FM + NB * T <= 4 ? 4 : FM + NB * T <= 6 ? 2 : 1;
-            skinny_mma<S, FM, T, NB, U>(w, ht, lo, kb, ke, d_ff, d_ff, acc);
+            constexpr int U = NB * T <= 2 ? 4 : NB * T <= 4 ? 2 : 1;
+            skinny_mma<S, T, NB, U>(w, ht, lo, kb, ke, d_ff, d_ff, acc);
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 if (i * 16 + (lane & 15) < rows) {
                     const float g = gate[as[i]];
+                    float *s = &sum[wv][as[i] / k][4 * (lane >> 4)];
 #pragma unroll
-                    for (int m = 0; m < FM; ++m) {
-                        float *s = &sum[wv][as[i] / k][16 * m + 4 * (lane >> 4)];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            s[q] = fmaf(g, acc[m][i][q], s[q]);
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        s[q] = fmaf(g, acc[i][q], s[q]);
                 }
             }
         };
@@ -575,21 +560,15 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
             const int r = lane & 7;
             const int as = plan->row[a][r < rows ? r : 0];
             const typename S::type *ht[1] = {H + (int64_t)as * d_ff + (lane & 8 ? lo : 0)};
-            f32x4 acc[FM][1];
-#pragma unroll
-            for (int m = 0; m < FM; ++m)
-                acc[m][0] = lane & 8 ? f32x4{0.f, 0.f, 0.f, 0.f} : bias[m];
-            skinny_mma<S, FM, 1, 1, FM == 1 ? 8 : 4>(w, ht, 0, kb, ke, d_ff, d_ff, acc);
+            f32x4 acc[1] = {lane & 8 ? f32x4{0.f, 0.f, 0.f, 0.f} : bias};
+            skinny_mma<S, 1, 1, 8>(w, ht, 0, kb, ke, d_ff, d_ff, acc);
             const float g = gate[as];
+            float *s = &sum[wv][as / k][4 * (lane >> 4)];
 #pragma unroll
-            for (int m = 0; m < FM; ++m) {
-                float *s = &sum[wv][as / k][16 * m + 4 * (lane >> 4)];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float y = acc[m][0][q] + __shfl_xor(acc[m][0][q], 8);
-                    if ((lane & 15) < rows)
-                        s[q] = fmaf(g, y, s[q]);
-                }
+            for (int q = 0; q < 4; ++q) {
+                const float y = acc[0][q] + __shfl_xor(acc[0][q], 8);
+                if ((lane & 15) < rows)
+                    s[q] = fmaf(g, y, s[q]);
             }
         } else if (TT == 1 || rows <= 16) {
             run(std::integral_constant<int, 1>{});
@@ -661,23 +640,157 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(
     }
 }
 
-// Weight rows per lane: two where an expert has more than about 8 rows, whose
-// two operand terms no longer share a tile (Mixtral-shaped layer, 64 tokens:
-// 500 against 620 us; at 2 rows per expert one is faster: fine-grained layer,
-// 61 tokens, 2192 against 2322 us).
-// (fp32 rows are one term, and their layers small: always one.)
-int rows_per_lane(bool bf16, int64_t N, int64_t E, int k) { return bf16 && N * k > 8 * E ? 2 : 1; }
+// ---- tiled products ------------------------------------------------------
+
+// One expert's product on the tiled form, 64 rows by kTileCols columns. UP:
+// H = act(W x + bias) as above, A the rows of x. Otherwise Y[range][assignment]
+// = W h + bias (bias in range 0), fp32: A holds both terms of the rows, 16 hi
+// and 16 lo rows per wave, whose products the same lane adds. K: row length of
+// W, cols: its rows. grid: (column tiles, min(E, N k), K-ranges). Stages are few
+// enough for two workgroups on a CU: one's products cover the other's waits
+// (Mixtral-shaped layer, 64 tokens: 398 us with one of 5 and 4 stages, 375 with
+// two; the weights alone are 313 us at 6 TB/s).
+constexpr int kTileCols = 128;
+template <bool UP>
+__global__ __launch_bounds__(512) void few_tile_kernel(
+    const unsigned short *__restrict__ A, const unsigned short *__restrict__ W,
+    const float *__restrict__ bias, const FewPlan *__restrict__ plan, int N, int K, int cols,
+    int k, int act, unsigned short *__restrict__ H, float *__restrict__ Y) {
+    typedef TileProduct<UP ? 64 : 128, kTileCols, 4, 2, UP ? 3 : 2, false, false> Tile;
+    static_assert(kFewTokens <= 64 && Tile::THREADS == 512, "an expert's rows fit the tile");
+    __shared__ __attribute__((aligned(1024))) char smem[Tile::LDS];
+    __shared__ int row[64];
+    const int a = blockIdx.y, n0 = blockIdx.x * kTileCols;
+    if (a >= plan->nhit)
+        return;
+    const int rows = plan->rows[a], e = plan->expert[a];
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (threadIdx.x < 64)
+        row[threadIdx.x] = plan->row[a][threadIdx.x < rows ? threadIdx.x : 0];
+    __syncthreads();
+    const int64_t lo = (int64_t)N * k * K;   // of the second term (down)
+    const int KT = (K + kStep - 1) / kStep;
+    const int kb = (int)((int64_t)blockIdx.z * KT / gridDim.z);
+    const int ke = (int)((int64_t)(blockIdx.z + 1) * KT / gridDim.z);
+    const unsigned short *We = W + (int64_t)e * cols * K;
+    f32x4 acc[Tile::FM][Tile::FN];
+#pragma unroll
+    for (int i = 0; i < Tile::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Tile::run(
+        smem,
+        [&](int r) {
+            if constexpr (UP)
+                return A + (int64_t)(row[r] / k) * K;
+            else
+                return A + (int64_t)row[r / 32 * 16 + r % 16] * K + (r & 16 ? lo : 0);
+        },
+        0, [&](int c) { return We + (int64_t)min(n0 + c, cols - 1) * K; }, 0, K, kb, ke, acc);
+    // lane: one row, 16 adjacent columns
+    const int r = wv / 2 * 16 + (lane & 15);
+    const int n = n0 + wv % 2 * 64 + 16 * (lane >> 4);
+    if (r >= rows || n >= cols)
+        return;
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f32x4 t = acc[0][j];
+        if constexpr (!UP)
+            t += acc[Tile::FM - 1][j];
+        if (bias && blockIdx.z == 0 && n + 4 * j < cols)
+            t += *reinterpret_cast<const f32x4 *>(bias + (int64_t)e * cols + n + 4 * j);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            v[4 * j + q] = t[q];
+    }
+    const int64_t o = (int64_t)row[r] * cols + n;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (n + 8 * h >= cols)   // (cols % 8 == 0)
+            continue;
+        float *p = &v[8 * h];
+        if constexpr (UP) {
+            u32x4 hi, low;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float z[2], rest[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    z[c] = activate(p[2 * q + c], act);
+                    rest[c] = second_term(z[c]);
+                }
+                hi[q] = pack_bf16x2(z[0], z[1]);
+                low[q] = pack_bf16x2(rest[0], rest[1]);
+            }
+            *reinterpret_cast<u32x4 *>(H + o + 8 * h) = hi;
+            *reinterpret_cast<u32x4 *>(H + (int64_t)N * k * cols + o + 8 * h) = low;
+        } else {
+            float *dst = Y + (int64_t)blockIdx.z * N * k * cols + o + 8 * h;
+            *reinterpret_cast<f32x4 *>(dst) = f32x4{p[0], p[1], p[2], p[3]};
+            *reinterpret_cast<f32x4 *>(dst + 4) = f32x4{p[4], p[5], p[6], p[7]};
+        }
+    }
+}
+
+// out[t] = sum over kept choices, in choice order, of gate * the sum of its
+// row's ranges. 8 columns per thread.
+__global__ __launch_bounds__(256) void few_combine_kernel(
+    const float *__restrict__ Y, int ranges, const float *__restrict__ gate,
+    const int32_t *__restrict__ slot, int N, int d, int k, unsigned short *__restrict__ out) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per = d / 8;
+    if (i >= (int64_t)N * per)
+        return;
+    const int t = (int)(i / per), c = (int)(i - (int64_t)t * per) * 8;
+    const int64_t step = (int64_t)N * k * d;
+    f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+    for (int j = 0; j < k; ++j) {
+        const int as = t * k + j;
+        if (slot[as] < 0)
+            continue;
+        const float *p = Y + (int64_t)as * d + c;
+        f32x4 y0 = *reinterpret_cast<const f32x4 *>(p), y1 = *reinterpret_cast<const f32x4 *>(p + 4);
+        for (int r = 1; r < ranges; ++r) {
+            y0 += *reinterpret_cast<const f32x4 *>(p + r * step);
+            y1 += *reinterpret_cast<const f32x4 *>(p + r * step + 4);
+        }
+        const float g = gate[as];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            s0[q] = fmaf(g, y0[q], s0[q]);
+            s1[q] = fmaf(g, y1[q], s1[q]);
+        }
+    }
+    *reinterpret_cast<u32x4 *>(out + (int64_t)t * d + c) =
+        u32x4{pack_bf16x2(s0[0], s0[1]), pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]),
+              pack_bf16x2(s1[2], s1[3])};
+}
+
+// Whether the experts' products run on the tiled form: bf16 layers of about 8
+// rows per expert on average or more (Mixtral-shaped layer: 379 against 421 us at
+// 32 tokens and 375 against 579 at 64; below, 385 against 382 at 24).
+bool tiled(bool bf16, int64_t N, int64_t E, int k) { return bf16 && N * k > 7 * E; }
+
+// Ranges of the tiled down product's reduction: about two workgroups per CU,
+// each of at least 8 K-steps.
+int tiled_ranges(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k) {
+    const int64_t blocks = (d + kTileCols - 1) / kTileCols * std::min<int64_t>(E, N * k);
+    const int64_t r = std::min<int64_t>(512 / blocks, (d_ff + kStep - 1) / kStep / 8);
+    return (int)std::min<int64_t>(std::max<int64_t>(r, 1), 8);
+}
 
 // Column blocks and ranges of the down product: about 4096 workgroups, each
 // wave with at least two chunks when every possible expert is hit.
 struct DownGrid {
-    int fm, blocks, ranges;
+    int blocks, ranges;
 };
-DownGrid down_grid(bool bf16, int64_t N, int64_t d, int64_t E, int64_t d_ff, int k) {
+DownGrid down_grid(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k) {
     const int64_t hits = std::min<int64_t>(E, N * k);
     DownGrid g;
-    g.fm = rows_per_lane(bf16, N, E, k);
-    g.blocks = (int)((d + 16 * g.fm - 1) / (16 * g.fm));
+    g.blocks = (int)((d + 15) / 16);
     const int64_t units = hits * ((d_ff + kChunk - 1) / kChunk);
     const int64_t r = std::min<int64_t>((4096 + g.blocks - 1) / g.blocks, units / (2 * kWaves));
     g.ranges = (int)std::min<int64_t>(std::max<int64_t>(r, 1), 64);
@@ -695,12 +808,16 @@ FewLayout few_layout(bool bf16, int64_t N, int64_t d, int64_t E, int64_t d_ff, i
     const size_t nk = (size_t)(N * k);
     L.idx = o;    o += up256(nk * 4);
     L.gate = o;   o += up256(nk * 4);
+    L.slot = o;   o += up256(nk * 4);
     L.plan = o;   o += up256(sizeof(FewPlan));
     L.done = o;   o += up256((size_t)((d + 15) / 16) * 4);
     L.scores = o; o += up256((size_t)score_ranges(d) * N * 64 * score_lanes((int)E) * 4);
     L.H = o;      o += up256(nk * d_ff * 4);   // fp32, or two bf16 terms
-    const DownGrid g = down_grid(bf16, N, d, E, d_ff, k);
-    L.part = o;   o += up256((size_t)g.ranges * N * g.blocks * (16 * g.fm) * 4);
+    const DownGrid g = down_grid(N, d, E, d_ff, k);
+    const size_t joined = (size_t)g.ranges * N * g.blocks * 16 * 4;
+    const size_t rows = tiled(bf16, N, E, k)
+                            ? (size_t)tiled_ranges(N, d, E, d_ff, k) * nk * d * 4 : 0;
+    L.part = o;   o += up256(std::max(joined, rows));
     L.total = o;
     return L;
 }
@@ -716,7 +833,7 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
     float *P = reinterpret_cast<float *>(ws + L.scores);
     T *H = reinterpret_cast<T *>(ws + L.H);
     const int ns = score_ranges(d);
-    const DownGrid g = down_grid(Kind<S>::bf16, N, d, E, d_ff, k);
+    const DownGrid g = down_grid(N, d, E, d_ff, k);
     const unsigned hits = (unsigned)std::min(E, N * k);
     r.plan = reinterpret_cast<FewPlan *>(ws + L.plan);
     r.done = reinterpret_cast<int *>(ws + L.done);
@@ -733,11 +850,11 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
         if (err != hipSuccess)
             return err;
     }
-    // The plan's one workgroup ranks a token per wave in about 2 us, four rounds
-    // of them at 64 tokens; with many experts the partial scores of a round are
-    // 64 times Q ns words a token, more than one CU reads quickly.
+    // The plan's one workgroup ranks a token per wave, so more than its 16 waves'
+    // worth are ranked by a launch of their own, spread over the CUs (64 tokens,
+    // 64 experts, k = 8: 21 us inside, 4 + 6 us apart).
     const int Q = score_lanes(E);
-    const bool inside = N <= kPlanWaves || Q == 1;
+    const bool inside = N <= kPlanWaves;
     r.P = inside ? P : nullptr;
     auto rank_and_plan = [&](auto lanes) {
         constexpr int QQ = decltype(lanes)::value;
@@ -762,28 +879,43 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
                    : rank_and_plan(std::integral_constant<int, 4>{});
     if (err != hipSuccess)
         return err;
-    auto up = [&](auto fm) {
-        constexpr int FM = decltype(fm)::value;
-        hipLaunchKernelGGL((few_up_kernel<S, FM, TT>),
-                           dim3((unsigned)((d_ff + 16 * FM - 1) / (16 * FM)), hits),
-                           dim3(kThreads), 0, s, x, static_cast<const T *>(wu), b_up,
-                           (const FewPlan *)r.plan, N, d, d_ff, k, act, H);
-        return hipGetLastError();
-    };
-    auto down = [&](auto fm) {
-        constexpr int FM = decltype(fm)::value;
-        hipLaunchKernelGGL((few_down_kernel<S, FM, TT>), dim3((unsigned)g.blocks, (unsigned)g.ranges),
-                           dim3(kThreads), 0, s, (const T *)H, static_cast<const T *>(wd), b_down,
-                           (const float *)r.gate, (const FewPlan *)r.plan, N, d, d_ff, k, r.done,
-                           reinterpret_cast<float *>(ws + L.part), static_cast<T *>(out));
-        return hipGetLastError();
-    };
-    const std::integral_constant<int, 1> one;
-    const std::integral_constant<int, 2> two;
-    err = rows_per_lane(Kind<S>::bf16, N, E, k) == 2 ? up(two) : up(one);
+    if constexpr (Kind<S>::bf16) {
+        if (tiled(true, N, E, k)) {
+            const int tr = tiled_ranges(N, d, E, d_ff, k);
+            float *Y = reinterpret_cast<float *>(ws + L.part);
+            hipLaunchKernelGGL(few_tile_kernel<true>,
+                               dim3((unsigned)((d_ff + kTileCols - 1) / kTileCols), hits),
+                               dim3(512), 0, s, x, static_cast<const T *>(wu), b_up,
+                               (const FewPlan *)r.plan, N, d, d_ff, k, act, H, (float *)nullptr);
+            err = hipGetLastError();
+            if (err != hipSuccess)
+                return err;
+            hipLaunchKernelGGL(
+                few_tile_kernel<false>,
+                dim3((unsigned)((d + kTileCols - 1) / kTileCols), hits, (unsigned)tr), dim3(512), 0,
+                s, (const T *)H, static_cast<const T *>(wd), b_down, (const FewPlan *)r.plan, N,
+                d_ff, d, k, act, (T *)nullptr, Y);
+            err = hipGetLastError();
+            if (err != hipSuccess)
+                return err;
+            hipLaunchKernelGGL(few_combine_kernel,
+                               dim3((unsigned)(((int64_t)N * (d / 8) + 255) / 256)), dim3(256), 0,
+                               s, (const float *)Y, tr, (const float *)r.gate,
+                               (const int32_t *)r.slot, N, d, k, static_cast<T *>(out));
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((few_up_kernel<S, TT>), dim3((unsigned)((d_ff + 15) / 16), hits),
+                       dim3(kThreads), 0, s, x, static_cast<const T *>(wu), b_up,
+                       (const FewPlan *)r.plan, N, d, d_ff, k, act, H);
+    err = hipGetLastError();
     if (err != hipSuccess)
         return err;
-    return g.fm == 2 ? down(two) : down(one);
+    hipLaunchKernelGGL((few_down_kernel<S, TT>), dim3((unsigned)g.blocks, (unsigned)g.ranges),
+                       dim3(kThreads), 0, s, (const T *)H, static_cast<const T *>(wd), b_down,
+                       (const float *)r.gate, (const FewPlan *)r.plan, N, d, d_ff, k, r.done,
+                       reinterpret_cast<float *>(ws + L.part), static_cast<T *>(out));
+    return hipGetLastError();
 }
 
 hipError_t launch_few(bool bf16, bool aligned, const void *x, const float *wg, const float *noise,
@@ -797,7 +929,7 @@ hipError_t launch_few(bool bf16, bool aligned, const void *x, const float *wg, c
     FewRoute r{};
     r.idx = idx ? idx : reinterpret_cast<int32_t *>(w + L.idx);
     r.gate = gate ? gate : reinterpret_cast<float *>(w + L.gate);
-    r.slot = slot;
+    r.slot = slot ? slot : reinterpret_cast<int32_t *>(w + L.slot);
     r.used = used;
     r.demand = demand;
     r.drops = drops;

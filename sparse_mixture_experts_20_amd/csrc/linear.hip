@@ -30,38 +30,12 @@
 #include "activation.hpp"
 #include "common.hpp"
 #include "skinny.hpp"
+#include "tile.hpp"
 
 namespace moe {
 namespace {
 
 constexpr int kXcdCount = 8;
-constexpr int kStep = 64;   // K-step of the tiled product
-
-__device__ __forceinline__ void barrier_lds() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_loads() {   // until at most N are in flight
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// Direct copy of 16 bytes per lane to LDS: lane l's bytes land at base + 16 l.
-// In asm so that the compiler does not wait for it before every LDS read; the
-// waits are explicit.
-__device__ __forceinline__ void copy_to_lds(unsigned base, const void *g) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 ::"s"(base), "v"(g)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ unsigned lds_address(const void *p) {
-    return (unsigned)(uintptr_t)((__attribute__((address_space(3))) const void *)p);
-}
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-// Transposing LDS read: within 16 lanes, lane l gets element l % 4 of the 8
-// bytes that lane 4 q + l / 4 addresses, as its element q.
-__device__ __forceinline__ s16x4 read_transposed(const void *p) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
-}
 
 struct Epilogue {
     unsigned short *out16;          // bf16 output, or NULL
@@ -120,14 +94,9 @@ template <int BM, int BN, int WM, int WN, int S, bool AT, bool BT>
 __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     const unsigned short *__restrict__ A, const unsigned short *__restrict__ B, int rows,
     int cols, int K, Epilogue ep, float *__restrict__ part) {
-    constexpr int NW = WM * WN;
-    constexpr int FM = BM / WM / 16, FN = 4;
-    static_assert(BN / WN == 64, "a wave holds 64 columns");
-    constexpr int ABYTES = BM * kStep * 2, BBYTES = BN * kStep * 2, STAGE = ABYTES + BBYTES;
-    constexpr int IA = ABYTES / (NW * 1024), IB = BBYTES / (NW * 1024);
-    static_assert(S >= 2 && (S - 2) * (IA + IB) < 64, "a wait counts to 63");
-    static_assert(IA * NW * 1024 == ABYTES && IB * NW * 1024 == BBYTES, "whole wave copies");
-    __shared__ __attribute__((aligned(1024))) char smem[S * STAGE];
+    typedef TileProduct<BM, BN, WM, WN, S, AT, BT> Tile;
+    constexpr int FM = Tile::FM, FN = Tile::FN;
+    __shared__ __attribute__((aligned(1024))) char smem[Tile::LDS];
 
     // Tile of this workgroup: block b runs on XCD b mod 8 and takes index
     // (b mod 8) T8/8 + b/8, one contiguous range per XCD; within it, column
@@ -149,158 +118,23 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wv / WN, wn = wv % WN;
 
-    // Copy sources: per wave copy one 16-byte chunk per lane. Row-major tile:
-    // row r of 8 chunks, chunk c kept at position c ^ f(r); tile stored the
-    // other way: row k of BM/8 (BN/8) chunks, chunk c at c ^ g(k). Rows and
-    // columns past the edge read a valid place (their products are not stored).
-    auto fa = [](int r) { return (r >> 1) & 7; };                       // 16 adjacent rows
-    auto fb = [](int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); };    // rows 16 i + 4 j + 0..3
-    auto ga = [](int k) {                                          // rows 8 i + 4 j + 0..3
-        return BM == 64 ? (k & 2) | ((k >> 1) & 4) : 2 * ((k & 3) | ((k >> 1) & 4));
-    };
-    auto gb = [](int k) { return (k & 1) | ((k & 2) << 2); };
-    const unsigned short *pa[IA], *pb[IB];
-    int ka[IA], kbb[IB];   // K offset (elements) of the lane's chunk within the step
-#pragma unroll
-    for (int i = 0; i < IA; ++i) {
-        const int q = (wv * IA + i) * 64 + lane;
-        if constexpr (AT) {
-            const int r = q / (BM / 8), c = (q % (BM / 8)) ^ ga(r);
-            ka[i] = r;
-            pa[i] = A + min(m0 + 8 * c, rows - 8);
-        } else {
-            const int r = q / 8, c = (q % 8) ^ fa(r);
-            ka[i] = 8 * c;
-            pa[i] = A + (int64_t)min(m0 + r, rows - 1) * K;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < IB; ++i) {
-        const int q = (wv * IB + i) * 64 + lane;
-        if constexpr (BT) {
-            const int r = q / (BN / 8), c = (q % (BN / 8)) ^ gb(r);
-            kbb[i] = r;
-            pb[i] = B + min(n0 + 8 * c, cols - 8);
-        } else {
-            const int r = q / 8, c = (q % 8) ^ fb(r);
-            kbb[i] = 8 * c;
-            pb[i] = B + (int64_t)min(n0 + r, cols - 1) * K;
-        }
-    }
-    const unsigned base = lds_address(smem);
-    auto issue = [&](int kt) {
-        const unsigned st = base + (unsigned)(kt % S) * STAGE;
-#pragma unroll
-        for (int i = 0; i < IA; ++i) {
-            const unsigned dst = st + (unsigned)(wv * IA + i) * 1024;
-            if constexpr (AT)
-                copy_to_lds(dst, pa[i] + (int64_t)min(kt * kStep + ka[i], K - 1) * rows);
-            else
-                copy_to_lds(dst, pa[i] + min(kt * kStep + ka[i], K - 8));
-        }
-#pragma unroll
-        for (int i = 0; i < IB; ++i) {
-            const unsigned dst = st + ABYTES + (unsigned)(wv * IB + i) * 1024;
-            if constexpr (BT)
-                copy_to_lds(dst, pb[i] + (int64_t)min(kt * kStep + kbb[i], K - 1) * cols);
-            else
-                copy_to_lds(dst, pb[i] + min(kt * kStep + kbb[i], K - 8));
-        }
-    };
-    // chunks of the last step that lie past K, in both operands
-    auto zero_tail = [&](int kt) {
-        char *st = smem + (kt % S) * STAGE;
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-        for (int q = threadIdx.x; q < ABYTES / 16; q += NW * 64) {
-            const int k = AT ? q / (BM / 8) : 8 * ((q % 8) ^ fa(q / 8));
-            if (kt * kStep + k >= K)
-                *reinterpret_cast<u32x4 *>(st + q * 16) = zero;
-        }
-        for (int q = threadIdx.x; q < BBYTES / 16; q += NW * 64) {
-            const int k = BT ? q / (BN / 8) : 8 * ((q % 8) ^ fb(q / 8));
-            if (kt * kStep + k >= K)
-                *reinterpret_cast<u32x4 *>(st + ABYTES + q * 16) = zero;
-        }
-    };
-    const int l16 = lane & 15, g = lane >> 4;
-    auto frag_a = [&](const char *st, int ks, int i) {
-        if constexpr (AT) {
-            const int col = wm * FM * 16 + i * 16 + 4 * (l16 & 3);
-            s16x4 q[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = ks * 32 + 8 * g + 4 * h + (l16 >> 2);
-                q[h] = read_transposed(st + k * BM * 2 + (((col >> 3) ^ ga(k)) << 4) +
-                                       (col & 7) * 2);
-            }
-            return __builtin_bit_cast(bf16x8,
-                                      __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            const int r = wm * FM * 16 + i * 16 + l16;
-            return *reinterpret_cast<const bf16x8 *>(st + r * 128 + (((ks * 4 + g) ^ fa(r)) << 4));
-        }
-    };
-    // fragment j of the wave's 64 columns: its index i is column 16 (i / 4) + 4 j + i % 4
-    auto frag_b = [&](const char *st, int ks, int j) {
-        st += ABYTES;
-        if constexpr (BT) {
-            const int col = wn * 64 + 16 * (l16 & 3) + 4 * j;
-            s16x4 q[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = ks * 32 + 8 * g + 4 * h + (l16 >> 2);
-                q[h] = read_transposed(st + k * BN * 2 + (((col >> 3) ^ gb(k)) << 4) +
-                                       (col & 7) * 2);
-            }
-            return __builtin_bit_cast(bf16x8,
-                                      __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            const int r = wn * 64 + 16 * (l16 >> 2) + 4 * j + (l16 & 3);
-            return *reinterpret_cast<const bf16x8 *>(st + r * 128 + (((ks * 4 + g) ^ fb(r)) << 4));
-        }
-    };
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s)
-        if (kb + s < ke)
-            issue(kb + s);
-    for (int kt = kb; kt < ke; ++kt) {
-        // step kt has landed; the later ones issued so far may stay in flight
-        // (the last S - 2 steps wait for all that is in flight)
-        if (kt + S - 2 < ke)
-            wait_loads<(S - 2) * (IA + IB)>();
-        else
-            wait_loads<0>();
-        barrier_lds();
-        if (kt + S - 1 < ke)
-            issue(kt + S - 1);
-        if (kt == KT - 1 && K % kStep != 0) {
-            zero_tail(kt);
-            barrier_lds();
-        }
-        const char *st = smem + (kt % S) * STAGE;
-#pragma unroll
-        for (int ks = 0; ks < kStep / 32; ++ks) {
-            bf16x8 fA[FM], fB[FN];
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                fB[j] = frag_b(st, ks, j);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                fA[i] = frag_a(st, ks, i);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fB[j], fA[i], acc[i][j], 0,
-                                                                         0, 0);
-        }
-    }
+    Tile::run(
+        smem,
+        [&](int r) {
+            return AT ? A + min(m0 + 8 * r, rows - 8) : A + (int64_t)min(m0 + r, rows - 1) * K;
+        },
+        rows,
+        [&](int r) {
+            return BT ? B + min(n0 + 8 * r, cols - 8) : B + (int64_t)min(n0 + r, cols - 1) * K;
+        },
+        cols, K, kb, ke, acc);
+    const int l16 = lane & 15, g = lane >> 4;
     // lane: row l16 of each 16-row strip, 16 adjacent columns
     const int n = n0 + wn * 64 + 16 * g, valid = min(16, cols - n);
     if (valid <= 0)
@@ -399,21 +233,21 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(
     // columns a wave's lanes walk together, and where this lane's start
     const int steps = HALF ? (K + 63) / 64 : (K + 31) / 32;
     const int shift = HALF && l16 >= 8 ? steps * 32 : 0;
-    const unsigned short *w[1] = {W + (int64_t)min(c0 + l16 % CB, M - 1) * K + shift};
+    const unsigned short *w = W + (int64_t)min(c0 + l16 % CB, M - 1) * K + shift;
     const unsigned short *xt[TT];
-    f32x4 acc[1][TT];
+    f32x4 acc[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         xt[i] = x + (int64_t)min(i * 16 + l16 % CB, N - 1) * K + shift;
-        acc[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     const int kb = (int)((int64_t)wv * steps / kFewWaves) * 32;
     const int ke = (int)((int64_t)(wv + 1) * steps / kFewWaves) * 32;
-    skinny_mma<SkinnyBf16, 1, TT, 1, TT == 1 ? 4 : TT == 2 ? 3 : 2>(
+    skinny_mma<SkinnyBf16, TT, 1, TT == 1 ? 4 : TT == 2 ? 3 : 2>(
         w, xt, 0, kb, ke, K - shift, HALF ? K - steps * 32 : K, acc);
 #pragma unroll
     for (int i = 0; i < TT; ++i)
-        part[wv][i][lane] = acc[0][i];
+        part[wv][i][lane] = acc[i];
     __syncthreads();
     // thread -> (row, 8 columns): lanes l and l + 16 of a tile hold columns
     // 4 (l / 16) + 0..3 and the next four of row l % 16

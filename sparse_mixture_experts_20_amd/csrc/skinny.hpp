@@ -65,21 +65,20 @@ struct SkinnyF32 {
 };
 
 // Product of K columns [kbeg, kend) (multiples of 32, kend possibly past K)
-// of FM weight rows and TT token rows per lane into acc (row 4 (l / 16) + q of
-// the weight rows, column l % 16 of the tokens). w[m] and xt[i] point at this
+// of a weight row and TT token rows per lane into acc (row 4 (l / 16) + q of
+// the weight rows, column l % 16 of the tokens). w and xt[i] point at this
 // lane's rows (column 0); NB operand terms per token row, `lo` elements apart,
 // are added (2: a row kept as the sum of two bf16 terms). K: columns the rows
-// have from w[m] and xt[i] on, which may differ between lanes (those past it
-// are zeros); all: the smallest K of the wave. Two weight rows per lane (FM =
-// 2) halve the token rows' loads.
-template <typename S, int FM, int TT, int NB, int U>
-__device__ __forceinline__ void skinny_mma(const typename S::type *const (&w)[FM],
+// have from w and xt[i] on, which may differ between lanes (those past it are
+// zeros); all: the smallest K of the wave.
+template <typename S, int TT, int NB, int U>
+__device__ __forceinline__ void skinny_mma(const typename S::type *w,
                                            const typename S::type *const (&xt)[TT], int64_t lo,
                                            int kbeg, int kend, int K, int all,
-                                           f32x4 (&acc)[FM][TT]) {
+                                           f32x4 (&acc)[TT]) {
     typedef typename S::frag frag;
     struct Step {
-        frag a[FM], b[TT][NB];
+        frag a, b[TT][NB];
     };
     const int ko = 8 * (int)(__lane_id() >> 4);
     const int full = min(kend, all / 32 * 32);   // steps that need no mask
@@ -88,9 +87,7 @@ __device__ __forceinline__ void skinny_mma(const typename S::type *const (&w)[FM
     auto load = [&](int k, Step (&s)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int m = 0; m < FM; ++m)
-                s[u].a[m] = S::load(w[m] + ko + k + 32 * u);
+            s[u].a = S::load(w + ko + k + 32 * u);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -101,12 +98,10 @@ __device__ __forceinline__ void skinny_mma(const typename S::type *const (&w)[FM
     };
     auto mma = [&](const Step &s) {
 #pragma unroll
-        for (int m = 0; m < FM; ++m)
+        for (int i = 0; i < TT; ++i)
 #pragma unroll
-            for (int i = 0; i < TT; ++i)
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    acc[m][i] = S::mma(s.a[m], s.b[i][n], acc[m][i]);
+            for (int n = 0; n < NB; ++n)
+                acc[i] = S::mma(s.a, s.b[i][n], acc[i]);
     };
     Step next[U];
     int k = kbeg;
@@ -130,9 +125,7 @@ __device__ __forceinline__ void skinny_mma(const typename S::type *const (&w)[FM
         // single steps, masked where they reach past K
         const int left = K - k - ko;
         Step s;
-#pragma unroll
-        for (int m = 0; m < FM; ++m)
-            s.a[m] = S::load_tail(w[m] + ko + k, left);
+        s.a = S::load_tail(w + ko + k, left);
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll

@@ -101,6 +101,28 @@ def test_against_float64(torch_mod, case):
     assert torch.equal(got, out) and torch.equal(gst.slot, st.slot)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [7, 9, 16, 20, 40, 64])
+def test_one_popular_expert(torch_mod, N, dtype):
+    """Every token takes expert 3 of 40 (none dropped) and one more: one expert
+    with N rows among many with few, on the streaming products."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain as P
+    d, d_ff, E = (264, 520, 40) if dtype == "bf16" else (75, 131, 40)
+    wl, dev = _layer(torch, N, d, E, 2, d_ff, dtype, 40.0, "gelu", 0.1, 0.5)
+    noise = dev["noise"].clone()
+    noise[:, 3] += 50.0
+    out, st = B.forward_few(dev["x"], dev["W_g"], noise, dev["W_up"], dev["W_down"], 2, 40.0,
+                            act="gelu", b_up=dev["b_up"], b_down=dev["b_down"])
+    torch.cuda.synchronize()
+    assert bool((st.idx[:, 0] == 3).all()) and int(st.used[3]) == N
+    assert bool((st.slot >= 0).all())
+    y, e = P.few(dev["x"], dev["W_up"], dev["W_down"], dev["b_up"], dev["b_down"], "gelu",
+                 st.idx.long(), st.gate, st.slot, 2.0 ** -16 if dtype == "bf16" else 2.0 ** -24)
+    P.close(out, y, P.stored(y, e, dev["x"].dtype), "out")
+
+
 def test_near_the_whole_layer(torch_mod):
     """The same layer through moe_forward: both round out once (2^-8), and
     moe_forward's hidden rows once more (2^-8 each, independent): relative
