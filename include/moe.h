@@ -72,7 +72,7 @@ enum {
 #define MOE_FEW_MAX_TOKENS 64      /* tokens of moe_forward_few */
 #define MOE_FEW_MAX_WIDTH (1 << 20)  /* d and d_ff of moe_forward_few */
 #define MOE_NORM_MAX_WIDTH 16384   /* row width of moe_layer_norm */
-#define MOE_LINEAR_MAX_EXTENT (1 << 30)  /* rows and widths of moe_linear */
+#define MOE_LINEAR_MAX_EXTENT (1 << 28)  /* rows and widths of moe_linear */
 
 /* A tensor view: data (device), element type, rank and extents (row-major,
  * contiguous). A 3-D activation [B, T, d] is read as [B*T, d]. */

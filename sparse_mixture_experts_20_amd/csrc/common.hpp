@@ -328,6 +328,10 @@ hipError_t launch_layer_norm_backward(bool bf16, bool vec, const void *x, const 
                                       const float *mean, const float *rstd, const void *dout,
                                       const void *dres, int64_t N, int64_t d, void *dx, float *dw,
                                       float *db, float *part, hipStream_t s);
+// a[d] (and, from column d on, b[d] if not NULL) = column sums of P partial rows
+// of ld elements, in a fixed order.
+hipError_t launch_column_sums(const float *part, int P, int64_t ld, int64_t d, float *a, float *b,
+                              hipStream_t s);
 
 // Linear product out = act(x W^T + bias) + residual (bf16, x [N, K], W [M, K];
 // K, M multiples of 8) and its backward; act: kActRelu, kActGelu or kActNone

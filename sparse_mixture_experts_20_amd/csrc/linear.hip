@@ -23,8 +23,10 @@
 // that a lane ends with 16 adjacent columns of one row: the epilogue stores
 // whole 128-byte lines from registers, with no pass through LDS. When the tiles
 // leave CUs idle, the reduction is cut into ranges whose fp32 partials go to
-// the workspace and a second kernel adds them in order (no atomics).
+// the workspace and a second kernel adds them in order (no atomics). The two
+// products of a small backward share one launch (linear_pair_kernel).
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "activation.hpp"
@@ -44,6 +46,7 @@ struct Epilogue {
     const unsigned short *res;      // bf16 like the output, or NULL
     unsigned short *z16;            // bf16 pre-activations, or NULL
     int act;
+    float *sums;                    // [rows] sums of A's rows (pair kernel), or NULL
 };
 
 // Epilogue of G adjacent columns (a multiple of 8) of one row at element
@@ -86,37 +89,20 @@ __device__ __forceinline__ void store_columns(const Epilogue &ep, int64_t o, flo
     }
 }
 
-// out [rows, cols] = A B over K. AT: A is [K][rows] (else [rows][K]); BT: B is
-// [K][cols] (else [cols][K]). grid: (tiles rounded up to the XCD count,
-// K-ranges); with more than one range, range s writes its fp32 partial tile
-// rows to part + s rows cols and the epilogue is left to the second kernel.
-template <int BM, int BN, int WM, int WN, int S, bool AT, bool BT>
-__global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
-    const unsigned short *__restrict__ A, const unsigned short *__restrict__ B, int rows,
-    int cols, int K, Epilogue ep, float *__restrict__ part) {
-    typedef TileProduct<BM, BN, WM, WN, S, AT, BT> Tile;
+// out [rows, cols] = A B over K-steps [kb, ke) of the tile at (m0, n0). AT: A is
+// [K][rows] (else [rows][K]); BT: B is [K][cols] (else [cols][K]). With part,
+// the fp32 partial products go there instead. SUMS: the first column tile also
+// writes ep.sums.
+template <typename Tile, bool AT, bool BT, bool SUMS = false>
+__device__ __forceinline__ void linear_tile(char *smem, const unsigned short *__restrict__ A,
+                                            const unsigned short *__restrict__ B, int rows,
+                                            int cols, int K, const Epilogue &ep,
+                                            float *__restrict__ part, int m0, int n0, int kb,
+                                            int ke) {
     constexpr int FM = Tile::FM, FN = Tile::FN;
-    __shared__ __attribute__((aligned(1024))) char smem[Tile::LDS];
-
-    // Tile of this workgroup: block b runs on XCD b mod 8 and takes index
-    // (b mod 8) T8/8 + b/8, one contiguous range per XCD; within it, column
-    // blocks of 8 row tiles, rows fastest, so that the tiles in flight on an
-    // XCD share operand panels in its L2.
-    const int tm = (rows + BM - 1) / BM, tn = (cols + BN - 1) / BN, T = tm * tn;
-    const int T8 = (T + kXcdCount - 1) / kXcdCount;
-    const int L = (int)(blockIdx.x % kXcdCount) * T8 + (int)(blockIdx.x / kXcdCount);
-    if (L >= T)
-        return;
-    constexpr int GM = 8;
-    const int band = L / (GM * tn), bm = min(GM, tm - band * GM), in = L - band * GM * tn;
-    const int m0 = (band * GM + in % bm) * BM, n0 = (in / bm) * BN;
-    const int KT = (K + kStep - 1) / kStep;
-    const int kb = (int)((int64_t)blockIdx.y * KT / gridDim.y);
-    const int ke = (int)((int64_t)(blockIdx.y + 1) * KT / gridDim.y);
-
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wv / WN, wn = wv % WN;
+    const int wm = wv / Tile::WAVES_N, wn = wv % Tile::WAVES_N;
 
     f32x4 acc[FM][FN];
 #pragma unroll
@@ -124,7 +110,12 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Tile::run(
+    const bool on = SUMS && ep.sums && n0 == 0 && wn == 0;
+    f32x4 sum[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Tile::template run<SUMS>(
         smem,
         [&](int r) {
             return AT ? A + min(m0 + 8 * r, rows - 8) : A + (int64_t)min(m0 + r, rows - 1) * K;
@@ -133,8 +124,18 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
         [&](int r) {
             return BT ? B + min(n0 + 8 * r, cols - 8) : B + (int64_t)min(n0 + r, cols - 1) * K;
         },
-        cols, K, kb, ke, acc);
+        cols, K, kb, ke, acc, on, sum);
     const int l16 = lane & 15, g = lane >> 4;
+    if (on && g == 0) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int m = m0 + wm * FM * 16 + i * 16 + l16;
+            if (m < rows)
+                ep.sums[m] = sum[i][0];
+        }
+    }
+    if (SUMS && !ep.out16 && !ep.out32)
+        return;
     // lane: row l16 of each 16-row strip, 16 adjacent columns
     const int n = n0 + wn * 64 + 16 * g, valid = min(16, cols - n);
     if (valid <= 0)
@@ -160,11 +161,10 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
             continue;
         const int64_t o = (int64_t)m * cols + n;
         if (part) {
-            float *dst = part + (int64_t)blockIdx.y * rows * cols + o;
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 if (4 * j < valid)
-                    *reinterpret_cast<f32x4 *>(dst + 4 * j) = acc[i][j];
+                    *reinterpret_cast<f32x4 *>(part + o + 4 * j) = acc[i][j];
             continue;
         }
         float v[16];
@@ -174,6 +174,100 @@ __global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
             for (int q = 0; q < 4; ++q)
                 v[4 * j + q] = acc[i][j][q];
         store_columns<16>(ep, o, v, bias, valid);
+    }
+}
+
+// Where tile t of tm x tn stands: column blocks of 8 row tiles, rows fastest, so
+// that the tiles in flight on an XCD share operand panels in its L2.
+struct Place {
+    int m, n;   // row and column tile
+};
+__device__ __forceinline__ Place place_of(int t, int tm, int tn) {
+    constexpr int GM = 8;
+    const int band = t / (GM * tn), bm = min(GM, tm - band * GM), in = t - band * GM * tn;
+    return {band * GM + in % bm, in / bm};
+}
+
+// The product by BM x BN tiles. Block b runs on XCD b mod 8; each XCD takes one
+// contiguous range of the tiles. grid: (8 x the blocks of an XCD, K-ranges);
+// with more than one range, range s writes its fp32 partials to part + s rows
+// cols and the epilogue is left to the second kernel.
+// whole: of an XCD's tiles, the first that are computed whole; the others by two
+// workgroups, the halves of their rows.
+template <int BM, int BN, int WM, int WN, int S, bool AT, bool BT>
+__global__ __launch_bounds__(WM *WN * 64) void linear_kernel(
+    const unsigned short *__restrict__ A, const unsigned short *__restrict__ B, int rows,
+    int cols, int K, int whole, Epilogue ep, float *__restrict__ part) {
+    constexpr bool HALVES = BM == 256;
+    typedef TileProduct<BM, BN, WM, WN, S, AT, BT> Tile;
+    typedef TileProduct<HALVES ? BM / 2 : BM, BN, WM, WN, HALVES ? S + 1 : S, AT, BT> Half;
+    __shared__ __attribute__((aligned(1024))) char smem[Half::LDS > Tile::LDS ? Half::LDS : Tile::LDS];
+
+    const int tm = (rows + BM - 1) / BM, tn = (cols + BN - 1) / BN, T = tm * tn;
+    const int T8 = (T + kXcdCount - 1) / kXcdCount;
+    int q = (int)(blockIdx.x / kXcdCount), half = 0;
+    const bool split = HALVES && q >= whole;
+    if (split) {
+        half = (q - whole) & 1;
+        q = whole + ((q - whole) >> 1);
+    }
+    const int L = (int)(blockIdx.x % kXcdCount) * T8 + q;
+    if (L >= T)
+        return;
+    const Place p = place_of(L, tm, tn);
+    const int m0 = p.m * BM, n0 = p.n * BN;
+    const int KT = (K + kStep - 1) / kStep;
+    if constexpr (HALVES) {   // (never in ranges)
+        if (!split)
+            linear_tile<Tile, AT, BT>(smem, A, B, rows, cols, K, ep, nullptr, m0, n0, 0, KT);
+        else if (m0 + half * (BM / 2) < rows)
+            linear_tile<Half, AT, BT>(smem, A, B, rows, cols, K, ep, nullptr,
+                                      m0 + half * (BM / 2), n0, 0, KT);
+    } else {
+        const int kb = (int)((int64_t)blockIdx.y * KT / gridDim.y);
+        const int ke = (int)((int64_t)(blockIdx.y + 1) * KT / gridDim.y);
+        linear_tile<Tile, AT, BT>(smem, A, B, rows, cols, K, ep,
+                                  part ? part + (int64_t)blockIdx.y * rows * cols : nullptr, m0,
+                                  n0, kb, ke);
+    }
+}
+
+// Both products of a backward in one launch: dx = dz W and dW = dz^T x, the tiles
+// of the longer reduction first. They need nothing of each other, and one's tiles
+// fill the CUs that the other leaves idle. ep.sums of dW: db, the sums of dz's
+// columns, from the tiles that read them. A gradient that is not wanted has no
+// tiles (tn = 0), except that db alone takes dW's first column of tiles, which
+// then write nothing else. grid: 8 x the blocks of an XCD.
+struct Product {
+    const unsigned short *A, *B;
+    int rows, cols, K, tn;   // tn: column tiles to compute
+    Epilogue ep;
+};
+__device__ __host__ __forceinline__ int pair_tiles(const Product &p) {   // of an XCD
+    return ((p.rows + 127) / 128 * p.tn + kXcdCount - 1) / kXcdCount;
+}
+__global__ __launch_bounds__(512) void linear_pair_kernel(Product dx, Product dw) {
+    typedef TileProduct<128, 128, 4, 2, 4, false, true> TileX;
+    typedef TileProduct<128, 128, 4, 2, 4, true, true> TileW;
+    __shared__ __attribute__((aligned(1024))) char smem[TileX::LDS];
+    const int X8 = pair_tiles(dx), W8 = pair_tiles(dw);
+    const bool w_first = dw.K >= dx.K;
+    const int q = (int)(blockIdx.x / kXcdCount), xcd = (int)(blockIdx.x % kXcdCount);
+    if (w_first ? q < W8 : q >= X8) {
+        const int t = xcd * W8 + (w_first ? q : q - X8), tm = (dw.rows + 127) / 128;
+        if (t >= tm * dw.tn)
+            return;
+        const Place p = place_of(t, tm, dw.tn);
+        linear_tile<TileW, true, true, true>(smem, dw.A, dw.B, dw.rows, dw.cols, dw.K, dw.ep,
+                                             nullptr, p.m * 128, p.n * 128, 0,
+                                             (dw.K + kStep - 1) / kStep);
+    } else {
+        const int t = xcd * X8 + (w_first ? q - W8 : q), tm = (dx.rows + 127) / 128;
+        if (t >= tm * dx.tn)
+            return;
+        const Place p = place_of(t, tm, dx.tn);
+        linear_tile<TileX, false, true>(smem, dx.A, dx.B, dx.rows, dx.cols, dx.K, dx.ep, nullptr,
+                                        p.m * 128, p.n * 128, 0, (dx.K + kStep - 1) / kStep);
     }
 }
 
@@ -385,9 +479,44 @@ Shape shape_of(int64_t rows, int64_t cols, int64_t K) {
             best = s;
     return {Tile::k128, (int)best};
 }
+// Whether the two products of a backward run as one launch: both on 128x128
+// tiles, and faster so by the times, in us, of a tile (3 and 0.6 a K-step, 0.7
+// where both operands are transposed) and of a split product's joining. Without
+// an activation the pair spares the pass for db (2047x3072x768: 39 us, against 51
+// apart; 8192x1024x1024: 87 us paired, 68 apart). Which gradients are
+// wanted does not enter, so that each has the same bits whatever the others.
+bool paired(int64_t N, int64_t K, int64_t M, bool act) {
+    const Shape x = shape_of(N, K, M), w = shape_of(M, K, N);
+    auto small = [](const Shape &s) { return s.tile == Tile::k128 || s.tile == Tile::k128x2; };
+    if (!small(x) || !small(w))
+        return false;
+    auto steps = [](int64_t k) { return (double)((k + kStep - 1) / kStep); };
+    auto tiles = [](int64_t rows, int64_t cols) {
+        return (double)(((rows + 127) / 128) * ((cols + 127) / 128));
+    };
+    const double tx = 3 + 0.6 * steps(M), tw = 3 + 0.7 * steps(N);
+    const double nx = tiles(N, K), nw = tiles(M, K);
+    auto alone = [](const Shape &s, double n, double t, double part) {
+        if (s.splits == 1)
+            return std::ceil(n / 256) * t;
+        return 3 + (t - 3) / s.splits + 4.5 + (s.splits + 1) * part / 4e6;
+    };
+    const double pair = std::max(std::max(tx, tw), (nx * tx + nw * tw) / 256 + std::min(tx, tw) / 2);
+    return pair <= alone(x, nx, tx, 4.0 * (double)(N * K)) + alone(w, nw, tw, 4.0 * (double)(M * K)) +
+                       (act ? 0 : 8);
+}
 size_t part_bytes(int64_t rows, int64_t cols, int64_t K) {
     const Shape sh = shape_of(rows, cols, K);
     return sh.splits > 1 ? (size_t)(sh.splits * rows * cols) * sizeof(float) : 0;
+}
+
+// Of an XCD's 256x256 tiles, one per CU at a time, those computed whole. A last
+// round that fills at most half of the 32 CUs is computed as half tiles instead,
+// which fill the others (8192x2048x7168, 3.5 rounds: 254 -> 242 us;
+// 4608x4096x4096, 1.1 rounds: 198 -> 165 us).
+int64_t whole_tiles(int64_t each) {
+    const int64_t last = each % 32;
+    return last <= 16 ? each - last : each;
 }
 
 template <bool AT, bool BT>
@@ -398,9 +527,12 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
     const auto *b = static_cast<const unsigned short *>(B);
     auto go = [&](auto kernel, int bm, int bn, int threads) {
         const int64_t T = ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
-        const int64_t grid = (T + kXcdCount - 1) / kXcdCount * kXcdCount;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)grid, (unsigned)sh.splits), dim3(threads), 0, s,
-                           a, b, (int)rows, (int)cols, (int)K, ep,
+        const int64_t each = (T + kXcdCount - 1) / kXcdCount;   // tiles of an XCD
+        const int64_t whole = bm == 256 ? whole_tiles(each) : each;
+        hipLaunchKernelGGL(kernel,
+                           dim3((unsigned)(kXcdCount * (whole + 2 * (each - whole))),
+                                (unsigned)sh.splits),
+                           dim3(threads), 0, s, a, b, (int)rows, (int)cols, (int)K, (int)whole, ep,
                            sh.splits > 1 ? part : (float *)nullptr);
     };
     if (sh.tile == Tile::k64)
@@ -419,13 +551,13 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
     return hipGetLastError();
 }
 
-// Workgroups of the dz pass along N (rows of its column-sum partials): about
-// 2048 in all, each with at least one row per thread.
-int dz_groups(int64_t N, int64_t M) {
-    const int64_t across = (M + 255) / 256;
-    const int64_t want = std::max<int64_t>(1, 2048 / across);
-    return (int)std::min<int64_t>(want, (N + 7) / 8);
+// Rows of a workgroup of the dz pass: whole groups of the 8 that it takes at a
+// time, about 2048 workgroups in all.
+int64_t dz_rows(int64_t N, int64_t M) {
+    const int64_t want = std::max<int64_t>(1, 2048 / ((M + 255) / 256));
+    return ((N + want - 1) / want + 7) / 8 * 8;
 }
+int dz_groups(int64_t N, int64_t M) { return (int)((N + dz_rows(N, M) - 1) / dz_rows(N, M)); }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -448,7 +580,7 @@ hipError_t launch_linear(const void *x, const void *W, const float *bias, int ac
                          void *ws, hipStream_t s) {
     const Epilogue ep{static_cast<unsigned short *>(out), nullptr, bias,
                       static_cast<const unsigned short *>(residual),
-                      static_cast<unsigned short *>(z), act};
+                      static_cast<unsigned short *>(z), act, nullptr};
     if (skinny(N, K, M)) {
         auto go = [&](auto tiles, auto half) {
             constexpr int TT = decltype(tiles)::value;
@@ -486,9 +618,11 @@ hipError_t launch_linear_backward(const void *x, const void *W, const void *z, i
     const LinearBackwardLayout L = linear_backward_layout(N, K, M, act != kActNone);
     char *w = static_cast<char *>(ws);
     const void *dz = dout;
-    if (act != kActNone || db) {
+    const bool pair = paired(N, K, M, act != kActNone);
+    const bool db_in_pair = pair && act == kActNone;
+    if (act != kActNone || (db && !db_in_pair)) {
         const int P = dz_groups(N, M);
-        const int per = (int)((N + P - 1) / P);
+        const int per = (int)dz_rows(N, M);
         float *sums = reinterpret_cast<float *>(w + L.sums);
         hipLaunchKernelGGL(linear_dz_kernel, dim3((unsigned)((M + 255) / 256), (unsigned)P),
                            dim3(256), 0, s, static_cast<const unsigned short *>(dout),
@@ -496,7 +630,7 @@ hipError_t launch_linear_backward(const void *x, const void *W, const void *z, i
                            reinterpret_cast<unsigned short *>(w + L.dz), db ? sums : nullptr);
         hipError_t err = hipGetLastError();
         if (err == hipSuccess && db)
-            err = launch_chunk_sum(sums, P, M, db, s);
+            err = launch_column_sums(sums, P, M, M, db, nullptr, s);
         if (err != hipSuccess)
             return err;
         if (act != kActNone)
@@ -506,8 +640,23 @@ hipError_t launch_linear_backward(const void *x, const void *W, const void *z, i
     auto plain = [](void *o, bool f32) {
         return Epilogue{f32 ? nullptr : static_cast<unsigned short *>(o),
                         f32 ? static_cast<float *>(o) : nullptr, nullptr, nullptr, nullptr,
-                        kActNone};
+                        kActNone, nullptr};
     };
+    if (pair) {
+        const auto *dz16 = static_cast<const unsigned short *>(dz);
+        const int tn = (int)((K + 127) / 128);
+        Product px{dz16, static_cast<const unsigned short *>(W), (int)N, (int)K, (int)M,
+                   dx ? tn : 0, plain(dx, dx32)};
+        Product pw{dz16, static_cast<const unsigned short *>(x), (int)M, (int)K, (int)N,
+                   dW ? tn : db_in_pair && db ? 1 : 0, plain(dW, dW32)};
+        pw.ep.sums = db_in_pair ? static_cast<float *>(db) : nullptr;
+        const int blocks = pair_tiles(px) + pair_tiles(pw);
+        if (blocks == 0)
+            return hipSuccess;
+        hipLaunchKernelGGL(linear_pair_kernel, dim3((unsigned)(kXcdCount * blocks)), dim3(512), 0, s,
+                           px, pw);
+        return hipGetLastError();
+    }
     if (dx) {
         hipError_t err = launch_product<false, true>(dz, W, N, K, M, plain(dx, dx32), part, s);
         if (err != hipSuccess)

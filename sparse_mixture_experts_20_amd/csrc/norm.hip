@@ -382,13 +382,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_backward_ker
     }
 }
 
-// dw[c] and db[c] = sum over the P partial rows, each of kSumGroups interleaved
-// sets in order and then the sets in order: a chain of P / 16 loads (the
+// a[c] and, from column d on, b[c] = sum over P partial rows of ld, each of
+// kSumGroups interleaved sets in order and then the sets in order: a chain of P / 16 loads (the
 // latency of a chain of P / 4 was most of this kernel's time). 64 columns per
 // workgroup.
 constexpr int kSumGroups = 16;
-__global__ __launch_bounds__(kSumGroups * 64) void norm_column_sums_kernel(
-    const float *__restrict__ part, int P, int d, float *__restrict__ dw, float *__restrict__ db) {
+__global__ __launch_bounds__(kSumGroups * 64) void column_sums_kernel(
+    const float *__restrict__ part, int P, int ld, int d, float *__restrict__ a,
+    float *__restrict__ b) {
     __shared__ float red[kSumGroups][64];
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(kSumGroups * 64) void norm_column_sums_kernel(
     if (c < d) {
 #pragma unroll 8
         for (int r = q; r < P; r += kSumGroups)
-            s += p[(int64_t)r * 2 * d];
+            s += p[(int64_t)r * ld];
     }
     red[q][lane] = s;
     __syncthreads();
@@ -406,7 +407,7 @@ __global__ __launch_bounds__(kSumGroups * 64) void norm_column_sums_kernel(
 #pragma unroll
         for (int g = 1; g < kSumGroups; ++g)
             t += red[g][lane];
-        (blockIdx.y == 0 ? dw : db)[c] = t;
+        (blockIdx.y == 0 ? a : b)[c] = t;
     }
 }
 
@@ -495,8 +496,13 @@ hipError_t launch_layer_norm_backward(bool bf16, bool vec, const void *x, const 
     });
     if (err != hipSuccess)
         return err;
-    hipLaunchKernelGGL(norm_column_sums_kernel, dim3((unsigned)((d + 63) / 64), db ? 2u : 1u),
-                       dim3(kSumGroups * 64), 0, s, (const float *)part, P, (int)d, dw, db);
+    return launch_column_sums(part, P, 2 * d, d, dw, db, s);
+}
+
+hipError_t launch_column_sums(const float *part, int P, int64_t ld, int64_t d, float *a, float *b,
+                              hipStream_t s) {
+    hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((d + 63) / 64), b ? 2u : 1u),
+                       dim3(kSumGroups * 64), 0, s, part, P, (int)ld, (int)d, a, b);
     return hipGetLastError();
 }
 

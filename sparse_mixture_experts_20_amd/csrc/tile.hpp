@@ -46,7 +46,7 @@ __device__ __forceinline__ s16x4 read_transposed(const void *p) {
 
 template <int BM, int BN, int WM, int WN, int S, bool AT, bool BT>
 struct TileProduct {
-    static constexpr int NW = WM * WN, THREADS = NW * 64;
+    static constexpr int NW = WM * WN, THREADS = NW * 64, WAVES_N = WN;
     static constexpr int FM = BM / WM / 16, FN = 4;
     static constexpr int ABYTES = BM * kStep * 2, BBYTES = BN * kStep * 2;
     static constexpr int STAGE = ABYTES + BBYTES, LDS = S * STAGE;
@@ -62,9 +62,14 @@ struct TileProduct {
     // for the tile's columns. Rows and columns past the edge may point at any
     // valid place (their products are not read). K % 8 == 0 for an operand that
     // runs along K. smem: LDS bytes, 1024-byte aligned; every thread calls.
-    template <typename PA, typename PB>
+    // SUMS: where `on` (per wave), sum[i][q] += the sum along K of A's row
+    // 16 i + l % 16 as well, one product with a fragment of ones.
+    template <bool SUMS, typename PA, typename PB>
     static __device__ __forceinline__ void run(char *smem, PA a, int lda, PB b, int ldb, int K,
-                                               int kb, int ke, f32x4 (&acc)[FM][FN]) {
+                                               int kb, int ke, f32x4 (&acc)[FM][FN], bool on,
+                                               f32x4 (&sum)[FM]) {
+        const bf16x8 ones = __builtin_bit_cast(
+            bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
         const int lane = threadIdx.x & 63;
         const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int wm = wv / WN, wn = wv % WN;
@@ -195,9 +200,17 @@ struct TileProduct {
                     for (int j = 0; j < FN; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fB[j], fA, acc[i][j],
                                                                              0, 0, 0);
+                    if (SUMS && on)
+                        sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, fA, sum[i], 0, 0, 0);
                 }
             }
         }
+    }
+    template <typename PA, typename PB>
+    static __device__ __forceinline__ void run(char *smem, PA a, int lda, PB b, int ldb, int K,
+                                               int kb, int ke, f32x4 (&acc)[FM][FN]) {
+        f32x4 none[FM];
+        run<false>(smem, a, lda, b, ldb, K, kb, ke, acc, false, none);
     }
 };
 
