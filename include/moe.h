@@ -488,7 +488,8 @@ size_t moe_few_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int
  *   z        [N, M] MOE_BF16 or NULL: the pre-activations, for the backward
  *            (a buffer of its own: MOE_ERR_ARG)
  * fp32 accumulation, bias, activation and residual; out and z are each rounded
- * once. out must not overlap x or W. K and M are multiples of 8 and N, K, M at
+ * once. Otherwise out and z must not overlap an input or each other
+ * (MOE_ERR_ARG). K and M are multiples of 8 and N, K, M at
  * most MOE_LINEAR_MAX_EXTENT (MOE_ERR_UNSUPPORTED); data 16-byte aligned
  * (MOE_ERR_ALIGN). workspace: device scratch of moe_linear_workspace_size()
  * bytes, 256-byte aligned (may be NULL when that is 0): fp32 partial products
@@ -507,7 +508,8 @@ size_t moe_linear_workspace_size(int64_t N, int64_t K, int64_t M);
  * MOE_BF16 or MOE_F32, dbias [M] MOE_F32; each may be NULL and is then not
  * computed (all three NULL: MOE_ERR_NULL). The products read dz rounded once
  * to bf16 (the dz of MOE_ACT_NONE is dout, exactly); dbias sums the fp32
- * values. dx must not be the buffer of x, z or dout (MOE_ERR_ARG). Widths and
+ * values. No output may overlap an input or another output (MOE_ERR_ARG). Each
+ * gradient has the same bits whichever others are computed with it. Widths and
  * alignment as moe_linear's. workspace:
  * moe_linear_backward_workspace_size() bytes, 256-byte aligned. N = 0: dW and
  * dbias are zero. */
@@ -532,7 +534,8 @@ size_t moe_linear_backward_workspace_size(int64_t N, int64_t K, int64_t M, int32
  *   mean, rstd  [N] MOE_F32 or NULL: what the backward needs
  * Statistics are fp32, of the values h holds after its rounding. out or h may
  * be the buffer of x or of residual (each element is read before it is
- * written), not both the same buffer (MOE_ERR_ARG). d <= MOE_NORM_MAX_WIDTH;
+ * written), but must not overlap each other, or one of those any other way
+ * (MOE_ERR_ARG). d <= MOE_NORM_MAX_WIDTH;
  * bf16 rows need d % 8 == 0 (MOE_ERR_UNSUPPORTED) and 16-byte aligned x,
  * residual, h, out, weight and bias (MOE_ERR_ALIGN); fp32 rows any d. */
 int moe_layer_norm(const moe_tensor *x, const moe_tensor *residual, const moe_tensor *weight,
@@ -546,7 +549,8 @@ int moe_layer_norm(const moe_tensor *x, const moe_tensor *residual, const moe_te
  *   dweight = sum over rows of dout xh, dbias = sum over rows of dout
  * x is the h of the forward (or its x without a residual); with a residual
  * dx is the gradient of both summands. dx, dout and dres have x's shape and
- * dtype (dx may be the buffer of dout or dres, not of x: MOE_ERR_ARG);
+ * dtype (dx may be the buffer of dout or dres, but must not overlap them
+ * another way, or x: MOE_ERR_ARG);
  * weight, dweight and dbias [d], mean and rstd [N] MOE_F32; dbias may be
  * NULL. Sums are fp32 in a fixed order. workspace: device scratch of
  * moe_layer_norm_backward_workspace_size() bytes, 256-byte aligned. Widths

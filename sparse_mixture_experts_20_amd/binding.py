@@ -802,7 +802,7 @@ def _on_stream(fn):
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
-        for t in args:
+        for t in (*args, *kw.values()):
             if isinstance(t, torch.Tensor):
                 if t.get_device() != stream.device.index:
                     raise ValueError(f"a tensor on {t.device}, the stream on {stream.device}")
@@ -905,6 +905,9 @@ class FewLayer:
 
     def __call__(self, x, noise=None, out=None, stream=None):
         if stream is not None:
+            if stream.device.index != self.index:
+                raise ValueError(f"the layer is on cuda:{self.index}, the stream on "
+                                 f"{stream.device}")
             with torch.cuda.stream(stream):
                 return self(x, noise, out)
         N = x.numel() // x.shape[-1]

@@ -1387,6 +1387,18 @@ int check_norm_x(const moe_tensor *x, int64_t &N, int64_t &d) {
 template <typename... P>
 bool all_aligned16(P... p) { return (aligned(p, 16) && ...); }
 
+// Bytes [p, p + n) of a buffer (none where p is NULL).
+struct Span {
+    const void *p;
+    int64_t n;
+};
+bool overlap(Span a, Span b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+// Whether a shares bytes with b other than by being the same buffer.
+bool crosses(Span a, Span b) { return a.p != b.p && overlap(a, b); }
+
 }  // namespace
 
 extern "C" {
@@ -1414,12 +1426,17 @@ int moe_layer_norm(const moe_tensor *x, const moe_tensor *residual, const moe_te
         return MOE_ERR_ARG;   // without a residual, h is x itself
     if (N == 0)
         return MOE_OK;
-    if (hp && hp == op)
-        return MOE_ERR_ARG;
     const bool al = all_aligned16((const void *)x->data, r, hp, op, w, b);
     const bool bf16 = x->dtype == MOE_BF16;
+    const int64_t bytes = N * d * (bf16 ? 2 : 4);
+    const Span in[2] = {{x->data, bytes}, {r, bytes}}, to[2] = {{hp, bytes}, {op, bytes}};
+    if (overlap(to[0], to[1]))
+        return MOE_ERR_ARG;
     if (bf16 && !al)
         return MOE_ERR_ALIGN;
+    for (const Span &i : in)
+        if (crosses(to[0], i) || crosses(to[1], i))
+            return MOE_ERR_ARG;
     return hip_status(moe::launch_layer_norm(bf16, bf16 || (al && d % 4 == 0), x->data, r, w, b,
                                              eps, N, d, hp, op, const_cast<float *>(mp),
                                              const_cast<float *>(rp),
@@ -1474,6 +1491,10 @@ int moe_layer_norm_backward(const moe_tensor *x, const moe_tensor *weight, const
         return MOE_ERR_ALIGN;
     if (workspace_bytes < moe::layer_norm_backward_bytes(N, d))
         return MOE_ERR_WORKSPACE;
+    const int64_t bytes = N * d * (bf16 ? 2 : 4);
+    const Span to{dxp, bytes};
+    if (overlap(to, {x->data, bytes}) || crosses(to, {g, bytes}) || crosses(to, {r, bytes}))
+        return MOE_ERR_ARG;
     return hip_status(moe::launch_layer_norm_backward(
         bf16, bf16 || (al && d % 4 == 0), x->data, w, m, rs, g, r, N, d, dxp,
         const_cast<float *>(dw), const_cast<float *>(db), static_cast<float *>(workspace), s));
@@ -1553,11 +1574,15 @@ int moe_linear(const moe_tensor *x, const moe_tensor *W, const moe_tensor *bias,
         return MOE_OK;
     if (!all_aligned16(b, r, o, zp))
         return MOE_ERR_ALIGN;
-    if (zp && (zp == o || zp == r))
+    const Span so{o, 2 * N * M}, sz{zp, 2 * N * M}, sr{r, 2 * N * M};
+    if (overlap(sz, so) || overlap(sz, sr) || crosses(so, sr))
         return MOE_ERR_ARG;
     rc = check_scratch(workspace, workspace_bytes, moe::linear_bytes(N, K, M));
     if (rc != MOE_OK)
         return rc;
+    for (const Span &i : {Span{x->data, 2 * N * K}, Span{W->data, 2 * M * K}, Span{b, 4 * M}})
+        if (overlap(so, i) || overlap(sz, i))
+            return MOE_ERR_ARG;
     return hip_status(moe::launch_linear(x->data, W->data, b, activation, r, N, K, M, o, zp,
                                          workspace, static_cast<hipStream_t>(stream)));
 }
@@ -1614,12 +1639,23 @@ int moe_linear_backward(const moe_tensor *x, const moe_tensor *W, const moe_tens
                                          0, s));
         return MOE_OK;
     }
-    if ((dxp && (dxp == x->data || dxp == g || dxp == zp)))
-        return MOE_ERR_ARG;   // the weight gradient reads them after dx is written
+    const Span to[3] = {{dxp, N * K * (dx && dx->dtype == MOE_F32 ? 4 : 2)},
+                        {dWp, M * K * (dW && dW->dtype == MOE_F32 ? 4 : 2)},
+                        {db, 4 * M}};
+    const Span in[4] = {{x->data, 2 * N * K}, {W->data, 2 * M * K}, {zp, 2 * N * M}, {g, 2 * N * M}};
+    if (overlap(to[0], in[0]) || overlap(to[0], in[2]) || overlap(to[0], in[3]))
+        return MOE_ERR_ARG;
     rc = check_scratch(workspace, workspace_bytes,
                        moe::linear_backward_layout(N, K, M, activation != MOE_ACT_NONE).total);
     if (rc != MOE_OK)
         return rc;
+    // the products run side by side and read every input
+    for (const Span &o : to)
+        for (const Span &i : in)
+            if (overlap(o, i))
+                return MOE_ERR_ARG;
+    if (overlap(to[0], to[1]) || overlap(to[0], to[2]) || overlap(to[1], to[2]))
+        return MOE_ERR_ARG;
     return hip_status(moe::launch_linear_backward(
         x->data, W->data, zp, activation, g, N, K, M, dxp, dx && dx->dtype == MOE_F32, dWp,
         dW && dW->dtype == MOE_F32, const_cast<float *>(db), workspace, s));

@@ -239,6 +239,34 @@ def test_layer_norm_backward_refusals(L):
     assert L.moe_layer_norm_backward_workspace_size(8, 1 << 20) == 0
 
 
+def test_overlapping_buffers_are_refused(L):
+    """An output that shares bytes with an input, or with another output, other
+    than by being the buffer it is documented to be allowed to be."""
+    P = FAKE
+    a, lo, hi = 16 * P, 16 * P - 16, 16 * P + 16        # a buffer and its neighbours' starts
+    for where in (a, lo, hi):
+        o = t(BF16, 128, 32, ptr=where)
+        assert _lin(L, x=t(BF16, 128, 64, ptr=a), W=t(BF16, 32, 64, ptr=P), out=o) == ARG
+        assert _lin(L, x=t(BF16, 128, 64, ptr=P), W=t(BF16, 32, 64, ptr=a), b=None, out=o) == ARG
+        assert _lin(L, x=t(BF16, 128, 64, ptr=a), W=t(BF16, 32, 64, ptr=P), b=None,
+                    out=t(BF16, 128, 32, ptr=2 * P), z=o) == ARG
+        if where != a:
+            assert _lin(L, r=t(BF16, 128, 32, ptr=a), out=o) == ARG
+            assert _norm(L, x=t(BF16, 8, 64, ptr=a), out=t(BF16, 8, 64, ptr=where)) == ARG
+            assert _norm(L, r=t(BF16, 8, 64, ptr=a), h=t(BF16, 8, 64, ptr=where)) == ARG
+            assert _normb(L, g=t(BF16, 8, 64, ptr=a), dx=t(BF16, 8, 64, ptr=where)) == ARG
+        assert _normb(L, x=t(BF16, 8, 64, ptr=a), dx=t(BF16, 8, 64, ptr=where)) == ARG
+        own = dict(x=t(BF16, 128, 64, ptr=4 * P), W=t(BF16, 32, 64, ptr=5 * P),
+                   z=t(BF16, 128, 32, ptr=6 * P), g=t(BF16, 128, 32, ptr=7 * P),
+                   db=t(F32, 32, ptr=8 * P))
+        for name, shape in (("x", (128, 64)), ("W", (32, 64)), ("z", (128, 32)), ("g", (128, 32))):
+            args = {**own, name: t(BF16, *shape, ptr=a)}
+            assert _linb(L, **args, dW=t(F32, 32, 64, ptr=where)) == ARG, name
+            assert _linb(L, **{**args, "db": t(F32, 32, ptr=where)}) == ARG, name
+            assert _linb(L, **args, dx=t(F32, 128, 64, ptr=where)) == ARG, name
+        assert _linb(L, **own, dx=t(F32, 128, 64, ptr=a), dW=t(F32, 32, 64, ptr=where)) == ARG
+
+
 # --------------------------------------------------------------------------
 def test_binding_refuses_host_tensors_and_names():
     import torch
