@@ -25,6 +25,11 @@
 // leave CUs idle, the reduction is cut into ranges whose fp32 partials go to
 // the workspace and a second kernel adds them in order (no atomics). The two
 // products of a small backward share one launch (linear_pair_kernel).
+//
+// Measured, in TFLOP/s of the products: 8192x2048x7168 with residual 990 (242
+// us), 4096x4096x14336 forward 1165 (412 us) and GELU backward 1090 to 1155 with
+// its dz pass (832 to 880 us), 2047x3072x768 backward 515 (37 us, both products
+// in one launch). 4x7168x2048 9.3 us on the GPU (29 MB of weights).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
