@@ -449,8 +449,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
 //    hide more LDS latency than the 8 waves of 128x64 save in LDS reads, 1061
 //    against 1018 TFLOP/s at 4096x4096x14336), when they fill the 256 CUs about
 //    once;
-//  - 128x128 tiles, two workgroups of 4 waves per CU, for more than 256 of them
-//    (2048x768x3072: 25 us, against 28 with the next form);
+//  - 128x128 tiles, two workgroups of 8 waves per CU, for more than 256 of them
+//    (2048x768x3072 with GELU and z: 22 us, against 28 with the next form; 25
+//    with 4 waves of 64x64, which are 2% faster only from K = 4096 on, where the
+//    epilogue's share is small);
 //  - 128x128 tiles, one workgroup of 8 waves per CU and a ring of four stages,
 //    for up to 256 of them: alone on its CU a workgroup waits for the latency
 //    of its loads, and three K-steps in flight instead of one take a K-step from
@@ -545,7 +547,7 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
     else if (sh.tile == Tile::k256)
         go(linear_kernel<256, 256, 4, 4, 2, AT, BT>, 256, 256, 1024);
     else if (sh.tile == Tile::k128x2)
-        go(linear_kernel<128, 128, 2, 2, 2, AT, BT>, 128, 128, 256);
+        go(linear_kernel<128, 128, 4, 2, 2, AT, BT>, 128, 128, 512);
     else
         go(linear_kernel<128, 128, 4, 2, 4, AT, BT>, 128, 128, 512);
     hipError_t err = hipGetLastError();
