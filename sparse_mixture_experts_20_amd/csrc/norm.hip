@@ -387,9 +387,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_backward_ker
 }
 
 // a[c] and, from column d on, b[c] = sum over P partial rows of ld, each of
-// kSumGroups interleaved sets in order and then the sets in order: a chain of P / 16 loads (the
-// latency of a chain of P / 4 was most of this kernel's time). 64 columns per
-// workgroup.
+// kSumGroups interleaved sets in order and then the sets in order: a chain of
+// P / 16 loads (the latency of a chain of P / 4 was most of this kernel's time).
+// 64 columns per workgroup.
 constexpr int kSumGroups = 16;
 __global__ __launch_bounds__(kSumGroups * 64) void column_sums_kernel(
     const float *__restrict__ part, int P, int ld, int d, float *__restrict__ a,

@@ -183,3 +183,59 @@ def test_no_tokens_and_limits(torch_mod):
         layer(dev["x"])
     with pytest.raises(ValueError):
         layer(dev["x"][:2].cpu())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_not_finite_among_many_experts(torch_mod, dtype):
+    """On the streaming products (few rows per expert): a NaN and an infinity
+    stay in their tokens' rows, though all tokens share their experts; a token
+    whose noise masks every expert still takes the lowest ids, and one with all
+    but two masked takes those two."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    wl, dev = _layer(torch, 20, 72, 48, 2, 136, dtype, 24.0, "gelu", 0.1, 0.0)
+    x, noise = dev["x"].clone(), torch.zeros((20, 48), device="cuda")
+    noise[:, 7], noise[:, 30] = 50.0, 40.0
+    noise[9] = float("-inf")
+    noise[11] = float("-inf")
+    noise[11, 5], noise[11, 47] = 0.0, -1e30
+    wg = torch.zeros_like(dev["W_g"])
+    x[4, 3], x[6, 5] = float("nan"), float("inf")
+    out, st = B.forward_few(x, wg, noise, dev["W_up"], dev["W_down"], 2, 24.0, act="gelu",
+                            b_up=dev["b_up"], b_down=dev["b_down"])
+    rest = [t for t in range(20) if t not in (4, 6, 9)]
+    assert bool(torch.isfinite(out[rest]).all())
+    assert not bool(torch.isfinite(out[4]).any()) and not bool(torch.isfinite(out[6]).all())
+    assert st.idx[9].tolist() == [0, 1] and st.idx[11].tolist() == [5, 47]
+    assert st.gate[11].tolist() == [1.0, 0.0]
+    ok = [t for t in rest if t != 11]
+    assert bool((st.idx[ok] == torch.tensor([7, 30], device="cuda")).all())
+    # the finite rows are those of a call without the others' values
+    y, _ = B.forward_few(torch.nan_to_num(x, 0.0, 0.0, 0.0), wg, noise, dev["W_up"], dev["W_down"],
+                         2, 24.0, act="gelu", b_up=dev["b_up"], b_down=dev["b_down"])
+    assert torch.equal(out[rest], y[rest])
+
+
+def test_offsets_past_32_bits(torch_mod):
+    """Weights of more than 2^31 elements: tokens sent to the last expert, few
+    (streaming products) and many (tiles)."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain as P
+    E, d, d_ff = 8, 16384, 16392
+    bf = torch.bfloat16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    wu = torch.empty((E, d_ff, d), dtype=bf, device="cuda").normal_(std=d ** -0.5, generator=g)
+    wd = torch.empty((E, d, d_ff), dtype=bf, device="cuda").normal_(std=d_ff ** -0.5, generator=g)
+    wg = torch.zeros((E, d), device="cuda")
+    for N in (3, 64):
+        G.say(f"[few] past 32 bits, N={N}")
+        x = torch.empty((N, d), dtype=bf, device="cuda").normal_(generator=g)
+        noise = torch.zeros((N, E), device="cuda")
+        noise[:, E - 1] = 9.0
+        out, st = B.forward_few(x, wg, noise, wu, wd, 1, 8.0)
+        torch.cuda.synchronize()
+        assert bool((st.idx == E - 1).all()) and bool((st.slot >= 0).all())
+        y, e = P.few(x, wu, wd, None, None, "relu", st.idx.long(), st.gate, st.slot, 2.0 ** -16)
+        P.close(out, y, P.stored(y, e, bf), "out")

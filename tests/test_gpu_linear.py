@@ -172,3 +172,32 @@ def test_gradient_against_differences(torch_mod):
             want = (f(*hi) - f(*lo)) / 2e-5
             got = float((g.double() * v).sum())
             assert abs(got - want) <= 2.0 ** -8 * float(g.double().norm() * v.norm()), (i, got, want)
+
+
+def test_offsets_past_32_bits(torch_mod):
+    """More than 2^31 elements of z, out and dout: the first and last rows, and
+    gradients of a dout that is zero but for some of those rows."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain as P
+    bf = torch.bfloat16
+    N, K, M = 262150, 64, 8200
+    rows = torch.tensor([0, 1, 777, 131073, N - 130, N - 2, N - 1], device="cuda")
+    x, W = _randn(torch, (N, K), bf, 1), _randn(torch, (M, K), bf, 2, K ** -0.5)
+    b = _randn(torch, (M,), torch.float32, 3)
+    out, z = B.linear(x, W, b, act="gelu", keep_z=True)
+    torch.cuda.synchronize()
+    y, z64, ey, ez = P.linear(x[rows], W, b, "gelu", None)
+    P.close(out[rows], y, P.stored(y, ey, bf), "out")
+    P.close(z[rows], z64, P.stored(z64, ez, bf), "z")
+    dout = out.zero_()
+    dout[rows] = _randn(torch, (len(rows), M), bf, 4)
+    G.say("[linear] past 32 bits: backward")
+    dx, dW, db = B.linear_backward(x, W, z, dout, act="gelu")
+    torch.cuda.synchronize()
+    ref = P.linear_backward(x[rows], W, z[rows], dout[rows], "gelu")
+    P.close(dx[rows], ref["dx"][0], P.stored(*ref["dx"], torch.float32), "dx")
+    P.close(dW, ref["dW"][0], P.stored(*ref["dW"], torch.float32), "dW")
+    P.close(db, ref["db"][0], P.stored(*ref["db"], torch.float32), "db")
+    dx[rows] = 0
+    assert not bool(dx.any())
