@@ -31,7 +31,6 @@
 // its dz pass (832 to 880 us), 2047x3072x768 backward 515 (37 us, both products
 // in one launch). 4x7168x2048 9.3 us on the GPU (29 MB of weights).
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "activation.hpp"
@@ -449,68 +448,71 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
 //    hide more LDS latency than the 8 waves of 128x64 save in LDS reads, 1061
 //    against 1018 TFLOP/s at 4096x4096x14336), when they fill the 256 CUs about
 //    once;
-//  - 128x128 tiles, two workgroups of 8 waves per CU, for more than 256 of them
-//    (2048x768x3072 with GELU and z: 22 us, against 28 with the next form; 25
+//  - 128x128 tiles in up to 256 workgroups: one of 8 waves per CU and a ring of
+//    four stages. Alone on its CU a workgroup waits for the latency of its loads,
+//    and three K-steps in flight instead of one take a K-step from 0.83 to 0.6 us;
+//  - 128x128 tiles in more of them: two of 8 waves per CU, two stages
+//    (2048x768x3072 with GELU and z: 22 us, against 28 with the form before; 25
 //    with 4 waves of 64x64, which are 2% faster only from K = 4096 on, where the
-//    epilogue's share is small);
-//  - 128x128 tiles, one workgroup of 8 waves per CU and a ring of four stages,
-//    for up to 256 of them: alone on its CU a workgroup waits for the latency
-//    of its loads, and three K-steps in flight instead of one take a K-step from
-//    0.83 to 0.6 us. The reduction is cut where the model below, in us, gains
-//    from it: K-steps, and for the joining pass its launch and the partials
-//    written and read at 4 TB/s (2048x3072x768: 29 us in 2 ranges, 32 in one;
-//    512x768x3072: 15 us in one, 21 in 2).
+//    epilogue's share is small).
+// On 128x128 tiles the reduction is cut where the model below, in us, gains from
+// it: a workgroup's start and end 3 to 5, a K-step from 0.5 with half of the CUs
+// busy to 0.66 with all and 1.2 with two workgroups on each, the joining launch
+// 4.5 and the partials written and read at 4 TB/s (2048x3072x768: 29 us in 2
+// ranges, 32 in one; 512x768x3072: 15 us in one, 21 in 2). Ranges that put two
+// workgroups on a CU have to gain a quarter, as the model errs most there
+// (2048x14336x1152: 100 us in 3 ranges, 129 in one; 4352x7424x512, where it sees
+// 15%: 70 in 3, 64 in one).
 enum class Tile { k64, k256, k128x2, k128 };
 struct Shape {
     Tile tile;
     int splits;
+    double us;   // modelled time, 128x128 tiles only
 };
 Shape shape_of(int64_t rows, int64_t cols, int64_t K) {
     const int64_t KT = (K + kStep - 1) / kStep;
     if (rows <= 64) {
         const int64_t s = std::min<int64_t>(256 / std::max<int64_t>((cols + 127) / 128, 1), KT / 4);
-        return {Tile::k64, (int)std::min<int64_t>(std::max<int64_t>(s, 1), 16)};
+        return {Tile::k64, (int)std::min<int64_t>(std::max<int64_t>(s, 1), 16), 0};
     }
     if (((rows + 255) / 256) * ((cols + 255) / 256) >= 192)
-        return {Tile::k256, 1};
+        return {Tile::k256, 1, 0};
     const int64_t tiles = ((rows + 127) / 128) * ((cols + 127) / 128);
-    if (tiles > 256)
-        return {Tile::k128x2, 1};
+    auto round = [](int64_t n, double steps) {   // n <= 512 workgroups
+        const double f = (double)n / 256;
+        return n == 0 ? 0 : n <= 256 ? 3 + (0.43 + 0.23 * f) * steps : 5 + (0.11 + 0.55 * f) * steps;
+    };
     auto cost = [&](int64_t s) {
+        const double steps = (double)((KT + s - 1) / s);
         const double join = 4.5 + (double)(s + 1) * (double)(rows * cols) * 4.0 / 4e6;
-        return 0.6 * (double)((KT + s - 1) / s) + (s > 1 ? join : 0.0);
+        const double us = (double)(s * tiles / 512) * round(512, steps) +
+                          round(s * tiles % 512, steps) + (s > 1 ? join : 0.0);
+        return s > 1 && s * tiles > 256 ? 1.25 * us : us;
     };
     int64_t best = 1;
-    for (int64_t s = 2; s <= 16 && s * tiles <= 256 && 4 * s <= KT; ++s)
+    for (int64_t s = 2; s <= 16 && 4 * s <= KT; ++s)
         if (cost(s) < cost(best))
             best = s;
-    return {Tile::k128, (int)best};
+    return {best * tiles > 256 ? Tile::k128x2 : Tile::k128, (int)best, cost(best)};
 }
 // Whether the two products of a backward run as one launch: both on 128x128
-// tiles, and faster so by the times, in us, of a tile (3 and 0.6 a K-step, 0.7
-// where both operands are transposed) and of a split product's joining. Without
-// an activation the pair spares the pass for db (2047x3072x768: 39 us, against 51
-// apart; 8192x1024x1024: 87 us paired, 68 apart). Which gradients are
-// wanted does not enter, so that each has the same bits whatever the others.
+// tiles, and faster so by the same model. Without an activation the pair spares
+// the pass for db (2047x3072x768: 39 us, against 51 apart; 8192x1024x1024: 87 us
+// paired, 68 apart). Which gradients are wanted does not enter, so that each has
+// the same bits whatever the others.
 bool paired(int64_t N, int64_t K, int64_t M, bool act) {
     const Shape x = shape_of(N, K, M), w = shape_of(M, K, N);
     auto small = [](const Shape &s) { return s.tile == Tile::k128 || s.tile == Tile::k128x2; };
     if (!small(x) || !small(w))
         return false;
-    auto steps = [](int64_t k) { return (double)((k + kStep - 1) / kStep); };
+    auto time = [](int64_t k) { return 3 + 0.65 * (double)((k + kStep - 1) / kStep); };
     auto tiles = [](int64_t rows, int64_t cols) {
         return (double)(((rows + 127) / 128) * ((cols + 127) / 128));
     };
-    const double tx = 3 + 0.6 * steps(M), tw = 3 + 0.7 * steps(N);
-    const double nx = tiles(N, K), nw = tiles(M, K);
-    auto alone = [](const Shape &s, double n, double t, double part) {
-        if (s.splits == 1)
-            return std::ceil(n / 256) * t;
-        return 3 + (t - 3) / s.splits + 4.5 + (s.splits + 1) * part / 4e6;
-    };
-    const double pair = std::max(std::max(tx, tw), (nx * tx + nw * tw) / 256 + std::min(tx, tw) / 2);
-    return pair <= alone(x, nx, tx, 4.0 * (double)(N * K)) + alone(w, nw, tw, 4.0 * (double)(M * K)) +
-                       (act ? 0 : 8);
+    const double tx = time(M), tw = time(N);
+    const double pair = std::max(std::max(tx, tw), (tiles(N, K) * tx + tiles(M, K) * tw) / 256 +
+                                                       std::min(tx, tw) / 2);
+    return pair <= x.us + w.us + (act ? 0 : 8);
 }
 size_t part_bytes(int64_t rows, int64_t cols, int64_t K) {
     const Shape sh = shape_of(rows, cols, K);
