@@ -40,6 +40,10 @@ SHAPES = [
     (40, 2056, 1544, "relu", True, True), (64, 4104, 1032, "gelu", False, True),
     (8, 264, 4088, "gelu", True, True), (8, 264, 4096, "relu", True, False),
     (5, 8, 40, "none", False, True), (8, 72, 16, "gelu", True, False),
+    # a last round of 256x256 tiles in halves (of 4 rows the lower one is empty),
+    # and ranges of the reduction that put two workgroups on a CU
+    (4100, 72, 4104, "gelu", True, True), (4612, 200, 4104, "none", True, True),
+    (2100, 14344, 1032, "gelu", True, True),
 ]
 
 
@@ -77,6 +81,8 @@ BACKWARD = [
     (3600, 3592, 136, "relu"), (3333, 3080, 3336, "gelu"),
     # weight gradients of at most 64 rows, over several K-steps
     (129, 8, 8, "none"), (300, 264, 56, "gelu"), (2000, 72, 64, "relu"), (640, 1000, 40, "none"),
+    # halves of the last round in dx and in dW, ranges with two workgroups a CU in dW
+    (4100, 4104, 72, "gelu"), (72, 4104, 4104, "relu"), (15000, 1032, 2056, "none"),
 ]
 
 
