@@ -197,8 +197,8 @@ size_t moe_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k,
                           float capacity_factor, int32_t dtype);
 
 /* Per-expert capacity C = ceil(capacity_factor * k * N / E), in double
- * (nanoMoE slide 14, get_capacity of the call's token count). -1 on
- * invalid arguments; 0 when N = 0. */
+ * (nanoMoE slide 14, get_capacity of the call's token count), INT64_MAX
+ * where that passes 64 bits. -1 on invalid arguments; 0 when N = 0. */
 int64_t moe_capacity(int64_t N, int64_t E, int k, float capacity_factor);
 
 /* Static description of a return code. */

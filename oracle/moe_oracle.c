@@ -97,7 +97,8 @@ int64_t oracle_capacity(int64_t N, int64_t E, int32_t k, double cf)
 {
     if (N <= 0)
         return 0;
-    return (int64_t)ceil(cf * (double)((int64_t)k * N) / (double)E);
+    double c = ceil(cf * (double)((int64_t)k * N) / (double)E);
+    return c < 0x1p63 ? (int64_t)c : INT64_MAX;
 }
 
 /* [P2 slides 14-23] slot of each assignment: its rank among the assignments

@@ -26,7 +26,9 @@ bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int64_t capacity_of(int64_t N, int64_t E, int k, float cf) {
     if (N <= 0)
         return 0;
-    return (int64_t)ceil((double)cf * (double)((int64_t)k * N) / (double)E);
+    // (a factor that stands for "no limit" may pass 64 bits)
+    const double c = ceil((double)cf * (double)((int64_t)k * N) / (double)E);
+    return c < 0x1p63 ? (int64_t)c : INT64_MAX;
 }
 
 // Sizes of one call, as validated.
