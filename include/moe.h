@@ -534,7 +534,8 @@ size_t moe_linear_backward_workspace_size(int64_t N, int64_t K, int64_t M, int32
  *   mean, rstd  [N] MOE_F32 or NULL: what the backward needs
  * Statistics are fp32, of the values h holds after its rounding. out or h may
  * be the buffer of x or of residual (each element is read before it is
- * written), but must not overlap each other, or one of those any other way
+ * written), but must not overlap each other, or one of those any other way;
+ * nor may mean or rstd overlap any tensor, or h or out weight or bias
  * (MOE_ERR_ARG). d <= MOE_NORM_MAX_WIDTH;
  * bf16 rows need d % 8 == 0 (MOE_ERR_UNSUPPORTED) and 16-byte aligned x,
  * residual, h, out, weight and bias (MOE_ERR_ALIGN); fp32 rows any d. */
@@ -549,8 +550,8 @@ int moe_layer_norm(const moe_tensor *x, const moe_tensor *residual, const moe_te
  *   dweight = sum over rows of dout xh, dbias = sum over rows of dout
  * x is the h of the forward (or its x without a residual); with a residual
  * dx is the gradient of both summands. dx, dout and dres have x's shape and
- * dtype (dx may be the buffer of dout or dres, but must not overlap them
- * another way, or x: MOE_ERR_ARG);
+ * dtype. dx may be the buffer of dout or dres; otherwise no output, nor the
+ * workspace, may overlap an input, another output or each other (MOE_ERR_ARG).
  * weight, dweight and dbias [d], mean and rstd [N] MOE_F32; dbias may be
  * NULL. Sums are fp32 in a fixed order. workspace: device scratch of
  * moe_layer_norm_backward_workspace_size() bytes, 256-byte aligned. Widths

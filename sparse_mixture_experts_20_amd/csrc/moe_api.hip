@@ -1400,6 +1400,20 @@ bool overlap(Span a, Span b) {
 }
 // Whether a shares bytes with b other than by being the same buffer.
 bool crosses(Span a, Span b) { return a.p != b.p && overlap(a, b); }
+// Whether any of the written buffers w shares bytes with another, or with one
+// of the read buffers r.
+template <size_t W, size_t R>
+bool collide(const Span (&w)[W], const Span (&r)[R]) {
+    for (size_t i = 0; i < W; ++i) {
+        for (size_t j = i + 1; j < W; ++j)
+            if (overlap(w[i], w[j]))
+                return true;
+        for (const Span &b : r)
+            if (overlap(w[i], b))
+                return true;
+    }
+    return false;
+}
 
 }  // namespace
 
@@ -1439,6 +1453,9 @@ int moe_layer_norm(const moe_tensor *x, const moe_tensor *residual, const moe_te
     for (const Span &i : in)
         if (crosses(to[0], i) || crosses(to[1], i))
             return MOE_ERR_ARG;
+    const Span rows[2] = {{mp, 4 * N}, {rp, 4 * N}}, vecs[2] = {{w, 4 * d}, {b, 4 * d}};
+    if (collide(rows, in) || collide(rows, to) || collide(rows, vecs) || collide(to, vecs))
+        return MOE_ERR_ARG;
     return hip_status(moe::launch_layer_norm(bf16, bf16 || (al && d % 4 == 0), x->data, r, w, b,
                                              eps, N, d, hp, op, const_cast<float *>(mp),
                                              const_cast<float *>(rp),
@@ -1496,6 +1513,13 @@ int moe_layer_norm_backward(const moe_tensor *x, const moe_tensor *weight, const
     const int64_t bytes = N * d * (bf16 ? 2 : 4);
     const Span to{dxp, bytes};
     if (overlap(to, {x->data, bytes}) || crosses(to, {g, bytes}) || crosses(to, {r, bytes}))
+        return MOE_ERR_ARG;
+    const int64_t scratch = (int64_t)moe::layer_norm_backward_bytes(N, d);
+    const Span written[4] = {to, {dw, 4 * d}, {db, 4 * d}, {workspace, scratch}};
+    const Span vecs[3] = {{w, 4 * d}, {m, 4 * N}, {rs, 4 * N}};
+    const Span apart[3] = {written[1], written[2], written[3]};
+    const Span rows[3] = {{x->data, bytes}, {g, bytes}, {r, bytes}};
+    if (collide(written, vecs) || collide(apart, rows))
         return MOE_ERR_ARG;
     return hip_status(moe::launch_layer_norm_backward(
         bf16, bf16 || (al && d % 4 == 0), x->data, w, m, rs, g, r, N, d, dxp,

@@ -1,0 +1,60 @@
+"""Calls whose buffers overlap where a kernel reads or writes them at once are
+refused on the host, before anything is enqueued (the pointers here are never
+dereferenced); the calls that may share a buffer are not."""
+import pytest
+
+from sparse_mixture_experts_20_amd import binding as B
+from tests.test_abi_block import ARG, BF16, F32, t
+
+P = 1 << 30     # apart from each other by more than any buffer here
+
+
+@pytest.fixture(scope="module")
+def L():
+    return B.lib()
+
+
+def _near(base, n, m):
+    """Starts of a buffer of m bytes that shares bytes with the n bytes at base."""
+    return {base, base + max(n, 256) - 256, base - max(m, 256) + 256}
+
+
+def _norm(L, p, N=64, d=4096):
+    return L.moe_layer_norm(t(BF16, N, d, ptr=p["x"]), t(BF16, N, d, ptr=p["r"]),
+                            t(F32, d, ptr=p["w"]), t(F32, d, ptr=p["b"]), 1e-5,
+                            t(BF16, N, d, ptr=p["h"]), t(BF16, N, d, ptr=p["out"]),
+                            t(F32, N, ptr=p["mean"]), t(F32, N, ptr=p["rstd"]), None)
+
+
+def test_layer_norm(L):
+    own = {n: (i + 1) * P for i, n in enumerate(("x", "r", "w", "b", "h", "out", "mean", "rstd"))}
+    size = dict(x=64 * 8192, r=64 * 8192, w=4 * 4096, b=4 * 4096, h=64 * 8192, out=64 * 8192,
+                mean=256, rstd=256)
+    for a in ("mean", "rstd", "h", "out"):
+        for b in own:
+            if a == b or (a in ("h", "out") and b in ("x", "r")):
+                continue
+            for where in _near(own[b], size[b], size[a]):
+                assert _norm(L, {**own, a: where}) == ARG, (a, b, where - own[b])
+
+
+def _normb(L, p, N=64, d=4096):
+    return L.moe_layer_norm_backward(
+        t(BF16, N, d, ptr=p["x"]), t(F32, d, ptr=p["w"]), t(F32, N, ptr=p["mean"]),
+        t(F32, N, ptr=p["rstd"]), t(BF16, N, d, ptr=p["g"]), t(BF16, N, d, ptr=p["r"]),
+        t(BF16, N, d, ptr=p["dx"]), t(F32, d, ptr=p["dw"]), t(F32, d, ptr=p["db"]), p["ws"],
+        1 << 40, None)
+
+
+def test_layer_norm_backward(L):
+    names = ("x", "w", "mean", "rstd", "g", "r", "dx", "dw", "db", "ws")
+    own = {n: (i + 1) * P for i, n in enumerate(names)}
+    size = {n: 64 * 8192 for n in ("x", "g", "r", "dx")}
+    size.update(w=4 * 4096, dw=4 * 4096, db=4 * 4096, mean=256, rstd=256,
+                ws=L.moe_layer_norm_backward_workspace_size(64, 4096))
+    for a in ("dx", "dw", "db", "ws"):
+        for b in names:
+            if a == b or (a == "dx" and b in ("g", "r")):
+                continue
+            for where in _near(own[b], size[b], size[a]):
+                assert _normb(L, {**own, a: where}) == ARG, (a, b, where - own[b])
