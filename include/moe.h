@@ -464,7 +464,8 @@ size_t moe_backward_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff
  * its own rounding; each token's choices are added in a fixed order.
  * stats->workspace holds moe_few_workspace_size() bytes (256-byte aligned;
  * a size for more tokens serves fewer). Bias data 16-byte aligned, as there.
- * out must not overlap x. */
+ * Neither out, the workspace nor an export may overlap an input or one of each
+ * other (MOE_ERR_ARG). */
 int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
                     const moe_tensor *W_up, const moe_tensor *W_down,
                     const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,

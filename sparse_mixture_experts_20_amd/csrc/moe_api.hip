@@ -1240,6 +1240,32 @@ static int forward_state(const BwdLayout &L, char *ws, const moe_tensor *x,
 // ---------------------------------------------------------------------------
 namespace {
 
+// Bytes [p, p + n) of a buffer (none where p is NULL).
+struct Span {
+    const void *p;
+    int64_t n;
+};
+bool overlap(Span a, Span b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+// Whether a shares bytes with b other than by being the same buffer.
+bool crosses(Span a, Span b) { return a.p != b.p && overlap(a, b); }
+// Whether any of the written buffers w shares bytes with another, or with one
+// of the read buffers r.
+template <size_t W, size_t R>
+bool collide(const Span (&w)[W], const Span (&r)[R]) {
+    for (size_t i = 0; i < W; ++i) {
+        for (size_t j = i + 1; j < W; ++j)
+            if (overlap(w[i], w[j]))
+                return true;
+        for (const Span &b : r)
+            if (overlap(w[i], b))
+                return true;
+    }
+    return false;
+}
+
 // Widths whose tiles fit the grid's second dimension and 32-bit counts.
 bool few_fits(const Dims &m) {
     return m.d <= MOE_FEW_MAX_WIDTH && m.d_ff <= MOE_FEW_MAX_WIDTH;
@@ -1318,8 +1344,24 @@ int moe_forward_few(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor
         (!aligned(W_up->data, 16) || !aligned(W_down->data, 16) || !aligned(out->data, 16)))
         return MOE_ERR_ALIGN;
     const bool bf16 = x->dtype == MOE_BF16;
-    if (stats->workspace_bytes < moe::few_layout(bf16, N, d, E, d_ff, k).total)
+    const int64_t scratch = (int64_t)moe::few_layout(bf16, N, d, E, d_ff, k).total;
+    if (stats->workspace_bytes < (size_t)scratch)
         return MOE_ERR_WORKSPACE;
+    const int64_t el = bf16 ? 2 : 4;
+    const Span written[9] = {{out->data, N * d * el},         {stats->workspace, scratch},
+                             {stats->topk_idx, 4 * N * k},    {stats->topk_gate, 4 * N * k},
+                             {stats->slot, 4 * N * k},        {stats->used_capacity, 4 * E},
+                             {stats->expert_demand, 4 * E},   {stats->expert_drops, 4 * E},
+                             {stats->expert_gate_sum, 4 * E}};
+    const Span read[7] = {{x->data, N * d * el},
+                          {W_g->data, 4 * E * d},
+                          {noise ? noise->data : nullptr, 4 * N * E},
+                          {W_up->data, E * d * d_ff * el},
+                          {W_down->data, E * d * d_ff * el},
+                          {o.b_up, 4 * E * d_ff},
+                          {o.b_down, 4 * E * d}};
+    if (collide(written, read))
+        return MOE_ERR_ARG;
     stats->capacity = m.C;
     const bool al = aligned(x->data, 16) && aligned(W_g->data, 16) && aligned(W_up->data, 16) &&
                     aligned(W_down->data, 16);
@@ -1388,32 +1430,6 @@ int check_norm_x(const moe_tensor *x, int64_t &N, int64_t &d) {
 
 template <typename... P>
 bool all_aligned16(P... p) { return (aligned(p, 16) && ...); }
-
-// Bytes [p, p + n) of a buffer (none where p is NULL).
-struct Span {
-    const void *p;
-    int64_t n;
-};
-bool overlap(Span a, Span b) {
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
-}
-// Whether a shares bytes with b other than by being the same buffer.
-bool crosses(Span a, Span b) { return a.p != b.p && overlap(a, b); }
-// Whether any of the written buffers w shares bytes with another, or with one
-// of the read buffers r.
-template <size_t W, size_t R>
-bool collide(const Span (&w)[W], const Span (&r)[R]) {
-    for (size_t i = 0; i < W; ++i) {
-        for (size_t j = i + 1; j < W; ++j)
-            if (overlap(w[i], w[j]))
-                return true;
-        for (const Span &b : r)
-            if (overlap(w[i], b))
-                return true;
-    }
-    return false;
-}
 
 }  // namespace
 
