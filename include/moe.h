@@ -489,8 +489,8 @@ size_t moe_few_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int
  *   z        [N, M] MOE_BF16 or NULL: the pre-activations, for the backward
  *            (a buffer of its own: MOE_ERR_ARG)
  * fp32 accumulation, bias, activation and residual; out and z are each rounded
- * once. Otherwise out and z must not overlap an input or each other
- * (MOE_ERR_ARG). K and M are multiples of 8 and N, K, M at
+ * once. Otherwise out, z and the workspace must not overlap an input or each
+ * other (MOE_ERR_ARG). K and M are multiples of 8 and N, K, M at
  * most MOE_LINEAR_MAX_EXTENT (MOE_ERR_UNSUPPORTED); data 16-byte aligned
  * (MOE_ERR_ALIGN). workspace: device scratch of moe_linear_workspace_size()
  * bytes, 256-byte aligned (may be NULL when that is 0): fp32 partial products
@@ -509,7 +509,8 @@ size_t moe_linear_workspace_size(int64_t N, int64_t K, int64_t M);
  * MOE_BF16 or MOE_F32, dbias [M] MOE_F32; each may be NULL and is then not
  * computed (all three NULL: MOE_ERR_NULL). The products read dz rounded once
  * to bf16 (the dz of MOE_ACT_NONE is dout, exactly); dbias sums the fp32
- * values. No output may overlap an input or another output (MOE_ERR_ARG). Each
+ * values. No output, nor the workspace, may overlap an input, another output or
+ * each other (MOE_ERR_ARG). Each
  * gradient has the same bits whichever others are computed with it. Widths and
  * alignment as moe_linear's. workspace:
  * moe_linear_backward_workspace_size() bytes, 256-byte aligned. N = 0: dW and

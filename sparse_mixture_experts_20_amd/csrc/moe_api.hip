@@ -1625,6 +1625,10 @@ int moe_linear(const moe_tensor *x, const moe_tensor *W, const moe_tensor *bias,
     for (const Span &i : {Span{x->data, 2 * N * K}, Span{W->data, 2 * M * K}, Span{b, 4 * M}})
         if (overlap(so, i) || overlap(sz, i))
             return MOE_ERR_ARG;
+    const Span scratch[1] = {{workspace, (int64_t)moe::linear_bytes(N, K, M)}};
+    const Span all[6] = {{x->data, 2 * N * K}, {W->data, 2 * M * K}, {b, 4 * M}, so, sz, sr};
+    if (collide(scratch, all))
+        return MOE_ERR_ARG;
     return hip_status(moe::launch_linear(x->data, W->data, b, activation, r, N, K, M, o, zp,
                                          workspace, static_cast<hipStream_t>(stream)));
 }
@@ -1697,6 +1701,11 @@ int moe_linear_backward(const moe_tensor *x, const moe_tensor *W, const moe_tens
             if (overlap(o, i))
                 return MOE_ERR_ARG;
     if (overlap(to[0], to[1]) || overlap(to[0], to[2]) || overlap(to[1], to[2]))
+        return MOE_ERR_ARG;
+    const Span scratch[1] = {
+        {workspace,
+         (int64_t)moe::linear_backward_layout(N, K, M, activation != MOE_ACT_NONE).total}};
+    if (collide(scratch, in) || collide(scratch, to))
         return MOE_ERR_ARG;
     return hip_status(moe::launch_linear_backward(
         x->data, W->data, zp, activation, g, N, K, M, dxp, dx && dx->dtype == MOE_F32, dWp,

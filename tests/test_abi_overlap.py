@@ -89,3 +89,28 @@ def test_few(L):
             if a != b:
                 for where in _near(own[b], size[b], size[a]):
                     assert _few(L, {**own, a: where}) == ARG, (a, b, where - own[b])
+
+
+def test_linear_workspaces(L):
+    N, K, M = 128, 4096, 128
+    n = L.moe_linear_workspace_size(N, K, M)
+    size = dict(x=2 * N * K, W=2 * M * K, b=4 * M, r=2 * N * M, out=2 * N * M, z=2 * N * M)
+    own = {a: (i + 1) * P for i, a in enumerate(size)}
+    assert n > 0
+    for b in size:
+        for ws in _near(own[b], size[b], n):
+            assert L.moe_linear(t(BF16, N, K, ptr=own["x"]), t(BF16, M, K, ptr=own["W"]),
+                                t(F32, M, ptr=own["b"]), B.MOE_ACT_GELU,
+                                t(BF16, N, M, ptr=own["r"]), t(BF16, N, M, ptr=own["out"]),
+                                t(BF16, N, M, ptr=own["z"]), ws, n, None) == ARG, (b, ws - own[b])
+    n = L.moe_linear_backward_workspace_size(N, K, M, B.MOE_ACT_GELU)
+    size = dict(x=2 * N * K, W=2 * M * K, z=2 * N * M, g=2 * N * M, dx=4 * N * K, dW=4 * M * K,
+                db=4 * M)
+    own = {a: (i + 1) * P for i, a in enumerate(size)}
+    for b in size:
+        for ws in _near(own[b], size[b], n):
+            assert L.moe_linear_backward(
+                t(BF16, N, K, ptr=own["x"]), t(BF16, M, K, ptr=own["W"]),
+                t(BF16, N, M, ptr=own["z"]), B.MOE_ACT_GELU, t(BF16, N, M, ptr=own["g"]),
+                t(F32, N, K, ptr=own["dx"]), t(F32, M, K, ptr=own["dW"]), t(F32, M, ptr=own["db"]),
+                ws, n, None) == ARG, (b, ws - own[b])
