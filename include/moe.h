@@ -504,7 +504,8 @@ size_t moe_linear_workspace_size(int64_t N, int64_t K, int64_t M);
 
 /* Its backward, for dout [N, M] MOE_BF16 the gradient of out:
  *   dz = dout act'(z),  dx = dz W,  dW = dz^T x,  dbias = sum of the dz rows
- * (the residual's gradient is dout itself). z: the forward's, required with an
+ * (the residual's gradient is dout itself; act' of MOE_ACT_RELU is 0 where
+ * z <= 0 and 1 elsewhere, a NaN included). z: the forward's, required with an
  * activation, NULL without one (MOE_ERR_ARG). dx [N, K] and dW [M, K] are
  * MOE_BF16 or MOE_F32, dbias [M] MOE_F32; each may be NULL and is then not
  * computed (all three NULL: MOE_ERR_NULL). The products read dz rounded once

@@ -408,9 +408,11 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
                 for (int i = 0; i < 4; ++i) {
                     const float zl = __uint_as_float(zr[i] << 16);
                     const float zh = __uint_as_float(zr[i] & 0xffff0000u);
-                    if (act == kActRelu) {   // a choice, so that a masked infinity gives 0
-                        v[2 * i] = zl > 0.f ? v[2 * i] : 0.f;
-                        v[2 * i + 1] = zh > 0.f ? v[2 * i + 1] : 0.f;
+                    if (act == kActRelu) {
+                        // a choice, so that a masked infinity gives 0; a NaN in z,
+                        // which the forward keeps, does not mask
+                        v[2 * i] = zl <= 0.f ? 0.f : v[2 * i];
+                        v[2 * i + 1] = zh <= 0.f ? 0.f : v[2 * i + 1];
                     } else {
                         v[2 * i] *= act_gelu_grad(zl);
                         v[2 * i + 1] *= act_gelu_grad(zh);
