@@ -159,7 +159,9 @@ int moe_forward(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *no
  * projection and GELU between them) for moe_forward_ex and moe_experts_ex.
  * activation: MOE_ACT_RELU (page 1 STEP 9) or MOE_ACT_GELU, x * Phi(x) with
  * Phi the standard normal distribution function (erf form), evaluated in
- * fp32 before H is rounded; MOE_ERR_ARG for any other value.
+ * fp32 before H is rounded (by a formula within 2.2e-7 of x Phi(x), besides
+ * fp32 rounding; an absolute bound: the far negative tail is not as close
+ * relative to its size); MOE_ERR_ARG for any other value.
  * b_up:   [E, d_ff] MOE_F32 added to W_up[e] x before the activation, or NULL
  * b_down: [E, d]    MOE_F32 added to W_down[e] h, or NULL
  * Bias data are device pointers, 16-byte aligned (MOE_ERR_ALIGN), checked
@@ -461,7 +463,10 @@ size_t moe_backward_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff
  * moe_forward's (scores differ from its only in fp32 summation order), except
  * that a bf16 layer keeps the hidden activation to 16 significant bits (two
  * bf16 terms) and the experts' output rows in fp32, so that out carries only
- * its own rounding; each token's choices are added in a fixed order.
+ * its own rounding (an infinite weight in W_down meets both terms: where
+ * moe_forward gives an infinity, out may be NaN); GELU of -inf is 0 (there:
+ * NaN) and ReLU keeps a NaN (there: 0); each token's choices are added in a
+ * fixed order.
  * stats->workspace holds moe_few_workspace_size() bytes (256-byte aligned;
  * a size for more tokens serves fewer). Bias data 16-byte aligned, as there.
  * Neither out, the workspace nor an export may overlap an input or one of each

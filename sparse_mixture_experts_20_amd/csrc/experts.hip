@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "activation.hpp"
 #include "common.hpp"
 
 namespace moe {
@@ -94,41 +95,8 @@ __device__ __forceinline__ v4i16 lds_read_tr16(const void *p) {
         (__attribute__((address_space(3))) v4i16 *)(p));
 }
 
-// GELU of the nanoMoE slides' expert (slide 32): z * Phi(z), Phi(z) =
-// (1 + erf(z / sqrt 2)) / 2, with erf from Abramowitz and Stegun, Handbook of
-// Mathematical Functions, formula 7.1.26: for u >= 0,
-// 1 - erf(u) = (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-u^2),
-// t = 1 / (1 + p u), with absolute error below 1.5e-7 (far below the bf16
-// rounding of H that follows). For z < 0 the complement is used directly, so
-// small GELU values keep their relative accuracy.
-__device__ __forceinline__ float gelu(float z) {
-    const float u = fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, u, 1.0f));
-    const float poly =
-        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f),
-                         -0.284496736f),
-                 0.254829592f);
-    const float q = poly * __expf(-u * u);   // 1 - erf(u)
-    return 0.5f * z * (z >= 0.f ? 2.0f - q : q);
-}
-
-// Its derivative Phi(z) + z phi(z): Phi from the same erf approximation,
-// phi(z) = exp(-z^2 / 2) / sqrt(2 pi) from the same exponential.
-__device__ __forceinline__ float gelu_grad(float z) {
-    const float u = fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, u, 1.0f));
-    const float poly =
-        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f),
-                         -0.284496736f),
-                 0.254829592f);
-    const float ex = __expf(-u * u);         // exp(-z^2 / 2)
-    const float q = poly * ex;               // 1 - erf(u)
-    const float Phi = 0.5f * (z >= 0.f ? 2.0f - q : q);
-    return fmaf(z * 0.39894228040143268f, ex, Phi);
-}
-
-// Expert activation: ReLU (page 1 STEP 9) or GELU, chosen at compile time so
-// that the ReLU epilogue carries no trace of the other.
+// Expert activation: ReLU (page 1 STEP 9) or GELU (nanoMoE slide 32), chosen at
+// compile time so that the ReLU epilogue carries no trace of the other.
 template <bool GELU>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (GELU)

@@ -74,7 +74,7 @@ __device__ __forceinline__ uint64_t wave_max_key(uint64_t x) {
 }
 
 // Top-k of one token's scores held by a whole wave (lane g holds experts g,
-// g+64, ...), as topk_softmax_group below for G = 64: every round takes the
+// g+64, ...), as the router's ranking by groups of lanes does: every round takes the
 // wave's largest ranking key by DPP moves (no LDS shuffles) and the softmax
 // sums the kept choices' terms in choice order from uniform reads.
 template <int Q>
