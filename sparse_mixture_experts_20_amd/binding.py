@@ -871,7 +871,8 @@ class FewLayer:
     ``moe_forward_few`` on the current stream and returns ``(out, Stats)``.
     Calls share the workspace and the routing buffers, so they must not overlap
     (calls on one stream do not; between streams, order them with events);
-    ``out`` is a new tensor unless given."""
+    ``out`` is a new tensor unless given. The routing in a returned ``Stats`` is
+    the layer's own buffers: valid until the next call."""
 
     def __init__(self, W_g, W_up, W_down, k, capacity_factor, act="relu", b_up=None, b_down=None,
                  max_tokens=MOE_FEW_MAX_TOKENS, export=False, router_stats=False):
@@ -916,8 +917,9 @@ class FewLayer:
         if out is None:
             out = torch.empty_like(x)
         index, w, st = self.index, self._w, self.stats
-        st.stream = _stream_of(index)
-        if st.stream != self._home:
+        handle = _stream_of(index)   # (a ctypes field reads a handle of 0 back as None)
+        st.stream = handle
+        if handle != self._home:
             # keep the buffers until that stream is done, should the layer go first
             s = torch.cuda.current_stream(index)
             for b in (self.workspace, *self._routing, *self._counts):
