@@ -870,7 +870,9 @@ class FewLayer:
     ``max_tokens`` tokens; ``layer(x, noise=None, out=None)`` runs
     ``moe_forward_few`` on the current stream and returns ``(out, Stats)``.
     Calls share the workspace and the routing buffers, so they must not overlap
-    (calls on one stream do not; between streams, order them with events);
+    (calls on one stream do not; between streams, order them with events).
+    The layer keeps the memory of the weights it was given: it sees updates in
+    place, and not memory that a tensor is given later (``W.data = ...``).
     ``out`` is a new tensor unless given. The routing in a returned ``Stats`` is
     the layer's own buffers: valid until the next call."""
 
@@ -878,7 +880,9 @@ class FewLayer:
                  max_tokens=MOE_FEW_MAX_TOKENS, export=False, router_stats=False):
         E, d_ff, d = W_up.shape
         dev, index = W_up.device, _device_of(W_up)
-        self.tensors = (W_g, W_up, W_down, b_up, b_down)
+        # the memory that the descriptors point at, whatever becomes of the tensors
+        self.tensors = tuple(t if t is None else t.detach() for t in
+                             (W_g, W_up, W_down, b_up, b_down))
         self.k, self.cf, self.max_tokens, self.index = k, capacity_factor, max_tokens, index
         n = few_workspace_size(max_tokens, d, E, d_ff, k, capacity_factor, W_up.dtype)
         if n == 0:

@@ -48,3 +48,16 @@ def test_buffers_are_recorded_on_other_streams_only(host, home):
     host.stream = home
     layer(x)
     assert host.used == []
+
+
+def test_weights_stay_when_a_tensor_is_given_other_memory(host):
+    import torch
+    w, layer = _layer(act="gelu", b_up=torch.zeros(4, 24), b_down=torch.zeros(4, 16))
+    held = [t.data_ptr() for t in layer.tensors]
+    assert held[:3] == [t.data_ptr() for t in w]
+    for t in w:
+        t.data = torch.ones_like(t)
+    assert [t.data_ptr() for t in layer.tensors] == held
+    # what the descriptors hold: the pointer is a moe_tensor's first field
+    assert [int.from_bytes(d[:8], "little") for d in layer._w] == held[:3]
+    assert not any(bool(t.any()) for t in layer.tensors)
