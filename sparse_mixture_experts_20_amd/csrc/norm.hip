@@ -505,6 +505,22 @@ hipError_t launch_layer_norm_backward(bool bf16, bool vec, const void *x, const 
 
 hipError_t launch_column_sums(const float *part, int P, int64_t ld, int64_t d, float *a, float *b,
                               hipStream_t s) {
+    // a launch has fewer than 2^32 threads: wider sums (the bias gradient of 2^28
+    // neurons) go in several
+    constexpr int64_t most = (int64_t)1 << 27;
+    if (d > most) {
+        for (int64_t c = 0; c < d; c += most)
+            for (float *o : {a, b}) {
+                if (!o)
+                    continue;
+                const hipError_t err =
+                    launch_column_sums(part + (o == b ? d : 0) + c, P, ld,
+                                       d - c < most ? d - c : most, o + c, nullptr, s);
+                if (err != hipSuccess)
+                    return err;
+            }
+        return hipSuccess;
+    }
     hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((d + 63) / 64), b ? 2u : 1u),
                        dim3(kSumGroups * 64), 0, s, part, P, (int)ld, (int)d, a, b);
     return hipGetLastError();

@@ -1,5 +1,5 @@
 """moe_linear and moe_linear_backward at values where a check of magnitudes
-would not tell a fault: NaN."""
+would not tell a fault: NaN, and the largest extents."""
 import pytest
 
 from tests import _gpu as G
@@ -38,3 +38,18 @@ def test_relu_gradient_where_z_is_nan(torch_mod):
     # one term per element: W and x are cut from the identity
     assert torch.equal(dx, want[:, :K])
     assert torch.equal(dW, want[:K].t())
+
+
+def test_bias_gradient_of_the_widest_product(torch_mod):
+    """M = 2^28 neurons, the most that is taken: sums of small whole numbers."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    bf = torch.bfloat16
+    M = 1 << 28
+    G.say(f"[linear backward] db of M={M}")
+    x = torch.zeros((3, 8), dtype=bf, device="cuda")
+    W = torch.empty((M, 8), dtype=bf, device="cuda")
+    dout = torch.randint(-8, 9, (3, M), device="cuda", dtype=torch.int8).to(bf)
+    _, _, db = B.linear_backward(x, W, None, dout, need_dx=False, need_dW=False)
+    torch.cuda.synchronize()
+    assert torch.equal(db, dout[0].float() + dout[1].float() + dout[2].float())
