@@ -514,7 +514,8 @@ size_t moe_linear_workspace_size(int64_t N, int64_t K, int64_t M);
  * activation, NULL without one (MOE_ERR_ARG). dx [N, K] and dW [M, K] are
  * MOE_BF16 or MOE_F32, dbias [M] MOE_F32; each may be NULL and is then not
  * computed (all three NULL: MOE_ERR_NULL). The products read dz rounded once
- * to bf16 (the dz of MOE_ACT_NONE is dout, exactly); dbias sums the fp32
+ * to bf16 (the dz of MOE_ACT_NONE is dout, exactly), so that with an activation
+ * an MOE_F32 dx or dW carries that rounding too; dbias sums the fp32
  * values. No output, nor the workspace, may overlap an input, another output or
  * each other (MOE_ERR_ARG). Each
  * gradient has the same bits whichever others are computed with it. Widths and

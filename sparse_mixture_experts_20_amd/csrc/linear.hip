@@ -6,7 +6,10 @@
 //   backward: dz = dout act'(z),  dx = dz W,  dW = dz^T x,  db = sum of dz rows
 //
 // bf16 operands, fp32 accumulation. dz is rounded to bf16 once, as the operand
-// of the two matrix products (they run on the bf16 matrix cores); db sums the
+// of the two matrix products (they run on the bf16 matrix cores; a second term
+// would double them): dx and dW carry that rounding, whatever type they are stored
+// in (4096x4096x14336 with GELU and bf16 gradients: 0.0024 from the float64
+// result in the 2-norm, where the storage alone is 0.0017). db sums the
 // fp32 values before that rounding. Without an activation dz is dout itself.
 //
 // Few rows and a small W: bound by latency, run on the skinny core
@@ -464,7 +467,11 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const unsigned short *__
 // ranges, 32 in one; 512x768x3072: 15 us in one, 21 in 2). Ranges that put two
 // workgroups on a CU have to gain a quarter, as the model errs most there
 // (2048x14336x1152: 100 us in 3 ranges, 129 in one; 4352x7424x512, where it sees
-// 15%: 70 in 3, 64 in one).
+// 15%: 70 in 3, 64 in one). At most 16 ranges: the joining launch walks them in
+// order, so a small gradient over many rows gains from more only where they are
+// very many (64x64 weight gradient, 16 against up to 64 ranges: over 16384 rows
+// 15.9 and 22.1 us, over 65536 38.0 and 37.2, over 262144 124 and 79; 256x128 over
+// 16384 22.7 and 38.1).
 enum class Tile { k64, k256, k128x2, k128 };
 struct Shape {
     Tile tile;
@@ -577,7 +584,14 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // Whether a forward product runs on the skinny kernel: up to 16 rows and 32 MB
 // of weights, or up to 64 rows and 4 MB. Beyond, the tiled kernel's stream is
 // faster (1x4096x14336: 24 against 34 us; 64x7168x2048: 19 against 35 us), below
-// its joining launch costs more (16x1024x1024: 6 against 9 us).
+// its joining launch costs more (16x1024x1024: 5.1 against 9.6 us; 64x1024x1024:
+// 7.9 against 11; 16x4096x512: 10.9 against 12.5; 8x8192x512: 11.3 against 13.9;
+// 4x7168x2048: 10.7 against 16). The rule sees K M and not K, which the skinny
+// kernel never cuts over workgroups: a narrow product with a long reduction is
+// slower on it, with 16 rows from about K = 6000 on (16x8192x512: 17.9 against
+// 14.1 us; 16x16384x256: 31.6 against 17.3), with 64 from about 2048 on
+// (64x2048x1024: 12.8 against 12.7; 64x4096x512: 21.8 against 14.5; 32x8192x256:
+// 25.7 against 14.3).
 static bool skinny(int64_t N, int64_t K, int64_t M) {
     return N <= kFewMaxTokens && K * M <= ((int64_t)(N <= 16 ? 16 : 2) << 20);
 }

@@ -179,8 +179,11 @@ struct TileProduct {
                 wait_loads<0>();
             barrier_lds();
             // (with transposing reads the next copies go out behind the first reads
-            // of the step, which the copies' issue would hold up: 4096x4096x14336
-            // GELU backward 882 -> 832 us; row by row it makes no difference)
+            // of the step, which the copies' issue would hold up. Both forms timed in
+            // turn, behind and before: GELU backward 4096x4096x14336 847 and 918 us,
+            // 8192x2048x7168 471 and 532, 16384x768x3072 263 and 255; 2047x3072x768
+            // 38.2 and 39.1. Row by row there is no difference: 4096x4096x14336
+            // forward 419 and 423 us, 8192x2048x7168 224 and 223)
             if (!BT && kt + S - 1 < ke)
                 issue(kt + S - 1);
             if (kt == KT - 1 && K % kStep != 0) {
