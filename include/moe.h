@@ -574,6 +574,90 @@ int moe_layer_norm_backward(const moe_tensor *x, const moe_tensor *weight, const
 /* Bytes of scratch of moe_layer_norm_backward (0 for N = 0 or invalid sizes). */
 size_t moe_layer_norm_backward_workspace_size(int64_t N, int64_t d);
 
+/* ---------------------------------------------------------------------------
+ * Weights of 4 bits with group scales, for decoding: the linear product and
+ * the routed experts for up to MOE_FEW_MAX_TOKENS rows. Same conventions as
+ * above.
+ * ------------------------------------------------------------------------- */
+
+/* A matrix (or E matrices) of 4-bit weights,
+ *   w[.., m, k] = (q[.., m, k] - zero[.., m, k / group]) scale[.., m, k / group]
+ *   data   [.., M, K / 2] bytes: q of columns 2i and 2i + 1 in the low and the
+ *          high half of byte i
+ *   scale  [.., M, K / group] bf16
+ *   zero   [.., M, K / group] bf16, or NULL: 8 everywhere
+ *   group  32, 64 or 128 (MOE_ERR_UNSUPPORTED otherwise); K % group == 0
+ *          (MOE_ERR_SHAPE)
+ *   ndim   2 ([M, K]) or 3 ([E, M, K]), and shape, the logical extents
+ * Device pointers of the caller; data 16-byte, scale and zero 2-byte aligned
+ * (MOE_ERR_ALIGN). */
+typedef struct {
+    void *data;
+    void *scale;
+    void *zero;
+    int32_t group;
+    int32_t ndim;      /* 2 or 3 */
+    int64_t shape[3];
+} moe_q4;
+
+/* Nearest 4-bit weights of W (MOE_F32 or MOE_BF16, finite, the extents of q,
+ * 16-byte aligned) into q's buffers, group by group. Without q->zero: scale =
+ * max |w| / 7 rounded to bf16, q = 8 + the nearest integer to w / scale in
+ * [-8, 7]. With it: the range [min(w, 0), max(w, 0)], scale = its length / 15
+ * rounded to bf16, zero = the nearest integer to -min / scale and q = zero +
+ * the nearest integer to w / scale, both in [0, 15]. Ties to even; a group
+ * whose scale is 0 stands for zeros. q's buffers must not overlap W or each
+ * other (MOE_ERR_ARG). */
+int moe_quantize(const moe_tensor *W, moe_q4 *q, void *stream);
+
+/* W (MOE_F32 or MOE_BF16, 16-byte aligned) = the values q stands for, each
+ * rounded once: the weights of moe_linear, moe_forward and the other entry
+ * points for more rows than the calls below take. */
+int moe_dequantize(const moe_q4 *q, moe_tensor *W, void *stream);
+
+/* moe_linear for N <= MOE_FEW_MAX_TOKENS rows (MOE_ERR_UNSUPPORTED beyond) and
+ * 4-bit weights:  out = act(x W^T + bias) + residual
+ *   x [N, K] MOE_BF16 (MOE_ERR_UNSUPPORTED for fp32), W [M, K] as moe_q4,
+ *   bias [M] MOE_F32 or NULL, activation as moe_linear's, residual [N, M]
+ *   MOE_BF16 or NULL (may be the buffer of out), out [N, M] MOE_BF16
+ * The weights enter exactly, sums are fp32, out is rounded once. An infinite
+ * activation of the input gives NaN in every output. K and M at most
+ * MOE_LINEAR_MAX_EXTENT; x 16-byte, the other data aligned to their types
+ * (MOE_ERR_ALIGN). out must not overlap an input otherwise (MOE_ERR_ARG).
+ * workspace: moe_linear_quant_workspace_size() bytes, 256-byte aligned (may be
+ * NULL when that is 0). N = 0 is valid. */
+int moe_linear_quant(const moe_tensor *x, const moe_q4 *W, const moe_tensor *bias,
+                  int32_t activation, const moe_tensor *residual, moe_tensor *out,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of scratch of moe_linear_quant (0 when it needs none, or for invalid sizes). */
+size_t moe_linear_quant_workspace_size(int64_t N, int64_t K, int64_t M, int32_t group);
+
+/* The routed experts of N <= MOE_FEW_MAX_TOKENS tokens with 4-bit weights:
+ *   out_t = sum over j of topk_gate[t, j] (W_down[e] act(W_up[e] x_t + b_up[e])
+ *           + b_down[e]),  e = topk_idx[t, j]
+ * for a routing given by the caller (moe_router, moe_router_ex): ids int32 and
+ * gates fp32 [N, k], device; an id outside [0, E) contributes nothing, and no
+ * capacity applies.
+ *   x, out [N, d] MOE_BF16; W_up [E, d_ff, d], W_down [E, d, d_ff] as moe_q4
+ *   of one group; opts as moe_forward_few's (activation, biases; no dropout)
+ * Numerics: weights as moe_linear_quant's; the hidden activation keeps 16
+ * significant bits, the experts' rows fp32; a token's choices are added in
+ * order and out is rounded once. An infinite value of x gives NaN. E and k
+ * within the layer's limits, d and d_ff multiples of group and at most
+ * MOE_FEW_MAX_WIDTH; x 16-byte aligned. workspace:
+ * moe_experts_quant_workspace_size() bytes, 256-byte aligned; calls that share
+ * one must not overlap. Neither out nor the workspace may overlap an input or
+ * each other (MOE_ERR_ARG). N = 0 is valid. */
+int moe_experts_quant(const moe_tensor *x, const int32_t *topk_idx, const float *topk_gate, int k,
+                   const moe_q4 *W_up, const moe_q4 *W_down, const moe_expert_opts *opts,
+                   moe_tensor *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of moe_experts_quant (0 for N = 0, invalid sizes, or beyond
+ * MOE_FEW_MAX_TOKENS). */
+size_t moe_experts_quant_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k,
+                                     int32_t group);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,9 @@ EXPORTS = ("moe_forward", "moe_workspace_size", "moe_capacity", "moe_error_strin
            "moe_combine_compact", "moe_forward_few", "moe_few_workspace_size", "moe_linear",
            "moe_linear_workspace_size", "moe_linear_backward",
            "moe_linear_backward_workspace_size", "moe_layer_norm", "moe_layer_norm_backward",
-           "moe_layer_norm_backward_workspace_size")
+           "moe_layer_norm_backward_workspace_size", "moe_quantize", "moe_dequantize",
+           "moe_linear_quant", "moe_linear_quant_workspace_size", "moe_experts_quant",
+           "moe_experts_quant_workspace_size")
 
 MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_NONE = 0, 1, 2
 ACTS = {"relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU}
@@ -61,6 +63,11 @@ class MoeExpertOpts(ctypes.Structure):
                 ("dropout_seed", ctypes.c_uint64), ("dropout_offset", ctypes.c_uint64)]
 
 
+class MoeQ4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("group", ctypes.c_int32), ("ndim", ctypes.c_int32), ("shape", ctypes.c_int64 * 3)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -69,6 +76,7 @@ class MoeError(RuntimeError):
 
 _lib = None
 _T = ctypes.POINTER(MoeTensor)
+_Q = ctypes.POINTER(MoeQ4)
 _D = ctypes.c_char_p
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -179,6 +187,20 @@ def lib():
         L.moe_layer_norm_backward.restype = ctypes.c_int
         L.moe_layer_norm_backward_workspace_size.argtypes = [_i64, _i64]
         L.moe_layer_norm_backward_workspace_size.restype = ctypes.c_size_t
+        L.moe_quantize.argtypes = [_D, _Q, _vp]
+        L.moe_quantize.restype = ctypes.c_int
+        L.moe_dequantize.argtypes = [_Q, _D, _vp]
+        L.moe_dequantize.restype = ctypes.c_int
+        L.moe_linear_quant.argtypes = [_D, _Q, _D, ctypes.c_int32, _D, _D, _vp, ctypes.c_size_t, _vp]
+        L.moe_linear_quant.restype = ctypes.c_int
+        L.moe_linear_quant_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int32]
+        L.moe_linear_quant_workspace_size.restype = ctypes.c_size_t
+        L.moe_experts_quant.argtypes = [_D, _vp, _vp, ctypes.c_int, _Q, _Q,
+                                     ctypes.POINTER(MoeExpertOpts), _D, _vp, ctypes.c_size_t, _vp]
+        L.moe_experts_quant.restype = ctypes.c_int
+        L.moe_experts_quant_workspace_size.argtypes = [_i64, _i64, _i64, _i64, ctypes.c_int,
+                                                    ctypes.c_int32]
+        L.moe_experts_quant_workspace_size.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -1039,3 +1061,137 @@ def layer_norm_backward(h, weight, mean, rstd, dout, dres=None, bias: bool = Tru
          _pack(dres, index), _pack(dx, index), _pack(dw, index), _pack(db, index), ws, wn,
          _stream_of(index))
     return dx, dw, db
+
+
+# --------------------------------------------------------------------------
+# Weights of 4 bits with group scales
+# --------------------------------------------------------------------------
+class Q4:
+    """4-bit weights: ``data`` uint8 [.., M, K / 2] (even column in the low
+    half of a byte), ``scale`` bf16 [.., M, K / group] and ``zero`` bf16 like
+    it, or None (8 everywhere), of one matrix or of E: the values
+    ``(q - zero) * scale``. Keeps the memory of the tensors it was given."""
+
+    def __init__(self, data, scale, zero=None, group=128):
+        if data.dtype != torch.uint8:
+            raise TypeError("data must be uint8, two weights to a byte")
+        if data.dim() not in (2, 3):
+            raise ValueError("data must have 2 or 3 dimensions")
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        K = data.shape[-1] * 2
+        index = _device_of(data)
+        for t in (scale, zero):
+            if t is None:
+                continue
+            if t.dtype != torch.bfloat16:
+                raise TypeError("scale and zero must be bfloat16")
+            if K % group or tuple(t.shape) != (*data.shape[:-1], K // group):
+                raise ValueError(f"scale and zero must be {(*data.shape[:-1], K // group)}")
+            if t.get_device() != index:
+                raise ValueError("the tensors are on different devices")
+        if not all(t is None or t.is_contiguous() for t in (data, scale, zero)):
+            raise ValueError("tensors must be contiguous")
+        self.data, self.scale = data.detach(), scale.detach()
+        self.zero = None if zero is None else zero.detach()
+        self.group, self.index = group, index
+        self.shape = (*data.shape[:-1], K)
+        self._c = MoeQ4(data.data_ptr(), scale.data_ptr(),
+                        None if zero is None else zero.data_ptr(), group, data.dim(),
+                        (ctypes.c_int64 * 3)(*self.shape))
+        self._ref = ctypes.byref(self._c)
+
+    def ref(self, index: int):
+        """The ``moe_q4`` for a call on device ``index``."""
+        if index != self.index:
+            raise ValueError(f"weights on cuda:{self.index}, other tensors on cuda:{index}: the "
+                             "library takes device pointers of one GPU")
+        return self._ref
+
+
+@_on_stream
+def quantize_q4(W, group: int = 128, zero: bool = False) -> Q4:
+    """The nearest 4-bit weights of ``W`` (fp32 or bf16, [M, K] or [E, M, K]),
+    with zero points or symmetric: a :class:`Q4`."""
+    index = _device_of(W)
+    if group not in (32, 64, 128) or W.shape[-1] % group:
+        raise ValueError("group must be 32, 64 or 128 and divide the last dimension")
+    lead, K = W.shape[:-1], W.shape[-1]
+    data = torch.empty((*lead, K // 2), dtype=torch.uint8, device=W.device)
+    scale = torch.empty((*lead, K // group), dtype=torch.bfloat16, device=W.device)
+    q = Q4(data, scale, torch.empty_like(scale) if zero else None, group)
+    _run(index, "moe_quantize", lib().moe_quantize, _pack(W, index), q.ref(index),
+         _stream_of(index))
+    return q
+
+
+@_on_stream
+def dequantize_q4(q: Q4, out=None, dtype=torch.bfloat16):
+    """The weights that ``q`` stands for (``out``, or a new tensor of ``dtype``)."""
+    index = q.index
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=q.data.device)
+    _run(index, "moe_dequantize", lib().moe_dequantize, q.ref(index), _pack(out, index),
+         _stream_of(index))
+    return out
+
+
+def linear_q4_workspace_size(N: int, K: int, M: int, group: int = 128) -> int:
+    return int(lib().moe_linear_quant_workspace_size(N, K, M, group))
+
+
+@_on_stream
+def linear_q4(x, W: Q4, bias=None, act: str = "none", residual=None, out=None, workspace=None):
+    """``act(x W^T + bias) + residual`` of at most ``MOE_FEW_MAX_TOKENS`` rows
+    (bf16; x [..., K]) with 4-bit weights [M, K]."""
+    M, K = W.shape[-2], x.shape[-1]
+    index = _device_of(x)
+    if out is None:
+        out = torch.empty((*x.shape[:-1], M), dtype=x.dtype, device=x.device)
+    if workspace is None:
+        n = linear_q4_workspace_size(x.numel() // K, K, M, W.group)
+        workspace = alloc_workspace(n, x.device) if n else None
+    ws, wn = _scratch(workspace, index)
+    _run(index, "moe_linear_quant", lib().moe_linear_quant, _pack(x, index), W.ref(index),
+         _pack(bias, index), _linear_act(act), _pack(residual, index), _pack(out, index), ws, wn,
+         _stream_of(index))
+    return out
+
+
+def experts_q4_workspace_size(N: int, d: int, E: int, d_ff: int, k: int, group: int = 128) -> int:
+    return int(lib().moe_experts_quant_workspace_size(N, d, E, d_ff, k, group))
+
+
+def _routing_ptrs(idx, gate, N, k, index):
+    """Pointers of a caller's routing: ids int32 and gates fp32 [N, k]."""
+    for t, dt, name in ((idx, torch.int32, "idx"), (gate, torch.float32, "gate")):
+        if t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}")
+        if t.numel() != N * k or t.shape[-1] != k or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{N}, {k}] tensor")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on another device")
+    return idx.data_ptr(), gate.data_ptr()
+
+
+@_on_stream
+def experts_q4(x, idx, gate, W_up: Q4, W_down: Q4, act: str = "relu", b_up=None, b_down=None,
+               out=None, workspace=None):
+    """The routed experts of at most ``MOE_FEW_MAX_TOKENS`` tokens with 4-bit
+    weights (W_up [E, d_ff, d], W_down [E, d, d_ff]) for the routing ``idx``
+    (int32) and ``gate`` (fp32) [N, k] of :func:`router` or :func:`route`."""
+    N, d, k = x.numel() // x.shape[-1], x.shape[-1], idx.shape[-1]
+    index = _device_of(x)
+    ip, gp = _routing_ptrs(idx, gate, N, k, index)
+    if out is None:
+        out = torch.empty_like(x)
+    if workspace is None:
+        n = experts_q4_workspace_size(N, d, W_up.shape[0], W_up.shape[-2], k, W_up.group)
+        workspace = alloc_workspace(n, x.device) if n else None
+    ws, wn = _scratch(workspace, index)
+    _pack(b_up, index), _pack(b_down, index)   # (same checks as every tensor)
+    o = _opts(act, b_up, b_down)
+    _run(index, "moe_experts_quant", lib().moe_experts_quant, _pack(x, index), ip, gp, k,
+         W_up.ref(index), W_down.ref(index), None if o is None else o.ref(), _pack(out, index),
+         ws, wn, _stream_of(index))
+    return out

@@ -352,3 +352,29 @@ hipError_t launch_linear_backward(const void *x, const void *W, const void *z, i
                                   hipStream_t s);
 
 }  // namespace moe
+
+// ---------------------------------------------------------------------------
+// Weights of 4 bits with group scales (q4.hip): data, scale and zero (or NULL)
+// of a matrix; K and the widths are multiples of group (32, 64 or 128).
+// ---------------------------------------------------------------------------
+namespace moe {
+
+hipError_t launch_linear_q4(const void *x, const void *data, const void *scale, const void *zero,
+                            int group, const float *bias, int act, const void *res, int64_t N,
+                            int64_t K, int64_t M, void *out, hipStream_t s);
+// Workspace regions (byte offsets): hidden rows, expert rows, counters.
+struct Q4ExpertsLayout {
+    size_t H, Y, done, total;
+};
+Q4ExpertsLayout experts_q4_layout(int64_t N, int64_t d, int64_t d_ff, int k);
+hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gate,
+                             const void *const (&up)[3], const void *const (&down)[3], int group,
+                             const float *b_up, const float *b_down, int64_t N, int64_t d, int E,
+                             int64_t d_ff, int k, int act, void *ws, void *out, hipStream_t s);
+// n weights (a multiple of group).
+hipError_t launch_quantize_q4(bool bf16, const void *W, int64_t n, int group, void *data,
+                              void *scale, void *zero, hipStream_t s);
+hipError_t launch_dequantize_q4(bool bf16, const void *data, const void *scale, const void *zero,
+                                int64_t n, int group, void *W, hipStream_t s);
+
+}  // namespace moe

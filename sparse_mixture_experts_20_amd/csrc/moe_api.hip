@@ -1713,3 +1713,214 @@ int moe_linear_backward(const moe_tensor *x, const moe_tensor *W, const moe_tens
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Weights of 4 bits
+// ---------------------------------------------------------------------------
+namespace {
+
+// A 4-bit matrix of the given rank: group, extents and pointers.
+int check_q4(const moe_q4 *q, int ndim) {
+    if (!q)
+        return MOE_ERR_NULL;
+    if (q->ndim != ndim)
+        return MOE_ERR_SHAPE;
+    if (q->group != 32 && q->group != 64 && q->group != 128)
+        return MOE_ERR_UNSUPPORTED;
+    for (int i = 0; i < ndim; ++i)
+        if (q->shape[i] <= 0)
+            return MOE_ERR_SHAPE;
+    const int64_t K = q->shape[ndim - 1];
+    if (K % q->group != 0)
+        return MOE_ERR_SHAPE;
+    // (extents whose product of bytes stays far inside 64 bits)
+    if (K > MOE_LINEAR_MAX_EXTENT || q->shape[ndim - 2] > MOE_LINEAR_MAX_EXTENT ||
+        (ndim == 3 && q->shape[0] > MOE_MAX_EXPERTS))
+        return MOE_ERR_UNSUPPORTED;
+    if (!q->data || !q->scale)
+        return MOE_ERR_NULL;
+    if (!aligned(q->data, 16) || !aligned(q->scale, 2) || !aligned(q->zero, 2))
+        return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+int64_t q4_count(const moe_q4 *q) {
+    int64_t n = 1;
+    for (int i = 0; i < q->ndim; ++i)
+        n *= q->shape[i];
+    return n;
+}
+// The three buffers of a 4-bit matrix.
+struct Q4Spans {
+    Span s[3];
+    explicit Q4Spans(const moe_q4 *q) {
+        const int64_t n = q4_count(q);
+        s[0] = {q->data, n / 2};
+        s[1] = {q->scale, n / q->group * 2};
+        s[2] = {q->zero, n / q->group * 2};
+    }
+};
+
+// W of a conversion: a full-precision tensor of q's extents.
+int check_q4_full(const moe_tensor *W, const moe_q4 *q) {
+    if (!W || !q)
+        return MOE_ERR_NULL;
+    if (!valid_dtype(W->dtype))
+        return MOE_ERR_DTYPE;
+    if (W->ndim != 2 && W->ndim != 3)
+        return MOE_ERR_SHAPE;
+    const int rc = check_q4(q, W->ndim);
+    if (rc != MOE_OK)
+        return rc;
+    for (int i = 0; i < W->ndim; ++i)
+        if (W->shape[i] != q->shape[i])
+            return MOE_ERR_SHAPE;
+    if (q4_count(q) / 8 > (int64_t)INT32_MAX * 256)   // workgroups of a launch
+        return MOE_ERR_UNSUPPORTED;
+    if (!W->data)
+        return MOE_ERR_NULL;
+    return aligned(W->data, 16) ? MOE_OK : MOE_ERR_ALIGN;
+}
+
+bool experts_q4_sizes_ok(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k, int32_t group) {
+    return N > 0 && N <= MOE_FEW_MAX_TOKENS && E > 0 && E <= MOE_MAX_EXPERTS && k >= 1 && k <= E &&
+           k <= MOE_MAX_TOPK && (group == 32 || group == 64 || group == 128) && d > 0 &&
+           d_ff > 0 && d % group == 0 && d_ff % group == 0 && d <= MOE_FEW_MAX_WIDTH &&
+           d_ff <= MOE_FEW_MAX_WIDTH;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_quantize(const moe_tensor *W, moe_q4 *q, void *stream) {
+    const int rc = check_q4_full(W, q);
+    if (rc != MOE_OK)
+        return rc;
+    const int64_t n = q4_count(q);
+    const Span in[1] = {{W->data, n * (W->dtype == MOE_BF16 ? 2 : 4)}};
+    if (collide(Q4Spans(q).s, in))
+        return MOE_ERR_ARG;
+    return hip_status(moe::launch_quantize_q4(W->dtype == MOE_BF16, W->data, n, q->group, q->data,
+                                              q->scale, q->zero,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+int moe_dequantize(const moe_q4 *q, moe_tensor *W, void *stream) {
+    const int rc = check_q4_full(W, q);
+    if (rc != MOE_OK)
+        return rc;
+    const int64_t n = q4_count(q);
+    const Span to[1] = {{W->data, n * (W->dtype == MOE_BF16 ? 2 : 4)}};
+    if (collide(to, Q4Spans(q).s))
+        return MOE_ERR_ARG;
+    return hip_status(moe::launch_dequantize_q4(W->dtype == MOE_BF16, q->data, q->scale, q->zero,
+                                                n, q->group, W->data,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_linear_quant_workspace_size(int64_t, int64_t, int64_t, int32_t) { return 0; }
+
+int moe_linear_quant(const moe_tensor *x, const moe_q4 *W, const moe_tensor *bias,
+                  int32_t activation, const moe_tensor *residual, moe_tensor *out,
+                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (!x || !out)
+        return MOE_ERR_NULL;
+    int64_t N, K;
+    if (!act_rows(x, N, K))
+        return MOE_ERR_SHAPE;
+    if (!valid_dtype(x->dtype))
+        return MOE_ERR_DTYPE;
+    int rc = check_q4(W, 2);
+    if (rc != MOE_OK)
+        return rc;
+    if (W->shape[1] != K)
+        return MOE_ERR_SHAPE;
+    const int64_t M = W->shape[0];
+    if (activation != MOE_ACT_NONE && activation != MOE_ACT_RELU && activation != MOE_ACT_GELU)
+        return MOE_ERR_ARG;
+    if (x->dtype != MOE_BF16 || N > MOE_FEW_MAX_TOKENS)
+        return MOE_ERR_UNSUPPORTED;
+    const float *b;
+    void *r, *o;
+    if ((rc = check_vec(bias, M, false, b)) != MOE_OK ||
+        (rc = check_rows(residual, N, M, MOE_BF16, false, r)) != MOE_OK ||
+        (rc = check_rows(out, N, M, MOE_BF16, true, o)) != MOE_OK)
+        return rc;
+    if (N == 0)
+        return MOE_OK;
+    if (!x->data)
+        return MOE_ERR_NULL;
+    if (!aligned(x->data, 16) || !aligned(b, 4) || !aligned(r, 2) || !aligned(o, 2))
+        return MOE_ERR_ALIGN;
+    rc = check_scratch(workspace, workspace_bytes,
+                       moe_linear_quant_workspace_size(N, K, M, W->group));
+    if (rc != MOE_OK)
+        return rc;
+    const Span to[1] = {{o, 2 * N * M}};
+    const Span in[2] = {{x->data, 2 * N * K}, {b, 4 * M}};
+    if (collide(to, in) || collide(to, Q4Spans(W).s) || crosses(to[0], {r, 2 * N * M}))
+        return MOE_ERR_ARG;
+    return hip_status(moe::launch_linear_q4(x->data, W->data, W->scale, W->zero, W->group, b,
+                                            activation, r, N, K, M, o,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_experts_quant_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k,
+                                     int32_t group) {
+    return experts_q4_sizes_ok(N, d, E, d_ff, k, group)
+               ? moe::experts_q4_layout(N, d, d_ff, k).total : 0;
+}
+
+int moe_experts_quant(const moe_tensor *x, const int32_t *topk_idx, const float *topk_gate, int k,
+                   const moe_q4 *W_up, const moe_q4 *W_down, const moe_expert_opts *opts,
+                   moe_tensor *out, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!x || !out)
+        return MOE_ERR_NULL;
+    int64_t N, d;
+    if (!act_rows(x, N, d))
+        return MOE_ERR_SHAPE;
+    if (!valid_dtype(x->dtype))
+        return MOE_ERR_DTYPE;
+    int rc;
+    if ((rc = check_q4(W_up, 3)) != MOE_OK || (rc = check_q4(W_down, 3)) != MOE_OK)
+        return rc;
+    const int64_t E = W_up->shape[0], d_ff = W_up->shape[1];
+    if (W_up->shape[2] != d || W_down->shape[0] != E || W_down->shape[1] != d ||
+        W_down->shape[2] != d_ff || W_down->group != W_up->group)
+        return MOE_ERR_SHAPE;
+    if (k < 1 || k > E)
+        return MOE_ERR_ARG;
+    ExpertOpts eo;
+    if ((rc = check_opts(opts, E, d, d_ff, eo)) != MOE_OK)
+        return rc;
+    void *o;
+    if ((rc = check_rows(out, N, d, x->dtype, true, o)) != MOE_OK)
+        return rc;
+    if (eo.drop.on || x->dtype != MOE_BF16 ||
+        (N > 0 && !experts_q4_sizes_ok(N, d, E, d_ff, k, W_up->group)))
+        return MOE_ERR_UNSUPPORTED;
+    if (N == 0)
+        return MOE_OK;
+    if (!x->data || !topk_idx || !topk_gate)
+        return MOE_ERR_NULL;
+    if (!aligned(x->data, 16) || !aligned(o, 2) || !aligned(topk_idx, 4) || !aligned(topk_gate, 4))
+        return MOE_ERR_ALIGN;
+    const size_t need = moe::experts_q4_layout(N, d, d_ff, k).total;
+    if ((rc = check_scratch(workspace, workspace_bytes, need)) != MOE_OK)
+        return rc;
+    const Span to[2] = {{o, 2 * N * d}, {workspace, (int64_t)need}};
+    const Span in[5] = {{x->data, 2 * N * d},
+                        {topk_idx, 4 * N * k},
+                        {topk_gate, 4 * N * k},
+                        {eo.b_up, 4 * E * d_ff},
+                        {eo.b_down, 4 * E * d}};
+    if (collide(to, in) || collide(to, Q4Spans(W_up).s) || collide(to, Q4Spans(W_down).s))
+        return MOE_ERR_ARG;
+    const void *const up[3] = {W_up->data, W_up->scale, W_up->zero};
+    const void *const down[3] = {W_down->data, W_down->scale, W_down->zero};
+    return hip_status(moe::launch_experts_q4(x->data, topk_idx, topk_gate, up, down, W_up->group,
+                                             eo.b_up, eo.b_down, N, d, (int)E, d_ff, k, eo.act,
+                                             workspace, o, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
