@@ -589,8 +589,7 @@ size_t moe_layer_norm_backward_workspace_size(int64_t N, int64_t d);
  *   group  32, 64 or 128 (MOE_ERR_UNSUPPORTED otherwise); K % group == 0
  *          (MOE_ERR_SHAPE)
  *   ndim   2 ([M, K]) or 3 ([E, M, K]), and shape, the logical extents
- * Device pointers of the caller; data 16-byte, scale and zero 2-byte aligned
- * (MOE_ERR_ALIGN). */
+ * Device pointers of the caller, 16-byte aligned (MOE_ERR_ALIGN). */
 typedef struct {
     void *data;
     void *scale;

@@ -362,9 +362,10 @@ namespace moe {
 hipError_t launch_linear_q4(const void *x, const void *data, const void *scale, const void *zero,
                             int group, const float *bias, int act, const void *res, int64_t N,
                             int64_t K, int64_t M, void *out, hipStream_t s);
-// Workspace regions (byte offsets): hidden rows, expert rows, counters.
+// Workspace regions (byte offsets): hidden rows, expert rows, counters, rows of
+// the hit experts.
 struct Q4ExpertsLayout {
-    size_t H, Y, done, total;
+    size_t H, Y, done, plan, total;
 };
 Q4ExpertsLayout experts_q4_layout(int64_t N, int64_t d, int64_t d_ff, int k);
 hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gate,

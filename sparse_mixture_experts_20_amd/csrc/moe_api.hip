@@ -1739,7 +1739,7 @@ int check_q4(const moe_q4 *q, int ndim) {
         return MOE_ERR_UNSUPPORTED;
     if (!q->data || !q->scale)
         return MOE_ERR_NULL;
-    if (!aligned(q->data, 16) || !aligned(q->scale, 2) || !aligned(q->zero, 2))
+    if (!aligned(q->data, 16) || !aligned(q->scale, 16) || !aligned(q->zero, 16))
         return MOE_ERR_ALIGN;
     return MOE_OK;
 }

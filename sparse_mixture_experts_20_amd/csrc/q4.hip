@@ -35,19 +35,26 @@ namespace {
 constexpr int kQ4Step = 128;   // weights of a row per wave load
 constexpr int kMaxAssign = kFewMaxTokens * kMaxTopK;
 
-// 8 packed weights as 128 + q in bf16, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 q4_weights(unsigned d) {
-    constexpr unsigned M = 0x000f000fu, C = 0x43004300u;
-    return __builtin_bit_cast(
-        bf16x8, u32x4{(d & M) | C, ((d >> 4) & M) | C, ((d >> 8) & M) | C, ((d >> 12) & M) | C});
+// (a barrier for LDS alone: the loads of the next weights stay in flight)
+__device__ __forceinline__ void barrier_lds() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
-// 8 activations in the same order.
-__device__ __forceinline__ bf16x8 q4_order(const u32x4 &v) {
-    return __builtin_bit_cast(bf16x8, u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u),
-                                            __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-                                            __builtin_amdgcn_perm(v[3], v[1], 0x05040100u),
-                                            __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)});
-}
+
+// 8 packed weights as 128 + q in bf16, in the order 0 4 1 5 2 6 3 7. (The masks
+// come in registers, one scalar and one vector: an instruction takes no two
+// literals, and as literals each would cost a second instruction.)
+struct Q4Masks {
+    unsigned low, one;
+    __device__ __forceinline__ Q4Masks() {
+        asm("s_mov_b32 %0, 0x000f000f" : "=s"(low));
+        asm("v_mov_b32 %0, 0x43004300" : "=v"(one));
+    }
+    __device__ __forceinline__ bf16x8 weights(unsigned d) const {
+        return __builtin_bit_cast(bf16x8,
+                                  u32x4{(d & low) | one, ((d >> 4) & low) | one,
+                                        ((d >> 8) & low) | one, ((d >> 12) & low) | one});
+    }
+};
 
 // Groups of 128 / GS weights. The registers of a 16-byte load put in an order
 // whose MFMA i holds positions of one group: quarter g's 8 positions of MFMA i
@@ -78,84 +85,189 @@ struct Q4Matrix {
     const unsigned short *scale, *zero;   // zero NULL: 8
 };
 
-// Scales of GS adjacent groups.
-template <int GS>
-struct Q4Groups {
-    unsigned short v[GS];
-    __device__ __forceinline__ void load(const unsigned short *p, int have) {
-        if (GS == 1 || have >= GS) {
-            __builtin_memcpy(v, p, sizeof(v));
-        } else {
-#pragma unroll
-            for (int i = 0; i < GS; ++i)
-                v[i] = i < have ? p[i] : (unsigned short)0;
-        }
-    }
+// How a workgroup covers its product: wm x wk waves, each RT tiles of 16 weight
+// rows, the waves of one row block taking every wk-th step of 128 columns.
+struct Q4Waves {
+    int wm, wk, lds;   // lds: bytes for the activations and the scales
 };
-
-// tot[rt][i] += products of K columns [kb, ke) (multiples of 128, ke possibly
-// past K) of RT row tiles of 16 weight rows with TT tiles of 16 token rows, by
-// one wave: lane l ends with weight row l % 16 of tile rt and tokens 4 (l / 16)
-// + q of tile i. m[rt]: this lane's weight row; xt[i]: this lane's token row
-// (column 0); NB terms per token row, `lo` elements apart, are added. U steps
-// are loaded while the previous ones are multiplied.
-template <int GS, int RT, int TT, int NB, int U>
-__device__ __forceinline__ void q4_product(const Q4Matrix &W, const int64_t (&m)[RT],
-                                           const unsigned short *const (&xt)[TT], int64_t lo,
-                                           int kb, int ke, int K, f32x4 (&tot)[RT][TT]) {
-    constexpr bool AHEAD = TT * NB <= 2;   // token rows are loaded with the weights
-    const int g = (int)(__lane_id() >> 4);
-    const int KG = K / (kQ4Step / GS);     // groups of a row
-    const unsigned char *w[RT];
-    const unsigned short *sc[RT], *zp[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        w[r] = W.data + m[r] * (K / 2) + 16 * g;
-        sc[r] = W.scale + m[r] * KG;
-        zp[r] = W.zero + (W.zero ? m[r] * KG : 0);
+// The activations in LDS, kc columns at a time, rows of 2^sh chunks of 8 columns:
+// all of K where R rows of it fit, else as many times wk D steps as fit (the host
+// sees to it that one does).
+struct Q4Tiling {
+    int wm, wk, kc, sh;
+};
+__device__ __host__ __forceinline__ int log2_up(int v) {
+    int s = 0;
+    while ((1 << s) < v)
+        ++s;
+    return s;
+}
+// Scales of a row are 2 bytes a group, rows a multiple of 16 bytes (and not of the
+// banks) apart.
+__device__ __host__ __forceinline__ int q4_scale_stride(int groups) {
+    return (groups + 7) / 8 * 8 + 8;
+}
+// Bytes of kc columns (a multiple of 128): R rows of activations, the scales and
+// zero points of WR weight rows.
+__device__ __host__ __forceinline__ int64_t q4_bytes(int R, int WR, int64_t kc, int GS, bool zero) {
+    return R * (2 * kc + 16) + (int64_t)WR * q4_scale_stride((int)(kc / kQ4Step * GS)) * (zero ? 4 : 2);
+}
+__device__ __host__ __forceinline__ Q4Tiling q4_tiling(const Q4Waves &w, int R, int WR, int K,
+                                                       int D, int GS, bool zero) {
+    Q4Tiling t;
+    t.wm = w.wm;
+    t.wk = w.wk;
+    t.kc = (K + kQ4Step - 1) / kQ4Step * kQ4Step;
+    if (q4_bytes(R, WR, t.kc, GS, zero) > w.lds) {
+        // (bytes a column, times 64, and those of no column)
+        const int per = 128 * R + WR * GS * (zero ? 2 : 1), none = 16 * R + WR * 32 * (zero ? 2 : 1);
+        const int unit = kQ4Step * w.wk * D;
+        t.kc = (int)((int64_t)(w.lds - none) * 64 / per) / unit * unit;
     }
+    t.sh = log2_up(t.kc / 8);
+    return t;
+}
+
+// Rows of activations in LDS, 8 numbers a chunk in the order of Q4Masks; rows
+// are 16 bytes apart modulo the banks.
+__device__ __forceinline__ u32x4 q4_order(const u32x4 &v) {
+    return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u),
+                 __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+                 __builtin_amdgcn_perm(v[3], v[1], 0x05040100u),
+                 __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+}
+
+// The product of the workgroup's 16 RT WM weight rows from m0 on (rows past
+// mlast repeat it) with its token rows: f(token row of the 16 TT, weight row of
+// the workgroup, value) for each result. src(r): row r < R of activations;
+// at(i, n): the row that this lane takes for tile i and term n of NB (whose
+// products are added). D: steps of weights in flight.
+template <int GS, bool ZERO, int RT, int TT, int NB, int D, typename SRC, typename AT,
+          typename F>
+__device__ __forceinline__ void q4_block(char *smem, const Q4Matrix &W, int64_t m0, int64_t mlast,
+                                         int K, const Q4Tiling &T, int R, SRC src, AT at, F f) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wv / T.wk, wk = wv % T.wk, threads = blockDim.x;
+    const int KG = K / (kQ4Step / GS);   // groups of a row
+    const int steps = (K + kQ4Step - 1) / kQ4Step;
+    const int mine = (steps - wk + T.wk - 1) / T.wk;   // steps of this wave
+
+    const unsigned char *w[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        w[r] = W.data + min(m0 + (wm * RT + r) * 16 + (lane & 15), mlast) * (K / 2) + 16 * g;
     struct Step {
         u32x4 w[RT];
-        Q4Groups<GS> s[RT], z[RT];
-        u32x4 x[AHEAD ? TT : 1][AHEAD ? NB : 1][4];
     };
-    auto load_x = [&](int i, int n, int k, int j) {
-        const int o = k + q4_position<GS>(g, j);
-        if (GS == 1 || o < K)
-            return *reinterpret_cast<const u32x4 *>(xt[i] + n * lo + o);
-        return u32x4{0u, 0u, 0u, 0u};
-    };
-    auto load = [&](int k, Step &s) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            s.w[r] = u32x4{0u, 0u, 0u, 0u};
-            if (GS == 1 || k + 32 * g < K)
-                s.w[r] = *reinterpret_cast<const u32x4 *>(w[r] + k / 2);
-        }
-        if constexpr (AHEAD)
-#pragma unroll
-            for (int i = 0; i < TT; ++i)
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s.x[i][n][j] = load_x(i, n, k, j);
-        const int at = k / (kQ4Step / GS);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            s.s[r].load(sc[r] + at, KG - at);
-            if (W.zero)
-                s.z[r].load(zp[r] + at, KG - at);
-        }
-    };
-    auto multiply = [&](int k, Step &s) {
-        const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
-        const bf16x8 ones = __builtin_bit_cast(
-            bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
-        f32x4 acc[RT][TT], sx[TT];
+    // Loads have no branches around them (past the end they repeat the last place,
+    // and what they bring is not used), so that a wait can count them.
+    auto load = [&](int n, Step &s) {
+        const int k = (wk + n * T.wk) * kQ4Step;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
+            s.w[r] = *reinterpret_cast<const u32x4 *>(
+                w[r] + (GS == 1 ? k / 2 : min(k / 2, K / 2 - 16 - 16 * g)));
+    };
+
+    // activations: chunk o of the buffer is chunk o % 2^sh of row o / 2^sh; columns
+    // past K are zeros (the weights there are not)
+    const int rowb = T.kc * 2 + 16;
+    const int chunks = R << T.sh, cmask = (1 << T.sh) - 1;
+    auto fetch = [&](int o, int k0) {
+        return *reinterpret_cast<const u32x4 *>(src(min(o >> T.sh, R - 1)) +
+                                                min(k0 + 8 * (o & cmask), K - 8));
+    };
+    auto put = [&](int o, int k0, const u32x4 &v) {
+        const int c = o & cmask;
+        if (o < chunks && 8 * c < T.kc)
+            *reinterpret_cast<u32x4 *>(smem + (o >> T.sh) * rowb + 16 * c) =
+                k0 + 8 * c < K ? q4_order(v) : u32x4{0u, 0u, 0u, 0u};
+    };
+    constexpr int XB = 4;   // chunks a thread loads at once
+    u32x4 first[XB];
+#pragma unroll
+    for (int i = 0; i < XB; ++i)
+        first[i] = fetch(threadIdx.x + i * threads, 0);
+    // scales (and zero points) of the buffer's groups, row by row: read by the lanes
+    // themselves, they took as many requests as the weights (fine-grained batch of
+    // 61 tokens: 1030 us, 760 without any)
+    const int WR = 16 * RT * T.wm, kcg = T.kc / (kQ4Step / GS), ss = q4_scale_stride(kcg);
+    unsigned short *sm_s = reinterpret_cast<unsigned short *>(smem + R * rowb);
+    unsigned short *sm_z = sm_s + WR * ss;
+    const bool vec = KG % 8 == 0 && kcg % 8 == 0;
+    auto stage_scales = [&](int k0) {
+        const int g0 = k0 / (kQ4Step / GS);
+        // (of a step that ends past K, groups past the last one are zeros; whole
+        // vectors have none)
+        const unsigned n = (unsigned)(vec ? min(kcg, KG - g0) / 8 : kcg);
+        for (unsigned o = threadIdx.x; o < WR * n; o += threads) {
+            const int r = (int)(o / n), c = (int)(o - r * n);
+            const int64_t from = min(m0 + r, mlast) * KG + g0;
+            if (vec) {
+                *reinterpret_cast<u32x4 *>(sm_s + r * ss + 8 * c) =
+                    *reinterpret_cast<const u32x4 *>(W.scale + from + 8 * c);
+                if (ZERO)
+                    *reinterpret_cast<u32x4 *>(sm_z + r * ss + 8 * c) =
+                        *reinterpret_cast<const u32x4 *>(W.zero + from + 8 * c);
+            } else {
+                const bool in = g0 + c < KG;
+                sm_s[r * ss + c] = in ? W.scale[from + c] : 0;
+                if (ZERO)
+                    sm_z[r * ss + c] = in ? W.zero[from + c] : 0;
+            }
+        }
+    };
+    Step ring[D];
+    const int end = mine - 1;   // (every wave has a step)
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+        load(min(u, end), ring[u]);
+    auto stage = [&](int o, int k0) {
+        for (; o < chunks; o += XB * threads) {
+            u32x4 v[XB];
+#pragma unroll
+            for (int i = 0; i < XB; ++i)
+                v[i] = fetch(o + i * threads, k0);
+#pragma unroll
+            for (int i = 0; i < XB; ++i)
+                put(o + i * threads, k0, v[i]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < XB; ++i)
+        put(threadIdx.x + i * threads, 0, first[i]);
+    stage(threadIdx.x + XB * threads, 0);
+    stage_scales(0);
+    barrier_lds();
+
+    f32x4 tot[RT][TT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            tot[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int xo[TT][NB];   // this lane's rows in a buffer
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            xo[i][n] = at(i, n) * rowb;
+    const bf16x8 ones = __builtin_bit_cast(
+        bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+    const Q4Masks masks;
+    auto multiply = [&](int k, Step &s) {   // k: column in the buffer
+        const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
+        f32x4 acc[RT][TT], sx[TT];
+        unsigned short sv[RT][GS], zv[RT][GS];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int at = ((wm * RT + r) * 16 + (lane & 15)) * ss + k / (kQ4Step / GS);
+            __builtin_memcpy(sv[r], __builtin_assume_aligned(sm_s + at, 2 * GS), 2 * GS);
+            if (ZERO)
+                __builtin_memcpy(zv[r], __builtin_assume_aligned(sm_z + at, 2 * GS), 2 * GS);
             q4_arrange<GS>(s.w[r]);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             constexpr int P = 4 / GS;   // MFMAs of a group
@@ -171,16 +283,13 @@ __device__ __forceinline__ void q4_product(const Q4Matrix &W, const int64_t (&m)
             bf16x8 q[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r)
-                q[r] = q4_weights(s.w[r][j]);
+                q[r] = masks.weights(s.w[r][j]);
+            const char *xb = smem + 2 * (k + q4_position<GS>(g, j));
 #pragma unroll
             for (int i = 0; i < TT; ++i)
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    bf16x8 a;
-                    if constexpr (AHEAD)
-                        a = q4_order(s.x[i][n][j]);
-                    else
-                        a = q4_order(load_x(i, n, k, j));
+                    const bf16x8 a = *reinterpret_cast<const bf16x8 *>(xb + xo[i][n]);
                     sx[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, sx[i], 0, 0, 0);
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
@@ -190,82 +299,75 @@ __device__ __forceinline__ void q4_product(const Q4Matrix &W, const int64_t (&m)
             if (j % P == P - 1) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const float f = bf16_bits_to_f32(s.s[r].v[j / P]);
-                    const float c =
-                        W.zero ? -128.f - bf16_bits_to_f32(s.z[r].v[j / P]) : -136.f;
+                    const float sr = bf16_bits_to_f32(sv[r][j / P]);
+                    const float c = ZERO ? -128.f - bf16_bits_to_f32(zv[r][j / P]) : -136.f;
 #pragma unroll
                     for (int i = 0; i < TT; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             tot[r][i][e] =
-                                fmaf(f, fmaf(c, sx[i][e], acc[r][i][e]), tot[r][i][e]);
+                                fmaf(sr, fmaf(c, sx[i][e], acc[r][i][e]), tot[r][i][e]);
                 }
             }
         }
     };
-    Step next[U];
-    int k = kb;
-    if (k + kQ4Step * U <= ke) {
+    // steps of a wave in the buffer (a multiple of D, or all of them)
+    const int per = T.kc / (kQ4Step * T.wk) + (T.kc >= K);
+    for (int n = 0, k0 = 0;; k0 += T.kc) {
+        const int n1 = min(mine, n + per);
+        for (; n + D <= n1; n += D) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            load(k + kQ4Step * u, next[u]);
-        for (k += kQ4Step * U; k + kQ4Step * U <= ke; k += kQ4Step * U) {
-            Step cur[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                cur[u] = next[u];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                load(k + kQ4Step * u, next[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                multiply(k + kQ4Step * (u - U), cur[u]);
+            for (int u = 0; u < D; ++u) {
+                // (in this order: gathered at the loop's end, the loads would all be
+                // waited for at its start)
+                multiply((wk + (n + u) * T.wk) * kQ4Step - k0, ring[u]);
+                __builtin_amdgcn_sched_barrier(0);
+                load(min(n + u + D, end), ring[u]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
+        if (k0 + T.kc >= K) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            multiply(k + kQ4Step * (u - U), next[u]);
+            for (int u = 0; u < D; ++u)
+                if (n + u < n1)
+                    multiply((wk + (n + u) * T.wk) * kQ4Step - k0, ring[u]);
+            break;
+        }
+        barrier_lds();
+        stage(threadIdx.x, k0 + T.kc);
+        stage_scales(k0 + T.kc);
+        barrier_lds();
     }
-    for (; k < ke; k += kQ4Step) {
-        load(k, next[0]);
-        multiply(k, next[0]);
+    if (T.wk == 1) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f(16 * i + 4 * g + e, (wm * RT + r) * 16 + (lane & 15), tot[r][i][e]);
+        return;
     }
-}
-
-// The product over a workgroup's K range by all its waves, added through LDS in
-// wave order: f(token row, weight row of the RT 16, value) for each result.
-// part: waves x RT x TT x 64 f32x4.
-template <int GS, int RT, int TT, int NB, typename F>
-__device__ __forceinline__ void q4_block(f32x4 *part, const Q4Matrix &W, const int64_t (&m)[RT],
-                                         const unsigned short *const (&xt)[TT], int64_t lo, int K,
-                                         F f) {
-    const int lane = threadIdx.x & 63;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
-    const int steps = (K + kQ4Step - 1) / kQ4Step;
-    const int kb = (int)((int64_t)wv * steps / waves) * kQ4Step;
-    const int ke = (int)((int64_t)(wv + 1) * steps / waves) * kQ4Step;
-    f32x4 tot[RT][TT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-            tot[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = TT * NB <= 1 ? 2 : 1;
-    q4_product<GS, RT, TT, NB, U>(W, m, xt, lo, kb, ke, K, tot);
+    // the waves of a row block add through LDS, in wave order
+    barrier_lds();
+    f32x4 *part = reinterpret_cast<f32x4 *>(smem);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int i = 0; i < TT; ++i)
             part[((wv * RT + r) * TT + i) * 64 + lane] = tot[r][i];
-    __syncthreads();
-    for (int o = threadIdx.x; o < RT * TT * 64; o += blockDim.x) {
-        f32x4 v = part[o];
-        for (int w = 1; w < waves; ++w)
-            v += part[w * RT * TT * 64 + o];
-        const int l = o & 63, i = (o >> 6) % TT, r = (o >> 6) / TT;
+    barrier_lds();
+    constexpr int PER = RT * TT * 64;
+    for (int o = threadIdx.x; o < T.wm * PER; o += threads) {
+        const int in = o % PER, b = o / PER;
+        const f32x4 *p = part + (int64_t)b * T.wk * PER + in;
+        f32x4 v = p[0];
+        for (int q = 1; q < T.wk; ++q)
+            v += p[q * PER];
+        const int l = in & 63, i = (in >> 6) % TT, r = (in >> 6) / TT;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            f(16 * i + 4 * (l >> 4) + e, 16 * r + (l & 15), v[e]);
+            f(16 * i + 4 * (l >> 4) + e, (b * RT + r) * 16 + (l & 15), v[e]);
     }
 }
 
@@ -279,34 +381,34 @@ struct Q4Linear {
     int64_t M;
 };
 
-// grid: tiles of 16 RT weight rows.
-template <int GS, int RT, int TT>
-__global__ __launch_bounds__(512) void q4_linear_kernel(Q4Linear p) {
-    extern __shared__ __attribute__((aligned(16))) f32x4 part[];
+// Steps of weights in flight, by tiles of 16 rows of activations.
+constexpr int q4_depth(int rows) { return rows == 1 ? 4 : rows <= 4 ? 2 : 1; }
+
+// grid: blocks of 16 RT WM weight rows.
+template <int GS, bool ZERO, int RT, int TT>
+__global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_linear_kernel(Q4Linear p, Q4Waves w) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63;
-    const int64_t m0 = (int64_t)blockIdx.x * (16 * RT);
-    int64_t m[RT];
-    const unsigned short *xt[TT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-        m[r] = min(m0 + 16 * r + (lane & 15), p.M - 1);
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-        xt[i] = p.x + (int64_t)min(16 * i + (lane & 15), p.N - 1) * p.K;
-    q4_block<GS, RT, TT, 1>(part, p.W, m, xt, 0, p.K, [&](int t, int r, float v) {
-        const int64_t c = m0 + r;
-        if (t >= p.N || c >= p.M)
-            return;
-        if (p.bias)
-            v += p.bias[c];
-        v = activate(v, p.act);
-        const int64_t o = (int64_t)t * p.M + c;
-        if (p.res)
-            v += bf16_bits_to_f32(p.res[o]);
-        p.out[o] = f32_to_bf16_bits(v);
-    });
+    const Q4Tiling T = q4_tiling(w, p.N, 16 * RT * w.wm, p.K, q4_depth(TT), GS, ZERO);
+    const int64_t m0 = (int64_t)blockIdx.x * (16 * RT * T.wm);
+    q4_block<GS, ZERO, RT, TT, 1, q4_depth(TT)>(
+        smem, p.W, m0, p.M - 1, p.K, T, p.N, [&](int r) { return p.x + (int64_t)r * p.K; },
+        [&](int i, int) { return min(16 * i + (lane & 15), p.N - 1); },
+        [&](int t, int r, float v) {
+            const int64_t c = m0 + r;
+            if (t >= p.N || c >= p.M)
+                return;
+            if (p.bias)
+                v += p.bias[c];
+            v = activate(v, p.act);
+            const int64_t o = (int64_t)t * p.M + c;
+            if (p.res)
+                v += bf16_bits_to_f32(p.res[o]);
+            p.out[o] = f32_to_bf16_bits(v);
+        });
 }
 
+struct Q4Plan;
 struct Q4Experts {
     const unsigned short *x;      // [N, d]
     const int32_t *idx;           // [N, k]
@@ -316,83 +418,162 @@ struct Q4Experts {
     unsigned short *H;            // [2][N k][d_ff]: two bf16 terms
     float *Y;                     // [N k][d]
     int *done;                    // finished workgroups per column block
+    const Q4Plan *plan;           // NULL with at most 64 assignments
     unsigned short *out;          // [N, d]
     int N, d, E, d_ff, k, act;
 };
 
-// The assignments (t k + j) of assignment a's expert, in ascending order, into
-// row[] by the whole workgroup: their number, or 0 when an earlier assignment
-// has the same expert (whose workgroup does the work) or a's id is no expert.
-__device__ __forceinline__ int q4_rows(const int32_t *__restrict__ idx, int A, int E, int a,
-                                       unsigned short *row) {
-    const int lane = threadIdx.x & 63;
-    const int e = idx[a];
-    int n = 0;
-    bool first = e >= 0 && e < E;
-    for (int c = 0; c < A; c += 64) {
-        const uint64_t same = __ballot(c + lane < A && idx[min(c + lane, A - 1)] == e);
-        if (c + 64 <= a) {
-            first = first && same == 0;
-        } else {
-            if (c <= a)
-                first = first && (same & ((1ull << (a - c)) - 1ull)) == 0;
-            if (threadIdx.x < 64 && (same >> lane & 1ull))
-                row[n + __popcll(same & lanemask_lt())] = (unsigned short)(c + lane);
-            n += __popcll(same);
+// Rows of a call's hit experts, written by q4_plan_kernel where a call has more
+// than 64 assignments.
+struct Q4Plan {
+    int hits;
+    int expert[kMaxExperts], first[kMaxExperts + 1];   // first: into row[]
+    unsigned short row[kMaxAssign];                    // assignments t k + j
+};
+
+// One workgroup, a thread per assignment: hit experts in ascending order, the
+// assignments of each in ascending order. Ids outside [0, E) are left out.
+__global__ __launch_bounds__(kMaxAssign) void q4_plan_kernel(const int32_t *__restrict__ idx,
+                                                             int A, int E, Q4Plan *plan) {
+    constexpr int NW = kMaxAssign / 64;
+    __shared__ int count[NW][kMaxExperts];   // of a wave; then those of the waves before
+    __shared__ int total[kMaxExperts], before[kMaxExperts], nhit[kMaxExperts / 64],
+        nrow[kMaxExperts / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    for (int i = tid; i < NW * kMaxExperts; i += kMaxAssign)
+        (&count[0][0])[i] = 0;
+    const int e = tid < A ? idx[tid] : -1;
+    const bool ok = e >= 0 && e < E;
+    uint64_t same = __ballot(ok);   // lanes of the wave with the same expert
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        const uint64_t ones = __ballot((e >> b) & 1);
+        same &= (e >> b) & 1 ? ones : ~ones;
+    }
+    __syncthreads();
+    const int rank = __popcll(same & lanemask_lt());
+    if (ok && rank == 0)
+        count[wv][e] = __popcll(same);
+    __syncthreads();
+    int n = 0, upto = 0;
+    uint64_t hits = 0;
+    if (tid < kMaxExperts) {
+        for (int w = 0; w < NW; ++w) {
+            const int c = count[w][tid];
+            count[w][tid] = n;
+            n += c;
         }
-        if (!first)
+        hits = __ballot(n > 0);
+        upto = n;
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const int u = __shfl_up(upto, s);
+            if (lane >= s)
+                upto += u;
+        }
+        if (lane == 63) {
+            nhit[wv] = __popcll(hits);
+            nrow[wv] = upto;
+        }
+    }
+    __syncthreads();
+    if (tid < kMaxExperts) {
+        int a = __popcll(hits & lanemask_lt()), b = upto - n;
+        for (int w = 0; w < wv; ++w) {
+            a += nhit[w];
+            b += nrow[w];
+        }
+        before[tid] = b;
+        if (n > 0) {
+            plan->expert[a] = tid;
+            plan->first[a] = b;
+            plan->first[a + 1] = b + n;   // (as the next one writes it)
+        }
+        if (tid == 0) {
+            int c = 0;
+            for (int w = 0; w < kMaxExperts / 64; ++w)
+                c += nhit[w];
+            plan->hits = c;
+        }
+    }
+    __syncthreads();
+    if (ok)
+        plan->row[before[e] + count[wv][e] + rank] = (unsigned short)tid;
+}
+
+// The rows of this workgroup's expert (blockIdx.y): by the plan, the expert of
+// that number; without one (at most 64 assignments) the expert of that
+// assignment, unless an earlier one has it too. row: their assignments in
+// ascending order (in LDS); returns their number, 0 where there is no work.
+__device__ __forceinline__ int q4_rows(const Q4Experts &p, int &e, unsigned short *row) {
+    const int lane = threadIdx.x & 63, A = p.N * p.k, a = blockIdx.y;
+    int n;
+    if (p.plan) {
+        if (a >= p.plan->hits)
             return 0;
+        const int f = p.plan->first[a];
+        n = p.plan->first[a + 1] - f;
+        e = p.plan->expert[a];
+        for (int i = threadIdx.x; i < n; i += blockDim.x)
+            row[i] = p.plan->row[f + i];
+    } else {
+        const int mine = lane < A ? p.idx[lane] : -1;
+        e = __builtin_amdgcn_readlane(mine, a);
+        const uint64_t same = __ballot(mine == e);
+        if (e < 0 || e >= p.E || (same & ((1ull << a) - 1ull)) != 0)
+            return 0;
+        n = __popcll(same);
+        if (threadIdx.x < 64 && (same >> lane & 1ull))
+            row[__popcll(same & lanemask_lt())] = (unsigned short)lane;
     }
     __syncthreads();
     return n;
 }
 
 // H = act(W_up[e] x + b_up[e]) of the rows of assignment blockIdx.y's expert.
-// grid: (tiles of 16 RT neurons, N k).
-template <int GS, int RT, int TT>
-__global__ __launch_bounds__(512) void q4_up_kernel(Q4Experts p, int blocks) {
-    extern __shared__ __attribute__((aligned(16))) f32x4 part[];
+// grid: (blocks of 16 RT wm neurons, N k). blocks: those of the down product.
+template <int GS, bool ZERO, int RT, int TT>
+__global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_up_kernel(Q4Experts p, Q4Waves w, int blocks) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ unsigned short row[kMaxAssign];
     const int lane = threadIdx.x & 63, A = p.N * p.k;
     if (blockIdx.y == 0)
         for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < blocks; i += gridDim.x * blockDim.x)
             p.done[i] = 0;
-    const int rows = q4_rows(p.idx, A, p.E, blockIdx.y, row);
+    int e;
+    const int rows = q4_rows(p, e, row);
     if (rows == 0)
         return;
-    const int e = p.idx[blockIdx.y], f0 = blockIdx.x * (16 * RT);
-    int64_t m[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-        m[r] = (int64_t)e * p.d_ff + min(f0 + 16 * r + (lane & 15), p.d_ff - 1);
+    const int f0 = blockIdx.x * (16 * RT * w.wm);
+    const int64_t m0 = (int64_t)e * p.d_ff;
     for (int t0 = 0; t0 < rows; t0 += 16 * TT) {
+        const int here = min(rows - t0, 16 * TT);
         auto run = [&](auto tiles) {
             constexpr int T = decltype(tiles)::value;
-            const unsigned short *xt[T];
-#pragma unroll
-            for (int i = 0; i < T; ++i)
-                xt[i] = p.x + (int64_t)(row[min(t0 + 16 * i + (lane & 15), rows - 1)] / p.k) * p.d;
-            q4_block<GS, RT, T, 1>(part, p.up, m, xt, 0, p.d, [&](int t, int r, float v) {
-                const int f = f0 + r;
-                if (t0 + t >= rows || f >= p.d_ff)
-                    return;
-                if (p.b_up)
-                    v += p.b_up[(int64_t)e * p.d_ff + f];
-                v = activate(v, p.act);
-                // the second term: what rounding to bf16 leaves (nothing of an
-                // infinity or a NaN)
-                const unsigned short hi = f32_to_bf16_bits(v);
-                const float rest = v - bf16_bits_to_f32(hi);
-                unsigned short *h = p.H + (int64_t)row[t0 + t] * p.d_ff + f;
-                h[0] = hi;
-                h[(int64_t)A * p.d_ff] =
-                    f32_to_bf16_bits(fabsf(rest) < __builtin_inff() ? rest : 0.f);
-            });
+            q4_block<GS, ZERO, RT, T, 1, q4_depth(T)>(
+                smem, p.up, m0 + f0, m0 + p.d_ff - 1, p.d, q4_tiling(w, here, 16 * RT * w.wm, p.d, q4_depth(T), GS, ZERO), here,
+                [&](int r) { return p.x + (int64_t)(row[t0 + r] / p.k) * p.d; },
+                [&](int i, int) { return min(16 * i + (lane & 15), here - 1); },
+                [&](int t, int r, float v) {
+                    const int f = f0 + r;
+                    if (t >= here || f >= p.d_ff)
+                        return;
+                    if (p.b_up)
+                        v += p.b_up[m0 + f];
+                    v = activate(v, p.act);
+                    // the second term: what rounding to bf16 leaves (nothing of
+                    // an infinity or a NaN)
+                    const unsigned short hi = f32_to_bf16_bits(v);
+                    const float rest = v - bf16_bits_to_f32(hi);
+                    unsigned short *h = p.H + (int64_t)row[t0 + t] * p.d_ff + f;
+                    h[0] = hi;
+                    h[(int64_t)A * p.d_ff] =
+                        f32_to_bf16_bits(fabsf(rest) < __builtin_inff() ? rest : 0.f);
+                });
         };
-        const int left = rows - t0;
-        if (TT == 1 || left <= 16)
+        if (TT == 1 || here <= 16)
             run(std::integral_constant<int, 1>{});
-        else if (TT == 2 || left <= 32)
+        else if (TT == 2 || here <= 32)
             run(std::integral_constant<int, TT < 2 ? TT : 2>{});
         else
             run(std::integral_constant<int, TT>{});
@@ -402,58 +583,58 @@ __global__ __launch_bounds__(512) void q4_up_kernel(Q4Experts p, int blocks) {
 
 // Y = W_down[e] h + b_down[e] of the same rows; the workgroup of a column block
 // that finishes last adds each token's choices in order. Y and the counter are
-// written and read past the XCD's own L2 (agent scope). grid: (tiles of 16 RT
-// columns, N k).
-template <int GS, int RT, int TT>
-__global__ __launch_bounds__(512) void q4_down_kernel(Q4Experts p) {
-    extern __shared__ __attribute__((aligned(16))) f32x4 part[];
+// written and read past the XCD's own L2 (agent scope). grid: (blocks of 16 RT
+// wm columns, N k).
+template <int GS, bool ZERO, int RT, int TT>
+__global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_down_kernel(Q4Experts p, Q4Waves w) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ unsigned short row[kMaxAssign];
     __shared__ int last;
     const int lane = threadIdx.x & 63, A = p.N * p.k;
-    const int rows = q4_rows(p.idx, A, p.E, blockIdx.y, row);
-    const int c0 = blockIdx.x * (16 * RT);
+    int e;
+    const int rows = q4_rows(p, e, row);
+    const int cols = 16 * RT * w.wm, c0 = blockIdx.x * cols;
     if (rows > 0) {
-        const int e = p.idx[blockIdx.y];
-        const int64_t lo = (int64_t)A * p.d_ff;
-        int64_t m[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-            m[r] = (int64_t)e * p.d + min(c0 + 16 * r + (lane & 15), p.d - 1);
-        auto store = [&](int t, int r, float v) {
-            if (p.b_down)
-                v += p.b_down[(int64_t)e * p.d + c0 + r];
-            __hip_atomic_store(p.Y + (int64_t)row[t] * p.d + c0 + r, v, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-        };
+        const int64_t m0 = (int64_t)e * p.d, lo = (int64_t)A * p.d_ff;
         for (int t0 = 0; t0 < rows; t0 += 16 * TT) {
-            const int left = rows - t0;
-            auto run = [&](auto tiles) {
-                constexpr int T = decltype(tiles)::value;
-                const unsigned short *ht[T];
-#pragma unroll
-                for (int i = 0; i < T; ++i)
-                    ht[i] = p.H + (int64_t)row[min(t0 + 16 * i + (lane & 15), rows - 1)] * p.d_ff;
-                q4_block<GS, RT, T, 2>(part, p.down, m, ht, lo, p.d_ff,
-                                       [&](int t, int r, float v) {
-                                           if (t < left && c0 + r < p.d)
-                                               store(t0 + t, r, v);
-                                       });
+            const int here = min(rows - t0, 16 * TT);
+            auto store = [&](int t, int r, float v) {
+                if (t >= here || c0 + r >= p.d)
+                    return;
+                if (p.b_down)
+                    v += p.b_down[m0 + c0 + r];
+                __hip_atomic_store(p.Y + (int64_t)row[t0 + t] * p.d + c0 + r, v, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
             };
-            if (left <= 8) {
-                // both terms of up to 8 rows fill one tile: its rows 0-7 the
-                // first terms, 8-15 the second ones, added at the end
-                const unsigned short *ht[1] = {
-                    p.H + (int64_t)row[min(t0 + (lane & 7), rows - 1)] * p.d_ff +
-                    (lane & 8 ? lo : 0)};
-                q4_block<GS, RT, 1, 1>(part, p.down, m, ht, 0, p.d_ff,
-                                       [&](int t, int r, float v) {
-                                           v += __shfl_xor(v, 32);
-                                           if (t < left && c0 + r < p.d)
-                                               store(t0 + t, r, v);
-                                       });
-            } else if (TT == 1 || left <= 16) {
+            // rows [0, here) hold the first terms, [here, 2 here) the second ones
+            auto src = [&](int r) {
+                const bool second = r >= here;
+                return p.H + (int64_t)row[t0 + (second ? r - here : r)] * p.d_ff +
+                       (second ? lo : 0);
+            };
+            auto run = [&](auto tiles) {
+                constexpr int T = decltype(tiles)::value, D = q4_depth(2 * T);
+                q4_block<GS, ZERO, RT, T, 2, D>(
+                    smem, p.down, m0 + c0, m0 + p.d - 1, p.d_ff,
+                    q4_tiling(w, 2 * here, cols, p.d_ff, D, GS, ZERO), 2 * here, src,
+                    [&](int i, int n) { return min(16 * i + (lane & 15), here - 1) + n * here; },
+                    store);
+            };
+            if (here <= 8) {
+                // both terms fill one tile: its rows 0-7 the first ones, 8-15 the
+                // second ones, added at the end
+                q4_block<GS, ZERO, RT, 1, 1, q4_depth(1)>(
+                    smem, p.down, m0 + c0, m0 + p.d - 1, p.d_ff,
+                    q4_tiling(w, 2 * here, cols, p.d_ff, q4_depth(1), GS, ZERO), 2 * here, src,
+                    [&](int, int) { return min(lane & 7, here - 1) + (lane & 8 ? here : 0); },
+                    [&](int t, int r, float v) {
+                        v += __shfl_xor(v, 32);
+                        if (t < 8)
+                            store(t, r, v);
+                    });
+            } else if (TT == 1 || here <= 16) {
                 run(std::integral_constant<int, 1>{});
-            } else if (TT == 2 || left <= 32) {
+            } else if (TT == 2 || here <= 32) {
                 run(std::integral_constant<int, TT < 2 ? TT : 2>{});
             } else {
                 run(std::integral_constant<int, TT>{});
@@ -467,18 +648,19 @@ __global__ __launch_bounds__(512) void q4_down_kernel(Q4Experts p) {
     __syncthreads();
     if (threadIdx.x == 0)
         last = __hip_atomic_fetch_add(p.done + blockIdx.x, 1, __ATOMIC_RELAXED,
-                                      __HIP_MEMORY_SCOPE_AGENT) == A - 1;
+                                      __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.y - 1;
     __syncthreads();
     if (!last)
         return;
-    for (int i = threadIdx.x; i < p.N * 16 * RT; i += blockDim.x) {
-        const int t = i / (16 * RT), c = c0 + i % (16 * RT);
+    // (agent-scope loads, as the stores)
+    for (int i = threadIdx.x; i < p.N * cols; i += blockDim.x) {
+        const int t = i / cols, c = c0 + i % cols;
         if (c >= p.d)
             continue;
         float s = 0.f;
         for (int j = 0; j < p.k; ++j) {
-            const int a = t * p.k + j, e = p.idx[a];
-            if (e >= 0 && e < p.E)
+            const int a = t * p.k + j, id = p.idx[a];
+            if (id >= 0 && id < p.E)
                 s = fmaf(p.gate[a],
                          __hip_atomic_load(p.Y + (int64_t)a * p.d + c, __ATOMIC_RELAXED,
                                            __HIP_MEMORY_SCOPE_AGENT),
@@ -580,37 +762,79 @@ __global__ __launch_bounds__(256) void q4_dequantize_kernel(const unsigned *__re
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Calls f(groups of a 128-weight step, row tiles, token tiles).
-template <typename F>
-hipError_t with_shape(int group, int rt, int tt, F f) {
-    auto tiles = [&](auto gs, auto r) {
-        if (tt == 1)
-            return f(gs, r, std::integral_constant<int, 1>{});
-        if (tt == 2)
-            return f(gs, r, std::integral_constant<int, 2>{});
-        return f(gs, r, std::integral_constant<int, 4>{});
-    };
-    auto rows = [&](auto gs) {
-        return rt == 1 ? tiles(gs, std::integral_constant<int, 1>{})
-                       : tiles(gs, std::integral_constant<int, 2>{});
-    };
-    return group == 128  ? rows(std::integral_constant<int, 1>{})
-           : group == 64 ? rows(std::integral_constant<int, 2>{})
-                         : rows(std::integral_constant<int, 4>{});
-}
 int token_tiles(int64_t n) { return n <= 16 ? 1 : n <= 32 ? 2 : 4; }
 
+template <typename F>
+hipError_t with_shape(int group, bool zero, int rt, int tt, F f) {
+    auto tiles = [&](auto gs, auto z, auto r) {
+        if (tt == 1)
+            return f(gs, z, r, std::integral_constant<int, 1>{});
+        if (tt == 2)
+            return f(gs, z, r, std::integral_constant<int, 2>{});
+        return f(gs, z, r, std::integral_constant<int, 4>{});
+    };
+    auto rows = [&](auto gs, auto z) {
+#ifdef Q4_SHAPE
+        if (rt == 2) return tiles(gs, z, std::integral_constant<int, 2>{});
+#endif
+        return tiles(gs, z, std::integral_constant<int, 1>{});
+    };
+    auto zeros = [&](auto gs) {
+        return zero ? rows(gs, std::true_type{}) : rows(gs, std::false_type{});
+    };
+    return group == 128  ? zeros(std::integral_constant<int, 1>{})
+           : group == 64 ? zeros(std::integral_constant<int, 2>{})
+                         : zeros(std::integral_constant<int, 4>{});
+}
+
+constexpr int kQ4MaxWaves = 8;
+constexpr int kQ4Lds = 72 * 1024;
+
+// Waves of a product of `blocks` times M rows of K weights, whose workgroups hold
+// up to R rows of activations in tt tiles.
 struct Q4Shape {
-    int rt, waves;
+    int rt;
+    Q4Waves w;
+    int threads, smem;
 };
-// Row tiles and waves of a product over `blocks` times M rows.
-Q4Shape q4_shape(int64_t M, int64_t K, int64_t blocks) {
+#ifdef Q4_SHAPE
+Q4Shape q4_shape(int64_t M, int64_t K, int64_t blocks, int tt, int R);
+#else
+Q4Shape q4_shape(int64_t M, int64_t K, int64_t blocks, int tt, int R) {
     Q4Shape s;
-    s.rt = blocks * M >= 16 * 2048 ? 2 : 1;
-    const int64_t steps = (K + kQ4Step - 1) / kQ4Step;
-    s.waves = steps >= 32 ? 8 : steps >= 8 ? 4 : 2;
+    const int64_t strips = blocks * ((M + 15) / 16);   // of 16 weight rows
+    s.rt = 1;
+    // about 4096 waves: 16 on a CU
+    int wk = 8;
+    while (wk > 1 && strips * wk > 4096)
+        wk /= 2;
+    s.w.wk = tt == 1 ? wk : std::min(wk, 2);
+    s.w.wm = tt == 1 && wk > 1 ? 1 : 4;
+    s.w.lds = (tt == 1 && wk < 8 ? 32 : 64) * 1024;
     return s;
 }
-size_t q4_lds(Q4Shape s, int tt) { return (size_t)s.waves * s.rt * tt * 64 * 16; }
+#endif
+Q4Shape q4_sized(int64_t M, int64_t K, int64_t blocks, int tt, int nb, int R, int group,
+                 bool zero) {
+    Q4Shape s = q4_shape(M, K, blocks, tt, R);
+    // wk D steps of activations for every form that the kernel takes; every wave has
+    // a step
+    const int64_t steps = (K + kQ4Step - 1) / kQ4Step;
+    auto least = [&] {
+        int n = 0;
+        for (int t = 1; t <= tt * nb; t *= 2)
+            n = std::max(n, (int)q4_bytes(std::min(R, 16 * t), 16 * s.rt * s.w.wm,
+                                          kQ4Step * s.w.wk * q4_depth(t), kQ4Step / group, zero) +
+                                16 * 16 * s.rt * s.w.wm * (zero ? 2 : 1));
+        return n;
+    };
+    while (s.w.wk > 1 && (s.w.wk > steps || s.w.wm * s.w.wk > kQ4MaxWaves || least() > kQ4Lds))
+        s.w.wk /= 2;
+    s.w.lds = std::max(s.w.lds, least());
+    s.threads = s.w.wm * s.w.wk * 64;
+    s.smem = std::max(s.w.lds, s.w.wk > 1 ? s.w.wm * s.w.wk * s.rt * tt * 1024 : 0);
+    return s;
+}
 
 }  // namespace
 
@@ -628,12 +852,12 @@ hipError_t launch_linear_q4(const void *x, const void *data, const void *scale, 
     p.K = (int)K;
     p.M = M;
     p.act = act;
-    const Q4Shape sh = q4_shape(M, K, 1);
-    return with_shape(group, sh.rt, token_tiles(N), [&](auto gs, auto rt, auto tt) {
+    const Q4Shape sh = q4_sized(M, K, 1, token_tiles(N), 1, (int)N, group, zero != nullptr);
+    return with_shape(group, zero != nullptr, sh.rt, token_tiles(N), [&](auto gs, auto z, auto rt, auto tt) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(tt)::value;
-        hipLaunchKernelGGL((q4_linear_kernel<GS, RT, TT>),
-                           dim3((unsigned)((M + 16 * RT - 1) / (16 * RT))), dim3(sh.waves * 64),
-                           q4_lds(sh, TT), s, p);
+        const int rows = 16 * RT * sh.w.wm;
+        hipLaunchKernelGGL((q4_linear_kernel<GS, decltype(z)::value, RT, TT>), dim3((unsigned)((M + rows - 1) / rows)),
+                           dim3(sh.threads), sh.smem, s, p, sh.w);
         return hipGetLastError();
     });
 }
@@ -644,6 +868,7 @@ Q4ExpertsLayout experts_q4_layout(int64_t N, int64_t d, int64_t d_ff, int k) {
     L.H = o;    o += up256((size_t)(N * k * d_ff) * 4);
     L.Y = o;    o += up256((size_t)(N * k * d) * 4);
     L.done = o; o += up256((size_t)((d + 15) / 16) * 4);
+    L.plan = o; o += up256(sizeof(Q4Plan));
     L.total = o;
     return L;
 }
@@ -675,25 +900,36 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     p.d_ff = (int)d_ff;
     p.k = k;
     p.act = act;
-    const unsigned A = (unsigned)(N * k);
-    const int64_t hits = std::min<int64_t>(E, A);
-    const Q4Shape us = q4_shape(d_ff, d, hits), ds = q4_shape(d, d_ff, hits);
-    const int tt = token_tiles(N);
-    const hipError_t err = with_shape(group, us.rt, tt, [&](auto gs, auto rt, auto t) {
+    const int64_t A = N * k, hits = std::min<int64_t>(E, A);
+    unsigned blocks = (unsigned)A;   // of a column: one for each assignment or hit expert
+    if (A > 64) {
+        Q4Plan *plan = reinterpret_cast<Q4Plan *>(w + L.plan);
+        hipLaunchKernelGGL(q4_plan_kernel, dim3(1), dim3(kMaxAssign), 0, s, idx, (int)A, E, plan);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess)
+            return err;
+        p.plan = plan;
+        blocks = (unsigned)hits;
+    }
+    // tiles for the rows an expert has on average, with room for more
+    const int64_t mean = (A + hits - 1) / hits;
+    const int tt = std::min(token_tiles(N), token_tiles(2 * mean + 4));
+    const int R = (int)std::min<int64_t>(A, 16 * tt);
+    const Q4Shape us = q4_sized(d_ff, d, hits, tt, 1, R, group, up[2] != nullptr);
+    const Q4Shape ds = q4_sized(d, d_ff, hits, tt, 2, 2 * R, group, down[2] != nullptr);
+    const int ur = 16 * us.rt * us.w.wm, dr = 16 * ds.rt * ds.w.wm;
+    const hipError_t err = with_shape(group, up[2] != nullptr, us.rt, tt, [&](auto gs, auto z, auto rt, auto t) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
-        hipLaunchKernelGGL((q4_up_kernel<GS, RT, TT>),
-                           dim3((unsigned)((d_ff + 16 * RT - 1) / (16 * RT)), A),
-                           dim3(us.waves * 64), q4_lds(us, TT), s, p,
-                           (int)((d + 16 * ds.rt - 1) / (16 * ds.rt)));
+        hipLaunchKernelGGL((q4_up_kernel<GS, decltype(z)::value, RT, TT>), dim3((unsigned)((d_ff + ur - 1) / ur), blocks),
+                           dim3(us.threads), us.smem, s, p, us.w, (int)((d + dr - 1) / dr));
         return hipGetLastError();
     });
     if (err != hipSuccess)
         return err;
-    return with_shape(group, ds.rt, tt, [&](auto gs, auto rt, auto t) {
+    return with_shape(group, down[2] != nullptr, ds.rt, tt, [&](auto gs, auto z, auto rt, auto t) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
-        hipLaunchKernelGGL((q4_down_kernel<GS, RT, TT>),
-                           dim3((unsigned)((d + 16 * RT - 1) / (16 * RT)), A), dim3(ds.waves * 64),
-                           q4_lds(ds, TT), s, p);
+        hipLaunchKernelGGL((q4_down_kernel<GS, decltype(z)::value, RT, TT>), dim3((unsigned)((d + dr - 1) / dr), blocks),
+                           dim3(ds.threads), ds.smem, s, p, ds.w);
         return hipGetLastError();
     });
 }
