@@ -657,6 +657,97 @@ int moe_experts_quant(const moe_tensor *x, const int32_t *topk_idx, const float 
 size_t moe_experts_quant_workspace_size(int64_t N, int64_t d, int64_t E, int64_t d_ff, int k,
                                      int32_t group);
 
+/* ---------------------------------------------------------------------------
+ * Routing with a balance bias, groups and renormalised gates, and the layer for
+ * a routing that the caller has. Same conventions as above.
+ * ------------------------------------------------------------------------- */
+
+/* How moe_router_ex chooses and weighs experts. Zero-initialise the struct and
+ * set the fields used: all zeros are softmax scores over all experts, the k
+ * largest of them as the gates.
+ * score        MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID of s = W_g x + noise: p
+ * bias         [E] MOE_F32 or NULL, added to p for the choice alone (c = p +
+ *              bias), as a balance of the experts' load adjusts it
+ * groups       the experts in this many groups of E / groups adjacent ones (0:
+ *              1; MOE_ERR_SHAPE unless it divides E, MOE_ERR_UNSUPPORTED past 64)
+ * keep_groups  groups whose experts may be chosen (0: all): those with the
+ *              largest scores, equal ones by the lower group
+ * group_best   1 or 2 (0: 1): a group's score is the sum of its that many
+ *              largest c (of one in a group of one)
+ * renormalize  nonzero: gates are divided by the sum of the chosen p
+ * scale        gates are multiplied by it; finite, >= 0 (0: 1) */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+    int32_t score;
+    const moe_tensor *bias;
+    int32_t groups;
+    int32_t keep_groups;
+    int32_t group_best;
+    int32_t renormalize;
+    float scale;
+} moe_router_opts;
+
+/* moe_router with these options (NULL: all zeros): topk_idx [N, k] int32, the k
+ * largest c in descending order (equal values: lower id first), and their gates
+ * topk_gate [N, k] fp32; scores, if not NULL, the p of all experts, [N, E]
+ * MOE_F32, for the backward or an auxiliary loss. k at most the experts of the
+ * kept groups (MOE_ERR_ARG). x, W_g and noise as moe_router's, all arithmetic
+ * fp32. A NaN score counts as -inf (p = 0); where the chosen p sum to 0,
+ * renormalised gates are 0 (those of a softmax are formed from the scores and do
+ * not underflow together); softmax scores with infinities share 1 equally. No
+ * output, nor the workspace, may overlap an input, another output or each other
+ * (MOE_ERR_ARG). workspace: moe_router_ex_workspace_size() bytes, 256-byte
+ * aligned (may be NULL when that is 0). N = 0 is valid. */
+int moe_router_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
+                  const moe_router_opts *opts, int k, int32_t *topk_idx, float *topk_gate,
+                  moe_tensor *scores, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of scratch of moe_router_ex (0 when it needs none, or on invalid sizes). */
+size_t moe_router_ex_workspace_size(int64_t N, int64_t d, int64_t E, int32_t dtype);
+
+/* Its backward, for dgate [N, k] MOE_F32 the gradient of the gates and dscores
+ * [N, E] MOE_F32 (or NULL) that of the exported scores, from an auxiliary loss:
+ *   ds the gradient of s: through the scaling, the renormalisation and the
+ *   softmax or sigmoid (the choice passes none),
+ *   dW_g = ds^T x,  dx = ds W_g + dres
+ * topk_idx and scores are the forward's; an id outside [0, E) has no gate.
+ * x [N, d] and W_g [E, d] as the forward's, bf16 x (MOE_ERR_UNSUPPORTED for
+ * fp32). dx [N, d] MOE_F32 or MOE_BF16, dres (or NULL) like it: a gradient that
+ * reaches x another way, as the layer's own; dx may be its buffer. dW_g [E, d]
+ * MOE_F32. dx or dW_g may be NULL and is then not computed (both:
+ * MOE_ERR_NULL; dres without dx: MOE_ERR_ARG). Sums are fp32 in a fixed order;
+ * products as accurate as fp32 ones, except that a bf16 dx of a softmax without
+ * renormalisation or of an auxiliary loss takes its operands to 16 bits. x, W_g,
+ * dres, dx and dW_g 16-byte aligned. No output, nor the workspace, may overlap
+ * an input otherwise, another output or each other (MOE_ERR_ARG). workspace:
+ * moe_router_backward_workspace_size() bytes, 256-byte aligned. N = 0: dW_g is
+ * zero. */
+int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_router_opts *opts,
+                        int k, const int32_t *topk_idx, const moe_tensor *scores,
+                        const moe_tensor *dgate, const moe_tensor *dscores,
+                        const moe_tensor *dres, moe_tensor *dx, moe_tensor *dW_g, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Bytes of scratch of moe_router_backward (0 for N = 0 or invalid sizes). */
+size_t moe_router_backward_workspace_size(int64_t N, int64_t d, int64_t E, int k);
+
+/* moe_forward_ex for a routing that the caller has: stats->topk_idx and
+ * stats->topk_gate are inputs (required for N > 0), the rest is as there (an id
+ * outside [0, E) takes no slot). The workspace of moe_forward serves it. */
+int moe_forward_routed(const moe_tensor *x, const moe_tensor *W_up, const moe_tensor *W_down,
+                       const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
+                       moe_stats *stats);
+
+/* Its backward: moe_backward_ex without the router. dx is the experts' part
+ * alone (moe_router_backward's dres), dgate [N, k] MOE_F32 the gradient of each
+ * gate, <dout, y> (0 for dropped choices): moe_router_backward's. The workspace
+ * of moe_backward serves it; stats as moe_forward_routed's. */
+int moe_backward_routed(const moe_tensor *x, const moe_tensor *W_up, const moe_tensor *W_down,
+                        const moe_expert_opts *opts, int k, float capacity_factor,
+                        const moe_tensor *dout, moe_tensor *dx, moe_tensor *dgate,
+                        moe_tensor *dW_up, moe_tensor *dW_down, moe_tensor *db_up,
+                        moe_tensor *db_down, moe_stats *stats);
+
 #ifdef __cplusplus
 }
 #endif

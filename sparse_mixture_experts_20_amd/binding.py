@@ -34,7 +34,9 @@ EXPORTS = ("moe_forward", "moe_workspace_size", "moe_capacity", "moe_error_strin
            "moe_linear_backward_workspace_size", "moe_layer_norm", "moe_layer_norm_backward",
            "moe_layer_norm_backward_workspace_size", "moe_quantize", "moe_dequantize",
            "moe_linear_quant", "moe_linear_quant_workspace_size", "moe_experts_quant",
-           "moe_experts_quant_workspace_size")
+           "moe_experts_quant_workspace_size", "moe_router_ex", "moe_router_ex_workspace_size",
+           "moe_router_backward", "moe_router_backward_workspace_size", "moe_forward_routed",
+           "moe_backward_routed")
 
 MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_NONE = 0, 1, 2
 ACTS = {"relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU}
@@ -66,6 +68,12 @@ class MoeExpertOpts(ctypes.Structure):
 class MoeQ4(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
                 ("group", ctypes.c_int32), ("ndim", ctypes.c_int32), ("shape", ctypes.c_int64 * 3)]
+
+
+class MoeRouterOpts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int32),
+                ("keep_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -201,6 +209,24 @@ def lib():
         L.moe_experts_quant_workspace_size.argtypes = [_i64, _i64, _i64, _i64, ctypes.c_int,
                                                     ctypes.c_int32]
         L.moe_experts_quant_workspace_size.restype = ctypes.c_size_t
+        _O = ctypes.POINTER(MoeRouterOpts)
+        L.moe_router_ex.argtypes = [_D, _D, _D, _O, ctypes.c_int, _vp, _vp, _D, _vp,
+                                    ctypes.c_size_t, _vp]
+        L.moe_router_ex.restype = ctypes.c_int
+        L.moe_router_ex_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int32]
+        L.moe_router_ex_workspace_size.restype = ctypes.c_size_t
+        L.moe_router_backward.argtypes = [_D, _D, _O, ctypes.c_int, _vp, _D, _D, _D, _D, _D, _D,
+                                          _vp, ctypes.c_size_t, _vp]
+        L.moe_router_backward.restype = ctypes.c_int
+        L.moe_router_backward_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int]
+        L.moe_router_backward_workspace_size.restype = ctypes.c_size_t
+        L.moe_forward_routed.argtypes = [_D, _D, _D, ctypes.POINTER(MoeExpertOpts), ctypes.c_int,
+                                         ctypes.c_float, _D, ctypes.POINTER(MoeStats)]
+        L.moe_forward_routed.restype = ctypes.c_int
+        L.moe_backward_routed.argtypes = [_D, _D, _D, ctypes.POINTER(MoeExpertOpts), ctypes.c_int,
+                                          ctypes.c_float, _D, _D, _D, _D, _D, _D, _D,
+                                          ctypes.POINTER(MoeStats)]
+        L.moe_backward_routed.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -1195,3 +1221,138 @@ def experts_q4(x, idx, gate, W_up: Q4, W_down: Q4, act: str = "relu", b_up=None,
          W_up.ref(index), W_down.ref(index), None if o is None else o.ref(), _pack(out, index),
          ws, wn, _stream_of(index))
     return out
+
+
+# --------------------------------------------------------------------------
+# Routing with a balance bias, groups and renormalised gates; the layer for a
+# routing that the caller has
+# --------------------------------------------------------------------------
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_opts(score, bias, groups, keep_groups, group_best, renormalize, scale, index):
+    """(``moe_router_opts`` by reference, what it points at)."""
+    if score not in SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    b = _pack(bias, index)
+    # (the bias' descriptor: the packed bytes, kept alive by the caller)
+    at = None if b is None else ctypes.cast(ctypes.c_char_p(b), ctypes.c_void_p)
+    o = MoeRouterOpts(SCORES[score], at, groups, keep_groups, group_best, int(renormalize), scale)
+    return ctypes.byref(o), (o, b)
+
+
+def route_workspace_size(N: int, d: int, E: int, dtype: torch.dtype) -> int:
+    code = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+    return int(lib().moe_router_ex_workspace_size(N, d, E, code))
+
+
+@_on_stream
+def route(x, W_g, k: int, noise=None, bias=None, score: str = "softmax", groups: int = 1,
+          keep_groups: int = 0, group_best: int = 1, renormalize: bool = False,
+          scale: float = 1.0, export_scores: bool = False, workspace=None):
+    """Run ``moe_router_ex``: ``(idx, gate, scores)``, idx int32 and gate fp32
+    [N, k], scores the fp32 [N, E] softmax or sigmoid scores with
+    ``export_scores`` (what the backward needs), else None."""
+    N, d, E = x.numel() // x.shape[-1], x.shape[-1], W_g.shape[0]
+    index, dev = _device_of(x), x.device
+    idx = torch.empty((N, k), dtype=torch.int32, device=dev)
+    gate = torch.empty((N, k), dtype=torch.float32, device=dev)
+    scores = torch.empty((N, E), dtype=torch.float32, device=dev) if export_scores else None
+    if workspace is None:
+        n = route_workspace_size(N, d, E, x.dtype)
+        workspace = alloc_workspace(n, dev) if n else None
+    ws, wn = _scratch(workspace, index)
+    o, keep = _route_opts(score, bias, groups, keep_groups, group_best, renormalize, scale, index)
+    _run(index, "moe_router_ex", lib().moe_router_ex, _pack(x, index), _pack(W_g, index),
+         _pack(noise, index), o, k, idx.data_ptr(), gate.data_ptr(), _pack(scores, index), ws, wn,
+         _stream_of(index))
+    return idx, gate, scores
+
+
+def route_backward_workspace_size(N: int, d: int, E: int, k: int) -> int:
+    return int(lib().moe_router_backward_workspace_size(N, d, E, k))
+
+
+@_on_stream
+def route_backward(x, W_g, idx, scores, dgate, dscores=None, dres=None, score: str = "softmax",
+                   renormalize: bool = False, scale: float = 1.0, need_dx: bool = True,
+                   need_dW: bool = True, dx_dtype=torch.float32, dx=None, workspace=None):
+    """Gradients of :func:`route` for ``dgate`` [N, k] (and ``dscores`` [N, E],
+    what an auxiliary loss gives the scores): ``(dx, dW_g)``, None for the ones
+    not asked for; ``dres`` is added to dx. idx and scores are the forward's."""
+    N, d, E, k = x.numel() // x.shape[-1], x.shape[-1], W_g.shape[0], idx.shape[-1]
+    index, dev = _device_of(x), x.device
+    ip, _ = _routing_ptrs(idx, dgate, N, k, index)
+    if dx is None and need_dx:
+        dx = torch.empty(x.shape, dtype=dx_dtype, device=dev)
+    dW = torch.empty((E, d), dtype=torch.float32, device=dev) if need_dW else None
+    if workspace is None:
+        n = route_backward_workspace_size(N, d, E, k)
+        workspace = alloc_workspace(n, dev) if n else None
+    ws, wn = _scratch(workspace, index)
+    o, keep = _route_opts(score, None, 1, 0, 1, renormalize, scale, index)
+    _run(index, "moe_router_backward", lib().moe_router_backward, _pack(x, index),
+         _pack(W_g, index), o, k, ip, _pack(scores, index), _pack(dgate, index),
+         _pack(dscores, index), _pack(dres, index), _pack(dx, index), _pack(dW, index), ws, wn,
+         _stream_of(index))
+    return dx, dW
+
+
+@_on_stream
+def forward_routed(x, idx, gate, W_up, W_down, capacity_factor: float, out=None, workspace=None,
+                   act: str = "relu", b_up=None, b_down=None, dropout=None,
+                   router_stats: bool = False):
+    """Run ``moe_forward_routed``: :func:`forward` for the routing ``idx`` (int32)
+    and ``gate`` (fp32) [N, k]. Returns ``(out, Stats)``."""
+    N, d, k = x.numel() // x.shape[-1], x.shape[-1], idx.shape[-1]
+    E, d_ff = W_up.shape[0], W_up.shape[1]
+    index, dev = _device_of(x), x.device
+    ip, gp = _routing_ptrs(idx, gate, N, k, index)
+    if out is None:
+        out = torch.empty_like(x)
+    if workspace is None:
+        workspace = alloc_workspace(workspace_size(N, d, E, d_ff, k, capacity_factor, x.dtype),
+                                    dev)
+    slot = torch.empty((N, k), dtype=torch.int32, device=dev)
+    used = torch.empty((E,), dtype=torch.int32, device=dev)
+    dem, drp, gsum = _router_stats(E, dev, router_stats)
+    ws, wn = _scratch(workspace, index)
+    st = MoeStats(_stream_of(index), ws, wn, ip, gp, _ptr(slot), _ptr(used), -1, _ptr(dem),
+                  _ptr(drp), _ptr(gsum), None)
+    _pack(b_up, index), _pack(b_down, index)   # (same checks as every tensor)
+    o = _opts(act, b_up, b_down, dropout)
+    _run(index, "moe_forward_routed", lib().moe_forward_routed, _pack(x, index),
+         _pack(W_up, index), _pack(W_down, index), None if o is None else o.ref(), k,
+         capacity_factor, _pack(out, index), ctypes.byref(st))
+    return out, Stats(idx, gate, slot, used, int(st.capacity), dem, drp, gsum)
+
+
+@_on_stream
+def backward_routed(x, idx, gate, W_up, W_down, capacity_factor: float, dout, workspace=None,
+                    act: str = "relu", b_up=None, b_down=None, dropout=None, aux_stream=None):
+    """Run ``moe_backward_routed``: ``(dx, dgate, dW_up, dW_down, db_up, db_down)``,
+    fp32 (None for a bias the layer lacks); dx is the experts' part, to be passed
+    to :func:`route_backward` as ``dres`` with ``dgate``."""
+    N, d, k = x.numel() // x.shape[-1], x.shape[-1], idx.shape[-1]
+    E, d_ff = W_up.shape[0], W_up.shape[1]
+    index, dev = _device_of(x), x.device
+    ip, gp = _routing_ptrs(idx, gate, N, k, index)
+    f32 = dict(dtype=torch.float32, device=dev)
+    dx, dgate = torch.empty(x.shape, **f32), torch.empty((N, k), **f32)
+    dwu, dwd = torch.empty((E, d_ff, d), **f32), torch.empty((E, d, d_ff), **f32)
+    dbu = None if b_up is None else torch.empty((E, d_ff), **f32)
+    dbd = None if b_down is None else torch.empty((E, d), **f32)
+    if workspace is None:
+        workspace = alloc_workspace(
+            backward_workspace_size(N, d, E, d_ff, k, capacity_factor, x.dtype), dev)
+    ws, wn = _scratch(workspace, index)
+    aux, handle = _aux_stream(aux_stream, dev)
+    st = MoeStats(_stream_of(index), ws, wn, ip, gp, None, None, -1, None, None, None, handle)
+    _pack(b_up, index), _pack(b_down, index)   # (same checks as every tensor)
+    o = _opts(act, b_up, b_down, dropout)
+    _run(index, "moe_backward_routed", lib().moe_backward_routed, _pack(x, index),
+         _pack(W_up, index), _pack(W_down, index), None if o is None else o.ref(), k,
+         capacity_factor, _pack(dout, index), _pack(dx, index), _pack(dgate, index),
+         _pack(dwu, index), _pack(dwd, index), _pack(dbu, index), _pack(dbd, index),
+         ctypes.byref(st))
+    return dx, dgate, dwu, dwd, dbu, dbd

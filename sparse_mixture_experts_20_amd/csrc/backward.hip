@@ -35,7 +35,7 @@ __device__ __forceinline__ void split3_bits(float a, unsigned short &hi, unsigne
 
 // One wave per token: dY rows (bf16, kept choices), dg by a wave reduction in
 // a fixed butterfly order, then ds for every choice (dropped ones have dg 0
-// but still took part in the softmax). Y holds the experts' outputs, the
+// but still took part in the softmax); with `gates`, dg itself. Y holds the experts' outputs, the
 // values the forward combined: fp32 rows, or (ysh not NULL) the compact fp16
 // rows with one exponent shift per kYGroup columns; 8 columns per lane and
 // load.
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
     const unsigned short *__restrict__ dout, const void *__restrict__ Y,
     const signed char *__restrict__ ysh, const float *__restrict__ gate,
     const int32_t *__restrict__ slot, int N, int d, int k, unsigned short *__restrict__ dY,
-    float *__restrict__ ds, Dropout dp) {
+    float *__restrict__ ds, Dropout dp, bool gates) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= N)
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
         float v = 0.f;
         for (int j = 0; j < k; ++j)
             if (j == lane)
-                v = gate[t * k + j] * (dg[j] - gdg);
+                v = gates ? dg[j] : gate[t * k + j] * (dg[j] - gdg);
         ds[t * k + lane] = v;
     }
 }
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(256) void transpose_rows_kernel(
 }
 
 // dx[t] = sum over kept j of dXa[t*k + j] + sum over j of ds[t, j] W_g[idx[t, j]],
-// in that order; one thread per 4 columns.
+// in that order (the first sum alone without Wg); one thread per 4 columns.
 __global__ __launch_bounds__(256) void dx_kernel(const float *__restrict__ dXa,
                                                  const float *__restrict__ ds,
                                                  const int32_t *__restrict__ idx,
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256) void dx_kernel(const float *__restrict__ dXa,
         if (slot[a] >= 0)
             acc += *reinterpret_cast<const f32x4 *>(dXa + a * d + c);
     }
-    for (int j = 0; j < k; ++j) {
+    for (int j = 0; Wg && j < k; ++j) {
         const int64_t a = t * k + j;
         const int e = idx[a];
         if (e < 0 || e >= E)   // not an expert: no score, no gradient (as in the dispatch)
@@ -325,12 +325,13 @@ __global__ __launch_bounds__(256) void dx_kernel(const float *__restrict__ dXa,
 
 hipError_t launch_combine_backward(const void *dout, const void *Y, const signed char *ysh,
                                    const float *gate, const int32_t *slot, int64_t N, int64_t d,
-                                   int k, void *dY, float *ds, hipStream_t s, Dropout dp) {
+                                   int k, void *dY, float *ds, hipStream_t s, Dropout dp,
+                                   bool gates) {
     if (N == 0)
         return hipSuccess;
     hipLaunchKernelGGL(combine_backward_kernel, dim3((unsigned)((N + 3) / 4)), dim3(256), 0, s,
                        static_cast<const unsigned short *>(dout), Y, ysh, gate, slot, (int)N,
-                       (int)d, k, static_cast<unsigned short *>(dY), ds, dp);
+                       (int)d, k, static_cast<unsigned short *>(dY), ds, dp, gates);
     return hipGetLastError();
 }
 

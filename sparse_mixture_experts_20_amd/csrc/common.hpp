@@ -243,10 +243,11 @@ hipError_t launch_batched_gemm_bf16(const void *A, const void *W, int64_t M, int
 // with dg = <dout, Y> (Y: the experts' outputs, assignment-major, fp32 or,
 // with ysh, compact as launch_expert_down writes them). d % 8 == 0.
 // With dropout, dY = gate * dout * (the dropout factor of each Y element).
+// gates: dg goes to ds instead.
 hipError_t launch_combine_backward(const void *dout, const void *Y, const signed char *ysh,
                                    const float *gate, const int32_t *slot, int64_t N, int64_t d,
                                    int k, void *dY, float *ds, hipStream_t s,
-                                   Dropout dp = Dropout{});
+                                   Dropout dp = Dropout{}, bool gates = false);
 // dsT3 [S][E][3*Tc] bf16: exact three-term split of ds(s*Tc + i, e) at columns
 // i, Tc + i, 2*Tc + i (tokens chunked by Tc).
 hipError_t launch_ds_split(const float *ds, const int32_t *idx, int64_t N, int64_t Tc, int64_t S,
@@ -267,7 +268,8 @@ hipError_t launch_chunk_sum(const float *part, int64_t S, int64_t n, float *out,
 hipError_t launch_transpose_rows(const void *src, int64_t C, int64_t ceff, const int32_t *used,
                                  int64_t nrows, const int32_t *slot_token, int k, int map,
                                  int64_t Kp, int copies, int batch, void *out, hipStream_t s);
-// dx = sum of the kept choices' dX rows + sum_j ds[t, j] W_g[idx[t, j]] (fp32, d % 4 == 0);
+// dx = sum of the kept choices' dX rows + sum_j ds[t, j] W_g[idx[t, j]] (fp32, d % 4 == 0;
+// the second sum only with Wg);
 // ids outside [0, E) contribute nothing.
 hipError_t launch_dx(const float *dXa, const float *ds, const int32_t *idx, const int32_t *slot,
                      const float *Wg, int64_t N, int64_t d, int E, int k, float *dx,
@@ -377,5 +379,47 @@ hipError_t launch_quantize_q4(bool bf16, const void *W, int64_t n, int group, vo
                               void *scale, void *zero, hipStream_t s);
 hipError_t launch_dequantize_q4(bool bf16, const void *data, const void *scale, const void *zero,
                                 int64_t n, int group, void *W, hipStream_t s);
+
+}  // namespace moe
+
+// ---------------------------------------------------------------------------
+// Routing with a balance bias, groups and renormalised gates (route.hip).
+// ---------------------------------------------------------------------------
+namespace moe {
+
+struct RouteRule {
+    int E, k;
+    int sigmoid;             // else softmax over all experts
+    int groups, keep, best;  // groups of E / groups experts; kept; best c of a group's score
+    int group_bits;          // 2^group_bits >= groups
+    int renorm;
+    float scale;
+    const float *bias;       // [E] or NULL
+};
+size_t route_workspace_bytes(bool bf16, int64_t N, int64_t d, int E);
+// aligned: 16-byte aligned data (fp32 rows; bf16 ones need it).
+hipError_t launch_route(bool bf16, bool aligned, const void *x, const float *wg,
+                        const float *noise, int64_t N, int64_t d, const RouteRule &r,
+                        int32_t *idx, float *gate, float *scores, void *ws, hipStream_t s);
+// The router's partial scores for more than 32 experts (router.hip): P (in ws),
+// [ns][N][router_padded_experts(E)].
+hipError_t launch_router_partials(const void *x, const float *wg, int64_t N, int64_t d, int E,
+                                  void *ws, float *&P, int &ns, hipStream_t s);
+
+// Its backward (route_backward.hip), bf16 x, d % 8 == 0: whether ds has E values a
+// token (else k); workspace regions (byte offsets) for `products` products of split
+// operands in dx (0: ds has k values); dx (fp32 or bf16) or dW may be NULL.
+inline bool route_backward_dense(bool sigmoid, bool renorm, bool dp) {
+    return dp || (!sigmoid && !renorm);
+}
+struct RouteBackwardLayout {
+    size_t ds, ds3, part, dsx, wx, total;
+};
+RouteBackwardLayout route_backward_layout(int64_t N, int64_t d, int E, int k, int products);
+hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *idx,
+                                 const float *p, const float *dgate, const float *dp,
+                                 const void *dres, int64_t N, int64_t d, int E, int k, int sigmoid,
+                                 int renorm, float scale, void *dx, bool dx32, float *dW,
+                                 void *ws, hipStream_t s);
 
 }  // namespace moe

@@ -256,6 +256,35 @@ int check_router_args(const moe_tensor *x, const moe_tensor *W_g, const moe_tens
     return MOE_OK;
 }
 
+// The same for a routing in stats: x, k and the experts' number, from W_up.
+int check_routed_args(const moe_tensor *x, const moe_tensor *W_up, int k, const moe_stats *stats,
+                      int64_t &N, int64_t &d, int64_t &E) {
+    if (!x)
+        return MOE_ERR_NULL;
+    if (!act_rows(x, N, d))
+        return MOE_ERR_SHAPE;
+    if (N > 0 && (!x->data || !stats->topk_idx || !stats->topk_gate))
+        return MOE_ERR_NULL;
+    if (!valid_dtype(x->dtype))
+        return MOE_ERR_DTYPE;
+    if (W_up->ndim != 3 || W_up->shape[0] <= 0)
+        return MOE_ERR_SHAPE;
+    E = W_up->shape[0];
+    if (k < 1 || k > E)
+        return MOE_ERR_ARG;
+    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK)
+        return MOE_ERR_UNSUPPORTED;
+    if (N * (int64_t)k >= ((int64_t)1 << 31) || d > INT32_MAX)
+        return MOE_ERR_UNSUPPORTED;
+    if (x->dtype == MOE_BF16) {
+        if (d % 8 != 0)
+            return MOE_ERR_UNSUPPORTED;
+        if (!aligned(x->data, 16))
+            return MOE_ERR_ALIGN;
+    }
+    return MOE_OK;
+}
+
 // Expert variant options: activation and fp32 biases [E, d_ff] / [E, d].
 struct ExpertOpts {
     int act = moe::kActRelu;
@@ -754,14 +783,16 @@ int moe_combine_compact(int64_t N, int64_t d, int k, const void *Y16, const int8
                                                   out->dtype, static_cast<hipStream_t>(stream)));
 }
 
-int moe_forward_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
-                   const moe_tensor *W_up, const moe_tensor *W_down,
-                   const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
-                   moe_stats *stats) {
+// The forward; `routed`: for the routing in stats (W_g and noise are not used).
+static int forward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
+                        const moe_tensor *W_up, const moe_tensor *W_down,
+                        const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
+                        moe_stats *stats, bool routed) {
     if (!stats || !W_up || !W_down || !out)
         return MOE_ERR_NULL;
     int64_t N, d, E;
-    int rc = check_router_args(x, W_g, noise, k, N, d, E);
+    int rc = routed ? check_routed_args(x, W_up, k, stats, N, d, E)
+                    : check_router_args(x, W_g, noise, k, N, d, E);
     if (rc != MOE_OK)
         return rc;
     if (!cf_ok(capacity_factor))
@@ -823,9 +854,11 @@ int moe_forward_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor 
     signed char *ysh = x->dtype == MOE_BF16 ? reinterpret_cast<signed char *>(ws + L.Ysh) : nullptr;
     stats->capacity = m.C;
 
-    rc = router_checked(x, W_g, noise, N, d, E, k, idx, gate, ws + L.router, s);
-    if (rc != MOE_OK)
-        return rc;
+    if (!routed) {
+        rc = router_checked(x, W_g, noise, N, d, E, k, idx, gate, ws + L.router, s);
+        if (rc != MOE_OK)
+            return rc;
+    }
     MOE_TRY(moe::launch_dispatch(idx, gate, N, (int)E, k, m.ceff, slot, used, slot_token, tiles,
                                  stats->expert_demand, stats->expert_drops,
                                  stats->expert_gate_sum, ws + L.dispatch, s));
@@ -844,6 +877,20 @@ int moe_forward_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor 
     else
         MOE_TRY(moe::launch_combine(Y, 0, gate, slot, N, d, k, out->data, out->dtype, s));
     return MOE_OK;
+}
+
+int moe_forward_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
+                   const moe_tensor *W_up, const moe_tensor *W_down,
+                   const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
+                   moe_stats *stats) {
+    return forward_call(x, W_g, noise, W_up, W_down, opts, k, capacity_factor, out, stats, false);
+}
+
+int moe_forward_routed(const moe_tensor *x, const moe_tensor *W_up, const moe_tensor *W_down,
+                       const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
+                       moe_stats *stats) {
+    return forward_call(x, nullptr, nullptr, W_up, W_down, opts, k, capacity_factor, out, stats,
+                        true);
 }
 
 int moe_forward(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
@@ -918,11 +965,13 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
                          const moe_expert_opts *opts, int k, float capacity_factor,
                          const moe_tensor *dout, moe_tensor *dx, moe_tensor *dW_g,
                          moe_tensor *dW_up, moe_tensor *dW_down, moe_tensor *db_up,
-                         moe_tensor *db_down, moe_stats *stats, bool saved) {
+                         moe_tensor *db_down, moe_stats *stats, bool saved,
+                         moe_tensor *dgate = nullptr, bool routed = false) {
     if (!stats || !W_up || !W_down || !dout)
         return MOE_ERR_NULL;
     int64_t N, d, E;
-    int rc = check_router_args(x, W_g, noise, k, N, d, E);
+    int rc = routed ? check_routed_args(x, W_up, k, stats, N, d, E)
+                    : check_router_args(x, W_g, noise, k, N, d, E);
     if (rc != MOE_OK)
         return rc;
     if (!cf_ok(capacity_factor))
@@ -943,14 +992,15 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
     {
         const int64_t e_dx[2] = {N, d}, e_wg[2] = {E, d}, e_up[3] = {E, d_ff, d},
                       e_dn[3] = {E, d, d_ff};
-        if (!dx || !dW_g || !dW_up || !dW_down)
+        const int64_t e_g[2] = {N, k};
+        if (!dx || (routed ? !dgate : !dW_g) || !dW_up || !dW_down)
             return MOE_ERR_NULL;
         int64_t xN, xd;
         if (dx->dtype != MOE_F32)
             return MOE_ERR_DTYPE;
         if (!act_rows(dx, xN, xd) || xN != e_dx[0] || xd != e_dx[1])
             return MOE_ERR_SHAPE;
-        if ((rc = check_grad(dW_g, 2, e_wg)) != MOE_OK ||
+        if ((rc = routed ? check_grad(dgate, 2, e_g) : check_grad(dW_g, 2, e_wg)) != MOE_OK ||
             (rc = check_grad(dW_up, 3, e_up)) != MOE_OK ||
             (rc = check_grad(dW_down, 3, e_dn)) != MOE_OK)
             return rc;
@@ -982,16 +1032,18 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
     if (rc != MOE_OK)
         return rc;
     // the weight gradients are written even without tokens
-    if (!dW_g->data || !dW_up->data || !dW_down->data)
+    if ((!routed && !dW_g->data) || !dW_up->data || !dW_down->data)
         return MOE_ERR_NULL;
-    if (!aligned(dW_g->data, 16) || !aligned(dW_up->data, 16) || !aligned(dW_down->data, 16))
+    if ((!routed && !aligned(dW_g->data, 16)) || !aligned(dW_up->data, 16) ||
+        !aligned(dW_down->data, 16))
         return MOE_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(stats->stream);
     if (N == 0) {
         // no tokens: every gradient is zero
         // (fill kernels, not memset nodes: the call may be captured in a graph)
         stats->capacity = 0;
-        MOE_TRY(moe::launch_fill_i32(static_cast<int32_t *>(dW_g->data), E * d, 0, s));
+        if (!routed)
+            MOE_TRY(moe::launch_fill_i32(static_cast<int32_t *>(dW_g->data), E * d, 0, s));
         MOE_TRY(moe::launch_fill_i32(static_cast<int32_t *>(dW_up->data), E * d_ff * d, 0, s));
         MOE_TRY(moe::launch_fill_i32(static_cast<int32_t *>(dW_down->data), E * d * d_ff, 0, s));
         if (db_up)
@@ -1003,8 +1055,10 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
         return zero_router_stats(E, stats->expert_demand, stats->expert_drops,
                                  stats->expert_gate_sum, s);
     }
-    if (!W_up->data || !W_down->data || !dout->data || !dx->data)
+    if (!W_up->data || !W_down->data || !dout->data || !dx->data || (routed && !dgate->data))
         return MOE_ERR_NULL;
+    if (routed && !aligned(dgate->data, 4))
+        return MOE_ERR_ALIGN;
     if (!stats->workspace)
         return MOE_ERR_NULL;
     if (!aligned(stats->workspace, kAlign))
@@ -1045,7 +1099,9 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
     // chunk on the exact split of ds, then the chunks summed in order
     MOE_TRY(moe::launch_combine_backward(dout->data, Y,
                                          reinterpret_cast<const signed char *>(ws + L.Ysh), gate,
-                                         slot, N, d, k, dY, ds, s, o.drop));
+                                         slot, N, d, k, dY,
+                                         routed ? static_cast<float *>(dgate->data) : ds, s,
+                                         o.drop, routed));
     // fork: the aux stream s2 takes the router-weight gradient and (when the
     // products read K-major) the down-projection weight gradient; both read
     // only the forward state, ds and dY, and write buffers of their own. The
@@ -1055,12 +1111,14 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
     if (rc != MOE_OK)
         return rc;
     const hipStream_t s2 = fork.s2;
-    MOE_TRY(moe::launch_ds_split(ds, idx, N, Tc, S, Ei, k, dsT3, s2));
-    MOE_TRY(moe::launch_transpose_rows(x->data, d, Tc, nullptr, N, nullptr, k, 0, Tc, 3, (int)S,
-                                       xT3, s2));
-    MOE_TRY(moe::launch_batched_gemm_bf16(dsT3, xT3, E, 3 * Tc, d, (int)S, E * 3 * Tc,
-                                          d * 3 * Tc, E * d, gpart, s2));
-    MOE_TRY(moe::launch_chunk_sum(gpart, S, E * d, static_cast<float *>(dW_g->data), s2));
+    if (!routed) {
+        MOE_TRY(moe::launch_ds_split(ds, idx, N, Tc, S, Ei, k, dsT3, s2));
+        MOE_TRY(moe::launch_transpose_rows(x->data, d, Tc, nullptr, N, nullptr, k, 0, Tc, 3, (int)S,
+                                           xT3, s2));
+        MOE_TRY(moe::launch_batched_gemm_bf16(dsT3, xT3, E, 3 * Tc, d, (int)S, E * 3 * Tc,
+                                              d * 3 * Tc, E * d, gpart, s2));
+        MOE_TRY(moe::launch_chunk_sum(gpart, S, E * d, static_cast<float *>(dW_g->data), s2));
+    }
     const bool kmajor = ceff <= moe::kGradMaxRows;
     if (kmajor) {
         MOE_TRY(moe::launch_weight_grad(dY, d, H, d_ff, Ei, ceff, used, st, 1, 0,
@@ -1075,8 +1133,9 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
                                   used, st, tiles, dZ, rpe, s));
     MOE_TRY(moe::launch_expert_rows_f32(dZ, W_up->data, d_ff, d, Ei, k, ceff, used, st, tiles,
                                         dXa, rpe, s));
-    MOE_TRY(moe::launch_dx(dXa, ds, idx, slot, static_cast<const float *>(W_g->data), N, d, Ei,
-                           k, static_cast<float *>(dx->data), s));
+    MOE_TRY(moe::launch_dx(dXa, ds, idx, slot,
+                           routed ? nullptr : static_cast<const float *>(W_g->data), N, d, Ei, k,
+                           static_cast<float *>(dx->data), s));
     // experts, weight side: dW_down = dY^T H (on the side stream, above),
     // dW_up = dZ^T X over each expert's kept rows, read K-major by the
     // products themselves
@@ -1113,6 +1172,15 @@ int moe_backward_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor
                     moe_stats *stats) {
     return backward_call(x, W_g, noise, W_up, W_down, opts, k, capacity_factor, dout, dx, dW_g,
                          dW_up, dW_down, db_up, db_down, stats, false);
+}
+
+int moe_backward_routed(const moe_tensor *x, const moe_tensor *W_up, const moe_tensor *W_down,
+                        const moe_expert_opts *opts, int k, float capacity_factor,
+                        const moe_tensor *dout, moe_tensor *dx, moe_tensor *dgate,
+                        moe_tensor *dW_up, moe_tensor *dW_down, moe_tensor *db_up,
+                        moe_tensor *db_down, moe_stats *stats) {
+    return backward_call(x, nullptr, nullptr, W_up, W_down, opts, k, capacity_factor, dout, dx,
+                         nullptr, dW_up, dW_down, db_up, db_down, stats, false, dgate, true);
 }
 
 int moe_backward_after_forward(const moe_tensor *x, const moe_tensor *W_g,
@@ -1215,9 +1283,12 @@ static int forward_state(const BwdLayout &L, char *ws, const moe_tensor *x,
     int32_t *st = reinterpret_cast<int32_t *>(ws + L.slot_token);
     const int Ei = (int)m.E;
     const int64_t rpe = rows_per_expert(m.N, m.k, m.E, m.ceff);
-    int rc = router_checked(x, W_g, noise, m.N, m.d, m.E, m.k, idx, gate, ws + L.router, s);
-    if (rc != MOE_OK)
-        return rc;
+    if (W_g) {   // (else the routing is the caller's)
+        const int rc = router_checked(x, W_g, noise, m.N, m.d, m.E, m.k, idx, gate, ws + L.router,
+                                      s);
+        if (rc != MOE_OK)
+            return rc;
+    }
     MOE_TRY(moe::launch_dispatch(idx, gate, m.N, Ei, m.k, m.ceff, slot, used, st, tiles,
                                  stats->expert_demand, stats->expert_drops,
                                  stats->expert_gate_sum, ws + L.dispatch, s));
@@ -1921,6 +1992,193 @@ int moe_experts_quant(const moe_tensor *x, const int32_t *topk_idx, const float 
     return hip_status(moe::launch_experts_q4(x->data, topk_idx, topk_gate, up, down, W_up->group,
                                              eo.b_up, eo.b_down, N, d, (int)E, d_ff, k, eo.act,
                                              workspace, o, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Routing with a balance bias, groups and renormalised gates
+// ---------------------------------------------------------------------------
+namespace {
+
+// opts as the kernels take them (k: experts chosen of E).
+int check_route(const moe_router_opts *o, int64_t E, int k, moe::RouteRule &r) {
+    r = moe::RouteRule{};
+    r.E = (int)E;
+    r.k = k;
+    r.groups = r.keep = r.best = 1;
+    r.scale = 1.f;
+    if (o) {
+        if (o->score != MOE_SCORE_SOFTMAX && o->score != MOE_SCORE_SIGMOID)
+            return MOE_ERR_ARG;
+        if (o->groups < 0 || o->keep_groups < 0 || o->group_best < 0 || o->group_best > 2 ||
+            !isfinite(o->scale) || o->scale < 0.f)
+            return MOE_ERR_ARG;
+        r.sigmoid = o->score == MOE_SCORE_SIGMOID;
+        r.groups = o->groups ? o->groups : 1;
+        if (E % r.groups != 0)
+            return MOE_ERR_SHAPE;
+        r.keep = o->keep_groups ? o->keep_groups : r.groups;
+        if (r.keep > r.groups)
+            return MOE_ERR_ARG;
+        if (r.groups > 64)
+            return MOE_ERR_UNSUPPORTED;
+        r.best = o->group_best ? o->group_best : 1;
+        r.renorm = o->renormalize != 0;
+        r.scale = o->scale != 0.f ? o->scale : 1.f;
+        const int rc = check_vec(o->bias, E, false, r.bias);
+        if (rc != MOE_OK)
+            return rc;
+        if (!aligned(r.bias, 4))
+            return MOE_ERR_ALIGN;
+    }
+    while ((1 << r.group_bits) < r.groups)
+        ++r.group_bits;
+    return k > E / r.groups * r.keep ? MOE_ERR_ARG : MOE_OK;
+}
+
+// A matrix [N, cols] of fp32 (optional: NULL stays NULL).
+int check_f32(const moe_tensor *t, int64_t N, int64_t cols, bool required, const float *&p) {
+    p = nullptr;
+    if (!t)
+        return required ? MOE_ERR_NULL : MOE_OK;
+    if (t->dtype != MOE_F32)
+        return MOE_ERR_DTYPE;
+    if (t->ndim != 2 || t->shape[0] != N || t->shape[1] != cols)
+        return MOE_ERR_SHAPE;
+    if (N > 0 && !t->data)
+        return MOE_ERR_NULL;
+    if (!aligned(t->data, 4))
+        return MOE_ERR_ALIGN;
+    p = static_cast<const float *>(t->data);
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_router_ex_workspace_size(int64_t N, int64_t d, int64_t E, int32_t dtype) {
+    if (!valid_dtype(dtype) || N < 0 || d <= 0 || d > INT32_MAX || E <= 0 || E > MOE_MAX_EXPERTS ||
+        N >= ((int64_t)1 << 31))
+        return 0;
+    return align_up(moe::route_workspace_bytes(dtype == MOE_BF16, N, d, (int)E));
+}
+
+int moe_router_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *noise,
+                  const moe_router_opts *opts, int k, int32_t *topk_idx, float *topk_gate,
+                  moe_tensor *scores, void *workspace, size_t workspace_bytes, void *stream) {
+    int64_t N, d, E;
+    int rc = check_router_args(x, W_g, noise, k, N, d, E);
+    if (rc != MOE_OK)
+        return rc;
+    moe::RouteRule r;
+    const float *sp;
+    if ((rc = check_route(opts, E, k, r)) != MOE_OK ||
+        (rc = check_f32(scores, N, E, false, sp)) != MOE_OK)
+        return rc;
+    if (N == 0)
+        return MOE_OK;
+    if (!topk_idx || !topk_gate)
+        return MOE_ERR_NULL;
+    const bool bf16 = x->dtype == MOE_BF16;
+    if (!aligned(topk_idx, 4) || !aligned(topk_gate, 4) || !aligned(W_g->data, 4) ||
+        !aligned(x->data, bf16 ? 16 : 4) || (noise && !aligned(noise->data, 4)))
+        return MOE_ERR_ALIGN;
+    const size_t need = moe::route_workspace_bytes(bf16, N, d, (int)E);
+    if ((rc = check_scratch(workspace, workspace_bytes, need)) != MOE_OK)
+        return rc;
+    const Span to[4] = {{topk_idx, 4 * N * k},
+                        {topk_gate, 4 * N * k},
+                        {sp, 4 * N * E},
+                        {need ? workspace : nullptr, (int64_t)need}};
+    const Span in[4] = {{x->data, N * d * (bf16 ? 2 : 4)},
+                        {W_g->data, 4 * E * d},
+                        {noise ? noise->data : nullptr, 4 * N * E},
+                        {r.bias, 4 * E}};
+    if (collide(to, in))
+        return MOE_ERR_ARG;
+    return hip_status(moe::launch_route(
+        bf16, aligned(x->data, 16) && aligned(W_g->data, 16), x->data,
+        static_cast<const float *>(W_g->data),
+        noise ? static_cast<const float *>(noise->data) : nullptr, N, d, r, topk_idx, topk_gate,
+        const_cast<float *>(sp), workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_router_backward_workspace_size(int64_t N, int64_t d, int64_t E, int k) {
+    if (N <= 0 || d <= 0 || d % 8 != 0 || d > INT32_MAX || E <= 0 || E > MOE_MAX_EXPERTS ||
+        k < 1 || k > E || k > MOE_MAX_TOPK || N * (int64_t)k >= ((int64_t)1 << 31))
+        return 0;
+    return moe::route_backward_layout(N, d, (int)E, k, 6).total;   // the largest form
+}
+
+int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_router_opts *opts,
+                        int k, const int32_t *topk_idx, const moe_tensor *scores,
+                        const moe_tensor *dgate, const moe_tensor *dscores,
+                        const moe_tensor *dres, moe_tensor *dx, moe_tensor *dW_g, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    int64_t N, d, E;
+    int rc = check_router_args(x, W_g, nullptr, k, N, d, E);
+    if (rc != MOE_OK)
+        return rc;
+    if (x->dtype != MOE_BF16)
+        return MOE_ERR_UNSUPPORTED;   // the backward runs on bf16 layers
+    moe::RouteRule r;
+    const float *p, *dg, *dp;
+    if ((rc = check_route(opts, E, k, r)) != MOE_OK ||
+        (rc = check_f32(scores, N, E, true, p)) != MOE_OK ||
+        (rc = check_f32(dgate, N, k, true, dg)) != MOE_OK ||
+        (rc = check_f32(dscores, N, E, false, dp)) != MOE_OK)
+        return rc;
+    void *dxp = nullptr, *rp = nullptr;
+    float *dW = nullptr;
+    if (!dx && !dW_g)
+        return MOE_ERR_NULL;   // nothing to compute
+    if (dres && !dx)
+        return MOE_ERR_ARG;
+    if (dx) {
+        if (!valid_dtype(dx->dtype))
+            return MOE_ERR_DTYPE;
+        if ((rc = check_rows(dx, N, d, dx->dtype, true, dxp)) != MOE_OK ||
+            (rc = check_rows(dres, N, d, dx->dtype, false, rp)) != MOE_OK)
+            return rc;
+    }
+    if (dW_g) {
+        const int64_t ext[2] = {E, d};
+        if ((rc = check_grad(dW_g, 2, ext)) != MOE_OK)
+            return rc;
+        if (!dW_g->data)
+            return MOE_ERR_NULL;
+        dW = static_cast<float *>(dW_g->data);
+    }
+    if (!all_aligned16(dxp, rp, dW))
+        return MOE_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (N == 0) {
+        // no rows: the sums over them are zero (a fill kernel: the call may be captured)
+        if (dW)
+            MOE_TRY(moe::launch_fill_i32(reinterpret_cast<int32_t *>(dW), E * d, 0, s));
+        return MOE_OK;
+    }
+    if (!topk_idx)
+        return MOE_ERR_NULL;
+    if (!aligned(topk_idx, 4))
+        return MOE_ERR_ALIGN;
+    const bool dx32 = dx && dx->dtype == MOE_F32;
+    const int products = !moe::route_backward_dense(r.sigmoid, r.renorm, dp) ? 0 : dx32 ? 6 : 3;
+    const size_t need = moe::route_backward_layout(N, d, (int)E, k, products).total;
+    if ((rc = check_scratch(workspace, workspace_bytes, need)) != MOE_OK)
+        return rc;
+    const int64_t bytes = N * d * (dx32 ? 4 : 2);
+    const Span to[3] = {{dxp, bytes}, {dW, 4 * E * d}, {workspace, (int64_t)need}};
+    const Span in[6] = {{x->data, 2 * N * d}, {W_g->data, 4 * E * d}, {topk_idx, 4 * N * k},
+                        {p, 4 * N * E},       {dg, 4 * N * k},        {dp, 4 * N * E}};
+    const Span res{rp, bytes};
+    if (collide(to, in) || crosses(to[0], res) || overlap(to[1], res) || overlap(to[2], res))
+        return MOE_ERR_ARG;
+    return hip_status(moe::launch_route_backward(
+        x->data, static_cast<const float *>(W_g->data), topk_idx, p, dg, dp, rp, N, d, (int)E, k,
+        r.sigmoid, r.renorm, r.scale, dxp, dx32, dW, workspace, s));
 }
 
 }  // extern "C"

@@ -395,6 +395,22 @@ size_t router_workspace_bytes(int64_t N, int64_t d, int E) {
     return (size_t)(3 * Ep * d * 2 + 255) / 256 * 256 + (size_t)(ns * N * Ep * 4 + 255) / 256 * 256;
 }
 
+hipError_t launch_router_partials(const void *x, const float *wg, int64_t N, int64_t d, int E,
+                                  void *ws, float *&P, int &ns, hipStream_t s) {
+    const int Ep = (int)router_padded_experts(E);
+    unsigned short *wsp = static_cast<unsigned short *>(ws);
+    const int64_t groups = (int64_t)Ep * (d / 8);
+    hipLaunchKernelGGL(split_router_weights_kernel, dim3((unsigned)((groups + 255) / 256)),
+                       dim3(256), 0, s, wg, E, Ep, (int)d, router_terms_interleaved(d), wsp);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return err;
+    P = reinterpret_cast<float *>(static_cast<char *>(ws) +
+                                  (size_t)(3 * Ep * d * 2 + 255) / 256 * 256);
+    ns = router_score_splits(N, d, Ep);
+    return launch_router_scores_bf16(x, wsp, N, d, Ep, P, s);
+}
+
 hipError_t launch_router_bf16(const void *x, const float *wg, const float *noise, int64_t N,
                               int64_t d, int E, int k, int32_t *idx, float *gate, void *ws,
                               hipStream_t s) {
@@ -403,19 +419,11 @@ hipError_t launch_router_bf16(const void *x, const float *wg, const float *noise
     const int Ep = (int)router_padded_experts(E);
     if (Ep <= 16) return launch_fused<1>(x, wg, noise, N, d, E, k, idx, gate, s);
     if (Ep <= 32) return launch_fused<2>(x, wg, noise, N, d, E, k, idx, gate, s);
-    unsigned short *wsp = static_cast<unsigned short *>(ws);
-    const int64_t groups = (int64_t)Ep * (d / 8);
-    hipLaunchKernelGGL(split_router_weights_kernel, dim3((unsigned)((groups + 255) / 256)),
-                       dim3(256), 0, s, wg, E, Ep, (int)d, router_terms_interleaved(d), wsp);
-    hipError_t err = hipGetLastError();
+    float *P;
+    int ns;
+    const hipError_t err = launch_router_partials(x, wg, N, d, E, ws, P, ns, s);
     if (err != hipSuccess)
         return err;
-    float *P = reinterpret_cast<float *>(static_cast<char *>(ws) +
-                                         (size_t)(3 * Ep * d * 2 + 255) / 256 * 256);
-    err = launch_router_scores_bf16(x, wsp, N, d, Ep, P, s);
-    if (err != hipSuccess)
-        return err;
-    const int ns = router_score_splits(N, d, Ep);
     if (Ep <= 64) return launch_rank<64, 1>(P, ns, noise, N, E, Ep, k, idx, gate, s);
     if (Ep <= 128) return launch_rank<64, 2>(P, ns, noise, N, E, Ep, k, idx, gate, s);
     return launch_rank<64, 4>(P, ns, noise, N, E, Ep, k, idx, gate, s);

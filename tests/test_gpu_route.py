@@ -1,0 +1,265 @@
+"""moe_router_ex and moe_router_backward against their float64 definitions: each
+form of the score product (one kernel, ranges, the tiled product), both types,
+softmax and sigmoid, bias, groups, renormalised gates, one token to many, odd
+widths and expert counts; masks, infinities and NaN; gradients against the
+formula and against differences."""
+import pytest
+
+from tests import _gpu as G
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch_mod():
+    if not G.have_gpu():
+        pytest.skip("no HIP device")
+    import torch
+    from sparse_mixture_experts_20_amd import binding as B
+    B.lib()
+    return torch
+
+
+def _gen(torch, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+# (dtype, N, d, E, k, groups, keep, best)
+SHAPES = [
+    # one kernel (up to 64 experts)
+    ("bf16", 1, 8, 1, 1, 1, 0, 1), ("bf16", 17, 64, 8, 2, 1, 0, 1), ("bf16", 100, 1032, 16, 4, 4, 2, 2),
+    ("bf16", 2047, 4096, 8, 2, 1, 0, 1), ("bf16", 333, 2048, 30, 5, 5, 3, 1),
+    ("bf16", 65, 1000, 64, 8, 8, 4, 2), ("bf16", 70, 328, 33, 16, 1, 0, 1),
+    ("f32", 1, 1, 2, 1, 1, 0, 1), ("f32", 777, 515, 60, 6, 5, 2, 1), ("f32", 50, 1028, 24, 3, 3, 2, 2),
+    # ranges over the rows (few tokens; fp32 with many experts)
+    ("bf16", 1, 7168, 256, 8, 8, 4, 2), ("bf16", 3, 4096, 64, 2, 1, 0, 1),
+    ("bf16", 20, 2056, 100, 6, 1, 0, 1), ("bf16", 64, 1024, 256, 16, 64, 7, 2),
+    ("bf16", 33, 64, 129, 3, 1, 0, 1), ("f32", 500, 300, 256, 8, 16, 5, 1),
+    ("f32", 5, 2051, 70, 7, 7, 1, 2),
+    # the tiled product
+    ("bf16", 65, 64, 65, 4, 1, 0, 1), ("bf16", 1000, 520, 256, 8, 8, 4, 2),
+    ("bf16", 4100, 1024, 128, 2, 2, 1, 1), ("bf16", 300, 7168, 256, 8, 8, 3, 2)]
+RULES = [dict(score="softmax"), dict(score="softmax", renormalize=True, bias=True),
+         dict(score="sigmoid", renormalize=True, bias=True, scale=2.5, sigma=True),
+         dict(score="sigmoid", scale=0.5)]
+
+
+@pytest.mark.parametrize("rule", range(len(RULES)))
+@pytest.mark.parametrize("dtype,N,d,E,k,groups,keep,best", SHAPES)
+def test_route(torch_mod, dtype, N, d, E, k, groups, keep, best, rule):
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain_route as R
+    r = dict(RULES[rule])
+    G.say(f"[route] {dtype} N={N} d={d} E={E} k={k} groups={groups} keep={keep} {r}")
+    g = _gen(torch, N + d + E + rule)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, W, noise = R.inputs(g, N, d, E, dt, r.pop("sigma", False))
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda") if r.pop("bias", False) else None
+    call = dict(noise=noise, bias=bias, groups=groups, keep_groups=keep, group_best=best, **r)
+    idx, gate, p = B.route(x, W, k, export_scores=True, **call)
+    torch.cuda.synchronize()
+    want = R.scores(x, W, noise, r["score"])
+    assert bool(((p.double() - want).abs() <= R.REL * want + 1e-38).all())
+    ids, near = R.choice(want, bias, k, groups, keep, best)
+    assert float(near.double().mean()) <= 0.05 + 1.0 / N
+    assert torch.equal(idx.long()[~near], ids[~near])
+    assert bool(((idx >= 0) & (idx < E)).all())
+    gw = R.gates(want, idx, r.get("renormalize", False), r.get("scale", 1.0))
+    assert bool(((gate.double() - gw).abs() <= 4 * R.REL * gw + 1e-38).all())
+    again = B.route(x, W, k, **call)
+    assert torch.equal(again[0], idx) and torch.equal(again[1], gate) and again[2] is None
+
+
+def test_default_options_are_softmax_over_all(torch_mod):
+    """With renormalised gates it is the layer's own router, whose ids it gives
+    and whose gates it gives to a few fp32 steps."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain_route as R
+    for N, d, E, k in ((50, 256, 8, 2), (200, 512, 100, 4), (7, 4096, 256, 8)):
+        x, W, noise = R.inputs(_gen(torch, N), N, d, E, torch.bfloat16, True)
+        i0, g0 = B.router(x, W, noise, k)
+        i1, g1, _ = B.route(x, W, k, noise=noise, renormalize=True)
+        assert torch.equal(i0, i1)
+        assert bool(((g0 - g1).abs() <= 2.0 ** -20 * g0).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N,d,E", [(6, 64, 8), (6, 4096, 200), (70, 64, 200)])
+def test_masked_and_non_finite_scores(torch_mod, score, N, d, E):
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain_route as R
+    inf, k = float("inf"), 4
+    x, W, noise = R.inputs(_gen(torch, E), N, d, E, torch.bfloat16, True)
+    lowest = torch.finfo(torch.float32).min
+    noise[0] = -inf                                  # nothing left
+    noise[1, 2:] = -inf                              # two experts left
+    noise[2] = lowest                                # the lowest value of the type
+    noise[3] = float("nan")
+    noise[4, 5], noise[4, 7] = inf, inf              # two infinite scores
+    noise[5, 3] = float("nan")
+    idx, gate, p = B.route(x, W, k, noise=noise, score=score, renormalize=True, export_scores=True)
+    plain = B.route(x, W, k, noise=noise, score=score)[1]
+    torch.cuda.synchronize()
+    assert bool(((idx >= 0) & (idx < E)).all())
+    for t in (0, 3):
+        assert idx[t].tolist() == [0, 1, 2, 3] and not bool(p[t].any())
+        assert not bool(gate[t].any()) and not bool(plain[t].any())
+    assert sorted(idx[1, :2].tolist()) == [0, 1] and not bool(gate[1, 2:].any())
+    assert abs(float(gate[1].sum()) - 1) <= 1e-6
+    # (the lowest value plus a score rounds back to it)
+    assert idx[2].tolist() == [0, 1, 2, 3]
+    if score == "softmax":
+        assert bool(((p[2] - 1.0 / E).abs() <= 2.0 ** -20 / E).all())
+        assert p[4, 5] == 0.5 and p[4, 7] == 0.5 and idx[4, :2].tolist() == [5, 7]
+    else:
+        assert not bool(p[2].any()) and not bool(gate[2].any())
+        assert p[4, 5] == 1 and p[4, 7] == 1
+    assert p[5, 3] == 0 and 3 not in idx[5].tolist()
+    assert bool(torch.isfinite(gate).all()) and bool(torch.isfinite(p).all())
+    # the other rows as without the masks
+    if N > 6:
+        clean = noise.clone()
+        clean[:6] = 0
+        ref = B.route(x, W, k, noise=clean, score=score, renormalize=True)
+        assert torch.equal(idx[6:], ref[0][6:]) and torch.equal(gate[6:], ref[1][6:])
+
+
+def test_gates_of_far_experts_do_not_underflow(torch_mod):
+    """A bias that forces experts whose softmax underflows: renormalised gates
+    come from the scores."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    x = torch.ones((1, 8), device="cuda", dtype=torch.bfloat16)
+    W = torch.zeros((4, 8), device="cuda")
+    noise = torch.tensor([[0.0, -200.0, -201.0, -300.0]], device="cuda")
+    bias = torch.tensor([0.0, 3.0, 2.0, 0.0], device="cuda")
+    idx, gate, _ = B.route(x, W, 2, noise=noise, bias=bias, renormalize=True)
+    want = torch.softmax(torch.tensor([0.0, -1.0], dtype=torch.float64), 0)
+    assert idx.tolist() == [[1, 2]]
+    assert float((gate.cpu().double() - want).abs().max()) <= 2.0 ** -20
+
+
+def test_ties_take_the_lower_id_and_group(torch_mod):
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    for N, d, E in ((3, 64, 16), (100, 64, 16), (5, 64, 256), (100, 64, 256)):
+        x = torch.ones((N, d), device="cuda", dtype=torch.bfloat16)
+        W = torch.zeros((E, d), device="cuda")
+        idx, _, _ = B.route(x, W, 6, groups=8, keep_groups=4, group_best=2, score="sigmoid")
+        assert bool((idx == torch.arange(6, device="cuda")).all())
+        W[E // 2:] = 1.0 / 64       # the upper groups win
+        idx, _, _ = B.route(x, W, 2, groups=8, keep_groups=2)
+        assert bool((idx == E // 2 + torch.arange(2, device="cuda")).all())
+
+
+# (N, d, E, k): term rows on both sides of every tile, tokens off the K-step
+BACK = [(1, 8, 1, 1), (3, 64, 5, 2), (64, 136, 8, 2), (333, 768, 8, 2), (100, 520, 21, 4),
+        (1000, 264, 60, 6), (65, 1024, 100, 16), (2047, 1032, 128, 4), (700, 2048, 200, 8),
+        (513, 7168, 256, 8)]
+
+
+@pytest.mark.parametrize("grads", ["f32", "bf16"])
+@pytest.mark.parametrize("score,renorm,aux", [("softmax", True, False), ("softmax", False, False),
+                                              ("sigmoid", True, False), ("sigmoid", False, False),
+                                              ("sigmoid", True, True), ("softmax", True, True)])
+@pytest.mark.parametrize("N,d,E,k", BACK)
+def test_backward(torch_mod, N, d, E, k, score, renorm, aux, grads):
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain as P, _plain_route as R
+    G.say(f"[route backward] N={N} d={d} E={E} k={k} {score} renorm={renorm} aux={aux} {grads}")
+    g = _gen(torch, N + d + E)
+    dt = torch.float32 if grads == "f32" else torch.bfloat16
+    x, W, _ = R.inputs(g, N, d, E, torch.bfloat16)
+    scale = 2.5 if E % 2 else 1.0
+    idx, _, p = B.route(x, W, k, score=score, export_scores=True)
+    if N > 2 and E > 2:
+        idx[1, 0], idx[2] = -1, E       # no experts: no gates
+    dgate = torch.randn((N, k), generator=g, device="cuda")
+    dp = torch.randn((N, E), generator=g, device="cuda") if aux else None
+    dres = torch.randn((N, d), generator=g, device="cuda").to(dt) if N % 2 else None
+    args = (x, W, idx, p, dgate)
+    kw = dict(dscores=dp, score=score, renormalize=renorm, scale=scale)
+    dx, dW = B.route_backward(*args, dres=dres, dx_dtype=dt, **kw)
+    torch.cuda.synchronize()
+    ref = R.backward(x, W, idx, p, dgate, dp, dres, score, renorm, scale)
+    ex = ref["dx"][1] + (ref["sixteen"] if grads == "bf16" else 0)
+    P.close(dx, ref["dx"][0], P.stored(ref["dx"][0], ex, dt), "dx")
+    P.close(dW, ref["dW"][0], P.stored(*ref["dW"], torch.float32), "dW")
+    # one alone, in place of dres, and again: the same bits
+    only, none = B.route_backward(*args, dres=dres, need_dW=False, dx_dtype=dt, **kw)
+    assert none is None and torch.equal(only, dx)
+    none, only = B.route_backward(*args, need_dx=False, **kw)
+    assert none is None and torch.equal(only, dW)
+    if dres is not None:
+        got, _ = B.route_backward(*args, dres=dres, dx=dres, need_dW=False, **kw)
+        assert got is dres and torch.equal(got, dx)
+
+
+def test_backward_accuracy(torch_mod):
+    """fp32 gradients stand within 2^-20 of the float64 ones in the 2-norm (a
+    sum of n products of random signs has an error of the order of sqrt(n) steps
+    of 2^-24, relative to a result of the order of sqrt(n) terms)."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain_route as R
+    for score, renorm in (("sigmoid", True), ("softmax", False)):
+        g = _gen(torch, 5)
+        N, d, E, k = 1024, 1024, 256, 8
+        x, W, _ = R.inputs(g, N, d, E, torch.bfloat16)
+        idx, _, p = B.route(x, W, k, score=score, export_scores=True)
+        dgate = torch.randn((N, k), generator=g, device="cuda")
+        dx, dW = B.route_backward(x, W, idx, p, dgate, score=score, renormalize=renorm)
+        ref = R.backward(x, W, idx, p, dgate, None, None, score, renorm, 1.0)
+        for got, want in ((dx, ref["dx"][0]), (dW, ref["dW"][0])):
+            assert float((got.double() - want).norm() / want.norm()) <= 2.0 ** -20
+
+
+def test_no_tokens(torch_mod):
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    x, W = torch.empty((0, 64), device="cuda", dtype=torch.bfloat16), torch.ones((6, 64), device="cuda")
+    idx, gate, p = B.route(x, W, 2, export_scores=True)
+    assert idx.shape == (0, 2) and gate.shape == (0, 2) and p.shape == (0, 6)
+    dx, dW = B.route_backward(x, W, idx, p, gate)
+    assert dx.shape == (0, 64) and not bool(dW.any())
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+def test_gradient_against_differences(torch_mod, score, renorm):
+    """Central differences of the kernel's own forward along directions of W_g,
+    all experts chosen (the choice then only orders the gates). Scores and gates
+    hold to about 2^-20 of values of order one, so with a step of 2^-6 the
+    quotient of a sum of 40 x 12 such terms holds to 2^-20 sqrt(480) / 2^-6 plus
+    third-order terms of the step (2^-12 of the gradient): 5e-3 of the norms."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    N, d, E = 40, 64, 12
+    g = _gen(torch, 3)
+    x = torch.randn((N, d), generator=g, device="cuda").to(torch.bfloat16)
+    W = torch.randn((E, d), generator=g, device="cuda") / 8
+    c = torch.randn((N, E), generator=g, device="cuda")
+    e = torch.randn((N, E), generator=g, device="cuda")
+
+    def run(W):
+        return B.route(x, W, E, score=score, renormalize=renorm, scale=1.5, export_scores=True)
+
+    def loss(W):
+        idx, gate, p = run(W)
+        return float((gate.double() * c.gather(1, idx.long()).double()).sum()
+                     + (p.double() * e.double()).sum())
+    idx, _, p = run(W)
+    _, dW = B.route_backward(x, W, idx, p, c.gather(1, idx.long()), dscores=e, score=score,
+                             renormalize=renorm, scale=1.5)
+    h = 2.0 ** -6
+    for seed in range(3):
+        v = torch.randn((E, d), generator=_gen(torch, 10 + seed), device="cuda")
+        v = v / v.norm()
+        want = (loss(W + h * v) - loss(W - h * v)) / (2 * h)
+        got = float((dW.double() * v.double()).sum())
+        assert abs(got - want) <= 5e-3 * float(dW.norm()), (got, want)
