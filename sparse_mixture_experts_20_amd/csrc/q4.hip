@@ -32,7 +32,12 @@
 namespace moe {
 namespace {
 
-constexpr int kQ4Step = 128;   // weights of a row per wave load
+constexpr int kQ4Load = 128;   // weights of a row per wave load
+// By tiles of 16 rows of activations: loads of a wave's step (two take the halves of
+// the weight rows' 128-byte lines one after the other) and steps in flight.
+constexpr int q4_loads(int tiles) { return tiles == 1 ? 2 : 1; }
+constexpr int q4_depth(int tiles) { return tiles <= 4 ? 2 : 1; }
+constexpr int q4_step(int tiles) { return kQ4Load * q4_loads(tiles); }
 constexpr int kMaxAssign = kFewMaxTokens * kMaxTopK;
 
 // (a barrier for LDS alone: the loads of the next weights stay in flight)
@@ -90,12 +95,13 @@ struct Q4Matrix {
 struct Q4Waves {
     int wm, wk, lds;   // lds: bytes for the activations and the scales
 };
-// The activations in LDS, kc columns at a time, rows of 2^sh chunks of 8 columns:
-// all of K where R rows of it fit, else as many times wk D steps as fit (the host
-// sees to it that one does).
+// The activations in LDS, rows of 2^sh chunks of 8 columns: all of K where R rows
+// of it fit, else kc columns at a time in two buffers, as many times wk D steps as
+// fit (the host sees to it that one does).
 struct Q4Tiling {
     int wm, wk, kc, sh;
 };
+constexpr int kQ4Chunks = 4;   // 16-byte chunks a thread loads at once
 __device__ __host__ __forceinline__ int log2_up(int v) {
     int s = 0;
     while ((1 << s) < v)
@@ -107,22 +113,25 @@ __device__ __host__ __forceinline__ int log2_up(int v) {
 __device__ __host__ __forceinline__ int q4_scale_stride(int groups) {
     return (groups + 7) / 8 * 8 + 8;
 }
-// Bytes of kc columns (a multiple of 128): R rows of activations, the scales and
+// Bytes of kc columns (a multiple of a step): R rows of activations, the scales and
 // zero points of WR weight rows.
 __device__ __host__ __forceinline__ int64_t q4_bytes(int R, int WR, int64_t kc, int GS, bool zero) {
-    return R * (2 * kc + 16) + (int64_t)WR * q4_scale_stride((int)(kc / kQ4Step * GS)) * (zero ? 4 : 2);
+    return R * (2 * kc + 16) + (int64_t)WR * q4_scale_stride((int)(kc / kQ4Load * GS)) * (zero ? 4 : 2);
 }
 __device__ __host__ __forceinline__ Q4Tiling q4_tiling(const Q4Waves &w, int R, int WR, int K,
-                                                       int D, int GS, bool zero) {
+                                                       int tiles, int GS, bool zero) {
+    const int step = q4_step(tiles);
     Q4Tiling t;
     t.wm = w.wm;
     t.wk = w.wk;
-    t.kc = (K + kQ4Step - 1) / kQ4Step * kQ4Step;
+    t.kc = (K + step - 1) / step * step;
     if (q4_bytes(R, WR, t.kc, GS, zero) > w.lds) {
         // (bytes a column, times 64, and those of no column)
         const int per = 128 * R + WR * GS * (zero ? 2 : 1), none = 16 * R + WR * 32 * (zero ? 2 : 1);
-        const int unit = kQ4Step * w.wk * D;
-        t.kc = (int)((int64_t)(w.lds - none) * 64 / per) / unit * unit;
+        const int unit = step * w.wk * q4_depth(tiles);
+        // no more than the threads load in one go, where that is a unit
+        const int most = max(kQ4Chunks * 64 * w.wm * w.wk * 8 / R / unit, 1);
+        t.kc = min((int)((int64_t)(w.lds / 2 - none) * 64 / per) / unit, most) * unit;
     }
     t.sh = log2_up(t.kc / 8);
     return t;
@@ -141,16 +150,17 @@ __device__ __forceinline__ u32x4 q4_order(const u32x4 &v) {
 // mlast repeat it) with its token rows: f(token row of the 16 TT, weight row of
 // the workgroup, value) for each result. src(r): row r < R of activations;
 // at(i, n): the row that this lane takes for tile i and term n of NB (whose
-// products are added). D: steps of weights in flight.
-template <int GS, bool ZERO, int RT, int TT, int NB, int D, typename SRC, typename AT,
+// products are added). TWO: K may take more than one buffer.
+template <int GS, bool ZERO, int RT, int TT, int NB, bool TWO, typename SRC, typename AT,
           typename F>
 __device__ __forceinline__ void q4_block(char *smem, const Q4Matrix &W, int64_t m0, int64_t mlast,
                                          int K, const Q4Tiling &T, int R, SRC src, AT at, F f) {
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wv / T.wk, wk = wv % T.wk, threads = blockDim.x;
-    const int KG = K / (kQ4Step / GS);   // groups of a row
-    const int steps = (K + kQ4Step - 1) / kQ4Step;
+    constexpr int NL = q4_loads(TT * NB), D = q4_depth(TT * NB), STEP = q4_step(TT * NB);
+    const int KG = K / (kQ4Load / GS);   // groups of a row
+    const int steps = (K + STEP - 1) / STEP;
     const int mine = (steps - wk + T.wk - 1) / T.wk;   // steps of this wave
 
     const unsigned char *w[RT];
@@ -158,16 +168,18 @@ __device__ __forceinline__ void q4_block(char *smem, const Q4Matrix &W, int64_t 
     for (int r = 0; r < RT; ++r)
         w[r] = W.data + min(m0 + (wm * RT + r) * 16 + (lane & 15), mlast) * (K / 2) + 16 * g;
     struct Step {
-        u32x4 w[RT];
+        u32x4 w[NL][RT];
     };
     // Loads have no branches around them (past the end they repeat the last place,
     // and what they bring is not used), so that a wait can count them.
     auto load = [&](int n, Step &s) {
-        const int k = (wk + n * T.wk) * kQ4Step;
+        const int k = (wk + n * T.wk) * STEP;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-            s.w[r] = *reinterpret_cast<const u32x4 *>(
-                w[r] + (GS == 1 ? k / 2 : min(k / 2, K / 2 - 16 - 16 * g)));
+#pragma unroll
+            for (int h = 0; h < NL; ++h)
+                s.w[h][r] = *reinterpret_cast<const u32x4 *>(
+                    w[r] + min((k + h * kQ4Load) / 2, K / 2 - 16 - 16 * g));
     };
 
     // activations: chunk o of the buffer is chunk o % 2^sh of row o / 2^sh; columns
@@ -178,67 +190,103 @@ __device__ __forceinline__ void q4_block(char *smem, const Q4Matrix &W, int64_t 
         return *reinterpret_cast<const u32x4 *>(src(min(o >> T.sh, R - 1)) +
                                                 min(k0 + 8 * (o & cmask), K - 8));
     };
-    auto put = [&](int o, int k0, const u32x4 &v) {
+    auto put = [&](char *buf, int o, int k0, const u32x4 &v) {
         const int c = o & cmask;
         if (o < chunks && 8 * c < T.kc)
-            *reinterpret_cast<u32x4 *>(smem + (o >> T.sh) * rowb + 16 * c) =
+            *reinterpret_cast<u32x4 *>(buf + (o >> T.sh) * rowb + 16 * c) =
                 k0 + 8 * c < K ? q4_order(v) : u32x4{0u, 0u, 0u, 0u};
     };
-    constexpr int XB = 4;   // chunks a thread loads at once
-    u32x4 first[XB];
-#pragma unroll
-    for (int i = 0; i < XB; ++i)
-        first[i] = fetch(threadIdx.x + i * threads, 0);
-    // scales (and zero points) of the buffer's groups, row by row: read by the lanes
-    // themselves, they took as many requests as the weights (fine-grained batch of
-    // 61 tokens: 1030 us, 760 without any)
-    const int WR = 16 * RT * T.wm, kcg = T.kc / (kQ4Step / GS), ss = q4_scale_stride(kcg);
-    unsigned short *sm_s = reinterpret_cast<unsigned short *>(smem + R * rowb);
-    unsigned short *sm_z = sm_s + WR * ss;
+    // scales (and zero points) of the buffer's groups, row by row, 8 at a time where
+    // every row's start and length allow: read by the lanes themselves, they took as
+    // many requests as the weights (fine-grained batch of 61 tokens: 1030 us, 760
+    // without any)
+    const int WR = 16 * RT * T.wm, kcg = T.kc / (kQ4Load / GS), ss = q4_scale_stride(kcg);
+    const int s_at = R * rowb, z_at = s_at + 2 * WR * ss;
     const bool vec = KG % 8 == 0 && kcg % 8 == 0;
-    auto stage_scales = [&](int k0) {
-        const int g0 = k0 / (kQ4Step / GS);
-        // (of a step that ends past K, groups past the last one are zeros; whole
-        // vectors have none)
-        const unsigned n = (unsigned)(vec ? min(kcg, KG - g0) / 8 : kcg);
-        for (unsigned o = threadIdx.x; o < WR * n; o += threads) {
-            const int r = (int)(o / n), c = (int)(o - r * n);
-            const int64_t from = min(m0 + r, mlast) * KG + g0;
-            if (vec) {
-                *reinterpret_cast<u32x4 *>(sm_s + r * ss + 8 * c) =
-                    *reinterpret_cast<const u32x4 *>(W.scale + from + 8 * c);
-                if (ZERO)
-                    *reinterpret_cast<u32x4 *>(sm_z + r * ss + 8 * c) =
-                        *reinterpret_cast<const u32x4 *>(W.zero + from + 8 * c);
-            } else {
-                const bool in = g0 + c < KG;
-                sm_s[r * ss + c] = in ? W.scale[from + c] : 0;
-                if (ZERO)
-                    sm_z[r * ss + c] = in ? W.zero[from + c] : 0;
-            }
+    const unsigned per_row = (unsigned)(vec ? kcg / 8 : kcg), items = WR * per_row;
+    struct Item {
+        u32x4 s, z;
+    };
+    auto fetch_scales = [&](unsigned o, int k0) {
+        o = min(o, items - 1);
+        const int r = (int)(o / per_row), c = (int)(o - r * per_row), g0 = k0 / (kQ4Load / GS);
+        const int64_t from = min(m0 + r, mlast) * KG;
+        Item v = {};
+        if (vec) {
+            const int64_t at = from + min(g0 + 8 * c, KG - 8);
+            v.s = *reinterpret_cast<const u32x4 *>(W.scale + at);
+            if (ZERO)
+                v.z = *reinterpret_cast<const u32x4 *>(W.zero + at);
+        } else {
+            const int64_t at = from + min(g0 + c, KG - 1);
+            v.s[0] = W.scale[at];
+            if (ZERO)
+                v.z[0] = W.zero[at];
         }
+        return v;
+    };
+    auto put_scales = [&](char *buf, unsigned o, int k0, const Item &v) {
+        if (o >= items)
+            return;
+        const int r = (int)(o / per_row), c = (int)(o - r * per_row);
+        if (vec) {
+            *reinterpret_cast<u32x4 *>(buf + s_at + 2 * (r * ss + 8 * c)) = v.s;
+            if (ZERO)
+                *reinterpret_cast<u32x4 *>(buf + z_at + 2 * (r * ss + 8 * c)) = v.z;
+        } else {
+            // (of a step that ends past K, groups past the last one are zeros; whole
+            // vectors have none)
+            const bool in = k0 / (kQ4Load / GS) + c < KG;
+            *reinterpret_cast<unsigned short *>(buf + s_at + 2 * (r * ss + c)) =
+                in ? (unsigned short)v.s[0] : 0;
+            if (ZERO)
+                *reinterpret_cast<unsigned short *>(buf + z_at + 2 * (r * ss + c)) =
+                    in ? (unsigned short)v.z[0] : 0;
+        }
+    };
+    // What a thread loads of a buffer at once; the rest, if any, follows in put_all.
+    constexpr int XR = kQ4Chunks, SR = 1;
+    struct Ahead {
+        u32x4 x[XR];
+        Item s[SR];
+    };
+    auto fetch_all = [&](Ahead &v, int k0) {
+#pragma unroll
+        for (int i = 0; i < SR; ++i)
+            v.s[i] = fetch_scales(threadIdx.x + i * threads, k0);
+#pragma unroll
+        for (int i = 0; i < XR; ++i)
+            v.x[i] = fetch(threadIdx.x + i * threads, k0);
+    };
+    auto put_all = [&](const Ahead &v, char *buf, int k0) {
+#pragma unroll
+        for (int i = 0; i < SR; ++i)
+            put_scales(buf, threadIdx.x + i * threads, k0, v.s[i]);
+#pragma unroll
+        for (int i = 0; i < XR; ++i)
+            put(buf, threadIdx.x + i * threads, k0, v.x[i]);
+        for (int o = threadIdx.x + XR * threads; o < chunks; o += 4 * threads) {
+            u32x4 t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                t[i] = fetch(o + i * threads, k0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                put(buf, o + i * threads, k0, t[i]);
+        }
+        for (unsigned o = threadIdx.x + SR * threads; o < items; o += threads)
+            put_scales(buf, o, k0, fetch_scales(o, k0));
     };
     Step ring[D];
     const int end = mine - 1;   // (every wave has a step)
+    {
+        Ahead v;
+        fetch_all(v, 0);
 #pragma unroll
-    for (int u = 0; u < D; ++u)
-        load(min(u, end), ring[u]);
-    auto stage = [&](int o, int k0) {
-        for (; o < chunks; o += XB * threads) {
-            u32x4 v[XB];
-#pragma unroll
-            for (int i = 0; i < XB; ++i)
-                v[i] = fetch(o + i * threads, k0);
-#pragma unroll
-            for (int i = 0; i < XB; ++i)
-                put(o + i * threads, k0, v[i]);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < XB; ++i)
-        put(threadIdx.x + i * threads, 0, first[i]);
-    stage(threadIdx.x + XB * threads, 0);
-    stage_scales(0);
+        for (int u = 0; u < D; ++u)
+            load(min(u, end), ring[u]);
+        put_all(v, smem, 0);
+    }
     barrier_lds();
 
     f32x4 tot[RT][TT];
@@ -253,20 +301,22 @@ __device__ __forceinline__ void q4_block(char *smem, const Q4Matrix &W, int64_t 
 #pragma unroll
         for (int n = 0; n < NB; ++n)
             xo[i][n] = at(i, n) * rowb;
-    const bf16x8 ones = __builtin_bit_cast(
-        bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+    // the factor of the sum of x: 1, or without zero points -(128 + 8) at once
+    constexpr unsigned one = ZERO ? 0x3f803f80u : 0xc308c308u;
+    const bf16x8 factor = __builtin_bit_cast(bf16x8, u32x4{one, one, one, one});
     const Q4Masks masks;
-    auto multiply = [&](int k, Step &s) {   // k: column in the buffer
+    auto part_of = [&](const char *buf, int k, u32x4 (&w)[RT]) {   // k: column in the buffer
         const f32x4 nil = {0.f, 0.f, 0.f, 0.f};
         f32x4 acc[RT][TT], sx[TT];
         unsigned short sv[RT][GS], zv[RT][GS];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const int at = ((wm * RT + r) * 16 + (lane & 15)) * ss + k / (kQ4Step / GS);
-            __builtin_memcpy(sv[r], __builtin_assume_aligned(sm_s + at, 2 * GS), 2 * GS);
+            const int at = ((wm * RT + r) * 16 + (lane & 15)) * ss + k / (kQ4Load / GS);
+            __builtin_memcpy(sv[r], __builtin_assume_aligned(buf + s_at + 2 * at, 2 * GS), 2 * GS);
             if (ZERO)
-                __builtin_memcpy(zv[r], __builtin_assume_aligned(sm_z + at, 2 * GS), 2 * GS);
-            q4_arrange<GS>(s.w[r]);
+                __builtin_memcpy(zv[r], __builtin_assume_aligned(buf + z_at + 2 * at, 2 * GS),
+                                 2 * GS);
+            q4_arrange<GS>(w[r]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -283,59 +333,76 @@ __device__ __forceinline__ void q4_block(char *smem, const Q4Matrix &W, int64_t 
             bf16x8 q[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r)
-                q[r] = masks.weights(s.w[r][j]);
-            const char *xb = smem + 2 * (k + q4_position<GS>(g, j));
+                q[r] = masks.weights(w[r][j]);
+            const char *xb = buf + 2 * (k + q4_position<GS>(g, j));
 #pragma unroll
             for (int i = 0; i < TT; ++i)
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     const bf16x8 a = *reinterpret_cast<const bf16x8 *>(xb + xo[i][n]);
-                    sx[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, sx[i], 0, 0, 0);
+                    if (ZERO || RT > 1)
+                        sx[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, factor, sx[i], 0, 0, 0);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                    for (int r = 0; r < RT; ++r) {
+                        if (!ZERO && RT == 1)
+                            acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                a, factor, acc[r][i], 0, 0, 0);
                         acc[r][i] =
                             __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[r], acc[r][i], 0, 0, 0);
+                    }
                 }
             if (j % P == P - 1) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     const float sr = bf16_bits_to_f32(sv[r][j / P]);
-                    const float c = ZERO ? -128.f - bf16_bits_to_f32(zv[r][j / P]) : -136.f;
+                    const float c = ZERO ? -128.f - bf16_bits_to_f32(zv[r][j / P]) : 1.f;
 #pragma unroll
                     for (int i = 0; i < TT; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            tot[r][i][e] =
-                                fmaf(sr, fmaf(c, sx[i][e], acc[r][i][e]), tot[r][i][e]);
+                            tot[r][i][e] = fmaf(sr,
+                                                ZERO || RT > 1 ? fmaf(c, sx[i][e], acc[r][i][e])
+                                                               : acc[r][i][e],
+                                                tot[r][i][e]);
                 }
             }
         }
     };
-    // steps of a wave in the buffer (a multiple of D, or all of them)
-    const int per = T.kc / (kQ4Step * T.wk) + (T.kc >= K);
+    auto multiply = [&](const char *buf, int k, Step &s) {
+#pragma unroll
+        for (int h = 0; h < NL; ++h)
+            part_of(buf, k + h * kQ4Load, s.w[h]);
+    };
+    // steps of a wave in a buffer (a multiple of D, or all of them)
+    const int per = T.kc / (STEP * T.wk) + (T.kc >= K);
+    const int bytes = TWO ? (z_at + (ZERO ? 2 * WR * ss : 0) + 15) / 16 * 16 : 0;
+    char *buf = smem;
     for (int n = 0, k0 = 0;; k0 += T.kc) {
+        const bool more = TWO && k0 + T.kc < K;
+        Ahead v;
+        if (more)
+            fetch_all(v, k0 + T.kc);
         const int n1 = min(mine, n + per);
         for (; n + D <= n1; n += D) {
 #pragma unroll
             for (int u = 0; u < D; ++u) {
                 // (in this order: gathered at the loop's end, the loads would all be
                 // waited for at its start)
-                multiply((wk + (n + u) * T.wk) * kQ4Step - k0, ring[u]);
+                multiply(buf, (wk + (n + u) * T.wk) * STEP - k0, ring[u]);
                 __builtin_amdgcn_sched_barrier(0);
                 load(min(n + u + D, end), ring[u]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (k0 + T.kc >= K) {
+        if (!more) {
 #pragma unroll
             for (int u = 0; u < D; ++u)
                 if (n + u < n1)
-                    multiply((wk + (n + u) * T.wk) * kQ4Step - k0, ring[u]);
+                    multiply(buf, (wk + (n + u) * T.wk) * STEP - k0, ring[u]);
             break;
         }
-        barrier_lds();
-        stage(threadIdx.x, k0 + T.kc);
-        stage_scales(k0 + T.kc);
+        buf = smem + (buf == smem ? bytes : 0);
+        put_all(v, buf, k0 + T.kc);
         barrier_lds();
     }
     if (T.wk == 1) {
@@ -381,17 +448,18 @@ struct Q4Linear {
     int64_t M;
 };
 
-// Steps of weights in flight, by tiles of 16 rows of activations.
-constexpr int q4_depth(int rows) { return rows == 1 ? 4 : rows <= 4 ? 2 : 1; }
+// Waves of a SIMD that a form's registers leave room for.
+constexpr int q4_waves(int tt, bool two) { return tt == 1 && !two ? 4 : tt < 4 ? 3 : 2; }
 
-// grid: blocks of 16 RT WM weight rows.
-template <int GS, bool ZERO, int RT, int TT>
-__global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_linear_kernel(Q4Linear p, Q4Waves w) {
+// grid: blocks of 16 RT wm weight rows.
+template <int GS, bool ZERO, int RT, int TT, bool TWO>
+__global__ __launch_bounds__(512, q4_waves(TT, TWO)) void q4_linear_kernel(Q4Linear p,
+                                                                           Q4Waves w) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63;
-    const Q4Tiling T = q4_tiling(w, p.N, 16 * RT * w.wm, p.K, q4_depth(TT), GS, ZERO);
+    const Q4Tiling T = q4_tiling(w, p.N, 16 * RT * w.wm, p.K, TT, GS, ZERO);
     const int64_t m0 = (int64_t)blockIdx.x * (16 * RT * T.wm);
-    q4_block<GS, ZERO, RT, TT, 1, q4_depth(TT)>(
+    q4_block<GS, ZERO, RT, TT, 1, TWO>(
         smem, p.W, m0, p.M - 1, p.K, T, p.N, [&](int r) { return p.x + (int64_t)r * p.K; },
         [&](int i, int) { return min(16 * i + (lane & 15), p.N - 1); },
         [&](int t, int r, float v) {
@@ -421,6 +489,7 @@ struct Q4Experts {
     const Q4Plan *plan;           // NULL with at most 64 assignments
     unsigned short *out;          // [N, d]
     int N, d, E, d_ff, k, act;
+    int block;                    // rows of an expert at a time, at most 16 TT
 };
 
 // Rows of a call's hit experts, written by q4_plan_kernel where a call has more
@@ -532,8 +601,9 @@ __device__ __forceinline__ int q4_rows(const Q4Experts &p, int &e, unsigned shor
 
 // H = act(W_up[e] x + b_up[e]) of the rows of assignment blockIdx.y's expert.
 // grid: (blocks of 16 RT wm neurons, N k). blocks: those of the down product.
-template <int GS, bool ZERO, int RT, int TT>
-__global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_up_kernel(Q4Experts p, Q4Waves w, int blocks) {
+template <int GS, bool ZERO, int RT, int TT, bool TWO>
+__global__ __launch_bounds__(512, q4_waves(TT, TWO)) void q4_up_kernel(Q4Experts p, Q4Waves w,
+                                                                       int blocks) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ unsigned short row[kMaxAssign];
     const int lane = threadIdx.x & 63, A = p.N * p.k;
@@ -546,12 +616,12 @@ __global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_up_kernel(Q4Experts p
         return;
     const int f0 = blockIdx.x * (16 * RT * w.wm);
     const int64_t m0 = (int64_t)e * p.d_ff;
-    for (int t0 = 0; t0 < rows; t0 += 16 * TT) {
-        const int here = min(rows - t0, 16 * TT);
+    for (int t0 = 0; t0 < rows; t0 += p.block) {
+        const int here = min(rows - t0, p.block);
         auto run = [&](auto tiles) {
             constexpr int T = decltype(tiles)::value;
-            q4_block<GS, ZERO, RT, T, 1, q4_depth(T)>(
-                smem, p.up, m0 + f0, m0 + p.d_ff - 1, p.d, q4_tiling(w, here, 16 * RT * w.wm, p.d, q4_depth(T), GS, ZERO), here,
+            q4_block<GS, ZERO, RT, T, 1, TWO>(
+                smem, p.up, m0 + f0, m0 + p.d_ff - 1, p.d, q4_tiling(w, here, 16 * RT * w.wm, p.d, T, GS, ZERO), here,
                 [&](int r) { return p.x + (int64_t)(row[t0 + r] / p.k) * p.d; },
                 [&](int i, int) { return min(16 * i + (lane & 15), here - 1); },
                 [&](int t, int r, float v) {
@@ -585,8 +655,9 @@ __global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_up_kernel(Q4Experts p
 // that finishes last adds each token's choices in order. Y and the counter are
 // written and read past the XCD's own L2 (agent scope). grid: (blocks of 16 RT
 // wm columns, N k).
-template <int GS, bool ZERO, int RT, int TT>
-__global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_down_kernel(Q4Experts p, Q4Waves w) {
+template <int GS, bool ZERO, int RT, int TT, bool TWO>
+__global__ __launch_bounds__(512, q4_waves(TT, TWO)) void q4_down_kernel(Q4Experts p,
+                                                                         Q4Waves w) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ unsigned short row[kMaxAssign];
     __shared__ int last;
@@ -596,8 +667,8 @@ __global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_down_kernel(Q4Experts
     const int cols = 16 * RT * w.wm, c0 = blockIdx.x * cols;
     if (rows > 0) {
         const int64_t m0 = (int64_t)e * p.d, lo = (int64_t)A * p.d_ff;
-        for (int t0 = 0; t0 < rows; t0 += 16 * TT) {
-            const int here = min(rows - t0, 16 * TT);
+        for (int t0 = 0; t0 < rows; t0 += p.block) {
+            const int here = min(rows - t0, p.block);
             auto store = [&](int t, int r, float v) {
                 if (t >= here || c0 + r >= p.d)
                     return;
@@ -613,19 +684,19 @@ __global__ __launch_bounds__(512, TT == 1 ? 4 : 2) void q4_down_kernel(Q4Experts
                        (second ? lo : 0);
             };
             auto run = [&](auto tiles) {
-                constexpr int T = decltype(tiles)::value, D = q4_depth(2 * T);
-                q4_block<GS, ZERO, RT, T, 2, D>(
+                constexpr int T = decltype(tiles)::value;
+                q4_block<GS, ZERO, RT, T, 2, TWO>(
                     smem, p.down, m0 + c0, m0 + p.d - 1, p.d_ff,
-                    q4_tiling(w, 2 * here, cols, p.d_ff, D, GS, ZERO), 2 * here, src,
+                    q4_tiling(w, 2 * here, cols, p.d_ff, 2 * T, GS, ZERO), 2 * here, src,
                     [&](int i, int n) { return min(16 * i + (lane & 15), here - 1) + n * here; },
                     store);
             };
             if (here <= 8) {
                 // both terms fill one tile: its rows 0-7 the first ones, 8-15 the
                 // second ones, added at the end
-                q4_block<GS, ZERO, RT, 1, 1, q4_depth(1)>(
+                q4_block<GS, ZERO, RT, 1, 1, TWO>(
                     smem, p.down, m0 + c0, m0 + p.d - 1, p.d_ff,
-                    q4_tiling(w, 2 * here, cols, p.d_ff, q4_depth(1), GS, ZERO), 2 * here, src,
+                    q4_tiling(w, 2 * here, cols, p.d_ff, 1, GS, ZERO), 2 * here, src,
                     [&](int, int) { return min(lane & 7, here - 1) + (lane & 8 ? here : 0); },
                     [&](int t, int r, float v) {
                         v += __shfl_xor(v, 32);
@@ -761,23 +832,24 @@ __global__ __launch_bounds__(256) void q4_dequantize_kernel(const unsigned *__re
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Calls f(groups of a 128-weight step, row tiles, token tiles).
+// Calls f(groups of a 128-weight step, zero points, row tiles, token tiles, more
+// than one buffer).
 int token_tiles(int64_t n) { return n <= 16 ? 1 : n <= 32 ? 2 : 4; }
 
 template <typename F>
-hipError_t with_shape(int group, bool zero, int rt, int tt, F f) {
+hipError_t with_shape(int group, bool zero, int rt, int tt, bool two, F f) {
     auto tiles = [&](auto gs, auto z, auto r) {
-        if (tt == 1)
-            return f(gs, z, r, std::integral_constant<int, 1>{});
-        if (tt == 2)
-            return f(gs, z, r, std::integral_constant<int, 2>{});
-        return f(gs, z, r, std::integral_constant<int, 4>{});
+        if constexpr (decltype(r)::value == 1)   // (one token tile: one weight tile)
+            if (tt == 1)
+                return two ? f(gs, z, r, std::integral_constant<int, 1>{}, std::true_type{})
+                           : f(gs, z, r, std::integral_constant<int, 1>{}, std::false_type{});
+        if (tt <= 2)
+            return f(gs, z, r, std::integral_constant<int, 2>{}, std::true_type{});
+        return f(gs, z, r, std::integral_constant<int, 4>{}, std::true_type{});
     };
     auto rows = [&](auto gs, auto z) {
-#ifdef Q4_SHAPE
-        if (rt == 2) return tiles(gs, z, std::integral_constant<int, 2>{});
-#endif
-        return tiles(gs, z, std::integral_constant<int, 1>{});
+        return rt == 2 ? tiles(gs, z, std::integral_constant<int, 2>{})
+                       : tiles(gs, z, std::integral_constant<int, 1>{});
     };
     auto zeros = [&](auto gs) {
         return zero ? rows(gs, std::true_type{}) : rows(gs, std::false_type{});
@@ -788,7 +860,7 @@ hipError_t with_shape(int group, bool zero, int rt, int tt, F f) {
 }
 
 constexpr int kQ4MaxWaves = 8;
-constexpr int kQ4Lds = 72 * 1024;
+constexpr int kQ4Lds = 144 * 1024;
 
 // Waves of a product of `blocks` times M rows of K weights, whose workgroups hold
 // up to R rows of activations in tt tiles.
@@ -796,41 +868,67 @@ struct Q4Shape {
     int rt;
     Q4Waves w;
     int threads, smem;
+    bool two;   // more than one buffer, for some number of rows
 };
-#ifdef Q4_SHAPE
-Q4Shape q4_shape(int64_t M, int64_t K, int64_t blocks, int tt, int R);
-#else
-Q4Shape q4_shape(int64_t M, int64_t K, int64_t blocks, int tt, int R) {
+Q4Shape q4_shape(int64_t M, int64_t blocks, int tt, int R) {
     Q4Shape s;
     const int64_t strips = blocks * ((M + 15) / 16);   // of 16 weight rows
-    s.rt = 1;
-    // about 4096 waves: 16 on a CU
+    // About 4096 waves, 16 on a CU, by cutting the reduction (one Mixtral-shaped
+    // token: 31 us with 2 and 8 waves along K in the two products, 35 with 4 and 4).
     int wk = 8;
     while (wk > 1 && strips * wk > 4096)
         wk /= 2;
-    s.w.wk = tt == 1 ? wk : std::min(wk, 2);
-    s.w.wm = tt == 1 && wk > 1 ? 1 : 4;
-    s.w.lds = (tt == 1 && wk < 8 ? 32 : 64) * 1024;
+    if (tt == 1) {
+        // Waves along the rows share the activations: two where an expert has more
+        // than two rows (16 tokens, 8 experts: 23 us, 26 with one), four where the
+        // reduction is not cut.
+        s.rt = 1;
+        s.w.wm = wk == 1 ? 4 : blocks > 1 && R > 2 ? 2 : 1;
+        s.w.wk = s.w.wm == 2 ? std::min(wk, 4) : wk;
+        s.w.lds = (wk == 8 ? 64 : wk == 1 ? 48 : 32) * 1024;
+    } else {
+        // Two weight tiles a wave, which halve the reads of the activations, where
+        // they leave enough waves (Mixtral-shaped, 64 tokens: 250 us, 335 with one;
+        // 33 rows of 4096 by 14336: 46 and 29).
+        s.rt = strips >= 4096 ? 2 : 1;
+        s.w.wm = 4;
+        s.w.wk = s.rt == 2 ? 2 : std::min(wk, 2);
+        s.w.lds = 64 * 1024;
+    }
     return s;
 }
-#endif
+// Rows of an expert that one pass over its weights takes. With few on average, few:
+// all of K then fits LDS (61 tokens of the 256-expert layer, 2 rows on average: 762
+// us with passes of 4, 805 with 16, the second passes of some experts included).
+int q4_row_block(int64_t N, int64_t mean, int tt) {
+    const int64_t most = tt == 1 ? std::max<int64_t>(2 * mean, 4) : 64;
+    return (int)std::min<int64_t>(std::min<int64_t>(N, most), 16 * tt);
+}
 Q4Shape q4_sized(int64_t M, int64_t K, int64_t blocks, int tt, int nb, int R, int group,
                  bool zero) {
-    Q4Shape s = q4_shape(M, K, blocks, tt, R);
-    // wk D steps of activations for every form that the kernel takes; every wave has
-    // a step
-    const int64_t steps = (K + kQ4Step - 1) / kQ4Step;
+    Q4Shape s = q4_shape(M, blocks, tt, R);
+    // every wave has a step; two buffers of wk D of them for every form that the kernel
+    // takes, unless all of K fits
+    const int64_t steps = (K + q4_step(1) - 1) / q4_step(1), Kr = steps * q4_step(1);
+    while (s.w.wk > 1 && (s.w.wk > steps || s.w.wm * s.w.wk > kQ4MaxWaves))
+        s.w.wk /= 2;
+    const int most = s.w.lds;   // (of the shape's choice)
+    const int GS = kQ4Load / group;
     auto least = [&] {
+        const int WR = 16 * s.rt * s.w.wm;
+        if (q4_bytes(R, WR, Kr, GS, zero) <= most)
+            return (int)q4_bytes(R, WR, Kr, GS, zero);
         int n = 0;
         for (int t = 1; t <= tt * nb; t *= 2)
-            n = std::max(n, (int)q4_bytes(std::min(R, 16 * t), 16 * s.rt * s.w.wm,
-                                          kQ4Step * s.w.wk * q4_depth(t), kQ4Step / group, zero) +
-                                16 * 16 * s.rt * s.w.wm * (zero ? 2 : 1));
+            n = std::max(n, 2 * ((int)q4_bytes(std::min(R, 16 * t), WR,
+                                               q4_step(t) * s.w.wk * q4_depth(t), GS, zero) +
+                                 16 * WR * (zero ? 2 : 1)));
         return n;
     };
-    while (s.w.wk > 1 && (s.w.wk > steps || s.w.wm * s.w.wk > kQ4MaxWaves || least() > kQ4Lds))
+    while (s.w.wk > 1 && least() > kQ4Lds)
         s.w.wk /= 2;
-    s.w.lds = std::max(s.w.lds, least());
+    s.two = q4_bytes(R, 16 * s.rt * s.w.wm, Kr, GS, zero) > most;
+    s.w.lds = s.two ? std::max(most, least()) : least();
     s.threads = s.w.wm * s.w.wk * 64;
     s.smem = std::max(s.w.lds, s.w.wk > 1 ? s.w.wm * s.w.wk * s.rt * tt * 1024 : 0);
     return s;
@@ -853,10 +951,11 @@ hipError_t launch_linear_q4(const void *x, const void *data, const void *scale, 
     p.M = M;
     p.act = act;
     const Q4Shape sh = q4_sized(M, K, 1, token_tiles(N), 1, (int)N, group, zero != nullptr);
-    return with_shape(group, zero != nullptr, sh.rt, token_tiles(N), [&](auto gs, auto z, auto rt, auto tt) {
+    return with_shape(group, zero != nullptr, sh.rt, token_tiles(N), sh.two,
+                      [&](auto gs, auto z, auto rt, auto tt, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(tt)::value;
         const int rows = 16 * RT * sh.w.wm;
-        hipLaunchKernelGGL((q4_linear_kernel<GS, decltype(z)::value, RT, TT>), dim3((unsigned)((M + rows - 1) / rows)),
+        hipLaunchKernelGGL((q4_linear_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((M + rows - 1) / rows)),
                            dim3(sh.threads), sh.smem, s, p, sh.w);
         return hipGetLastError();
     });
@@ -914,21 +1013,25 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     // tiles for the rows an expert has on average, with room for more
     const int64_t mean = (A + hits - 1) / hits;
     const int tt = std::min(token_tiles(N), token_tiles(2 * mean + 4));
-    const int R = (int)std::min<int64_t>(A, 16 * tt);
+    // (an expert has more rows than tokens only where a token names it twice)
+    const int R = q4_row_block(N, mean, tt);
+    p.block = R;
     const Q4Shape us = q4_sized(d_ff, d, hits, tt, 1, R, group, up[2] != nullptr);
     const Q4Shape ds = q4_sized(d, d_ff, hits, tt, 2, 2 * R, group, down[2] != nullptr);
     const int ur = 16 * us.rt * us.w.wm, dr = 16 * ds.rt * ds.w.wm;
-    const hipError_t err = with_shape(group, up[2] != nullptr, us.rt, tt, [&](auto gs, auto z, auto rt, auto t) {
+    const hipError_t err = with_shape(group, up[2] != nullptr, us.rt, tt, us.two,
+                                      [&](auto gs, auto z, auto rt, auto t, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
-        hipLaunchKernelGGL((q4_up_kernel<GS, decltype(z)::value, RT, TT>), dim3((unsigned)((d_ff + ur - 1) / ur), blocks),
+        hipLaunchKernelGGL((q4_up_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((d_ff + ur - 1) / ur), blocks),
                            dim3(us.threads), us.smem, s, p, us.w, (int)((d + dr - 1) / dr));
         return hipGetLastError();
     });
     if (err != hipSuccess)
         return err;
-    return with_shape(group, down[2] != nullptr, ds.rt, tt, [&](auto gs, auto z, auto rt, auto t) {
+    return with_shape(group, down[2] != nullptr, ds.rt, tt, ds.two,
+                      [&](auto gs, auto z, auto rt, auto t, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
-        hipLaunchKernelGGL((q4_down_kernel<GS, decltype(z)::value, RT, TT>), dim3((unsigned)((d + dr - 1) / dr), blocks),
+        hipLaunchKernelGGL((q4_down_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((d + dr - 1) / dr), blocks),
                            dim3(ds.threads), ds.smem, s, p, ds.w);
         return hipGetLastError();
     });
