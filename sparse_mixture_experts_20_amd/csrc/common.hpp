@@ -397,10 +397,9 @@ struct RouteRule {
     const float *bias;       // [E] or NULL
 };
 size_t route_workspace_bytes(bool bf16, int64_t N, int64_t d, int E);
-// aligned: 16-byte aligned data (fp32 rows; bf16 ones need it).
-hipError_t launch_route(bool bf16, bool aligned, const void *x, const float *wg,
-                        const float *noise, int64_t N, int64_t d, const RouteRule &r,
-                        int32_t *idx, float *gate, float *scores, void *ws, hipStream_t s);
+hipError_t launch_route(bool bf16, const void *x, const float *wg, const float *noise, int64_t N,
+                        int64_t d, const RouteRule &r, int32_t *idx, float *gate, float *scores,
+                        void *ws, hipStream_t s);
 // The router's partial scores for more than 32 experts (router.hip): P (in ws),
 // [ns][N][router_padded_experts(E)].
 hipError_t launch_router_partials(const void *x, const float *wg, int64_t N, int64_t d, int E,

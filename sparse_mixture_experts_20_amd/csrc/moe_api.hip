@@ -2099,8 +2099,7 @@ int moe_router_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *
     if (collide(to, in))
         return MOE_ERR_ARG;
     return hip_status(moe::launch_route(
-        bf16, aligned(x->data, 16) && aligned(W_g->data, 16), x->data,
-        static_cast<const float *>(W_g->data),
+        bf16, x->data, static_cast<const float *>(W_g->data),
         noise ? static_cast<const float *>(noise->data) : nullptr, N, d, r, topk_idx, topk_gate,
         const_cast<float *>(sp), workspace, static_cast<hipStream_t>(stream)));
 }

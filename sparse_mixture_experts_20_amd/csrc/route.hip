@@ -210,6 +210,20 @@ __device__ __forceinline__ void route_rank(const float (&s)[Q], const RouteRule 
 
 // ---- scores --------------------------------------------------------------
 
+// Eight fp32 columns of a row from p on, of which n exist: two 16-byte loads at any
+// 4-byte address where the whole step exists.
+__device__ __forceinline__ f32x8 load_f32(const float *p, int n, bool whole) {
+    f32x8 v;
+    if (whole) {
+        __builtin_memcpy(&v, p, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i < n ? p[i] : 0.f;
+    }
+    return v;
+}
+
 // One workgroup: scores of 16 tokens for NT tiles of 16 experts, its NW waves
 // taking every NW-th step of 32 columns, added in wave order, then a wave a token
 // ranks them. (E <= 64)
@@ -230,7 +244,7 @@ __global__ __launch_bounds__(NW * 64) void route_fused_kernel(
     for (int n = 0; n < NT; ++n)
         acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int steps = (d + 31) / 32;
-    constexpr int U = NT >= 4 ? 1 : 2;
+    constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;   // steps loaded at once
     for (int c0 = wv; c0 < steps; c0 += NW * U) {
         if constexpr (BF16) {
             u32x4 a[U];
@@ -263,13 +277,18 @@ __global__ __launch_bounds__(NW * 64) void route_fused_kernel(
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = (c0 + u * NW) * 32 + ko;
-                const typename S::frag xa = S::load_tail(xr + k, d - k);
+                const int b = (c0 + u * NW) * 32, k = b + ko;
+                const bool whole = b + 32 <= d;
+                if (b >= d)
+                    break;
+                const f32x8 xa = load_f32(xr + k, d - k, whole);
+                f32x8 w[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    acc[n] = S::mma(
-                        xa, S::load_tail(wg + (int64_t)min(n * 16 + row, r.E - 1) * d + k, d - k),
-                        acc[n]);
+                    w[n] = load_f32(wg + (int64_t)min(n * 16 + row, r.E - 1) * d + k, d - k, whole);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[n] = S::mma(xa, w[n], acc[n]);
             }
         }
     }
@@ -351,11 +370,18 @@ __global__ __launch_bounds__(256) void route_scores_kernel(
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = (c + u) * 32 + ko, left = c + u < e ? d - k : 0;
-                const typename S::frag wf = S::load_tail(w + k, left);
+                const int k = (c + u) * 32 + ko;
+                const bool whole = (c + u) * 32 + 32 <= d;
+                if (c + u >= e)
+                    break;
+                const f32x8 wf = load_f32(w + k, d - k, whole);
+                f32x8 xa[TT];
 #pragma unroll
                 for (int i = 0; i < TT; ++i)
-                    acc[i] = S::mma(S::load_tail(xt[i] + k, left), wf, acc[i]);
+                    xa[i] = load_f32(xt[i] + k, d - k, whole);
+#pragma unroll
+                for (int i = 0; i < TT; ++i)
+                    acc[i] = S::mma(xa[i], wf, acc[i]);
             }
         }
     }
@@ -464,9 +490,9 @@ size_t route_workspace_bytes(bool bf16, int64_t N, int64_t d, int E) {
     return up256((size_t)p.ranges * N * p.ld * 4);
 }
 
-hipError_t launch_route(bool bf16, bool aligned, const void *xv, const float *wg,
-                        const float *noise, int64_t N, int64_t d, const RouteRule &r,
-                        int32_t *idx, float *gate, float *scores, void *ws, hipStream_t s) {
+hipError_t launch_route(bool bf16, const void *xv, const float *wg, const float *noise, int64_t N,
+                        int64_t d, const RouteRule &r, int32_t *idx, float *gate, float *scores,
+                        void *ws, hipStream_t s) {
     const RoutePlan p = route_plan(bf16, N, d, r.E);
     const RouteOut o{idx, gate, scores};
     float *P = static_cast<float *>(ws);
@@ -482,11 +508,11 @@ hipError_t launch_route(bool bf16, bool aligned, const void *xv, const float *wg
                                    s, x, wg, noise, (int)N, (int)d, r, o);
                 return hipGetLastError();
             };
-            // wide rows keep more loads in flight with more waves
+            // wide rows, and few workgroups, keep more loads in flight with more waves
             auto by_width = [&](auto nt) {
                 constexpr int most = decltype(nt)::value == 4 ? 8 : 16;
-                return d >= 1024 ? go(nt, std::integral_constant<int, most>{})
-                                 : go(nt, std::integral_constant<int, 4>{});
+                return d >= 1024 || blocks <= 512 ? go(nt, std::integral_constant<int, most>{})
+                                                  : go(nt, std::integral_constant<int, 4>{});
             };
             return r.E <= 16   ? by_width(std::integral_constant<int, 1>{})
                    : r.E <= 32 ? by_width(std::integral_constant<int, 2>{})
@@ -509,10 +535,8 @@ hipError_t launch_route(bool bf16, bool aligned, const void *xv, const float *wg
         err = launch_router_partials(xv, wg, N, d, r.E, ws, P, ns, s);
     else if (bf16)
         err = scores_by(SkinnyBf16{});
-    else if (aligned && d % 4 == 0)
-        err = scores_by(SkinnyF32<true>{});
     else
-        err = scores_by(SkinnyF32<false>{});
+        err = scores_by(SkinnyF32<true>{});   // (its products; the loads are load_f32's)
     if (err != hipSuccess || p.form == kFused)
         return err;
     auto rank = [&](auto q) {

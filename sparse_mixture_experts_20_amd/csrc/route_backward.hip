@@ -60,9 +60,39 @@ struct RouteGrad {
     int products;
 };
 
-// ds of one token per wave; lane l holds experts l, l + 64, ... and choice l.
+// The terms of W_g [E, d] as the products of dx take them: [products Ep][d].
+__device__ __forceinline__ void route_split(const float *__restrict__ wg, int E, int Ep, int d,
+                                            int products, unsigned short *__restrict__ out,
+                                            int64_t i) {   // 8 columns
+    const int per = d / 8;
+    if (i >= (int64_t)Ep * per)
+        return;
+    const int e = (int)(i / per), c = (int)(i - (int64_t)e * per) * 8;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    if (e < E) {
+        a = *reinterpret_cast<const f32x4 *>(wg + (int64_t)e * d + c);
+        b = *reinterpret_cast<const f32x4 *>(wg + (int64_t)e * d + c + 4);
+    }
+    u32x4 t[3];
+    split8(a, b, t[0], t[1], t[2]);
+#pragma unroll
+    for (int m = 0; m < 6; ++m)
+        if (m < products)
+            *reinterpret_cast<u32x4 *>(out + ((int64_t)m * Ep + e) * d + c) = t[kWgTerm[m]];
+}
+
+// ds of one token per wave; lane l holds experts l, l + 64, ... and choice l. The
+// workgroups past the tokens' (with E values a token) split W_g into wx.
 template <int Q>
-__global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N) {
+__global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
+                                                       const float *__restrict__ wg, int width,
+                                                       unsigned short *__restrict__ wx) {
+    const int blocks = (N + 3) / 4;
+    if ((int)blockIdx.x >= blocks) {
+        route_split(wg, r.E, r.Ep, width, r.products, wx,
+                    (int64_t)(blockIdx.x - blocks) * 256 + threadIdx.x);
+        return;
+    }
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= N)
@@ -153,28 +183,6 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N) {
     }
 }
 
-// The terms of W_g [E, d] as the products of dx take them: [products Ep][d].
-__global__ __launch_bounds__(256) void route_split_kernel(const float *__restrict__ wg, int E,
-                                                          int Ep, int d, int products,
-                                                          unsigned short *__restrict__ out) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // 8 columns
-    const int per = d / 8;
-    if (i >= (int64_t)Ep * per)
-        return;
-    const int e = (int)(i / per), c = (int)(i - (int64_t)e * per) * 8;
-    f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-    if (e < E) {
-        a = *reinterpret_cast<const f32x4 *>(wg + (int64_t)e * d + c);
-        b = *reinterpret_cast<const f32x4 *>(wg + (int64_t)e * d + c + 4);
-    }
-    u32x4 t[3];
-    split8(a, b, t[0], t[1], t[2]);
-#pragma unroll
-    for (int m = 0; m < 6; ++m)
-        if (m < products)
-            *reinterpret_cast<u32x4 *>(out + ((int64_t)m * Ep + e) * d + c) = t[kWgTerm[m]];
-}
-
 // Partial dW_g terms: part[range][3 Ep][d] = ds3^T x over the range's tokens.
 // grid: (tiles, ranges).
 template <int BM, int BN, int WM, int WN, int S>
@@ -222,9 +230,19 @@ __global__ __launch_bounds__(256) void route_dw_sum_kernel(const float *__restri
     const int64_t plane = (int64_t)Ep * d;
     const float *p = part + i * 4;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int m = 2; m >= 0; --m)
-        for (int s = 0; s < S; ++s)
-            v += *reinterpret_cast<const f32x4 *>(p + (s * 3 + m) * plane);
+    constexpr int B = 8;   // loads in flight
+    for (int q = 0; q < 3 * S; q += B) {
+        f32x4 u[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int o = min(q + b, 3 * S - 1);   // term 2 - o / S of range o % S
+            u[b] = *reinterpret_cast<const f32x4 *>(p + ((o % S) * 3 + 2 - o / S) * plane);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (q + b < 3 * S)
+                v += u[b];
+    }
     *reinterpret_cast<f32x4 *>(dW + i * 4) = v;
 }
 
@@ -283,28 +301,54 @@ __global__ __launch_bounds__(1024) void route_dx_kernel(
         *reinterpret_cast<f32x4 *>(w + e * C + q) = v;
     }
     __syncthreads();
-    constexpr int U = 4;   // tokens in flight of a wave
+    // U tokens of a wave in flight; lane 16 u + j holds choice j of token u (its id
+    // and ds are broadcast from there: read one by one they were a chain of scalar
+    // loads, 217 us for the fine-grained batch)
+    constexpr int U = 4;
+    static_assert(kMaxTopK <= 16 && U * 16 <= 64, "a lane per choice");
     const int64_t waves = (int64_t)gridDim.y * 16;
-    for (int64_t t0 = (int64_t)blockIdx.y * 16 + wv; t0 < N; t0 += waves * U) {
+    const int hu = lane >> 4, hj = lane & 15;
+    struct Choice {
+        int e;
+        float g;
+    };
+    auto choices = [&](int64_t t0) {
+        const int64_t t = t0 + hu * waves;
+        Choice c{0, 0.f};
+        if (hj < k && t < N) {
+            c.e = idx[t * k + hj];
+            c.g = ds[t * k + hj];
+        }
+        if (c.e < 0 || c.e >= E)   // no expert: ds is 0
+            c = Choice{0, 0.f};
+        return c;
+    };
+    int64_t t0 = (int64_t)blockIdx.y * 16 + wv;
+    if (t0 >= N)
+        return;
+    Choice next = choices(t0);
+    for (; t0 < N; t0 += waves * U) {
+        const Choice mine = next;
         typename R::vec a[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t t = min(t0 + u * waves, (int64_t)N - 1);
             a[u] = typename R::vec{};
-            if (dres && ok)
-                a[u] = R::load(dres, t * d + c);
+            if (dres)
+                a[u] = R::load(dres, t * d + min(c, d - V));
         }
+        next = choices(t0 + waves * U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t t = t0 + u * waves;
             if (t >= N)
                 break;
             typename R::vec s = {};
+#pragma unroll 4
             for (int j = 0; j < k; ++j) {
-                const int e = idx[t * k + j];
-                if (e < 0 || e >= E)
-                    continue;
-                const float g = ds[t * k + j];
+                const int e = __builtin_amdgcn_readlane(mine.e, 16 * u + j);
+                const float g = __uint_as_float((unsigned)__builtin_amdgcn_readlane(
+                    (int)__float_as_uint(mine.g), 16 * u + j));
                 const typename R::vec v =
                     *reinterpret_cast<const typename R::vec *>(w + e * C + V * lane);
 #pragma unroll
@@ -410,13 +454,14 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
     RouteGrad r{idx, p, dgate, dp, E, Ep, k, sigmoid, renorm, scale, ds, ds3, nullptr, products};
     if (dense)
         r.dsx = dsx;
-    const unsigned tb = (unsigned)((N + 3) / 4);
+    const bool split = dense && dx;
+    const dim3 tb((unsigned)((N + 3) / 4 + (split ? ((int64_t)Ep * (d / 8) + 255) / 256 : 0)));
     if (E <= 64)
-        hipLaunchKernelGGL(route_ds_kernel<1>, dim3(tb), dim3(256), 0, s, r, (int)N);
+        hipLaunchKernelGGL(route_ds_kernel<1>, tb, dim3(256), 0, s, r, (int)N, wg, (int)d, wx);
     else if (E <= 128)
-        hipLaunchKernelGGL(route_ds_kernel<2>, dim3(tb), dim3(256), 0, s, r, (int)N);
+        hipLaunchKernelGGL(route_ds_kernel<2>, tb, dim3(256), 0, s, r, (int)N, wg, (int)d, wx);
     else
-        hipLaunchKernelGGL(route_ds_kernel<4>, dim3(tb), dim3(256), 0, s, r, (int)N);
+        hipLaunchKernelGGL(route_ds_kernel<4>, tb, dim3(256), 0, s, r, (int)N, wg, (int)d, wx);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
@@ -445,10 +490,6 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
         return hipSuccess;
     if (dense) {
         const int K = products * Ep;
-        hipLaunchKernelGGL(route_split_kernel, dim3((unsigned)((Ep * (d / 8) + 255) / 256)),
-                           dim3(256), 0, s, wg, E, Ep, (int)d, products, wx);
-        if ((err = hipGetLastError()) != hipSuccess)
-            return err;
         const dim3 grid((unsigned)((N + 127) / 128 * ((d + 127) / 128)));
         if (dx32)
             hipLaunchKernelGGL(route_dx_dense_kernel<true>, grid, dim3(512), 0, s, dsx, wx, dres,
