@@ -392,6 +392,8 @@ struct RouteRule {
     int sigmoid;             // else softmax over all experts
     int groups, keep, best;  // groups of E / groups experts; kept; best c of a group's score
     int group_bits;          // 2^group_bits >= groups
+    int group_size;          // E / groups
+    unsigned group_factor;   // 65536 / group_size + 1
     int renorm;
     float scale;
     const float *bias;       // [E] or NULL

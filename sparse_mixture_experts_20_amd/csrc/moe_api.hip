@@ -2034,6 +2034,8 @@ int check_route(const moe_router_opts *o, int64_t E, int k, moe::RouteRule &r) {
     }
     while ((1 << r.group_bits) < r.groups)
         ++r.group_bits;
+    r.group_size = (int)(E / r.groups);
+    r.group_factor = 65536u / (unsigned)r.group_size + 1u;
     return k > E / r.groups * r.keep ? MOE_ERR_ARG : MOE_OK;
 }
 

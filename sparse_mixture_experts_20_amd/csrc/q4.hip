@@ -485,7 +485,8 @@ struct Q4Experts {
     const float *b_up, *b_down;   // [E, d_ff], [E, d] or NULL
     unsigned short *H;            // [2][N k][d_ff]: two bf16 terms
     float *Y;                     // [N k][d]
-    int *done;                    // finished workgroups per column block
+    int *done;                    // finished workgroups per column block, or NULL: the
+                                  // choices are added by a launch of their own
     const Q4Plan *plan;           // NULL with at most 64 assignments
     unsigned short *out;          // [N, d]
     int N, d, E, d_ff, k, act;
@@ -495,8 +496,9 @@ struct Q4Experts {
 // Rows of a call's hit experts, written by q4_plan_kernel where a call has more
 // than 64 assignments.
 struct Q4Plan {
-    int hits;
-    int expert[kMaxExperts], first[kMaxExperts + 1];   // first: into row[]
+    struct {
+        int expert, rows, first, pad;                  // first: into row[]
+    } hit[kMaxExperts];                                // (rows 0 past the last one)
     unsigned short row[kMaxAssign];                    // assignments t k + j
 };
 
@@ -554,16 +556,15 @@ __global__ __launch_bounds__(kMaxAssign) void q4_plan_kernel(const int32_t *__re
         }
         before[tid] = b;
         if (n > 0) {
-            plan->expert[a] = tid;
-            plan->first[a] = b;
-            plan->first[a + 1] = b + n;   // (as the next one writes it)
+            plan->hit[a].expert = tid;
+            plan->hit[a].rows = n;
+            plan->hit[a].first = b;
         }
-        if (tid == 0) {
-            int c = 0;
-            for (int w = 0; w < kMaxExperts / 64; ++w)
-                c += nhit[w];
-            plan->hits = c;
-        }
+        int all = 0;
+        for (int w = 0; w < kMaxExperts / 64; ++w)
+            all += nhit[w];
+        if (tid >= all)
+            plan->hit[tid].rows = 0;
     }
     __syncthreads();
     if (ok)
@@ -578,11 +579,11 @@ __device__ __forceinline__ int q4_rows(const Q4Experts &p, int &e, unsigned shor
     const int lane = threadIdx.x & 63, A = p.N * p.k, a = blockIdx.y;
     int n;
     if (p.plan) {
-        if (a >= p.plan->hits)
+        const int f = p.plan->hit[a].first;
+        n = p.plan->hit[a].rows;
+        e = p.plan->hit[a].expert;
+        if (n == 0)
             return 0;
-        const int f = p.plan->first[a];
-        n = p.plan->first[a + 1] - f;
-        e = p.plan->expert[a];
         for (int i = threadIdx.x; i < n; i += blockDim.x)
             row[i] = p.plan->row[f + i];
     } else {
@@ -607,7 +608,7 @@ __global__ __launch_bounds__(512, q4_waves(TT, TWO)) void q4_up_kernel(Q4Experts
     extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ unsigned short row[kMaxAssign];
     const int lane = threadIdx.x & 63, A = p.N * p.k;
-    if (blockIdx.y == 0)
+    if (p.done && blockIdx.y == 0)
         for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < blocks; i += gridDim.x * blockDim.x)
             p.done[i] = 0;
     int e;
@@ -674,8 +675,11 @@ __global__ __launch_bounds__(512, q4_waves(TT, TWO)) void q4_down_kernel(Q4Exper
                     return;
                 if (p.b_down)
                     v += p.b_down[m0 + c0 + r];
-                __hip_atomic_store(p.Y + (int64_t)row[t0 + t] * p.d + c0 + r, v, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
+                float *y = p.Y + (int64_t)row[t0 + t] * p.d + c0 + r;
+                if (p.done)
+                    __hip_atomic_store(y, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                else
+                    *y = v;
             };
             // rows [0, here) hold the first terms, [here, 2 here) the second ones
             auto src = [&](int r) {
@@ -713,6 +717,8 @@ __global__ __launch_bounds__(512, q4_waves(TT, TWO)) void q4_down_kernel(Q4Exper
             __syncthreads();
         }
     }
+    if (!p.done)
+        return;
     // Y has reached memory before the workgroup counts (agent-scope stores write
     // through; the wait is for their completion)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -739,6 +745,36 @@ __global__ __launch_bounds__(512, q4_waves(TT, TWO)) void q4_down_kernel(Q4Exper
         }
         p.out[(int64_t)t * p.d + c] = f32_to_bf16_bits(s);
     }
+}
+
+// out[t] = sum of its choices' rows, in choice order: 4 columns a thread (d % 4 == 0).
+__global__ __launch_bounds__(256) void q4_combine_kernel(Q4Experts p) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per = p.d / 4;
+    if (i >= (int64_t)p.N * per)
+        return;
+    const int t = (int)(i / per), c = (int)(i - (int64_t)t * per) * 4;
+    f32x4 y[kMaxTopK];
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j)   // (all loads in flight)
+        if (j < p.k)
+            y[j] = *reinterpret_cast<const f32x4 *>(p.Y + (int64_t)(t * p.k + j) * p.d + c);
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) {
+        if (j >= p.k)
+            break;
+        const int id = p.idx[t * p.k + j];
+        const float g = p.gate[t * p.k + j];
+        if (id >= 0 && id < p.E)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                s[q] = fmaf(g, y[j][q], s[q]);
+    }
+    unsigned short *o = p.out + (int64_t)t * p.d + c;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        o[q] = f32_to_bf16_bits(s[q]);
 }
 
 // ---- the format ----------------------------------------------------------
@@ -1019,6 +1055,11 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     const Q4Shape us = q4_sized(d_ff, d, hits, tt, 1, R, group, up[2] != nullptr);
     const Q4Shape ds = q4_sized(d, d_ff, hits, tt, 2, 2 * R, group, down[2] != nullptr);
     const int ur = 16 * us.rt * us.w.wm, dr = 16 * ds.rt * ds.w.wm;
+    // The last workgroup of a column block adds the choices where that saves a launch;
+    // with many workgroups a CU, each one's wait for its rows to reach memory costs more.
+    const bool apart = (d + dr - 1) / dr * (int64_t)blocks > 4096;
+    if (apart)
+        p.done = nullptr;
     const hipError_t err = with_shape(group, up[2] != nullptr, us.rt, tt, us.two,
                                       [&](auto gs, auto z, auto rt, auto t, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
@@ -1028,13 +1069,18 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     });
     if (err != hipSuccess)
         return err;
-    return with_shape(group, down[2] != nullptr, ds.rt, tt, ds.two,
+    const hipError_t rc = with_shape(group, down[2] != nullptr, ds.rt, tt, ds.two,
                       [&](auto gs, auto z, auto rt, auto t, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
         hipLaunchKernelGGL((q4_down_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((d + dr - 1) / dr), blocks),
                            dim3(ds.threads), ds.smem, s, p, ds.w);
         return hipGetLastError();
     });
+    if (rc != hipSuccess || !apart)
+        return rc;
+    hipLaunchKernelGGL(q4_combine_kernel, dim3((unsigned)((N * (d / 4) + 255) / 256)), dim3(256), 0,
+                       s, p);
+    return hipGetLastError();
 }
 
 hipError_t launch_quantize_q4(bool bf16, const void *W, int64_t n, int group, void *data,
