@@ -851,6 +851,8 @@ def _on_stream(fn):
         if stream is None:
             return fn(*args, **kw)
         for t in (*args, *kw.values()):
+            if isinstance(t, Q4):
+                t = t.data
             if isinstance(t, torch.Tensor):
                 if t.get_device() != stream.device.index:
                     raise ValueError(f"a tensor on {t.device}, the stream on {stream.device}")

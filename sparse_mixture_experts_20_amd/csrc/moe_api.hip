@@ -1845,7 +1845,7 @@ int check_q4_full(const moe_tensor *W, const moe_q4 *q) {
     for (int i = 0; i < W->ndim; ++i)
         if (W->shape[i] != q->shape[i])
             return MOE_ERR_SHAPE;
-    if (q4_count(q) / 8 > (int64_t)INT32_MAX * 256)   // workgroups of a launch
+    if (q4_count(q) / 8 >= ((int64_t)1 << 32) - 256)   // threads of a launch
         return MOE_ERR_UNSUPPORTED;
     if (!W->data)
         return MOE_ERR_NULL;

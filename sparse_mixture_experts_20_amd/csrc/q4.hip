@@ -754,22 +754,27 @@ __global__ __launch_bounds__(256) void q4_combine_kernel(Q4Experts p) {
     if (i >= (int64_t)p.N * per)
         return;
     const int t = (int)(i / per), c = (int)(i - (int64_t)t * per) * 4;
-    f32x4 y[kMaxTopK];
-#pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j)   // (all loads in flight)
-        if (j < p.k)
-            y[j] = *reinterpret_cast<const f32x4 *>(p.Y + (int64_t)(t * p.k + j) * p.d + c);
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    constexpr int B = 8;   // rows in flight
+    for (int j0 = 0; j0 < p.k; j0 += B) {
+        f32x4 y[B];
+        float g[B];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-        if (j >= p.k)
-            break;
-        const int id = p.idx[t * p.k + j];
-        const float g = p.gate[t * p.k + j];
-        if (id >= 0 && id < p.E)
+        for (int b = 0; b < B; ++b) {
+            const int a = t * p.k + min(j0 + b, p.k - 1), id = p.idx[a];
+            y[b] = *reinterpret_cast<const f32x4 *>(p.Y + (int64_t)a * p.d + c);
+            g[b] = p.gate[a];
+            // (a row without an expert was not written)
+            if (j0 + b >= p.k || id < 0 || id >= p.E) {
+                g[b] = 0.f;
+                y[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                s[q] = fmaf(g, y[j][q], s[q]);
+                s[q] = fmaf(g[b], y[b][q], s[q]);
     }
     unsigned short *o = p.out + (int64_t)t * p.d + c;
 #pragma unroll

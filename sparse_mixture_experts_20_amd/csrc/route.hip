@@ -10,9 +10,9 @@
 //   gate_j = scale p_j, or scale p_j / sum of the chosen p
 //
 // Scores: an fp32 weight is three exact bf16 terms on the matrix cores (fp32
-// activations: fp32 MFMAs). Up to 64 experts one kernel computes the scores of 16
-// tokens and ranks them; a few tokens cut the rows into ranges over many
-// workgroups; more experts with many tokens take the router's own tiled product.
+// activations: fp32 MFMAs). With few weights one kernel computes the scores of 16
+// tokens and ranks them; otherwise workgroups take 16 experts, up to 64 tokens and
+// a range of the columns each; very large products run on the router's own tiles.
 // The last two leave partial scores that the ranking adds in range order.
 //
 // Ranking: one wave a token, lane l holding experts l, l + 64, ...: the scores
@@ -485,13 +485,20 @@ RoutePlan route_plan(bool bf16, int64_t N, int64_t d, int E) {
     RoutePlan p{};
     p.Q = E <= 64 ? 1 : E <= 128 ? 2 : 4;
     p.ld = E <= 64 ? (E + 15) / 16 * 16 : 64 * p.Q;
-    // A fused workgroup reads all of W_g: with few of them and more than 64 K
-    // weights, ranges over many workgroups.
-    if (E <= 64 && (N > 64 || (int64_t)E * d <= 65536)) {
+    const int64_t weights = (int64_t)(E + 15) / 16 * 16 * d;
+    // A fused workgroup reads all of W_g, which saves a launch where that is little: as
+    // graphs of calls 64 tokens and 8 experts of width 768 7.9 us (ranges 8.8), of 4096
+    // 11.8 (8.7); as calls 2047 of these 13.5 (15.6), 777 of 60 experts of 515 14.5 (16.5).
+    if (E <= 64 && weights <= (N > 1024 ? 65536 : 36864)) {
         p.form = kFused;
         return p;
     }
-    if (bf16 && N > 64) {
+    // The tiled product (its scratch is laid out for more than 32 experts) costs a
+    // launch that splits W_g and the start of its large tiles, and then less per token:
+    // measured (us, with the ranking) 26 + 25 for each 2^20 weights + 3.2 for each 10^9
+    // products, ranges 8 + 27 (256 experts of 7168: 512 tokens 73 and 34, 2048 tokens 63
+    // and 87; of 1024: 2048 tokens 38 and 21).
+    if (bf16 && E > 32 && (double)N * weights > 0.75e9 + 1040.0 * p.ld * d) {
         p.form = kTiled;
         return p;
     }

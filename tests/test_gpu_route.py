@@ -1,5 +1,5 @@
 """moe_router_ex and moe_router_backward against their float64 definitions: each
-form of the score product (one kernel, ranges, the tiled product), both types,
+form of the score product (one kernel, ranges of the columns, tiles), both types,
 softmax and sigmoid, bias, groups, renormalised gates, one token to many, odd
 widths and expert counts; masks, infinities and NaN; gradients against the
 formula and against differences."""
@@ -28,7 +28,7 @@ def _gen(torch, seed):
 
 # (dtype, N, d, E, k, groups, keep, best)
 SHAPES = [
-    # one kernel (up to 64 experts)
+    # few experts (one kernel, or ranges with wide rows)
     ("bf16", 1, 8, 1, 1, 1, 0, 1), ("bf16", 17, 64, 8, 2, 1, 0, 1), ("bf16", 100, 1032, 16, 4, 4, 2, 2),
     ("bf16", 2047, 4096, 8, 2, 1, 0, 1), ("bf16", 333, 2048, 30, 5, 5, 3, 1),
     ("bf16", 65, 1000, 64, 8, 8, 4, 2), ("bf16", 70, 328, 33, 16, 1, 0, 1),
@@ -38,9 +38,11 @@ SHAPES = [
     ("bf16", 20, 2056, 100, 6, 1, 0, 1), ("bf16", 64, 1024, 256, 16, 64, 7, 2),
     ("bf16", 33, 64, 129, 3, 1, 0, 1), ("f32", 500, 300, 256, 8, 16, 5, 1),
     ("f32", 5, 2051, 70, 7, 7, 1, 2),
-    # the tiled product
     ("bf16", 65, 64, 65, 4, 1, 0, 1), ("bf16", 1000, 520, 256, 8, 8, 4, 2),
-    ("bf16", 4100, 1024, 128, 2, 2, 1, 1), ("bf16", 300, 7168, 256, 8, 8, 3, 2)]
+    ("bf16", 4100, 1024, 128, 2, 2, 1, 1), ("bf16", 300, 7168, 256, 8, 8, 3, 2),
+    # the tiled product (33 to 48, 100, 130 and 256 experts)
+    ("bf16", 6001, 4096, 48, 4, 4, 2, 2), ("bf16", 4000, 7168, 100, 6, 1, 0, 1),
+    ("bf16", 3300, 4096, 130, 3, 13, 5, 1), ("bf16", 9001, 1024, 256, 8, 8, 4, 2)]
 RULES = [dict(score="softmax"), dict(score="softmax", renormalize=True, bias=True),
          dict(score="sigmoid", renormalize=True, bias=True, scale=2.5, sigma=True),
          dict(score="sigmoid", scale=0.5)]
