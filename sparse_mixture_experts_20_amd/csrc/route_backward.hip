@@ -18,6 +18,10 @@
 // LDS in fp32, 2 or 4 a lane, and a wave adds k rows of them for each token: bound
 // by dres and dx. dx with E values: the tiled product of split operands, six
 // products of terms for fp32 dx (fp32's accuracy), three for bf16 dx (2^-16).
+//
+// Measured: 8192 tokens, 256 experts of 7168, fp32 dx with dres 235 us: ds 10, dW_g
+// 98 to 110 (90 GFLOP of terms, 0.85 PFLOP/s) and 13 for the sums, dx 123 (470 MB, 3.8
+// TB/s). 2047 tokens, 8 experts of 768 with an auxiliary loss 25 us in four launches.
 #include <algorithm>
 #include <type_traits>
 
