@@ -710,7 +710,8 @@ size_t moe_router_ex_workspace_size(int64_t N, int64_t d, int64_t E, int32_t dty
  *   ds the gradient of s: through the scaling, the renormalisation and the
  *   softmax or sigmoid (the choice passes none),
  *   dW_g = ds^T x,  dx = ds W_g + dres
- * topk_idx and scores are the forward's; an id outside [0, E) has no gate.
+ * topk_idx and scores are the forward's; an id outside [0, E) has no gate, and
+ * renormalised gates whose p are all 0 (underflown) pass no gradient.
  * x [N, d] and W_g [E, d] as the forward's, bf16 x (MOE_ERR_UNSUPPORTED for
  * fp32). dx [N, d] MOE_F32 or MOE_BF16, dres (or NULL) like it: a gradient that
  * reaches x another way, as the layer's own; dx may be its buffer. dW_g [E, d]

@@ -112,28 +112,33 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
             pc = r.p[t * r.E + e];
         }
     }
-    float dc = r.scale * dg;   // of the chosen p
+    // Gates of a sigmoid, or renormalised, pass their gradient to the chosen scores
+    // alone (the sum of dp p over the choices is 0): dc is then of s, else of p.
+    const bool direct = r.renorm || r.sigmoid;
+    float dc = r.scale * dg;
     if (r.renorm) {
         float S = 0.f, ug = 0.f;
-        for (int j = 0; j < r.k; ++j) {   // choice order
-            const float pj = __uint_as_float(
+        for (int j = 0; j < r.k; ++j)   // choice order
+            S += __uint_as_float(
                 (unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(pc), j));
+        const float share = S > 0.f ? pc / S : 0.f;   // (1 / S may be past fp32)
+        for (int j = 0; j < r.k; ++j) {
+            const float sj = __uint_as_float(
+                (unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(share), j));
             const float gj = __uint_as_float(
                 (unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(dg), j));
-            S += pj;
-            ug = fmaf(pj, gj, ug);
+            ug = fmaf(sj, gj, ug);
         }
-        dc = S > 0.f ? r.scale / S * (dg - ug / S) : 0.f;
+        dc = r.scale * share * (dg - ug);
+    } else if (r.sigmoid) {
+        dc *= pc;
     }
+    if (r.sigmoid)
+        dc *= 1.f - pc;
     if (e < 0)
         dc = 0.f;
-    if (!r.dsx) {
-        // (a softmax whose gates are renormalised: sum of dp p over the chosen is 0)
-        const float v = r.sigmoid ? dc * pc * (1.f - pc) : dc * pc;
-        if (lane < r.k)
-            r.ds[t * r.k + lane] = v;
-        dc = v;
-    }
+    if (r.ds && lane < r.k)
+        r.ds[t * r.k + lane] = dc;
     float p[Q], d[Q];
     float dot = 0.f;
 #pragma unroll
@@ -142,15 +147,19 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
         p[q] = r.dsx && ex < r.E ? r.p[t * r.E + ex] : 0.f;
         d[q] = r.dp && ex < r.E ? r.dp[t * r.E + ex] : 0.f;
     }
-    for (int j = 0; j < r.k; ++j) {
-        const int ej = __builtin_amdgcn_readlane(e, j);
-        const float v = __uint_as_float(
-            (unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(dc), j));
+    auto choices = [&] {
+        for (int j = 0; j < r.k; ++j) {
+            const int ej = __builtin_amdgcn_readlane(e, j);
+            const float v = __uint_as_float(
+                (unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(dc), j));
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (ej == lane + 64 * q)
-                d[q] += v;
-    }
+            for (int q = 0; q < Q; ++q)
+                if (ej == lane + 64 * q)
+                    d[q] += v;
+        }
+    };
+    if (!direct)
+        choices();
     if (r.dsx) {
         if (r.sigmoid) {
 #pragma unroll
@@ -166,6 +175,8 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
                 d[q] = p[q] * (d[q] - dot);
         }
     }
+    if (direct)
+        choices();
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         const int ex = lane + 64 * q;
