@@ -36,12 +36,12 @@
 // (one small launch). A hidden row is kept as two bf16 terms, as the few-token layer
 // keeps it: out then carries its own rounding alone.
 //
-// Measured (calls on inputs out of cache): one row of 7168 by 2048 9.4 us, of which
-// the kernel 6.7 (7.6 MB); 5 rows of 14336 by 4096 with zero points 16.7 (32 MB, 1.9
+// Measured (calls on inputs out of cache): one row of 7168 by 2048 9.3 us, of which
+// the kernel 8 (7.6 MB); 5 rows of 14336 by 4096 with zero points 16.7 (32 MB, 1.9
 // TB/s: the activations of all of K are read by each of 256 workgroups); 33 rows of
-// 4096 by 14336, groups of 32, 27.6 (the fp32 scaling of each group of four tiles); one
-// Mixtral-shaped token 33 (121 MB, 3.7 TB/s), 61 tokens of 256 experts 726 (3.3 GB, 4.6
-// TB/s).
+// 4096 by 14336, groups of 32, 27.6 (the fp32 scaling of each group of three tiles); one
+// Mixtral-shaped token 33 (121 MB, 3.7 TB/s), 61 tokens of 256 experts 697 to 726 (3.3
+// GB, 4.6 to 4.8 TB/s).
 #include <algorithm>
 #include <type_traits>
 
