@@ -716,10 +716,8 @@ size_t moe_router_ex_workspace_size(int64_t N, int64_t d, int64_t E, int32_t dty
  * fp32). dx [N, d] MOE_F32 or MOE_BF16, dres (or NULL) like it: a gradient that
  * reaches x another way, as the layer's own; dx may be its buffer. dW_g [E, d]
  * MOE_F32. dx or dW_g may be NULL and is then not computed (both:
- * MOE_ERR_NULL; dres without dx: MOE_ERR_ARG). Sums are fp32 in a fixed order;
- * products as accurate as fp32 ones, except that a bf16 dx of a softmax without
- * renormalisation or of an auxiliary loss takes its operands to 16 bits. x, W_g,
- * dres, dx and dW_g 16-byte aligned. No output, nor the workspace, may overlap
+ * MOE_ERR_NULL; dres without dx: MOE_ERR_ARG). Sums are fp32 in a fixed order,
+ * products as accurate as fp32 ones. x, W_g, dres, dx and dW_g 16-byte aligned. No output, nor the workspace, may overlap
  * an input otherwise, another output or each other (MOE_ERR_ARG). workspace:
  * moe_router_backward_workspace_size() bytes, 256-byte aligned. N = 0: dW_g is
  * zero. */

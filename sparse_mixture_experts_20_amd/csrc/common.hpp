@@ -408,15 +408,15 @@ hipError_t launch_router_partials(const void *x, const float *wg, int64_t N, int
                                   void *ws, float *&P, int &ns, hipStream_t s);
 
 // Its backward (route_backward.hip), bf16 x, d % 8 == 0: whether ds has E values a
-// token (else k); workspace regions (byte offsets) for `products` products of split
-// operands in dx (0: ds has k values); dx (fp32 or bf16) or dW may be NULL.
+// token (`dense`, else k); workspace regions (byte offsets); dx (fp32 or bf16) or dW
+// may be NULL.
 inline bool route_backward_dense(bool sigmoid, bool renorm, bool dp) {
     return dp || (!sigmoid && !renorm);
 }
 struct RouteBackwardLayout {
     size_t ds, ds3, part, dsx, wx, total;
 };
-RouteBackwardLayout route_backward_layout(int64_t N, int64_t d, int E, int k, int products);
+RouteBackwardLayout route_backward_layout(int64_t N, int64_t d, int E, int k, bool dense);
 hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *idx,
                                  const float *p, const float *dgate, const float *dp,
                                  const void *dres, int64_t N, int64_t d, int E, int k, int sigmoid,

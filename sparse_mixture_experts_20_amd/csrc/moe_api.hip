@@ -2110,7 +2110,7 @@ size_t moe_router_backward_workspace_size(int64_t N, int64_t d, int64_t E, int k
     if (N <= 0 || d <= 0 || d % 8 != 0 || d > INT32_MAX || E <= 0 || E > MOE_MAX_EXPERTS ||
         k < 1 || k > E || k > MOE_MAX_TOPK || N * (int64_t)k >= ((int64_t)1 << 31))
         return 0;
-    return moe::route_backward_layout(N, d, (int)E, k, 6).total;   // the largest form
+    return moe::route_backward_layout(N, d, (int)E, k, true).total;   // the largest form
 }
 
 int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_router_opts *opts,
@@ -2166,8 +2166,8 @@ int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_ro
     if (!aligned(topk_idx, 4))
         return MOE_ERR_ALIGN;
     const bool dx32 = dx && dx->dtype == MOE_F32;
-    const int products = !moe::route_backward_dense(r.sigmoid, r.renorm, dp) ? 0 : dx32 ? 6 : 3;
-    const size_t need = moe::route_backward_layout(N, d, (int)E, k, products).total;
+    const bool dense = moe::route_backward_dense(r.sigmoid, r.renorm, dp);
+    const size_t need = moe::route_backward_layout(N, d, (int)E, k, dense).total;
     if ((rc = check_scratch(workspace, workspace_bytes, need)) != MOE_OK)
         return rc;
     const int64_t bytes = N * d * (dx32 ? 4 : 2);

@@ -17,7 +17,9 @@
 // adds, terms and ranges in a fixed order. dx with k values: W_g's columns lie in
 // LDS in fp32, 2 or 4 a lane, and a wave adds k rows of them for each token: bound
 // by dres and dx. dx with E values: the tiled product of split operands, six
-// products of terms for fp32 dx (fp32's accuracy), three for bf16 dx (2^-16).
+// products of terms (fp32's accuracy, for bf16 dx too: three of them, 2^-16, rounded
+// one element of 90 otherwise; 8192 tokens, 256 experts of 7168 then took 283 us, now
+// 377, 2047 tokens, 8 experts of 768 24 as now).
 //
 // Measured: 8192 tokens, 256 experts of 7168, fp32 dx with dres 235 us: ds 10, dW_g
 // 98 to 110 (90 GFLOP of terms, 0.85 PFLOP/s) and 13 for the sums, dx 123 (470 MB, 3.8
@@ -46,9 +48,10 @@ __device__ __forceinline__ void terms_of(float v, unsigned short (&t)[3]) {
     t[1] = (unsigned short)m;
     t[2] = (unsigned short)l;
 }
-// Terms of ds and of W_g in each of the products of dx.
-constexpr int kDsTerm[6] = {0, 0, 1, 1, 0, 2};
-constexpr int kWgTerm[6] = {0, 1, 0, 1, 2, 0};
+// Terms of ds and of W_g in each of the products of dx (those below 2^-24 left out).
+constexpr int kProducts = 6;
+constexpr int kDsTerm[kProducts] = {0, 0, 1, 1, 0, 2};
+constexpr int kWgTerm[kProducts] = {0, 1, 0, 1, 2, 0};
 
 struct RouteGrad {
     const int32_t *idx;       // [N, k]
@@ -60,13 +63,12 @@ struct RouteGrad {
     float scale;
     float *ds;                // [N, k] (k values a token), or NULL
     unsigned short *ds3;      // [N][3][Ep]
-    unsigned short *dsx;      // [N][products][Ep] (E values a token), or NULL
-    int products;
+    unsigned short *dsx;      // [N][kProducts][Ep] (E values a token), or NULL
 };
 
-// The terms of W_g [E, d] as the products of dx take them: [products Ep][d].
+// The terms of W_g [E, d] as the products of dx take them: [kProducts Ep][d].
 __device__ __forceinline__ void route_split(const float *__restrict__ wg, int E, int Ep, int d,
-                                            int products, unsigned short *__restrict__ out,
+                                            unsigned short *__restrict__ out,
                                             int64_t i) {   // 8 columns
     const int per = d / 8;
     if (i >= (int64_t)Ep * per)
@@ -80,9 +82,8 @@ __device__ __forceinline__ void route_split(const float *__restrict__ wg, int E,
     u32x4 t[3];
     split8(a, b, t[0], t[1], t[2]);
 #pragma unroll
-    for (int m = 0; m < 6; ++m)
-        if (m < products)
-            *reinterpret_cast<u32x4 *>(out + ((int64_t)m * Ep + e) * d + c) = t[kWgTerm[m]];
+    for (int m = 0; m < kProducts; ++m)
+        *reinterpret_cast<u32x4 *>(out + ((int64_t)m * Ep + e) * d + c) = t[kWgTerm[m]];
 }
 
 // ds of one token per wave; lane l holds experts l, l + 64, ... and choice l. The
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
                                                        unsigned short *__restrict__ wx) {
     const int blocks = (N + 3) / 4;
     if ((int)blockIdx.x >= blocks) {
-        route_split(wg, r.E, r.Ep, width, r.products, wx,
+        route_split(wg, r.E, r.Ep, width, wx,
                     (int64_t)(blockIdx.x - blocks) * 256 + threadIdx.x);
         return;
     }
@@ -189,11 +190,10 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
         for (int m = 0; m < 3; ++m)
             o[m * r.Ep] = term[m];
         if (r.dsx) {
-            unsigned short *ox = r.dsx + t * r.products * r.Ep + ex;
+            unsigned short *ox = r.dsx + t * kProducts * r.Ep + ex;
 #pragma unroll
-            for (int m = 0; m < 6; ++m)
-                if (m < r.products)
-                    ox[m * r.Ep] = term[kDsTerm[m]];
+            for (int m = 0; m < kProducts; ++m)
+                ox[m * r.Ep] = term[kDsTerm[m]];
         }
     }
 }
@@ -440,9 +440,9 @@ int padded(int E) { return (E + 7) / 8 * 8; }
 
 }  // namespace
 
-RouteBackwardLayout route_backward_layout(int64_t N, int64_t d, int E, int k, int products) {
+RouteBackwardLayout route_backward_layout(int64_t N, int64_t d, int E, int k, bool dense) {
     RouteBackwardLayout L;
-    const int Ep = padded(E);
+    const int Ep = padded(E), products = dense ? kProducts : 0;
     size_t o = 0;
     L.ds = o;   o += up256((size_t)N * k * 4);
     L.ds3 = o;  o += up256((size_t)N * 3 * Ep * 2);
@@ -459,14 +459,14 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
                                  int renorm, float scale, void *dx, bool dx32, float *dW,
                                  void *ws, hipStream_t s) {
     const bool dense = route_backward_dense(sigmoid, renorm, dp != nullptr);
-    const int products = !dense ? 0 : dx32 ? 6 : 3, Ep = padded(E);
-    const RouteBackwardLayout L = route_backward_layout(N, d, E, k, products);
+    const int Ep = padded(E);
+    const RouteBackwardLayout L = route_backward_layout(N, d, E, k, dense);
     char *w = static_cast<char *>(ws);
     float *ds = reinterpret_cast<float *>(w + L.ds), *part = reinterpret_cast<float *>(w + L.part);
     unsigned short *ds3 = reinterpret_cast<unsigned short *>(w + L.ds3);
     unsigned short *dsx = reinterpret_cast<unsigned short *>(w + L.dsx);
     unsigned short *wx = reinterpret_cast<unsigned short *>(w + L.wx);
-    RouteGrad r{idx, p, dgate, dp, E, Ep, k, sigmoid, renorm, scale, ds, ds3, nullptr, products};
+    RouteGrad r{idx, p, dgate, dp, E, Ep, k, sigmoid, renorm, scale, ds, ds3, nullptr};
     if (dense)
         r.dsx = dsx;
     const bool split = dense && dx;
@@ -504,7 +504,7 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
     if (!dx)
         return hipSuccess;
     if (dense) {
-        const int K = products * Ep;
+        const int K = kProducts * Ep;
         const dim3 grid((unsigned)((N + 127) / 128 * ((d + 127) / 128)));
         if (dx32)
             hipLaunchKernelGGL(route_dx_dense_kernel<true>, grid, dim3(512), 0, s, dsx, wx, dres,

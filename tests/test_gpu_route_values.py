@@ -1,0 +1,48 @@
+"""moe_router_ex and moe_router_backward where an elementwise bound would not tell
+a fault: bf16 gradients against the rounded float64 ones."""
+import pytest
+
+from tests import _gpu as G
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch_mod():
+    if not G.have_gpu():
+        pytest.skip("no HIP device")
+    import torch
+    from sparse_mixture_experts_20_amd import binding as B
+    B.lib()
+    return torch
+
+
+def _gen(torch, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+@pytest.mark.parametrize("score,renorm,aux", [("softmax", False, False), ("softmax", True, True),
+                                              ("sigmoid", False, True)])
+def test_bf16_dx_of_all_scores(torch_mod, score, renorm, aux):
+    """A bf16 dx of E values a token is the float64 one rounded, but for values next
+    to the border of two steps. Products as accurate as fp32 ones leave a relative
+    error of about 2^-22, so the border (every 2^-8 to 2^-7 of the value) is met by 2^-14
+    to 2^-13 of the elements; with operands of 16 bits by 2^-10 to 2^-8. Limit: 2^-11."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain_route as R
+    N, d, E, k = 512, 1024, 64, 4
+    g = _gen(torch, 3)
+    x = torch.randn((N, d), generator=g, device="cuda").to(torch.bfloat16)
+    W = torch.randn((E, d), generator=g, device="cuda") / d ** 0.5
+    idx, _, p = B.route(x, W, k, score=score, export_scores=True)
+    dgate = torch.randn((N, k), generator=g, device="cuda")
+    dp = torch.randn((N, E), generator=g, device="cuda") if aux else None
+    dx, _ = B.route_backward(x, W, idx, p, dgate, dscores=dp, score=score, renormalize=renorm,
+                             dx_dtype=torch.bfloat16)
+    want = R.backward(x, W, idx, p, dgate, dp, None, score, renorm, 1.0)["dx"][0]
+    off = float((dx != want.to(torch.bfloat16)).double().mean())
+    G.say(f"[route backward] {score} renorm={renorm} aux={aux}: {off:.2e} of dx rounded otherwise")
+    assert off <= 2.0 ** -11
