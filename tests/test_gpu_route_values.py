@@ -46,3 +46,14 @@ def test_bf16_dx_of_all_scores(torch_mod, score, renorm, aux):
     off = float((dx != want.to(torch.bfloat16)).double().mean())
     G.say(f"[route backward] {score} renorm={renorm} aux={aux}: {off:.2e} of dx rounded otherwise")
     assert off <= 2.0 ** -11
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,E", [(7168, 256), (4096, 64)])
+def test_no_tokens_of_many_experts(torch_mod, d, E, dtype):
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, W = torch.empty((0, d), device="cuda", dtype=dt), torch.ones((E, d), device="cuda")
+    idx, gate, p = B.route(x, W, 4, groups=8, keep_groups=2, export_scores=True)
+    assert idx.shape == (0, 4) and gate.shape == (0, 4) and p.shape == (0, E)
