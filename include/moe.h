@@ -731,8 +731,9 @@ int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_ro
 size_t moe_router_backward_workspace_size(int64_t N, int64_t d, int64_t E, int k);
 
 /* moe_forward_ex for a routing that the caller has: stats->topk_idx and
- * stats->topk_gate are inputs (required for N > 0), the rest is as there (an id
- * outside [0, E) takes no slot). The workspace of moe_forward serves it. */
+ * stats->topk_gate are inputs (required for N > 0, 4-byte aligned), the rest is as
+ * there (an id outside [0, E) takes no slot). The workspace of moe_forward serves it;
+ * no written buffer may overlap the routing or another one (MOE_ERR_ARG). */
 int moe_forward_routed(const moe_tensor *x, const moe_tensor *W_up, const moe_tensor *W_down,
                        const moe_expert_opts *opts, int k, float capacity_factor, moe_tensor *out,
                        moe_stats *stats);
@@ -740,7 +741,8 @@ int moe_forward_routed(const moe_tensor *x, const moe_tensor *W_up, const moe_te
 /* Its backward: moe_backward_ex without the router. dx is the experts' part
  * alone (moe_router_backward's dres), dgate [N, k] MOE_F32 the gradient of each
  * gate, <dout, y> (0 for dropped choices): moe_router_backward's. The workspace
- * of moe_backward serves it; stats as moe_forward_routed's. */
+ * of moe_backward serves it; stats as moe_forward_routed's. No written buffer may
+ * overlap the routing or another one, nor dgate any input (MOE_ERR_ARG). */
 int moe_backward_routed(const moe_tensor *x, const moe_tensor *W_up, const moe_tensor *W_down,
                         const moe_expert_opts *opts, int k, float capacity_factor,
                         const moe_tensor *dout, moe_tensor *dx, moe_tensor *dgate,

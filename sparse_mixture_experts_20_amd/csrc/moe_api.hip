@@ -31,6 +31,32 @@ int64_t capacity_of(int64_t N, int64_t E, int k, float cf) {
     return c < 0x1p63 ? (int64_t)c : INT64_MAX;
 }
 
+// Bytes [p, p + n) of a buffer (none where p is NULL).
+struct Span {
+    const void *p;
+    int64_t n;
+};
+bool overlap(Span a, Span b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+// Whether a shares bytes with b other than by being the same buffer.
+bool crosses(Span a, Span b) { return a.p != b.p && overlap(a, b); }
+// Whether any of the written buffers w shares bytes with another, or with one
+// of the read buffers r.
+template <size_t W, size_t R>
+bool collide(const Span (&w)[W], const Span (&r)[R]) {
+    for (size_t i = 0; i < W; ++i) {
+        for (size_t j = i + 1; j < W; ++j)
+            if (overlap(w[i], w[j]))
+                return true;
+        for (const Span &b : r)
+            if (overlap(w[i], b))
+                return true;
+    }
+    return false;
+}
+
 // Sizes of one call, as validated.
 struct Dims {
     int64_t N, d, E, d_ff;
@@ -282,7 +308,26 @@ int check_routed_args(const moe_tensor *x, const moe_tensor *W_up, int k, const 
         if (!aligned(x->data, 16))
             return MOE_ERR_ALIGN;
     }
+    if (N > 0 && (!aligned(stats->topk_idx, 4) || !aligned(stats->topk_gate, 4)))
+        return MOE_ERR_ALIGN;
     return MOE_OK;
+}
+// Whether a buffer that a call for a given routing writes shares bytes with that
+// routing or with another one: the written buffers w beside stats' own.
+template <size_t W>
+bool routed_collide(const Span (&w)[W], const moe_stats *stats, size_t ws_bytes, int64_t nk,
+                    int64_t E) {
+    Span all[W + 6];
+    for (size_t i = 0; i < W; ++i)
+        all[i] = w[i];
+    all[W] = {stats->workspace, (int64_t)ws_bytes};
+    all[W + 1] = {stats->slot, 4 * nk};
+    all[W + 2] = {stats->used_capacity, 4 * E};
+    all[W + 3] = {stats->expert_demand, 4 * E};
+    all[W + 4] = {stats->expert_drops, 4 * E};
+    all[W + 5] = {stats->expert_gate_sum, 4 * E};
+    const Span routing[2] = {{stats->topk_idx, 4 * nk}, {stats->topk_gate, 4 * nk}};
+    return collide(all, routing);
 }
 
 // Expert variant options: activation and fp32 biases [E, d_ff] / [E, d].
@@ -840,6 +885,11 @@ static int forward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_te
     const Layout L = layout_of(m);
     if (stats->workspace_bytes < L.total)
         return MOE_ERR_WORKSPACE;
+    if (routed) {
+        const Span to[1] = {{out->data, N * d * (int64_t)dtype_size(x->dtype)}};
+        if (routed_collide(to, stats, L.total, N * k, E))
+            return MOE_ERR_ARG;
+    }
 
     char *ws = static_cast<char *>(stats->workspace);
     int32_t *idx = stats->topk_idx ? stats->topk_idx : reinterpret_cast<int32_t *>(ws + L.idx);
@@ -1069,6 +1119,22 @@ static int backward_call(const moe_tensor *x, const moe_tensor *W_g, const moe_t
     const BwdLayout L = bwd_layout_of(m);
     if (stats->workspace_bytes < L.total)
         return MOE_ERR_WORKSPACE;
+    if (routed) {
+        const Span to[6] = {{dx->data, 4 * N * d},
+                            {dgate->data, 4 * N * k},
+                            {dW_up->data, 4 * E * d_ff * d},
+                            {dW_down->data, 4 * E * d * d_ff},
+                            {db_up ? db_up->data : nullptr, 4 * E * d_ff},
+                            {db_down ? db_down->data : nullptr, 4 * E * d}};
+        if (routed_collide(to, stats, L.total, N * k, E))
+            return MOE_ERR_ARG;
+        for (const Span &r : {Span{x->data, 2 * N * d}, Span{dout->data, 2 * N * d},
+                              Span{W_up->data, 2 * E * d_ff * d},
+                              Span{W_down->data, 2 * E * d * d_ff}, Span{o.b_up, 4 * E * d_ff},
+                              Span{o.b_down, 4 * E * d}})
+            if (overlap(to[1], r))
+                return MOE_ERR_ARG;
+    }
     stats->capacity = m.C;
 
     char *ws = static_cast<char *>(stats->workspace);
@@ -1310,32 +1376,6 @@ static int forward_state(const BwdLayout &L, char *ws, const moe_tensor *x,
 // The layer for a few tokens
 // ---------------------------------------------------------------------------
 namespace {
-
-// Bytes [p, p + n) of a buffer (none where p is NULL).
-struct Span {
-    const void *p;
-    int64_t n;
-};
-bool overlap(Span a, Span b) {
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
-}
-// Whether a shares bytes with b other than by being the same buffer.
-bool crosses(Span a, Span b) { return a.p != b.p && overlap(a, b); }
-// Whether any of the written buffers w shares bytes with another, or with one
-// of the read buffers r.
-template <size_t W, size_t R>
-bool collide(const Span (&w)[W], const Span (&r)[R]) {
-    for (size_t i = 0; i < W; ++i) {
-        for (size_t j = i + 1; j < W; ++j)
-            if (overlap(w[i], w[j]))
-                return true;
-        for (const Span &b : r)
-            if (overlap(w[i], b))
-                return true;
-    }
-    return false;
-}
 
 // Widths whose tiles fit the grid's second dimension and 32-bit counts.
 bool few_fits(const Dims &m) {

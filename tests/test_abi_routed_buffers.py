@@ -1,0 +1,84 @@
+"""The layer for a given routing on the host: a misaligned routing, and a written
+buffer that shares bytes with the routing, with another one or (dgate) with an input,
+are refused before anything is enqueued (the pointers are never dereferenced)."""
+import ctypes
+
+import pytest
+
+from sparse_mixture_experts_20_amd import binding as B
+from tests.test_abi_block import ALIGN, ARG, BF16, F32, t
+
+P = 1 << 34     # apart from each other by more than any buffer here
+N, D, E, FF, K = 40, 64, 4, 128, 2
+NAMES = ("x", "wu", "wd", "out", "ws", "idx", "gate", "slot", "used", "demand", "drops", "sum",
+         "dout", "dx", "dg", "dwu", "dwd", "bu", "bd", "dbu", "dbd")
+OWN = {n: (i + 1) * P for i, n in enumerate(NAMES)}
+
+
+@pytest.fixture(scope="module")
+def L():
+    return B.lib()
+
+
+def _size(L, name, back):
+    return dict(x=2 * N * D, out=2 * N * D, dout=2 * N * D, idx=4 * N * K, gate=4 * N * K,
+                slot=4 * N * K, used=4 * E, demand=4 * E, drops=4 * E, sum=4 * E, dx=4 * N * D,
+                dg=4 * N * K, wu=2 * E * FF * D, wd=2 * E * FF * D, dwu=4 * E * FF * D,
+                dwd=4 * E * FF * D, bu=4 * E * FF, bd=4 * E * D, dbu=4 * E * FF, dbd=4 * E * D,
+                ws=(L.moe_backward_workspace_size if back else L.moe_workspace_size)(
+                    N, D, E, FF, K, 1.0, BF16))[name]
+
+
+def _call(L, back, p):
+    st = B.MoeStats(None, p["ws"], 1 << 40, p["idx"], p["gate"], p["slot"], p["used"], -1,
+                    p["demand"], p["drops"], p["sum"], None)
+    bu, bd = t(F32, E, FF, ptr=p["bu"]), t(F32, E, D, ptr=p["bd"])
+    at = [ctypes.cast(ctypes.c_char_p(b), ctypes.c_void_p) for b in (bu, bd)]
+    o = ctypes.byref(B.MoeExpertOpts(B.MOE_ACT_GELU, *at, 0.0, 0, 0))
+    x = t(BF16, N, D, ptr=p["x"])
+    wu, wd = t(BF16, E, FF, D, ptr=p["wu"]), t(BF16, E, D, FF, ptr=p["wd"])
+    if back:
+        rc = L.moe_backward_routed(
+            x, wu, wd, o, K, 1.0, t(BF16, N, D, ptr=p["dout"]), t(F32, N, D, ptr=p["dx"]),
+            t(F32, N, K, ptr=p["dg"]), t(F32, E, FF, D, ptr=p["dwu"]),
+            t(F32, E, D, FF, ptr=p["dwd"]), t(F32, E, FF, ptr=p["dbu"]),
+            t(F32, E, D, ptr=p["dbd"]), ctypes.byref(st))
+    else:
+        rc = L.moe_forward_routed(x, wu, wd, o, K, 1.0, t(BF16, N, D, ptr=p["out"]),
+                                  ctypes.byref(st))
+    assert st.capacity == -1      # refused before anything was written
+    return rc
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_misaligned_routing(L, back):
+    for name in ("idx", "gate"):
+        for off in (1, 2, 3):
+            assert _call(L, back, {**OWN, name: OWN[name] + off}) == ALIGN, name
+
+
+WRITTEN = {False: ("out", "ws", "slot", "used", "demand", "drops", "sum"),
+           True: ("dx", "dg", "dwu", "dwd", "dbu", "dbd", "ws", "slot", "used", "demand",
+                  "drops", "sum")}
+
+
+def _pairs(back):
+    for a in WRITTEN[back]:
+        for b in ("idx", "gate", *WRITTEN[back]):
+            if a != b:
+                yield a, b
+        if a == "dg":
+            yield from ((a, b) for b in ("x", "dout", "wu", "wd", "bu", "bd"))
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_overlaps(L, back):
+    for a, b in _pairs(back):
+        n, m = _size(L, b, back), _size(L, a, back)
+        first = 256 if a == "ws" else 16     # (kept aligned, so that the overlap is the fault)
+        last = OWN[b] + (n - 1) // first * first
+        starts = {OWN[b], last}
+        if m > first:
+            starts.add(OWN[b] - (m - 1) // first * first)
+        for where in starts:
+            assert _call(L, back, {**OWN, a: where}) == ARG, (a, b, where - OWN[b])
