@@ -73,6 +73,8 @@ enum {
 #define MOE_FEW_MAX_WIDTH (1 << 20)  /* d and d_ff of moe_forward_few */
 #define MOE_NORM_MAX_WIDTH 16384   /* row width of moe_layer_norm */
 #define MOE_LINEAR_MAX_EXTENT (1 << 28)  /* rows and widths of moe_linear */
+#define MOE_ROUTE_MAX_WIDTH (1 << 25)    /* d of moe_router_ex and moe_router_backward */
+#define MOE_ROUTE_MAX_GRAD_ROWS (1 << 29)  /* tokens of moe_router_backward */
 
 /* A tensor view: data (device), element type, rank and extents (row-major,
  * contiguous). A 3-D activation [B, T, d] is read as [B*T, d]. */
@@ -691,8 +693,8 @@ typedef struct {
  * largest c in descending order (equal values: lower id first), and their gates
  * topk_gate [N, k] fp32; scores, if not NULL, the p of all experts, [N, E]
  * MOE_F32, for the backward or an auxiliary loss. k at most the experts of the
- * kept groups (MOE_ERR_ARG). x, W_g and noise as moe_router's, all arithmetic
- * fp32. A NaN score counts as -inf (p = 0); where the chosen p sum to 0,
+ * kept groups (MOE_ERR_ARG). x, W_g and noise as moe_router's, d at most
+ * MOE_ROUTE_MAX_WIDTH (MOE_ERR_UNSUPPORTED), all arithmetic fp32. A NaN score counts as -inf (p = 0); where the chosen p sum to 0,
  * renormalised gates are 0 (those of a softmax are formed from the scores and do
  * not underflow together); softmax scores with infinities share 1 equally. No
  * output, nor the workspace, may overlap an input, another output or each other
@@ -713,7 +715,7 @@ size_t moe_router_ex_workspace_size(int64_t N, int64_t d, int64_t E, int32_t dty
  * topk_idx and scores are the forward's; an id outside [0, E) has no gate, and
  * renormalised gates whose p are all 0 (underflown) pass no gradient.
  * x [N, d] and W_g [E, d] as the forward's, bf16 x (MOE_ERR_UNSUPPORTED for
- * fp32). dx [N, d] MOE_F32 or MOE_BF16, dres (or NULL) like it: a gradient that
+ * fp32, and past MOE_ROUTE_MAX_GRAD_ROWS tokens). dx [N, d] MOE_F32 or MOE_BF16, dres (or NULL) like it: a gradient that
  * reaches x another way, as the layer's own; dx may be its buffer. dW_g [E, d]
  * MOE_F32. dx or dW_g may be NULL and is then not computed (both:
  * MOE_ERR_NULL; dres without dx: MOE_ERR_ARG). Sums are fp32 in a fixed order,

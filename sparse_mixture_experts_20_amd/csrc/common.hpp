@@ -387,6 +387,8 @@ hipError_t launch_dequantize_q4(bool bf16, const void *data, const void *scale, 
 // ---------------------------------------------------------------------------
 namespace moe {
 
+// Tokens of a launch: 64 threads each, of the 2^32 that one holds.
+constexpr int64_t kRouteTokens = (int64_t)1 << 25;
 struct RouteRule {
     int E, k;
     int sigmoid;             // else softmax over all experts

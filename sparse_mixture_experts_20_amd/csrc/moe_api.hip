@@ -2101,8 +2101,8 @@ int check_f32(const moe_tensor *t, int64_t N, int64_t cols, bool required, const
 extern "C" {
 
 size_t moe_router_ex_workspace_size(int64_t N, int64_t d, int64_t E, int32_t dtype) {
-    if (!valid_dtype(dtype) || N < 0 || d <= 0 || d > INT32_MAX || E <= 0 || E > MOE_MAX_EXPERTS ||
-        N >= ((int64_t)1 << 31))
+    if (!valid_dtype(dtype) || N < 0 || d <= 0 || d > MOE_ROUTE_MAX_WIDTH || E <= 0 ||
+        E > MOE_MAX_EXPERTS || N >= ((int64_t)1 << 31))
         return 0;
     return align_up(moe::route_workspace_bytes(dtype == MOE_BF16, N, d, (int)E));
 }
@@ -2114,6 +2114,8 @@ int moe_router_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *
     int rc = check_router_args(x, W_g, noise, k, N, d, E);
     if (rc != MOE_OK)
         return rc;
+    if (d > MOE_ROUTE_MAX_WIDTH)
+        return MOE_ERR_UNSUPPORTED;
     moe::RouteRule r;
     const float *sp;
     if ((rc = check_route(opts, E, k, r)) != MOE_OK ||
@@ -2147,8 +2149,9 @@ int moe_router_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *
 }
 
 size_t moe_router_backward_workspace_size(int64_t N, int64_t d, int64_t E, int k) {
-    if (N <= 0 || d <= 0 || d % 8 != 0 || d > INT32_MAX || E <= 0 || E > MOE_MAX_EXPERTS ||
-        k < 1 || k > E || k > MOE_MAX_TOPK || N * (int64_t)k >= ((int64_t)1 << 31))
+    if (N <= 0 || N > MOE_ROUTE_MAX_GRAD_ROWS || d <= 0 || d % 8 != 0 || d > MOE_ROUTE_MAX_WIDTH ||
+        E <= 0 || E > MOE_MAX_EXPERTS || k < 1 || k > E || k > MOE_MAX_TOPK ||
+        N * (int64_t)k >= ((int64_t)1 << 31))
         return 0;
     return moe::route_backward_layout(N, d, (int)E, k, true).total;   // the largest form
 }
@@ -2162,8 +2165,8 @@ int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_ro
     int rc = check_router_args(x, W_g, nullptr, k, N, d, E);
     if (rc != MOE_OK)
         return rc;
-    if (x->dtype != MOE_BF16)
-        return MOE_ERR_UNSUPPORTED;   // the backward runs on bf16 layers
+    if (x->dtype != MOE_BF16 || d > MOE_ROUTE_MAX_WIDTH || N > MOE_ROUTE_MAX_GRAD_ROWS)
+        return MOE_ERR_UNSUPPORTED;   // (the backward runs on bf16 layers)
     moe::RouteRule r;
     const float *p, *dg, *dp;
     if ((rc = check_route(opts, E, k, r)) != MOE_OK ||

@@ -484,6 +484,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
 size_t route_workspace_bytes(bool bf16, int64_t N, int64_t d, int E) {
+    N = std::min(N, kRouteTokens);
     const RoutePlan p = route_plan(bf16, N, d, E);
     if (p.form == kFused)
         return 0;
@@ -492,10 +493,10 @@ size_t route_workspace_bytes(bool bf16, int64_t N, int64_t d, int E) {
     return up256((size_t)p.ranges * N * p.ld * 4);
 }
 
-hipError_t launch_route(bool bf16, const void *xv, const float *wg, const float *noise, int64_t N,
-                        int64_t d, const RouteRule &r, int32_t *idx, float *gate, float *scores,
-                        void *ws, hipStream_t s) {
-    const RoutePlan p = route_plan(bf16, N, d, r.E);
+// The launches of at most kRouteTokens tokens.
+static hipError_t route_part(bool bf16, const RoutePlan &p, const void *xv, const float *wg,
+                             const float *noise, int64_t N, int64_t d, const RouteRule &r,
+                             int32_t *idx, float *gate, float *scores, void *ws, hipStream_t s) {
     const RouteOut o{idx, gate, scores};
     float *P = static_cast<float *>(ws);
     int ns = p.ranges;
@@ -550,6 +551,22 @@ hipError_t launch_route(bool bf16, const void *xv, const float *wg, const float 
     return p.Q == 1   ? rank(std::integral_constant<int, 1>{})
            : p.Q == 2 ? rank(std::integral_constant<int, 2>{})
                       : rank(std::integral_constant<int, 4>{});
+}
+
+hipError_t launch_route(bool bf16, const void *x, const float *wg, const float *noise, int64_t N,
+                        int64_t d, const RouteRule &r, int32_t *idx, float *gate, float *scores,
+                        void *ws, hipStream_t s) {
+    // one part after the other in the same scratch
+    const RoutePlan p = route_plan(bf16, std::min(N, kRouteTokens), d, r.E);
+    for (int64_t t = 0; t < N; t += kRouteTokens) {
+        const hipError_t err = route_part(
+            bf16, p, static_cast<const char *>(x) + t * d * (bf16 ? 2 : 4), wg,
+            noise ? noise + t * r.E : nullptr, std::min(N - t, kRouteTokens), d, r, idx + t * r.k,
+            gate + t * r.k, scores ? scores + t * r.E : nullptr, ws, s);
+        if (err != hipSuccess)
+            return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moe

@@ -469,17 +469,28 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
     RouteGrad r{idx, p, dgate, dp, E, Ep, k, sigmoid, renorm, scale, ds, ds3, nullptr};
     if (dense)
         r.dsx = dsx;
-    const bool split = dense && dx;
-    const dim3 tb((unsigned)((N + 3) / 4 + (split ? ((int64_t)Ep * (d / 8) + 255) / 256 : 0)));
-    if (E <= 64)
-        hipLaunchKernelGGL(route_ds_kernel<1>, tb, dim3(256), 0, s, r, (int)N, wg, (int)d, wx);
-    else if (E <= 128)
-        hipLaunchKernelGGL(route_ds_kernel<2>, tb, dim3(256), 0, s, r, (int)N, wg, (int)d, wx);
-    else
-        hipLaunchKernelGGL(route_ds_kernel<4>, tb, dim3(256), 0, s, r, (int)N, wg, (int)d, wx);
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess)
-        return err;
+    hipError_t err;
+    for (int64_t t = 0; t < N; t += kRouteTokens) {
+        const int n = (int)std::min(N - t, kRouteTokens);
+        const bool split = dense && dx && t == 0;   // the first launch takes W_g as well
+        const dim3 tb((unsigned)((n + 3) / 4 + (split ? ((int64_t)Ep * (d / 8) + 255) / 256 : 0)));
+        RouteGrad q = r;
+        q.idx += t * k;
+        q.p += t * E;
+        q.dgate += t * k;
+        q.dp += dp ? t * E : 0;
+        q.ds += t * k;
+        q.ds3 += t * 3 * Ep;
+        q.dsx += dense ? t * kProducts * Ep : 0;
+        if (E <= 64)
+            hipLaunchKernelGGL(route_ds_kernel<1>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
+        else if (E <= 128)
+            hipLaunchKernelGGL(route_ds_kernel<2>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
+        else
+            hipLaunchKernelGGL(route_ds_kernel<4>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
+        if ((err = hipGetLastError()) != hipSuccess)
+            return err;
+    }
     if (dW) {
         const int rows = 3 * Ep;
         const DwShape sh = dw_shape(N, d, rows);

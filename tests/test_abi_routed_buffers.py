@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from sparse_mixture_experts_20_amd import binding as B
-from tests.test_abi_block import ALIGN, ARG, BF16, F32, t
+from tests.test_abi_block import ALIGN, ARG, BF16, F32, UNSUP, t
 
 P = 1 << 34     # apart from each other by more than any buffer here
 N, D, E, FF, K = 40, 64, 4, 128, 2
@@ -82,3 +82,26 @@ def test_overlaps(L, back):
             starts.add(OWN[b] - (m - 1) // first * first)
         for where in starts:
             assert _call(L, back, {**OWN, a: where}) == ARG, (a, b, where - OWN[b])
+
+
+def test_routing_limits(L):
+    """Widths past MOE_ROUTE_MAX_WIDTH and, for the backward, rows past
+    MOE_ROUTE_MAX_GRAD_ROWS are refused (a launch could not hold them)."""
+    wide, rows = (1 << 25) + 8, (1 << 29) + 1
+    P40 = 1 << 44
+    a = [(i + 1) * P40 for i in range(8)]
+
+    def back(n, d):
+        return L.moe_router_backward(
+            t(BF16, n, d, ptr=a[0]), t(F32, 8, d, ptr=a[1]), None, 2, a[2],
+            t(F32, n, 8, ptr=a[3]), t(F32, n, 2, ptr=a[4]), None, None, t(F32, n, d, ptr=a[5]),
+            t(F32, 8, d, ptr=a[6]), a[7], 1 << 43, None)
+    for dt in (F32, BF16):
+        assert L.moe_router_ex(t(dt, 4, wide, ptr=a[0]), t(F32, 8, wide, ptr=a[1]), None, None, 2,
+                               a[2], a[3], None, a[4], 1 << 43, None) == UNSUP
+        assert L.moe_router_ex_workspace_size(4, wide, 256, dt) == 0
+        assert L.moe_router_ex_workspace_size(4, 1 << 25, 256, dt) > 0
+    assert back(4, wide) == UNSUP and back(rows, 8) == UNSUP
+    f = L.moe_router_backward_workspace_size
+    assert f(4, wide, 8, 2) == 0 and f(rows, 8, 8, 2) == 0
+    assert f(4, 1 << 25, 8, 2) > 0 and f(1 << 29, 8, 8, 2) > 0

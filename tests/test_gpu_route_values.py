@@ -57,3 +57,41 @@ def test_no_tokens_of_many_experts(torch_mod, d, E, dtype):
     x, W = torch.empty((0, d), device="cuda", dtype=dt), torch.ones((E, d), device="cuda")
     idx, gate, p = B.route(x, W, 4, groups=8, keep_groups=2, export_scores=True)
     assert idx.shape == (0, 4) and gate.shape == (0, 4) and p.shape == (0, E)
+
+
+def test_more_tokens_than_a_launch_holds(torch_mod):
+    """64 threads a token pass a launch's 2^32 at 2^26 tokens: rows at both ends and on
+    both sides of the parts' borders are those of calls of their own, dW_g the sum of
+    the rows' terms (fp32: 2^-20 of the sum of magnitudes, ds's own roundings; sums of n
+    random signs add about sqrt(n) 2^-24 of one term, far less)."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    N, d, E, k = (1 << 26) + 77, 8, 2, 1
+    g = _gen(torch, 1)
+    x = torch.randint(-3, 4, (N, d), generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    W = torch.randint(-16, 17, (E, d), generator=g, device="cuda").float() / 16
+    dgate = torch.randint(-2, 3, (N, k), generator=g, device="cuda", dtype=torch.int8).float()
+    part = 1 << 25
+    ends = [slice(0, 1000), slice(N - 999, N)] + [slice(i * part - 500, i * part + 500)
+                                                  for i in (1, 2)]
+    for score in ("sigmoid", "softmax"):      # k and E values a token
+        G.say(f"[route] {N} tokens, {score}")
+        idx, gate, p = B.route(x, W, k, score=score, export_scores=True)
+        dx, dW = B.route_backward(x, W, idx, p, dgate, score=score)
+        for s in ends:
+            one = B.route(x[s], W, k, score=score, export_scores=True)
+            assert all(torch.equal(a[s], b) for a, b in zip((idx, gate, p), one))
+            alone, _ = B.route_backward(x[s], W, idx[s], p[s], dgate[s], score=score)
+            assert torch.equal(dx[s], alone)
+        want = torch.zeros((E, d), dtype=torch.float64, device="cuda")
+        size = torch.zeros_like(want)
+        for t in range(0, N, 1 << 23):
+            q, i, xs = p[t:t + (1 << 23)].double(), idx[t:t + (1 << 23)].long(), x[t:t + (1 << 23)]
+            up = torch.zeros_like(q).scatter_(1, i, dgate[t:t + (1 << 23)].double())
+            ds = q * (1 - q) * up if score == "sigmoid" else q * (up - (q * up).sum(1, keepdim=True))
+            for e in range(E):    # (a product of so many rows is slow in float64)
+                terms = ds[:, e:e + 1] * xs.double()
+                want[e] += terms.sum(0)
+                size[e] += terms.abs().sum(0)
+        assert bool(((dW.double() - want).abs() <= 2.0 ** -20 * size).all())
+        del idx, gate, p, dx
