@@ -607,7 +607,8 @@ typedef struct {
  * [-8, 7]. With it: the range [min(w, 0), max(w, 0)], scale = its length / 15
  * rounded to bf16, zero = the nearest integer to -min / scale and q = zero +
  * the nearest integer to w / scale, both in [0, 15]. Ties to even; a group
- * whose scale is 0 stands for zeros. q's buffers must not overlap W or each
+ * whose scale is 0 stands for zeros (past 2^127 a weight's value may round to
+ * infinity, as the scale is rounded). q's buffers must not overlap W or each
  * other (MOE_ERR_ARG). */
 int moe_quantize(const moe_tensor *W, moe_q4 *q, void *stream);
 

@@ -841,8 +841,11 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const void *__restrict
         hi = fmaxf(hi, __shfl_xor(hi, o));
         lo = fminf(lo, __shfl_xor(lo, o));
     }
-    const unsigned short sb =
-        f32_to_bf16_bits(zero ? (hi - lo) * (1.f / 15.f) : fmaxf(hi, -lo) * (1.f / 7.f));
+    const float range = hi - lo;   // (of finite weights past 2^127 it may be past fp32)
+    const unsigned short sb = f32_to_bf16_bits(
+        !zero                       ? fmaxf(hi, -lo) * (1.f / 7.f)
+        : range < __builtin_inff() ? range * (1.f / 15.f)
+                                   : hi * (1.f / 15.f) - lo * (1.f / 15.f));
     const float s = bf16_bits_to_f32(sb);
     float z = 8.f;
     if (zero)
