@@ -66,7 +66,9 @@ enum {
 
 /* Limits (MOE_ERR_UNSUPPORTED beyond them): E <= 256 experts, k <= 16,
  * N * k < 2^31 assignments, E * min(C, N) < 2^31 slots. bf16 tensors need
- * d and d_ff to be multiples of 8 and 16-byte aligned data pointers. */
+ * d and d_ff to be multiples of 8 and 16-byte aligned data pointers. A launch
+ * holds fewer than 2^32 threads: moe_router and the whole layer take up to 64 a
+ * token and return MOE_ERR_HIP for the tokens (2^26) that pass it. */
 #define MOE_MAX_EXPERTS 256
 #define MOE_MAX_TOPK 16
 #define MOE_FEW_MAX_TOKENS 64      /* tokens of moe_forward_few */

@@ -329,7 +329,7 @@ hipError_t launch_combine_backward(const void *dout, const void *Y, const signed
                                    bool gates) {
     if (N == 0)
         return hipSuccess;
-    hipLaunchKernelGGL(combine_backward_kernel, dim3((unsigned)((N + 3) / 4)), dim3(256), 0, s,
+    moeLaunchKernelGGL(combine_backward_kernel, dim3((unsigned)((N + 3) / 4)), dim3(256), 0, s,
                        static_cast<const unsigned short *>(dout), Y, ysh, gate, slot, (int)N,
                        (int)d, k, static_cast<unsigned short *>(dY), ds, dp, gates);
     return hipGetLastError();
@@ -340,7 +340,7 @@ hipError_t launch_ds_split(const float *ds, const int32_t *idx, int64_t N, int64
     const int64_t n = S * E * Tc;
     if (n == 0)
         return hipSuccess;
-    hipLaunchKernelGGL(ds_split_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, ds,
+    moeLaunchKernelGGL(ds_split_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, ds,
                        idx, (int)N, (int)Tc, (int)S, E, k, static_cast<unsigned short *>(dsT3));
     return hipGetLastError();
 }
@@ -350,7 +350,7 @@ hipError_t launch_row_sums(const void *T, int64_t rows, int64_t Kp, float *out, 
         return hipSuccess;
     if (Kp % 8 != 0)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL(row_sums_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s,
+    moeLaunchKernelGGL(row_sums_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s,
                        static_cast<const unsigned short *>(T), rows, (int)Kp, out);
     return hipGetLastError();
 }
@@ -362,7 +362,7 @@ hipError_t launch_colsum_rows(const void *src, int64_t C, int E, int64_t ceff,
         return hipSuccess;
     if (C % 8 != 0 || kdiv < 1)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL(colsum_rows_kernel, dim3((unsigned)((C + 511) / 512), (unsigned)E),
+    moeLaunchKernelGGL(colsum_rows_kernel, dim3((unsigned)((C + 511) / 512), (unsigned)E),
                        dim3(kColsumWaves * 64), 0, s, static_cast<const unsigned short *>(src),
                        (int)C, ceff,
                        used, slot_token, kdiv, out);
@@ -372,7 +372,7 @@ hipError_t launch_colsum_rows(const void *src, int64_t C, int E, int64_t ceff,
 hipError_t launch_chunk_sum(const float *part, int64_t S, int64_t n, float *out, hipStream_t s) {
     if (n == 0)
         return hipSuccess;
-    hipLaunchKernelGGL(chunk_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, part,
+    moeLaunchKernelGGL(chunk_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, part,
                        (int)S, n, out);
     return hipGetLastError();
 }
@@ -384,7 +384,7 @@ hipError_t launch_transpose_rows(const void *src, int64_t C, int64_t ceff, const
         return hipSuccess;
     if (C % 8 != 0 || Kp % 8 != 0 || map < 0 || map > 2)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL(transpose_rows_kernel,
+    moeLaunchKernelGGL(transpose_rows_kernel,
                        dim3((unsigned)((Kp + 63) / 64), (unsigned)((C + 63) / 64),
                             (unsigned)batch),
                        dim3(256), 0, s, static_cast<const unsigned short *>(src), (int)C, ceff,
@@ -399,7 +399,7 @@ hipError_t launch_dx(const float *dXa, const float *ds, const int32_t *idx, cons
     const int64_t n = N * (d / 4);
     if (n == 0)
         return hipSuccess;
-    hipLaunchKernelGGL(dx_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, dXa, ds,
+    moeLaunchKernelGGL(dx_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, dXa, ds,
                        idx, slot, Wg, N, (int)d, E, k, dx);
     return hipGetLastError();
 }

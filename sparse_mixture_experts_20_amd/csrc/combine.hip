@@ -214,7 +214,7 @@ hipError_t launch(const void *Y, const float *gate, const int32_t *slot, int64_t
     int64_t blocks = (total + 255) / 256;
     if (blocks > 65536)
         blocks = 65536;
-    hipLaunchKernelGGL((combine_kernel<YT, BF16, VEC>), dim3((unsigned)blocks), dim3(256), 0, s,
+    moeLaunchKernelGGL((combine_kernel<YT, BF16, VEC>), dim3((unsigned)blocks), dim3(256), 0, s,
                        static_cast<const YT *>(Y), gate, slot, N, (int)d, k, out);
     return hipGetLastError();
 }
@@ -239,7 +239,7 @@ hipError_t launch_combine_compact(const void *Y, const signed char *ysh, const f
         int64_t blocks = (N * (d / vec) + 255) / 256;
         if (blocks > 65536)
             blocks = 65536;
-        hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, s,
+        moeLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, s,
                            static_cast<const unsigned short *>(Y), ysh, gate, slot, N, (int)d, k,
                            out);
         return hipGetLastError();

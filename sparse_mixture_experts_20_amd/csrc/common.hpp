@@ -7,6 +7,21 @@
 
 namespace moe {
 
+// The grid of a launch of blocks b. HIP runs 2^32 threads or more along a dimension
+// as their number's low 32 bits, without an error: such a grid becomes an empty one,
+// which it refuses (hipErrorInvalidConfiguration).
+inline dim3 launch_grid(const dim3 &g, const dim3 &b) {
+    const uint64_t most = 0xffffffffull;
+    const bool fits = (uint64_t)g.x * b.x <= most && (uint64_t)g.y * b.y <= most &&
+                      (uint64_t)g.z * b.z <= most;
+    return fits ? g : dim3(0, 0, 0);
+}
+#define moeLaunchKernelGGL(kernel, grid, block, lds, stream, ...)                             \
+    do {                                                                                      \
+        const dim3 block_ = (block);                                                          \
+        (kernel)<<<moe::launch_grid((grid), block_), block_, (lds), (stream)>>>(__VA_ARGS__); \
+    } while (0)
+
 constexpr int kWave = 64;
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTopK = 16;

@@ -425,7 +425,7 @@ hipError_t launch_dispatch(const int32_t *idx, const float *gate, int64_t N, int
         return hipSuccess;
     const float *g = gate_sum ? gate : nullptr;
     if (chunks == 1) {
-        hipLaunchKernelGGL(dispatch_kernel<4>, dim3(1), dim3(kThreads), 0, s, idx, g, (int)N, E,
+        moeLaunchKernelGGL(dispatch_kernel<4>, dim3(1), dim3(kThreads), 0, s, idx, g, (int)N, E,
                            k, (int)ceff, (const int32_t *)nullptr, (const float *)nullptr, 0,
                            slot, used, slot_token, tiles, demand, drops, gate_sum);
         return hipGetLastError();
@@ -433,19 +433,19 @@ hipError_t launch_dispatch(const int32_t *idx, const float *gate, int64_t N, int
     int32_t *hist = static_cast<int32_t *>(ws);
     float *gpart = reinterpret_cast<float *>(static_cast<char *>(ws) +
                                              (size_t)(chunks * E * 4 + 255) / 256 * 256);
-    hipLaunchKernelGGL(chunk_hist_kernel, dim3((unsigned)chunks), dim3(kThreads), 0, s, idx, g,
+    moeLaunchKernelGGL(chunk_hist_kernel, dim3((unsigned)chunks), dim3(kThreads), 0, s, idx, g,
                        (int)N, E, k, hist, gpart);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
     const int scanned = chunks > kInlineChunks;
     if (scanned) {
-        hipLaunchKernelGGL(chunk_scan_kernel, dim3(1), dim3(256), 0, s, hist, (int)chunks, E);
+        moeLaunchKernelGGL(chunk_scan_kernel, dim3(1), dim3(256), 0, s, hist, (int)chunks, E);
         err = hipGetLastError();
         if (err != hipSuccess)
             return err;
     }
-    hipLaunchKernelGGL(dispatch_kernel<1>, dim3((unsigned)chunks), dim3(kThreads), 0, s, idx, g,
+    moeLaunchKernelGGL(dispatch_kernel<1>, dim3((unsigned)chunks), dim3(kThreads), 0, s, idx, g,
                        (int)N, E, k, (int)ceff, (const int32_t *)hist, (const float *)gpart,
                        scanned, slot, used, slot_token, tiles, demand, drops, gate_sum);
     return hipGetLastError();
@@ -454,7 +454,7 @@ hipError_t launch_dispatch(const int32_t *idx, const float *gate, int64_t N, int
 hipError_t launch_fill_i32(int32_t *p, int64_t n, int32_t v, hipStream_t s) {
     if (n <= 0)
         return hipSuccess;
-    hipLaunchKernelGGL(fill_i32_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p, n,
+    moeLaunchKernelGGL(fill_i32_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p, n,
                        v);
     return hipGetLastError();
 }

@@ -1376,13 +1376,13 @@ hipError_t launch_tiles(const unsigned short *A, const unsigned short *W, int64_
     // a multiple of the XCD count (the kernel walks the items)
     if (BM == 320 && (MODE == 0 || MODE == 1 || MODE == 5) && P >= kXcds)
         grid = std::min<int64_t>(grid, P / kXcds * kXcds);
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(NTHR), 0, s, A, W, (int)K, (int)Nout, E,
+    moeLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(NTHR), 0, s, A, W, (int)K, (int)Nout, E,
                        k, (int)ceff, used, slot_token, mt, O16, O32, split ? part : nullptr,
                        P, act, bias, mask, Z16, dp, (int64_t)0, (int64_t)0, (int64_t)0, ysh);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || !split)
         return err;
-    hipLaunchKernelGGL((split_fixup_kernel<BM, BN, BKT, MODE == 0 ? 0 : 1>),
+    moeLaunchKernelGGL((split_fixup_kernel<BM, BN, BKT, MODE == 0 ? 0 : 1>),
                        dim3((unsigned)(P * (BM / 16))),
                        dim3(256), 0, s, (int)K, (int)Nout, E, (int)ceff, used, slot_token, mt,
                        (const float *)part, P, O16, O32, act, bias, dp, Z16, ysh, k);
@@ -1468,7 +1468,7 @@ hipError_t launch_router_scores_bf16(const void *x, const void *wsp, int64_t N, 
     const int ns = router_score_splits(N, d, Ep);
     const int64_t tiles = ((N + 255) / 256) * ((Ep + 255) / 256);
     const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((expert_gemm_kernel<256, 256, 4, 4, 1, kBK, 2, 7>),
+    moeLaunchKernelGGL((expert_gemm_kernel<256, 256, 4, 4, 1, kBK, 2, 7>),
                        dim3((unsigned)grid, (unsigned)ns), dim3(1024), 0, s,
                        static_cast<const unsigned short *>(x),
                        static_cast<const unsigned short *>(wsp), (int)(3 * d), (int)Ep, 1, 1,
@@ -1496,7 +1496,7 @@ hipError_t launch_expert_up(bool bf16, const void *x, const void *w_up, int64_t 
                               static_cast<unsigned short *>(Z));
     if (Z)
         return hipErrorInvalidValue;   // pre-activations are kept for bf16 layers only
-    hipLaunchKernelGGL(experts_f32_kernel<0>,
+    moeLaunchKernelGGL(experts_f32_kernel<0>,
                        dim3((unsigned)((d_ff + 63) / 64), (unsigned)((ceff + 63) / 64), E),
                        dim3(256), 0, s, static_cast<const float *>(x),
                        static_cast<const float *>(w_up), (int)d, (int)d_ff, k, (int)ceff, used,
@@ -1530,7 +1530,7 @@ hipError_t launch_expert_down(bool bf16, const void *H, const void *w_down, int6
                               static_cast<const unsigned short *>(w_down), d_ff, d, E, k, ceff,
                               used, slot_token, tiles, y16, part, part_bytes, kActRelu,
                               b_down, s, nullptr, y32, nullptr, Dropout{}, ysh);
-    hipLaunchKernelGGL(experts_f32_kernel<1>,
+    moeLaunchKernelGGL(experts_f32_kernel<1>,
                        dim3((unsigned)((d + 63) / 64), (unsigned)((ceff + 63) / 64), E),
                        dim3(256), 0, s, static_cast<const float *>(H),
                        static_cast<const float *>(w_down), (int)d_ff, (int)d, k, (int)ceff, used,
@@ -1600,7 +1600,7 @@ hipError_t launch_weight_grad(const void *A, int64_t M, const void *B, int64_t N
     const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256);
     if (M >= 512 && N >= 512 && t256 * E >= 1024) {
         const int64_t grid = (t256 + kXcds - 1) / kXcds * kXcds;
-        hipLaunchKernelGGL((expert_gemm_kernel<256, 256, 2, 4, 1, kBK, 2, 6>),
+        moeLaunchKernelGGL((expert_gemm_kernel<256, 256, 2, 4, 1, kBK, 2, 6>),
                            dim3((unsigned)grid, (unsigned)E), dim3(512), 0, s, a, w, 0, (int)N,
                            E, kdiv, (int)ceff, used, slot_token, (const int32_t *)nullptr,
                            (unsigned short *)nullptr, out, (float *)nullptr, 0, gathered,
@@ -1610,7 +1610,7 @@ hipError_t launch_weight_grad(const void *A, int64_t M, const void *B, int64_t N
         return hipGetLastError();
     }
     const int64_t grid = (((M + 127) / 128) * ((N + 127) / 128) + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((expert_gemm_kernel<128, 128, 2, 2, 1, kBK, 2, 6>),
+    moeLaunchKernelGGL((expert_gemm_kernel<128, 128, 2, 2, 1, kBK, 2, 6>),
                        dim3((unsigned)grid, (unsigned)E), dim3(256), 0, s, a, w, 0, (int)N, E,
                        kdiv, (int)ceff, used, slot_token, (const int32_t *)nullptr,
                        (unsigned short *)nullptr, out, (float *)nullptr, 0, gathered,
@@ -1632,7 +1632,7 @@ hipError_t launch_batched_gemm_bf16(const void *A, const void *W, int64_t M, int
     const int64_t t256 = ((M + 255) / 256) * ((Nout + 255) / 256);
     if (M >= 512 && Nout >= 512 && K >= 256 && t256 * batch >= 1024) {
         const int64_t grid = (t256 + kXcds - 1) / kXcds * kXcds;
-        hipLaunchKernelGGL((expert_gemm_kernel<256, 256, 2, 4, 1, kBK, 2, 2>),
+        moeLaunchKernelGGL((expert_gemm_kernel<256, 256, 2, 4, 1, kBK, 2, 2>),
                            dim3((unsigned)grid, (unsigned)batch), dim3(512), 0, s, a, w, (int)K,
                            (int)Nout, 1, 1, (int)M, (const int32_t *)nullptr,
                            (const int32_t *)nullptr, (const int32_t *)nullptr,
@@ -1642,7 +1642,7 @@ hipError_t launch_batched_gemm_bf16(const void *A, const void *W, int64_t M, int
         return hipGetLastError();
     }
     const int64_t grid = (((M + 127) / 128) * ((Nout + 127) / 128) + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((expert_gemm_kernel<128, 128, 2, 2, 1, kBK, 2, 2>),
+    moeLaunchKernelGGL((expert_gemm_kernel<128, 128, 2, 2, 1, kBK, 2, 2>),
                        dim3((unsigned)grid, (unsigned)batch), dim3(256), 0, s, a, w, (int)K,
                        (int)Nout, 1, 1, (int)M, (const int32_t *)nullptr,
                        (const int32_t *)nullptr, (const int32_t *)nullptr,

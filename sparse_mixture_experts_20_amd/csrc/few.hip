@@ -849,7 +849,7 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
     hipError_t err = hipSuccess;
     const bool score = scores_in_plan(N, d, E);
     if (!score) {
-        hipLaunchKernelGGL((few_scores_kernel<S, TT>),
+        moeLaunchKernelGGL((few_scores_kernel<S, TT>),
                            dim3((unsigned)((E + 15) / 16), (unsigned)ns), dim3(kThreads), 0, s, x,
                            wg, N, d, E, P);
         err = hipGetLastError();
@@ -865,7 +865,7 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
     auto rank_and_plan = [&](auto lanes) {
         constexpr int QQ = decltype(lanes)::value;
         if (!inside) {
-            hipLaunchKernelGGL(few_rank_kernel<QQ>, dim3((unsigned)((N + kWaves - 1) / kWaves)),
+            moeLaunchKernelGGL(few_rank_kernel<QQ>, dim3((unsigned)((N + kWaves - 1) / kWaves)),
                                dim3(kThreads), 0, s, (const float *)P, ns, noise, N, E, k, r.idx,
                                r.gate);
             const hipError_t rc = hipGetLastError();
@@ -873,10 +873,10 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
                 return rc;
         }
         if (QQ == 1 && TT == 1 && score)
-            hipLaunchKernelGGL((few_plan_kernel<S, 1, true>), dim3(1), dim3(kPlanWaves * 64), 0, s,
+            moeLaunchKernelGGL((few_plan_kernel<S, 1, true>), dim3(1), dim3(kPlanWaves * 64), 0, s,
                                x, wg, r, N, d, E, k, cap);
         else
-            hipLaunchKernelGGL((few_plan_kernel<S, QQ, false>), dim3(1), dim3(kPlanWaves * 64), 0,
+            moeLaunchKernelGGL((few_plan_kernel<S, QQ, false>), dim3(1), dim3(kPlanWaves * 64), 0,
                                s, x, wg, r, N, d, E, k, cap);
         return hipGetLastError();
     };
@@ -889,14 +889,14 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
         if (tiled(true, N, E, k)) {
             const int tr = tiled_ranges(N, d, E, d_ff, k);
             float *Y = reinterpret_cast<float *>(ws + L.part);
-            hipLaunchKernelGGL(few_tile_kernel<true>,
+            moeLaunchKernelGGL(few_tile_kernel<true>,
                                dim3((unsigned)((d_ff + kTileCols - 1) / kTileCols), hits),
                                dim3(512), 0, s, x, static_cast<const T *>(wu), b_up,
                                (const FewPlan *)r.plan, N, d, d_ff, k, act, H, (float *)nullptr);
             err = hipGetLastError();
             if (err != hipSuccess)
                 return err;
-            hipLaunchKernelGGL(
+            moeLaunchKernelGGL(
                 few_tile_kernel<false>,
                 dim3((unsigned)((d + kTileCols - 1) / kTileCols), hits, (unsigned)tr), dim3(512), 0,
                 s, (const T *)H, static_cast<const T *>(wd), b_down, (const FewPlan *)r.plan, N,
@@ -904,20 +904,20 @@ static hipError_t few_call(const void *xv, const float *wg, const float *noise, 
             err = hipGetLastError();
             if (err != hipSuccess)
                 return err;
-            hipLaunchKernelGGL(few_combine_kernel,
+            moeLaunchKernelGGL(few_combine_kernel,
                                dim3((unsigned)(((int64_t)N * (d / 8) + 255) / 256)), dim3(256), 0,
                                s, (const float *)Y, tr, (const float *)r.gate,
                                (const int32_t *)r.slot, N, d, k, static_cast<T *>(out));
             return hipGetLastError();
         }
     }
-    hipLaunchKernelGGL((few_up_kernel<S, TT>), dim3((unsigned)((d_ff + 15) / 16), hits),
+    moeLaunchKernelGGL((few_up_kernel<S, TT>), dim3((unsigned)((d_ff + 15) / 16), hits),
                        dim3(kThreads), 0, s, x, static_cast<const T *>(wu), b_up,
                        (const FewPlan *)r.plan, N, d, d_ff, k, act, H);
     err = hipGetLastError();
     if (err != hipSuccess)
         return err;
-    hipLaunchKernelGGL((few_down_kernel<S, TT>), dim3((unsigned)g.blocks, (unsigned)g.ranges),
+    moeLaunchKernelGGL((few_down_kernel<S, TT>), dim3((unsigned)g.blocks, (unsigned)g.ranges),
                        dim3(kThreads), 0, s, (const T *)H, static_cast<const T *>(wd), b_down,
                        (const float *)r.gate, (const FewPlan *)r.plan, N, d, d_ff, k, r.done,
                        reinterpret_cast<float *>(ws + L.part), static_cast<T *>(out));

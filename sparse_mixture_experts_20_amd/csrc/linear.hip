@@ -547,7 +547,7 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
         const int64_t T = ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn);
         const int64_t each = (T + kXcdCount - 1) / kXcdCount;   // tiles of an XCD
         const int64_t whole = bm == 256 ? whole_tiles(each) : each;
-        hipLaunchKernelGGL(kernel,
+        moeLaunchKernelGGL(kernel,
                            dim3((unsigned)(kXcdCount * (whole + 2 * (each - whole))),
                                 (unsigned)sh.splits),
                            dim3(threads), 0, s, a, b, (int)rows, (int)cols, (int)K, (int)whole, ep,
@@ -564,7 +564,7 @@ hipError_t launch_product(const void *A, const void *B, int64_t rows, int64_t co
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || sh.splits == 1)
         return err;
-    hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)((rows * cols / 8 + 255) / 256)),
+    moeLaunchKernelGGL(linear_join_kernel, dim3((unsigned)((rows * cols / 8 + 255) / 256)),
                        dim3(256), 0, s, (const float *)part, sh.splits, rows, (int)cols, ep);
     return hipGetLastError();
 }
@@ -611,7 +611,7 @@ hipError_t launch_linear(const void *x, const void *W, const float *bias, int ac
             constexpr int TT = decltype(tiles)::value;
             constexpr bool HALF = decltype(half)::value;
             constexpr int CB = HALF ? 8 : 16;
-            hipLaunchKernelGGL((linear_few_kernel<TT, HALF>), dim3((unsigned)((M + CB - 1) / CB)),
+            moeLaunchKernelGGL((linear_few_kernel<TT, HALF>), dim3((unsigned)((M + CB - 1) / CB)),
                                dim3(kFewWaves * 64), 0, s, static_cast<const unsigned short *>(x),
                                static_cast<const unsigned short *>(W), (int)N, (int)M, (int)K, ep);
             return hipGetLastError();
@@ -649,7 +649,7 @@ hipError_t launch_linear_backward(const void *x, const void *W, const void *z, i
         const int P = dz_groups(N, M);
         const int per = (int)dz_rows(N, M);
         float *sums = reinterpret_cast<float *>(w + L.sums);
-        hipLaunchKernelGGL(linear_dz_kernel, dim3((unsigned)((M + 255) / 256), (unsigned)P),
+        moeLaunchKernelGGL(linear_dz_kernel, dim3((unsigned)((M + 255) / 256), (unsigned)P),
                            dim3(256), 0, s, static_cast<const unsigned short *>(dout),
                            static_cast<const unsigned short *>(z), (int)N, (int)M, act, per,
                            reinterpret_cast<unsigned short *>(w + L.dz), db ? sums : nullptr);
@@ -678,7 +678,7 @@ hipError_t launch_linear_backward(const void *x, const void *W, const void *z, i
         const int blocks = pair_tiles(px) + pair_tiles(pw);
         if (blocks == 0)
             return hipSuccess;
-        hipLaunchKernelGGL(linear_pair_kernel, dim3((unsigned)(kXcdCount * blocks)), dim3(512), 0, s,
+        moeLaunchKernelGGL(linear_pair_kernel, dim3((unsigned)(kXcdCount * blocks)), dim3(512), 0, s,
                            px, pw);
         return hipGetLastError();
     }

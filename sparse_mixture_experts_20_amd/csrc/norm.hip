@@ -471,7 +471,7 @@ hipError_t launch_layer_norm(bool bf16, bool vec, const void *x, const void *res
         const int64_t blocks = (N + groups - 1) / groups;
         // a grid of 2048 threads per CU (256 CUs) walks the rows
         const int64_t most = 2048 * 256 / (C::tpr < 256 ? 256 : C::tpr);
-        hipLaunchKernelGGL((layer_norm_kernel<T, C::vec, C::tpr, C::nv>),
+        moeLaunchKernelGGL((layer_norm_kernel<T, C::vec, C::tpr, C::nv>),
                            dim3((unsigned)(blocks < most ? blocks : most)),
                            dim3(C::tpr < 256 ? 256 : C::tpr), 0, s, static_cast<const T *>(x),
                            static_cast<const T *>(res), w, b, eps, N, (int)d,
@@ -492,7 +492,7 @@ hipError_t launch_layer_norm_backward(bool bf16, bool vec, const void *x, const 
         const int64_t blocks = (N + groups - 1) / groups;
         const int64_t most = backward_groups(C::tpr);
         P = (int)(blocks < most ? blocks : most);
-        hipLaunchKernelGGL((layer_norm_backward_kernel<T, C::vec, C::tpr, C::nv>),
+        moeLaunchKernelGGL((layer_norm_backward_kernel<T, C::vec, C::tpr, C::nv>),
                            dim3((unsigned)P), dim3(C::tpr < 256 ? 256 : C::tpr), 0, s,
                            static_cast<const T *>(x), w, mean, rstd, static_cast<const T *>(dout),
                            static_cast<const T *>(dres), N, (int)d, static_cast<T *>(dx), part);
@@ -521,7 +521,7 @@ hipError_t launch_column_sums(const float *part, int P, int64_t ld, int64_t d, f
             }
         return hipSuccess;
     }
-    hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((d + 63) / 64), b ? 2u : 1u),
+    moeLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((d + 63) / 64), b ? 2u : 1u),
                        dim3(kSumGroups * 64), 0, s, part, P, (int)ld, (int)d, a, b);
     return hipGetLastError();
 }

@@ -1017,7 +1017,7 @@ hipError_t launch_linear_q4(const void *x, const void *data, const void *scale, 
                       [&](auto gs, auto z, auto rt, auto tt, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(tt)::value;
         const int rows = 16 * RT * sh.w.wm;
-        hipLaunchKernelGGL((q4_linear_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((M + rows - 1) / rows)),
+        moeLaunchKernelGGL((q4_linear_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((M + rows - 1) / rows)),
                            dim3(sh.threads), sh.smem, s, p, sh.w);
         return hipGetLastError();
     });
@@ -1065,7 +1065,7 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     unsigned blocks = (unsigned)A;   // of a column: one for each assignment or hit expert
     if (A > 64) {
         Q4Plan *plan = reinterpret_cast<Q4Plan *>(w + L.plan);
-        hipLaunchKernelGGL(q4_plan_kernel, dim3(1), dim3(kMaxAssign), 0, s, idx, (int)A, E, plan);
+        moeLaunchKernelGGL(q4_plan_kernel, dim3(1), dim3(kMaxAssign), 0, s, idx, (int)A, E, plan);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess)
             return err;
@@ -1089,7 +1089,7 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     const hipError_t err = with_shape(group, up[2] != nullptr, us.rt, tt, us.two,
                                       [&](auto gs, auto z, auto rt, auto t, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
-        hipLaunchKernelGGL((q4_up_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((d_ff + ur - 1) / ur), blocks),
+        moeLaunchKernelGGL((q4_up_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((d_ff + ur - 1) / ur), blocks),
                            dim3(us.threads), us.smem, s, p, us.w, (int)((d + dr - 1) / dr));
         return hipGetLastError();
     });
@@ -1098,13 +1098,13 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     const hipError_t rc = with_shape(group, down[2] != nullptr, ds.rt, tt, ds.two,
                       [&](auto gs, auto z, auto rt, auto t, auto two) {
         constexpr int GS = decltype(gs)::value, RT = decltype(rt)::value, TT = decltype(t)::value;
-        hipLaunchKernelGGL((q4_down_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((d + dr - 1) / dr), blocks),
+        moeLaunchKernelGGL((q4_down_kernel<GS, decltype(z)::value, RT, TT, decltype(two)::value>), dim3((unsigned)((d + dr - 1) / dr), blocks),
                            dim3(ds.threads), ds.smem, s, p, ds.w);
         return hipGetLastError();
     });
     if (rc != hipSuccess || !apart)
         return rc;
-    hipLaunchKernelGGL(q4_combine_kernel, dim3((unsigned)((N * (d / 4) + 255) / 256)), dim3(256), 0,
+    moeLaunchKernelGGL(q4_combine_kernel, dim3((unsigned)((N * (d / 4) + 255) / 256)), dim3(256), 0,
                        s, p);
     return hipGetLastError();
 }
@@ -1114,11 +1114,11 @@ hipError_t launch_quantize_q4(bool bf16, const void *W, int64_t n, int group, vo
     const int64_t n8 = n / 8;
     const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
     if (bf16)
-        hipLaunchKernelGGL(q4_quantize_kernel<true>, grid, block, 0, s, W, n8, group,
+        moeLaunchKernelGGL(q4_quantize_kernel<true>, grid, block, 0, s, W, n8, group,
                            static_cast<unsigned *>(data), static_cast<unsigned short *>(scale),
                            static_cast<unsigned short *>(zero));
     else
-        hipLaunchKernelGGL(q4_quantize_kernel<false>, grid, block, 0, s, W, n8, group,
+        moeLaunchKernelGGL(q4_quantize_kernel<false>, grid, block, 0, s, W, n8, group,
                            static_cast<unsigned *>(data), static_cast<unsigned short *>(scale),
                            static_cast<unsigned short *>(zero));
     return hipGetLastError();
@@ -1129,12 +1129,12 @@ hipError_t launch_dequantize_q4(bool bf16, const void *data, const void *scale, 
     const int64_t n8 = n / 8;
     const dim3 grid((unsigned)((n8 + 255) / 256)), block(256);
     if (bf16)
-        hipLaunchKernelGGL(q4_dequantize_kernel<true>, grid, block, 0, s,
+        moeLaunchKernelGGL(q4_dequantize_kernel<true>, grid, block, 0, s,
                            static_cast<const unsigned *>(data),
                            static_cast<const unsigned short *>(scale),
                            static_cast<const unsigned short *>(zero), n8, group, W);
     else
-        hipLaunchKernelGGL(q4_dequantize_kernel<false>, grid, block, 0, s,
+        moeLaunchKernelGGL(q4_dequantize_kernel<false>, grid, block, 0, s,
                            static_cast<const unsigned *>(data),
                            static_cast<const unsigned short *>(scale),
                            static_cast<const unsigned short *>(zero), n8, group, W);

@@ -507,7 +507,7 @@ static hipError_t route_part(bool bf16, const RoutePlan &p, const void *xv, cons
             const unsigned blocks = (unsigned)((N + 15) / 16);
             auto go = [&](auto nt, auto nw) {
                 constexpr int NT = decltype(nt)::value, NW = decltype(nw)::value;
-                hipLaunchKernelGGL((route_fused_kernel<S, NT, NW>), dim3(blocks), dim3(NW * 64), 0,
+                moeLaunchKernelGGL((route_fused_kernel<S, NT, NW>), dim3(blocks), dim3(NW * 64), 0,
                                    s, x, wg, noise, (int)N, (int)d, r, o);
                 return hipGetLastError();
             };
@@ -523,7 +523,7 @@ static hipError_t route_part(bool bf16, const RoutePlan &p, const void *xv, cons
         }
         auto go = [&](auto tiles) {
             constexpr int TT = decltype(tiles)::value;
-            hipLaunchKernelGGL((route_scores_kernel<S, TT>),
+            moeLaunchKernelGGL((route_scores_kernel<S, TT>),
                                dim3((unsigned)((r.E + 15) / 16 * ((N + 16 * TT - 1) / (16 * TT))),
                                     (unsigned)p.ranges),
                                dim3(256), 0, s, x, wg, (int)N, (int)d, r.E, p.Q, p.ld, P);
@@ -544,7 +544,7 @@ static hipError_t route_part(bool bf16, const RoutePlan &p, const void *xv, cons
         return err;
     auto rank = [&](auto q) {
         constexpr int Q = decltype(q)::value;
-        hipLaunchKernelGGL((route_rank_kernel<Q>), dim3((unsigned)((N + 3) / 4)), dim3(256), 0, s,
+        moeLaunchKernelGGL((route_rank_kernel<Q>), dim3((unsigned)((N + 3) / 4)), dim3(256), 0, s,
                            (const float *)P, ns, p.ld, noise, (int)N, r, o);
         return hipGetLastError();
     };

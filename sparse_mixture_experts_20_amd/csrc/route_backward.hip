@@ -483,11 +483,11 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
         q.ds3 += t * 3 * Ep;
         q.dsx += dense ? t * kProducts * Ep : 0;
         if (E <= 64)
-            hipLaunchKernelGGL(route_ds_kernel<1>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
+            moeLaunchKernelGGL(route_ds_kernel<1>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
         else if (E <= 128)
-            hipLaunchKernelGGL(route_ds_kernel<2>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
+            moeLaunchKernelGGL(route_ds_kernel<2>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
         else
-            hipLaunchKernelGGL(route_ds_kernel<4>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
+            moeLaunchKernelGGL(route_ds_kernel<4>, tb, dim3(256), 0, s, q, n, wg, (int)d, wx);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
     }
@@ -497,17 +497,17 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
         const unsigned short *xs = static_cast<const unsigned short *>(x);
         const dim3 grid((unsigned)sh.tiles, (unsigned)sh.ranges);
         if (sh.bm == 256)
-            hipLaunchKernelGGL((route_dw_kernel<256, 256, 4, 4, 2>), grid, dim3(1024), 0, s, ds3,
+            moeLaunchKernelGGL((route_dw_kernel<256, 256, 4, 4, 2>), grid, dim3(1024), 0, s, ds3,
                                xs, rows, (int)d, (int)N, part);
         else if (sh.bm == 128)
-            hipLaunchKernelGGL((route_dw_kernel<128, 128, 4, 2, 2>), grid, dim3(512), 0, s, ds3,
+            moeLaunchKernelGGL((route_dw_kernel<128, 128, 4, 2, 2>), grid, dim3(512), 0, s, ds3,
                                xs, rows, (int)d, (int)N, part);
         else
-            hipLaunchKernelGGL((route_dw_kernel<64, 128, 4, 2, 2>), grid, dim3(512), 0, s, ds3, xs,
+            moeLaunchKernelGGL((route_dw_kernel<64, 128, 4, 2, 2>), grid, dim3(512), 0, s, ds3, xs,
                                rows, (int)d, (int)N, part);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
-        hipLaunchKernelGGL(route_dw_sum_kernel, dim3((unsigned)((E * (d / 4) + 255) / 256)),
+        moeLaunchKernelGGL(route_dw_sum_kernel, dim3((unsigned)((E * (d / 4) + 255) / 256)),
                            dim3(256), 0, s, (const float *)part, sh.ranges, E, Ep, (int)d, dW);
         if ((err = hipGetLastError()) != hipSuccess)
             return err;
@@ -518,10 +518,10 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
         const int K = kProducts * Ep;
         const dim3 grid((unsigned)((N + 127) / 128 * ((d + 127) / 128)));
         if (dx32)
-            hipLaunchKernelGGL(route_dx_dense_kernel<true>, grid, dim3(512), 0, s, dsx, wx, dres,
+            moeLaunchKernelGGL(route_dx_dense_kernel<true>, grid, dim3(512), 0, s, dsx, wx, dres,
                                (int)N, (int)d, K, dx);
         else
-            hipLaunchKernelGGL(route_dx_dense_kernel<false>, grid, dim3(512), 0, s, dsx, wx, dres,
+            moeLaunchKernelGGL(route_dx_dense_kernel<false>, grid, dim3(512), 0, s, dsx, wx, dres,
                                (int)N, (int)d, K, dx);
         return hipGetLastError();
     }
@@ -533,7 +533,7 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
         const int64_t per_cu = lds <= 40 * 1024 ? 2 : 1;   // (1024 threads each)
         const int64_t groups = std::min<int64_t>(std::max<int64_t>(256 * per_cu / blocks, 1),
                                                  (N + 15) / 16);
-        hipLaunchKernelGGL((route_dx_kernel<decltype(f32)::value, V>),
+        moeLaunchKernelGGL((route_dx_kernel<decltype(f32)::value, V>),
                            dim3((unsigned)blocks, (unsigned)groups), dim3(1024), lds, s,
                            (const float *)ds, idx, wg, dres, (int)N, (int)d, E, k, dx);
         return hipGetLastError();

@@ -360,11 +360,11 @@ hipError_t launch_fused(const void *x, const float *wg, const float *noise, int6
                         int64_t d, int E, int k, int32_t *idx, float *gate, hipStream_t s) {
     const int blocks = (int)((N + kTokTile - 1) / kTokTile);
     if (d >= 2048)
-        hipLaunchKernelGGL((router_bf16_kernel<NT, 16>), dim3(blocks), dim3(1024), 0, s,
+        moeLaunchKernelGGL((router_bf16_kernel<NT, 16>), dim3(blocks), dim3(1024), 0, s,
                            static_cast<const unsigned short *>(x), wg, noise, (int)N, (int)d, E,
                            k, idx, gate);
     else
-        hipLaunchKernelGGL((router_bf16_kernel<NT, 4>), dim3(blocks), dim3(256), 0, s,
+        moeLaunchKernelGGL((router_bf16_kernel<NT, 4>), dim3(blocks), dim3(256), 0, s,
                            static_cast<const unsigned short *>(x), wg, noise, (int)N, (int)d, E,
                            k, idx, gate);
     return hipGetLastError();
@@ -375,7 +375,7 @@ hipError_t launch_rank(const float *P, int ns, const float *noise, int64_t N, in
                        int k, int32_t *idx, float *gate, hipStream_t s) {
     const int64_t tokens_per_block = 4 * (64 / G);
     const int blocks = (int)((N + tokens_per_block - 1) / tokens_per_block);
-    hipLaunchKernelGGL((rank_scores_kernel<G, Q>), dim3(blocks), dim3(256), 0, s, P, ns, noise,
+    moeLaunchKernelGGL((rank_scores_kernel<G, Q>), dim3(blocks), dim3(256), 0, s, P, ns, noise,
                        (int)N, E, Ep, k, idx, gate);
     return hipGetLastError();
 }
@@ -400,7 +400,7 @@ hipError_t launch_router_partials(const void *x, const float *wg, int64_t N, int
     const int Ep = (int)router_padded_experts(E);
     unsigned short *wsp = static_cast<unsigned short *>(ws);
     const int64_t groups = (int64_t)Ep * (d / 8);
-    hipLaunchKernelGGL(split_router_weights_kernel, dim3((unsigned)((groups + 255) / 256)),
+    moeLaunchKernelGGL(split_router_weights_kernel, dim3((unsigned)((groups + 255) / 256)),
                        dim3(256), 0, s, wg, E, Ep, (int)d, router_terms_interleaved(d), wsp);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess)
@@ -435,7 +435,7 @@ hipError_t launch_router_f32(const float *x, const float *wg, const float *noise
     if (N == 0)
         return hipSuccess;
     const int blocks = (int)((N + 3) / 4);
-    hipLaunchKernelGGL(router_f32_kernel, dim3(blocks), dim3(256), 0, s, x, wg, noise, (int)N,
+    moeLaunchKernelGGL(router_f32_kernel, dim3(blocks), dim3(256), 0, s, x, wg, noise, (int)N,
                        (int)d, E, k, idx, gate);
     return hipGetLastError();
 }
