@@ -680,7 +680,9 @@ size_t moe_experts_quant_workspace_size(int64_t N, int64_t d, int64_t E, int64_t
  * group_best   1 or 2 (0: 1): a group's score is the sum of its that many
  *              largest c (of one in a group of one)
  * renormalize  nonzero: gates are divided by the sum of the chosen p
- * scale        gates are multiplied by it; finite, >= 0 (0: 1) */
+ * scale        gates are multiplied by it; finite, >= 0 (0: 1)
+ * gates        moe_router_backward with renormalize alone: the topk_gate that the
+ *              forward wrote (fp32 [N, k], device, 4-byte aligned), or NULL */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 typedef struct {
     int32_t score;
@@ -690,6 +692,7 @@ typedef struct {
     int32_t group_best;
     int32_t renormalize;
     float scale;
+    const float *gates;
 } moe_router_opts;
 
 /* moe_router with these options (NULL: all zeros): topk_idx [N, k] int32, the k
@@ -715,8 +718,11 @@ size_t moe_router_ex_workspace_size(int64_t N, int64_t d, int64_t E, int32_t dty
  *   ds the gradient of s: through the scaling, the renormalisation and the
  *   softmax or sigmoid (the choice passes none),
  *   dW_g = ds^T x,  dx = ds W_g + dres
- * topk_idx and scores are the forward's; an id outside [0, E) has no gate, and
- * renormalised gates whose p are all 0 (underflown) pass no gradient.
+ * topk_idx and scores are the forward's; an id outside [0, E) has no gate. The
+ * gradient of renormalised gates takes each one's share p / sum of the chosen p from
+ * opts->gates; without them from the scores, which for a softmax underflow where the
+ * forward's gates do not: chosen p below fp32's normal range (2^-126) then give shares
+ * of as few bits as they have, and where all are 0 no gradient.
  * x [N, d] and W_g [E, d] as the forward's, bf16 x (MOE_ERR_UNSUPPORTED for
  * fp32, and past MOE_ROUTE_MAX_GRAD_ROWS tokens). dx [N, d] MOE_F32 or MOE_BF16, dres (or NULL) like it: a gradient that
  * reaches x another way, as the layer's own; dx may be its buffer. dW_g [E, d]

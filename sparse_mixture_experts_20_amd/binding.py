@@ -73,7 +73,8 @@ class MoeQ4(ctypes.Structure):
 class MoeRouterOpts(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int32),
                 ("keep_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
-                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("gates", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -1232,14 +1233,16 @@ def experts_q4(x, idx, gate, W_up: Q4, W_down: Q4, act: str = "relu", b_up=None,
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _route_opts(score, bias, groups, keep_groups, group_best, renormalize, scale, index):
+def _route_opts(score, bias, groups, keep_groups, group_best, renormalize, scale, index,
+                gates=None):
     """(``moe_router_opts`` by reference, what it points at)."""
     if score not in SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     b = _pack(bias, index)
     # (the bias' descriptor: the packed bytes, kept alive by the caller)
     at = None if b is None else ctypes.cast(ctypes.c_char_p(b), ctypes.c_void_p)
-    o = MoeRouterOpts(SCORES[score], at, groups, keep_groups, group_best, int(renormalize), scale)
+    o = MoeRouterOpts(SCORES[score], at, groups, keep_groups, group_best, int(renormalize), scale,
+                      gates)
     return ctypes.byref(o), (o, b)
 
 
@@ -1278,10 +1281,13 @@ def route_backward_workspace_size(N: int, d: int, E: int, k: int) -> int:
 @_on_stream
 def route_backward(x, W_g, idx, scores, dgate, dscores=None, dres=None, score: str = "softmax",
                    renormalize: bool = False, scale: float = 1.0, need_dx: bool = True,
-                   need_dW: bool = True, dx_dtype=torch.float32, dx=None, workspace=None):
+                   need_dW: bool = True, dx_dtype=torch.float32, dx=None, workspace=None,
+                   gate=None):
     """Gradients of :func:`route` for ``dgate`` [N, k] (and ``dscores`` [N, E],
     what an auxiliary loss gives the scores): ``(dx, dW_g)``, None for the ones
-    not asked for; ``dres`` is added to dx. idx and scores are the forward's."""
+    not asked for; ``dres`` is added to dx. idx and scores are the forward's, and
+    gate, if given: renormalised softmax gates of experts whose scores underflow
+    (chosen by a bias far above them) have their gradient from it alone."""
     N, d, E, k = x.numel() // x.shape[-1], x.shape[-1], W_g.shape[0], idx.shape[-1]
     index, dev = _device_of(x), x.device
     ip, _ = _routing_ptrs(idx, dgate, N, k, index)
@@ -1292,7 +1298,8 @@ def route_backward(x, W_g, idx, scores, dgate, dscores=None, dres=None, score: s
         n = route_backward_workspace_size(N, d, E, k)
         workspace = alloc_workspace(n, dev) if n else None
     ws, wn = _scratch(workspace, index)
-    o, keep = _route_opts(score, None, 1, 0, 1, renormalize, scale, index)
+    gp = None if gate is None else _routing_ptrs(idx, gate, N, k, index)[1]
+    o, keep = _route_opts(score, None, 1, 0, 1, renormalize, scale, index, gp)
     _run(index, "moe_router_backward", lib().moe_router_backward, _pack(x, index),
          _pack(W_g, index), o, k, ip, _pack(scores, index), _pack(dgate, index),
          _pack(dscores, index), _pack(dres, index), _pack(dx, index), _pack(dW, index), ws, wn,

@@ -437,7 +437,7 @@ RouteBackwardLayout route_backward_layout(int64_t N, int64_t d, int E, int k, bo
 hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *idx,
                                  const float *p, const float *dgate, const float *dp,
                                  const void *dres, int64_t N, int64_t d, int E, int k, int sigmoid,
-                                 int renorm, float scale, void *dx, bool dx32, float *dW,
-                                 void *ws, hipStream_t s);
+                                 int renorm, float scale, const float *gates, void *dx, bool dx32,
+                                 float *dW, void *ws, hipStream_t s);
 
 }  // namespace moe

@@ -2206,7 +2206,8 @@ int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_ro
     }
     if (!topk_idx)
         return MOE_ERR_NULL;
-    if (!aligned(topk_idx, 4))
+    const float *gates = opts && r.renorm ? opts->gates : nullptr;
+    if (!aligned(topk_idx, 4) || !aligned(gates, 4))
         return MOE_ERR_ALIGN;
     const bool dx32 = dx && dx->dtype == MOE_F32;
     const bool dense = moe::route_backward_dense(r.sigmoid, r.renorm, dp);
@@ -2215,14 +2216,15 @@ int moe_router_backward(const moe_tensor *x, const moe_tensor *W_g, const moe_ro
         return rc;
     const int64_t bytes = N * d * (dx32 ? 4 : 2);
     const Span to[3] = {{dxp, bytes}, {dW, 4 * E * d}, {workspace, (int64_t)need}};
-    const Span in[6] = {{x->data, 2 * N * d}, {W_g->data, 4 * E * d}, {topk_idx, 4 * N * k},
-                        {p, 4 * N * E},       {dg, 4 * N * k},        {dp, 4 * N * E}};
+    const Span in[7] = {{x->data, 2 * N * d}, {W_g->data, 4 * E * d}, {topk_idx, 4 * N * k},
+                        {p, 4 * N * E},       {dg, 4 * N * k},        {dp, 4 * N * E},
+                        {gates, 4 * N * k}};
     const Span res{rp, bytes};
     if (collide(to, in) || crosses(to[0], res) || overlap(to[1], res) || overlap(to[2], res))
         return MOE_ERR_ARG;
     return hip_status(moe::launch_route_backward(
         x->data, static_cast<const float *>(W_g->data), topk_idx, p, dg, dp, rp, N, d, (int)E, k,
-        r.sigmoid, r.renorm, r.scale, dxp, dx32, dW, workspace, s));
+        r.sigmoid, r.renorm, r.scale, gates, dxp, dx32, dW, workspace, s));
 }
 
 }  // extern "C"

@@ -1,7 +1,7 @@
 // Backward of the routing (route.hip): from the gradient of the gates (and, for
 // an auxiliary loss, of the scores p) to those of the router's input and weights.
 //
-//   renormalised gates: S = sum of the chosen p, u_j = p_j / S,
+//   renormalised gates: S = sum of the chosen p, u_j = p_j / S (the gates over scale),
 //                       dp_j = scale / S (dg_j - sum_l u_l dg_l)
 //   gates as they are:  dp_j = scale dg_j
 //   sigmoid: ds = dp p (1 - p);  softmax: ds = p (dp - sum over all E of dp p)
@@ -57,6 +57,7 @@ struct RouteGrad {
     const int32_t *idx;       // [N, k]
     const float *p;           // [N, E]
     const float *dgate;       // [N, k]
+    const float *gates;       // [N, k], or NULL: the shares are formed from p
     const float *dp;          // [N, E] or NULL
     int E, Ep, k;             // Ep: E rounded up to 8
     int sigmoid, renorm;
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
     if (t >= N)
         return;
     int e = -1;
-    float dg = 0.f, pc = 0.f;
+    float dg = 0.f, pc = 0.f, gate = 0.f;
     if (lane < r.k) {
         e = r.idx[t * r.k + lane];
         if (e < 0 || e >= r.E) {
@@ -111,6 +112,7 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
         } else {
             dg = r.dgate[t * r.k + lane];
             pc = r.p[t * r.E + e];
+            gate = r.renorm && r.gates ? r.gates[t * r.k + lane] : 0.f;
         }
     }
     // Gates of a sigmoid, or renormalised, pass their gradient to the chosen scores
@@ -122,7 +124,8 @@ __global__ __launch_bounds__(256) void route_ds_kernel(RouteGrad r, int N,
         for (int j = 0; j < r.k; ++j)   // choice order
             S += __uint_as_float(
                 (unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(pc), j));
-        const float share = S > 0.f ? pc / S : 0.f;   // (1 / S may be past fp32)
+        // (1 / S may be past fp32; the forward's gates do not underflow with p)
+        const float share = r.gates ? gate / r.scale : S > 0.f ? pc / S : 0.f;
         for (int j = 0; j < r.k; ++j) {
             const float sj = __uint_as_float(
                 (unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(share), j));
@@ -456,8 +459,8 @@ RouteBackwardLayout route_backward_layout(int64_t N, int64_t d, int E, int k, bo
 hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *idx,
                                  const float *p, const float *dgate, const float *dp,
                                  const void *dres, int64_t N, int64_t d, int E, int k, int sigmoid,
-                                 int renorm, float scale, void *dx, bool dx32, float *dW,
-                                 void *ws, hipStream_t s) {
+                                 int renorm, float scale, const float *gates, void *dx, bool dx32,
+                                 float *dW, void *ws, hipStream_t s) {
     const bool dense = route_backward_dense(sigmoid, renorm, dp != nullptr);
     const int Ep = padded(E);
     const RouteBackwardLayout L = route_backward_layout(N, d, E, k, dense);
@@ -466,7 +469,7 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
     unsigned short *ds3 = reinterpret_cast<unsigned short *>(w + L.ds3);
     unsigned short *dsx = reinterpret_cast<unsigned short *>(w + L.dsx);
     unsigned short *wx = reinterpret_cast<unsigned short *>(w + L.wx);
-    RouteGrad r{idx, p, dgate, dp, E, Ep, k, sigmoid, renorm, scale, ds, ds3, nullptr};
+    RouteGrad r{idx, p, dgate, gates, dp, E, Ep, k, sigmoid, renorm, scale, ds, ds3, nullptr};
     if (dense)
         r.dsx = dsx;
     hipError_t err;
@@ -478,6 +481,7 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
         q.idx += t * k;
         q.p += t * E;
         q.dgate += t * k;
+        q.gates += gates ? t * k : 0;
         q.dp += dp ? t * E : 0;
         q.ds += t * k;
         q.ds3 += t * 3 * Ep;

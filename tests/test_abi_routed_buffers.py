@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from sparse_mixture_experts_20_amd import binding as B
-from tests.test_abi_block import ALIGN, ARG, BF16, F32, UNSUP, t
+from tests.test_abi_block import ALIGN, ARG, BF16, F32, UNSUP, WS, t
 
 P = 1 << 34     # apart from each other by more than any buffer here
 N, D, E, FF, K = 40, 64, 4, 128, 2
@@ -105,3 +105,24 @@ def test_routing_limits(L):
     f = L.moe_router_backward_workspace_size
     assert f(4, wide, 8, 2) == 0 and f(rows, 8, 8, 2) == 0
     assert f(4, 1 << 25, 8, 2) > 0 and f(1 << 29, 8, 8, 2) > 0
+
+
+def test_gates_of_the_backward(L):
+    """A misaligned array of gates, or a written buffer over it, where they are read (with
+    renormalised gates); elsewhere they are not looked at."""
+    a = [(i + 1) * P for i in range(10)]
+
+    def back(gates, renorm=1, **kw):
+        o = B.MoeRouterOpts(0, None, 0, 0, 0, renorm, 0.0, gates)
+        w = dict(dx=a[6], dW=a[7], ws=a[8], wn=1 << 33)
+        w.update(kw)
+        return L.moe_router_backward(
+            t(BF16, N, D, ptr=a[0]), t(F32, E, D, ptr=a[1]), ctypes.byref(o), K, a[2],
+            t(F32, N, E, ptr=a[3]), t(F32, N, K, ptr=a[4]), None, None,
+            t(F32, N, D, ptr=w["dx"]), t(F32, E, D, ptr=w["dW"]), w["ws"], w["wn"], None)
+    for off in (1, 2, 3):
+        assert back(a[5] + off) == ALIGN
+        assert back(a[5] + off, renorm=0, wn=16) == WS     # (the next check)
+    for name in ("dx", "dW", "ws"):
+        assert back(a[5], **{name: a[5]}) == ARG
+        assert back(a[5] + 4 * N * K - 4, **{name: a[5]}) == ARG
