@@ -624,8 +624,10 @@ int moe_dequantize(const moe_q4 *q, moe_tensor *W, void *stream);
  *   x [N, K] MOE_BF16 (MOE_ERR_UNSUPPORTED for fp32), W [M, K] as moe_q4,
  *   bias [M] MOE_F32 or NULL, activation as moe_linear's, residual [N, M]
  *   MOE_BF16 or NULL (may be the buffer of out), out [N, M] MOE_BF16
- * The weights enter exactly, sums are fp32, out is rounded once. An infinite
- * activation of the input gives NaN in every output. K and M at most
+ * The weights enter exactly, sums are fp32, out is rounded once. The kernels add
+ * x (128 + q) and x (128 + zero) of a group apart, so sum |x| over each group of
+ * columns must stay below 2^119 (zero points in [0, 15]): past it finite values may
+ * give infinities or NaN, and an infinite one gives NaN in every output of its row. K and M at most
  * MOE_LINEAR_MAX_EXTENT; x 16-byte, the other data aligned to their types
  * (MOE_ERR_ALIGN). out must not overlap an input otherwise (MOE_ERR_ARG).
  * workspace: moe_linear_quant_workspace_size() bytes, 256-byte aligned (may be
@@ -645,9 +647,10 @@ size_t moe_linear_quant_workspace_size(int64_t N, int64_t K, int64_t M, int32_t 
  * capacity applies.
  *   x, out [N, d] MOE_BF16; W_up [E, d_ff, d], W_down [E, d, d_ff] as moe_q4
  *   of one group; opts as moe_forward_few's (activation, biases; no dropout)
- * Numerics: weights as moe_linear_quant's; the hidden activation keeps 16
- * significant bits, the experts' rows fp32; a token's choices are added in
- * order and out is rounded once. An infinite value of x gives NaN. E and k
+ * Numerics: weights as moe_linear_quant's, whose range x and the hidden activations
+ * have to keep; the hidden activation keeps 16 significant bits, the experts' rows
+ * fp32; a token's choices are added in order and out is rounded once. An infinite
+ * value of x gives NaN. E and k
  * within the layer's limits, d and d_ff multiples of group and at most
  * MOE_FEW_MAX_WIDTH; x 16-byte aligned. workspace:
  * moe_experts_quant_workspace_size() bytes, 256-byte aligned; calls that share

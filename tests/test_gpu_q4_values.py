@@ -48,3 +48,48 @@ def test_quantize_whose_range_is_past_fp32(torch_mod, dtype):
     got = B.dequantize_q4(q, dtype=torch.float32).double()
     assert bool(torch.isfinite(got).all())
     assert bool(((got - w).abs() <= s[:, None] * (1.0 + 15 * 2.0 ** -8)).all())
+
+
+def _rows_norm(got, want):
+    """The largest distance of a row, relative, in the 2-norm."""
+    return float(((got.double() - want).norm(dim=1) / want.norm(dim=1)).max())
+
+
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("N", [1, 20, 40])
+def test_large_finite_activations(torch_mod, N, group, zero):
+    """Activations, and hidden values of the experts, up to the stated range: sum |x| over
+    a group just below 2^119. (bf16 output: half a step of 2^-8 at most, fp32 sums on
+    top: 2^-16 of the magnitudes.)"""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    from tests import _plain_q4 as Q
+    K, M = 512, 96
+    g = _gen(torch, N + group)
+    x = torch.randn((N, K), generator=g, device="cuda")
+    big = 2.0 ** 118.99 / float(x.abs().reshape(N, -1, group).sum(2).max())
+    x = (x * big).to(torch.bfloat16)
+    assert 2.0 ** 118 < float(x.double().abs().reshape(N, -1, group).sum(2).max()) < 2.0 ** 119
+    data, sc, zp, W = Q.weights(g, (M, K), group, zero)
+    out = B.linear_q4(x, B.Q4(data, sc, zp, group=group))
+    assert _rows_norm(out, x.double() @ W.t()) <= 2.0 ** -8
+    # the experts: one that leads up to the range and one that leads back
+    E, k, d, d_ff = 3, 2, 256, K
+    up, down = Q.weights(g, (E, d_ff, d), group, zero), Q.weights(g, (E, d, d_ff), group, zero)
+    x = torch.randn((N, d), generator=g, device="cuda").to(torch.bfloat16)
+    h = torch.relu(x.double() @ up[3].reshape(E * d_ff, d).t()).reshape(N, E, -1, group)
+    shift = 118 - int(torch.log2(h.sum(3).max()).ceil())
+    upv, downv = up[3] * 2.0 ** shift, down[3]
+    idx = torch.rand((N, E), generator=g, device="cuda").topk(k, dim=1).indices.int()
+    gate = torch.rand((N, k), generator=g, device="cuda") + 0.1
+    scale = (up[1].float() * 2.0 ** shift).to(torch.bfloat16)     # (a power of two: exact)
+    out = B.experts_q4(x, idx, gate, B.Q4(up[0], scale, up[2], group=group),
+                       B.Q4(*down[:3], group=group))
+    want = torch.zeros((N, d), dtype=torch.float64, device="cuda")
+    for e in range(E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        y = torch.relu(x[t].double() @ upv[e].t()) @ downv[e].t()
+        want.index_add_(0, t, gate[t, j].double()[:, None] * y)
+    assert bool(torch.isfinite(out).all())
+    assert _rows_norm(out, want) <= 2.0 ** -8
