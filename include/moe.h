@@ -701,7 +701,7 @@ typedef struct {
 /* moe_router with these options (NULL: all zeros): topk_idx [N, k] int32, the k
  * largest c in descending order (equal values: lower id first), and their gates
  * topk_gate [N, k] fp32; scores, if not NULL, the p of all experts, [N, E]
- * MOE_F32, for the backward or an auxiliary loss. k at most the experts of the
+ * MOE_F32, for an auxiliary loss or the backward (which takes bf16 x alone). k at most the experts of the
  * kept groups (MOE_ERR_ARG). x, W_g and noise as moe_router's, d at most
  * MOE_ROUTE_MAX_WIDTH (MOE_ERR_UNSUPPORTED), all arithmetic fp32. A NaN score counts as -inf (p = 0); where the chosen p sum to 0,
  * renormalised gates are 0 (those of a softmax are formed from the scores and do

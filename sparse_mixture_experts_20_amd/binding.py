@@ -1257,7 +1257,7 @@ def route(x, W_g, k: int, noise=None, bias=None, score: str = "softmax", groups:
           scale: float = 1.0, export_scores: bool = False, workspace=None):
     """Run ``moe_router_ex``: ``(idx, gate, scores)``, idx int32 and gate fp32
     [N, k], scores the fp32 [N, E] softmax or sigmoid scores with
-    ``export_scores`` (what the backward needs), else None."""
+    ``export_scores`` (what the backward, of bf16 x alone, needs), else None."""
     N, d, E = x.numel() // x.shape[-1], x.shape[-1], W_g.shape[0]
     index, dev = _device_of(x), x.device
     idx = torch.empty((N, k), dtype=torch.int32, device=dev)
