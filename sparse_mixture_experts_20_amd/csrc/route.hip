@@ -511,15 +511,21 @@ static hipError_t route_part(bool bf16, const RoutePlan &p, const void *xv, cons
                                    s, x, wg, noise, (int)N, (int)d, r, o);
                 return hipGetLastError();
             };
-            // wide rows, and few workgroups, keep more loads in flight with more waves
-            auto by_width = [&](auto nt) {
-                constexpr int most = decltype(nt)::value == 4 ? 8 : 16;
-                return d >= 1024 || blocks <= 512 ? go(nt, std::integral_constant<int, most>{})
-                                                  : go(nt, std::integral_constant<int, 4>{});
+            // A workgroup that has its CU to itself keeps more loads in flight with more
+            // waves; more workgroups do that for each other. 4 and 16 waves, us: 4096 tokens
+            // of 8 experts of 512 8.0 and 8.7, of 2304 12.9 and 10.8, 32 of 2048 16.4 and
+            // 13.7; 8192 of 8 of 768 10.8 and 14.2, of 2048 15.3 and 14.8, 32 of 768 13.5
+            // and 15.3; 65536 of 8 of 1024 43 and 102, 32 of 1024 78 and 110. fp32: 8192 of
+            // 8 of 768 12.0 and 9.5, 16384 of 16 of 1000 20.2 and 19.5, 65536 84 and 89.
+            // With 64 experts 8 waves throughout (4096 of 576 11.8 and 9.2, 65536 79 and 76).
+            auto by_blocks = [&](auto nt) {
+                return blocks <= (bf16 ? 256u : 1024u) ? go(nt, std::integral_constant<int, 16>{})
+                                                       : go(nt, std::integral_constant<int, 4>{});
             };
-            return r.E <= 16   ? by_width(std::integral_constant<int, 1>{})
-                   : r.E <= 32 ? by_width(std::integral_constant<int, 2>{})
-                               : by_width(std::integral_constant<int, 4>{});
+            return r.E <= 16   ? by_blocks(std::integral_constant<int, 1>{})
+                   : r.E <= 32 ? by_blocks(std::integral_constant<int, 2>{})
+                               : go(std::integral_constant<int, 4>{},
+                                    std::integral_constant<int, 8>{});
         }
         auto go = [&](auto tiles) {
             constexpr int TT = decltype(tiles)::value;

@@ -19,10 +19,16 @@ inline RoutePlan route_plan(bool bf16, int64_t N, int64_t d, int E) {
     p.Q = E <= 64 ? 1 : E <= 128 ? 2 : 4;
     p.ld = E <= 64 ? (E + 15) / 16 * 16 : 64 * p.Q;
     const int64_t weights = (int64_t)(E + 15) / 16 * 16 * d;
-    // A fused workgroup reads all of W_g, which saves a launch where that is little: as
-    // graphs of calls 64 tokens and 8 experts of width 768 7.9 us (ranges 8.8), of 4096
-    // 11.8 (8.7); as calls 2047 of these 13.5 (15.6), 777 of 60 experts of 515 14.5 (16.5).
-    if (N == 0 || (E <= 64 && weights <= (N > 1024 ? 65536 : 36864))) {
+    // A fused workgroup of 16 tokens reads all of W_g, which saves a launch where that is
+    // little. Timed in turn, one kernel and ranges, in graphs of calls (us): 256 tokens, 8
+    // experts of 768 7.8 and 8.5, of 2048 7.9 and 8.9, of 3000 10.0 and 8.0, 16 of 2304
+    // 11.6 and 9.0, 64 of 800 10.3 and 8.2: to 36864 weights. As calls, whose second
+    // launch the host takes 2 us longer for, 1536 tokens, 32 experts of 1536 12.7 and 14.5,
+    // 64 of 1024 12.4 and 14.2, 8 of 4104 12.2 and 14.4, of 5120 16.4 and 14.6, of 7168
+    // 20.0 and 14.1: to 73728 for a batch. (Past 4096 tokens, in a second round of the
+    // CUs, either may be faster: 5000 tokens, 8 of 2304 17.5 and 14.7, 32 of 2048 24.9 and
+    // 21.8, 8192 tokens, 8 of 512 9.5 and 10.8, of 2304 17.7 and 19.2, of 4096 23.7 and 23.3.)
+    if (N == 0 || (E <= 64 && weights <= (N > 1024 ? 73728 : 36864))) {
         p.form = kFused;
         return p;
     }
