@@ -422,8 +422,14 @@ __global__ __launch_bounds__(512) void route_dx_dense_kernel(
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Tiles and token ranges of dW_g: 256x256 tiles where their rows are filled, about
-// a workgroup a CU; otherwise 64 or 128 rows by 128 columns, about four.
+// Tiles and token ranges of dW_g, timed in turn (with ds and the sums, us). 256x256
+// tiles, a workgroup a CU, for long products whose rows fill them: 256 experts of 7168,
+// 4096 tokens 72 (128x128 77), 8192 109 (130), 16384 180 (228), 160 experts 8192 91 (100);
+// but 2048 57 (49), 256 experts of 2048, 8192 62 (51), of 4096, 4096 58 (52), 128 of 7168,
+// 8192 83 (77). Otherwise 64 or 128 rows by 128 columns; more ranges give more workgroups
+// and more partial sums, so one a CU, or two where the tiles are many: for 256, 512 and
+// 1024 workgroups 8 experts of 4096, 8192 tokens 25, 27, 35, 16 of 768, 32768 44, 60, 76,
+// 32 of 2048, 16384 37, 45, 66, 64 of 7168, 8192 67, 54, 67, 128 of 7168, 8192 132, 77, 93.
 struct DwShape {
     int bm, bn;
     int64_t tiles;
@@ -431,10 +437,10 @@ struct DwShape {
 };
 DwShape dw_shape(int64_t N, int64_t d, int rows) {
     DwShape s;
-    s.bm = rows >= 512 ? 256 : rows > 64 ? 128 : 64;
+    s.bm = rows >= 448 && (double)N * d * rows > 2.1e10 ? 256 : rows > 64 ? 128 : 64;
     s.bn = s.bm == 256 ? 256 : 128;
     s.tiles = (rows + s.bm - 1) / s.bm * ((d + s.bn - 1) / s.bn);
-    const int64_t want = s.bm == 256 ? 256 : 1024, steps = (N + kStep - 1) / kStep;
+    const int64_t want = s.bm == 128 && s.tiles >= 80 ? 512 : 256, steps = (N + kStep - 1) / kStep;
     s.ranges = (int)std::min<int64_t>(std::max<int64_t>(want / s.tiles, 1),
                                       std::max<int64_t>(steps / 4, 1));
     return s;
