@@ -947,7 +947,12 @@ Q4Shape q4_shape(int64_t M, int64_t blocks, int tt, int R) {
         s.rt = 1;
         s.w.wm = wk == 1 ? 4 : blocks > 1 && R > 2 ? 2 : 1;
         s.w.wk = s.w.wm == 2 ? std::min(wk, 4) : wk;
-        s.w.lds = (wk == 8 ? 64 : wk == 1 ? 48 : 32) * 1024;
+        // Where K takes two buffers: few steps of all the waves in one cost barriers, many
+        // the workgroups beside it on the CU. 32, 48 and 64 KB, us: not cut, 8 rows of 7168
+        // by 70000 87, 70, 83, 61 tokens of 256 experts 794, 717, 740; cut in 2 or 4, 6 rows
+        // of 14336 by 12288 37, 35, 53, 2, 6 and 16 Mixtral-shaped tokens 69, 60, 53, 111,
+        // 103, 109 and 165, 162, 167; cut in 8, one such token, whose K fits 64, 46, 46, 33.
+        s.w.lds = (wk == 8 ? 64 : 48) * 1024;
     } else {
         // Two weight tiles a wave, which halve the reads of the activations, where
         // they leave enough waves (Mixtral-shaped, 64 tokens: 250 us, 335 with one;
@@ -974,8 +979,13 @@ Q4Shape q4_sized(int64_t M, int64_t K, int64_t blocks, int tt, int nb, int R, in
     const int64_t steps = (K + q4_step(1) - 1) / q4_step(1), Kr = steps * q4_step(1);
     while (s.w.wk > 1 && (s.w.wk > steps || s.w.wm * s.w.wk > kQ4MaxWaves))
         s.w.wk /= 2;
-    const int most = s.w.lds;   // (of the shape's choice)
-    const int GS = kQ4Load / group;
+    const int GS = kQ4Load / group, one = 64 * 1024;
+    // (cut reductions keep all of K in one buffer where that takes no more than 64 KB: 12
+    // rows of 2048 by 12288 9.1 us, 16.9 in two of 48 KB; 3 of 7168 by 12000, groups of 32,
+    // 16.0 and 18.7; 32 tokens, 32 experts of 1024 by 1536 39.5 and 42.4; 4 rows of 7168 by
+    // 14336 21.7 and 25.8)
+    const bool fits = tt == 1 && s.w.wk > 1 && q4_bytes(R, 16 * s.w.wm, Kr, GS, zero) <= one;
+    const int most = fits ? one : s.w.lds;
     auto least = [&] {
         const int WR = 16 * s.rt * s.w.wm;
         if (q4_bytes(R, WR, Kr, GS, zero) <= most)
