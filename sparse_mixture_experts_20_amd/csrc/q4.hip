@@ -1091,9 +1091,15 @@ hipError_t launch_experts_q4(const void *x, const int32_t *idx, const float *gat
     const Q4Shape us = q4_sized(d_ff, d, hits, tt, 1, R, group, up[2] != nullptr);
     const Q4Shape ds = q4_sized(d, d_ff, hits, tt, 2, 2 * R, group, down[2] != nullptr);
     const int ur = 16 * us.rt * us.w.wm, dr = 16 * ds.rt * ds.w.wm;
-    // The last workgroup of a column block adds the choices where that saves a launch;
-    // with many workgroups a CU, each one's wait for its rows to reach memory costs more.
-    const bool apart = (d + dr - 1) / dr * (int64_t)blocks > 4096;
+    // The last workgroup of a column block adds the choices where no thread of it has more
+    // than one to read (past the L2, one after the other); a launch of its own costs less
+    // elsewhere. By the last workgroup and apart, us: one token of 8 experts of 768 by 2048
+    // 12.4 and 12.9 (as calls 12.0 and 14.2), 4 15.0 and 15.7, 4 Mixtral-shaped 87.7 and
+    // 89.2; one of 256 experts, k 8, of 7168 (2 a thread) 36.4 and 36.0, 16 of 8 of 768 by
+    // 2048 (2) 24.4 and 22.8, 8 of 32, k 4, of 512 by 512 (4) 16.5 and 14.5, 64 of 4 of 256
+    // by 256 35 and 23, 33 of 128, k 4, of 4096 by 512 92 and 61, 64 of 256, k 16, of 1024
+    // by 128 171 and 40.
+    const bool apart = N * dr * k > ds.threads;
     if (apart)
         p.done = nullptr;
     const hipError_t err = with_shape(group, up[2] != nullptr, us.rt, tt, us.two,
