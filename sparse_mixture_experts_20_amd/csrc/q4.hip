@@ -910,8 +910,10 @@ hipError_t with_shape(int group, bool zero, int rt, int tt, bool two, F f) {
         return f(gs, z, r, std::integral_constant<int, 4>{}, std::true_type{});
     };
     auto rows = [&](auto gs, auto z) {
-        return rt == 2 ? tiles(gs, z, std::integral_constant<int, 2>{})
-                       : tiles(gs, z, std::integral_constant<int, 1>{});
+        if constexpr (!decltype(z)::value)   // (one weight tile with zero points)
+            if (rt == 2)
+                return tiles(gs, z, std::integral_constant<int, 2>{});
+        return tiles(gs, z, std::integral_constant<int, 1>{});
     };
     auto zeros = [&](auto gs) {
         return zero ? rows(gs, std::true_type{}) : rows(gs, std::false_type{});
@@ -925,14 +927,14 @@ constexpr int kQ4MaxWaves = 8;
 constexpr int kQ4Lds = 144 * 1024;
 
 // Waves of a product of `blocks` times M rows of K weights, whose workgroups hold
-// up to R rows of activations in tt tiles.
+// up to R rows of activations, of nb terms, in tt tiles.
 struct Q4Shape {
     int rt;
     Q4Waves w;
     int threads, smem;
     bool two;   // more than one buffer, for some number of rows
 };
-Q4Shape q4_shape(int64_t M, int64_t blocks, int tt, int R) {
+Q4Shape q4_shape(int64_t M, int64_t blocks, int tt, int nb, int R, bool zero) {
     Q4Shape s;
     const int64_t strips = blocks * ((M + 15) / 16);   // of 16 weight rows
     // About 4096 waves, 16 on a CU, by cutting the reduction (one Mixtral-shaped
@@ -954,10 +956,16 @@ Q4Shape q4_shape(int64_t M, int64_t blocks, int tt, int R) {
         // 103, 109 and 165, 162, 167; cut in 8, one such token, whose K fits 64, 46, 46, 33.
         s.w.lds = (wk == 8 ? 64 : 48) * 1024;
     } else {
-        // Two weight tiles a wave, which halve the reads of the activations, where
-        // they leave enough waves (Mixtral-shaped, 64 tokens: 250 us, 335 with one;
-        // 33 rows of 4096 by 14336: 46 and 29).
-        s.rt = strips >= 4096 ? 2 : 1;
+        // Two weight tiles a wave, which halve the reads of the activations (of two terms
+        // in the down product), where they leave enough waves. One and two, us: rows of
+        // 4096 by 14336, 33 30 and 47, by 65536, 64 124 and 120, 20 of 2048 by 131072 86
+        // and 75; experts, up and down product apart, 64 Mixtral-shaped tokens 325 to 295
+        // and 295 to 228, 64 of 16 of 7168 by 4096, k 4, 320 to 279 and 279 to 230, 64 of
+        // 8 of 2048 by 4096 (2048 and 1024 strips) 65 to 60 and 65 to 70; 32 Mixtral-shaped
+        // tokens, k 4, 311 to 306 and 306 to 337. With zero points, whose sums of x take
+        // registers, one: 64 rows of 4096 by 131072 231 and 449, 64 Mixtral-shaped tokens
+        // 308 and 333.
+        s.rt = !zero && strips >= (nb == 2 ? 2048 : 4096) ? 2 : 1;
         s.w.wm = 4;
         s.w.wk = s.rt == 2 ? 2 : std::min(wk, 2);
         s.w.lds = 64 * 1024;
@@ -973,7 +981,7 @@ int q4_row_block(int64_t N, int64_t mean, int tt) {
 }
 Q4Shape q4_sized(int64_t M, int64_t K, int64_t blocks, int tt, int nb, int R, int group,
                  bool zero) {
-    Q4Shape s = q4_shape(M, blocks, tt, R);
+    Q4Shape s = q4_shape(M, blocks, tt, nb, R, zero);
     // every wave has a step; two buffers of wk D of them for every form that the kernel
     // takes, unless all of K fits
     const int64_t steps = (K + q4_step(1) - 1) / q4_step(1), Kr = steps * q4_step(1);
