@@ -55,6 +55,11 @@ __device__ __forceinline__ float bf16_bits_to_f32(unsigned short b) {
     return __builtin_bit_cast(float, (unsigned int)b << 16);
 }
 
+// A barrier for LDS alone: loads from global memory stay in flight.
+__device__ __forceinline__ void barrier_lds() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Compact expert output rows (the fused entry points of bf16 layers): each
 // group of kYGroup columns of a row of Y is stored as the fp16 values of
 // y * 2^sh with one exponent shift sh (int8) per group, sh chosen from the

@@ -59,11 +59,6 @@ constexpr int q4_depth(int tiles) { return tiles <= 4 ? 2 : 1; }
 constexpr int q4_step(int tiles) { return kQ4Load * q4_loads(tiles); }
 constexpr int kMaxAssign = kFewMaxTokens * kMaxTopK;
 
-// (a barrier for LDS alone: the loads of the next weights stay in flight)
-__device__ __forceinline__ void barrier_lds() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // 8 packed weights as 128 + q in bf16, in the order 0 4 1 5 2 6 3 7. (The masks
 // come in registers, one scalar and one vector: an instruction takes no two
 // literals, and as literals each would cost a second instruction.)

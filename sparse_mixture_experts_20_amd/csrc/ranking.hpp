@@ -39,17 +39,22 @@ __device__ __forceinline__ void split8(const f32x4 &w0, const f32x4 &w1, u32x4 &
     lo = u32x4{l[0], l[1], l[2], l[3]};
 }
 
+// Order of scores as unsigned numbers above 0 (NaN ranks as -inf; -0 as +0, which
+// compare equal), and back.
+__device__ __forceinline__ unsigned order_of(float v) {
+    const unsigned b = __float_as_uint(v != v ? -INFINITY : v + 0.f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(unsigned o) {
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
 // Ranking key of (score, expert): ordered as the scores, descending, then the
-// ids, ascending (NaN ranks as -inf; -0 as +0, which compare equal).
+// ids, ascending.
 __device__ __forceinline__ uint64_t rank_key(float v, int e) {
-    const float c = v != v ? -INFINITY : v + 0.f;
-    const unsigned b = __float_as_uint(c);
-    const unsigned o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return ((uint64_t)o << 32) | (uint64_t)(0xffffffffu - (unsigned)e);
+    return ((uint64_t)order_of(v) << 32) | (uint64_t)(0xffffffffu - (unsigned)e);
 }
 __device__ __forceinline__ float key_score(uint64_t key) {
-    const unsigned o = (unsigned)(key >> 32);
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+    return order_value((unsigned)(key >> 32));
 }
 template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ uint64_t dpp_max(uint64_t x) {

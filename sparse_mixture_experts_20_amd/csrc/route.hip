@@ -36,11 +36,6 @@ namespace {
 
 // ---- ranking -------------------------------------------------------------
 
-// Order of floats as unsigned numbers, above 0 (NaN ranks as -inf, -0 as +0).
-__device__ __forceinline__ unsigned order_of(float v) {
-    const unsigned b = __float_as_uint(v != v ? -INFINITY : v + 0.f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
 template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ unsigned dpp_max32(unsigned x) {
     const unsigned o = (unsigned)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, ROWS, 0xf, false);
@@ -54,9 +49,6 @@ __device__ __forceinline__ unsigned wave_max32(unsigned x) {
     x = dpp_max32<0x142, 0xa>(x);    // row_bcast:15 into rows 1 and 3
     x = dpp_max32<0x143, 0xc>(x);    // row_bcast:31 into rows 2 and 3
     return (unsigned)__builtin_amdgcn_readlane((int)x, 63);
-}
-__device__ __forceinline__ float order_value(unsigned o) {
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ float dpp_add(float v) {   // (0 where a lane gets nothing)

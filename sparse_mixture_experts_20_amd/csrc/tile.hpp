@@ -17,9 +17,6 @@ namespace {
 
 constexpr int kStep = 64;   // K-step of the tiled product
 
-__device__ __forceinline__ void barrier_lds() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
 template <int N>
 __device__ __forceinline__ void wait_loads() {   // until at most N are in flight
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -42,7 +39,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ s16x4 read_transposed(const void *p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
 }
-
 
 template <int BM, int BN, int WM, int WN, int S, bool AT, bool BT>
 struct TileProduct {
