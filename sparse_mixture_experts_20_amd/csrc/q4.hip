@@ -36,12 +36,14 @@
 // (one small launch). A hidden row is kept as two bf16 terms, as the few-token layer
 // keeps it: out then carries its own rounding alone.
 //
-// Measured (calls on inputs out of cache): one row of 7168 by 2048 9.3 us, of which
-// the kernel 8 (7.6 MB); 5 rows of 14336 by 4096 with zero points 16.7 (32 MB, 1.9
-// TB/s: the activations of all of K are read by each of 256 workgroups); 33 rows of
-// 4096 by 14336, groups of 32, 27.6 (the fp32 scaling of each group of three tiles); one
-// Mixtral-shaped token 33 (121 MB, 3.7 TB/s), 61 tokens of 256 experts 697 to 726 (3.3
-// GB, 4.6 to 4.8 TB/s).
+// Measured (calls in turn on inputs past the last-level cache, 256 MB; in brackets on
+// three sets, which it keeps where they are small): one row of 7168 by 2048 9.8 us (9.4),
+// of which the kernel 7.5; 5 rows of 14336 by 4096 with zero points 19.6 (17.7; 32 MB, 1.7
+// TB/s: the activations of all of K are read by each of 256 workgroups); 33 rows of 4096 by
+// 14336, groups of 32, 31.2 (29.3; the fp32 scaling of each group of four row tiles, one of
+// them nearly empty); one Mixtral-shaped token 35.6 (121 MB, 3.4 TB/s: 15 and 18 for the
+// products), 64 of them 231; 61 tokens of 256 experts 705 to 720 (3.3 GB, 4.6 to 4.7 TB/s).
+// Conversions: 470 M bf16 weights to 4 bits 332 us (3.6 TB/s), back 233 (5.1).
 #include <algorithm>
 #include <type_traits>
 

@@ -19,9 +19,11 @@
 // and their sum by DPP moves, groups through LDS, each choice by a 32-bit
 // maximum over the wave and a ballot for the lowest id that has it.
 //
-// Measured: one token, 256 experts of 7168 in 8 groups 15 us (two launches, 5.3 and 6.3
-// us on the GPU); 8192 tokens 119 (the tiled product 104 to 110 for 90 GFLOP of terms,
-// the ranking 21 beside the scores' export); 2047 tokens, 8 experts of 4096 13.5.
+// Measured (calls in turn on inputs past the last-level cache; kernels from a trace of
+// the same): one token, 256 experts of 7168 in 8 groups 15.5 us (two launches, 4.7 and 5.6
+// on the GPU: the host takes longer); 8192 tokens 127, in short runs 119 (split of W_g 5,
+// the tiled product 101 to 104 for 90 GFLOP of terms, the ranking 21 beside the scores'
+// export); 2047 tokens, 8 experts of 4096 14.3.
 #include <algorithm>
 #include <type_traits>
 

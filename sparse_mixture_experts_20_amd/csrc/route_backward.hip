@@ -18,12 +18,14 @@
 // LDS in fp32, 2 or 4 a lane, and a wave adds k rows of them for each token: bound
 // by dres and dx. dx with E values: the tiled product of split operands, six
 // products of terms (fp32's accuracy, for bf16 dx too: three of them, 2^-16, rounded
-// one element of 90 otherwise; 8192 tokens, 256 experts of 7168 then took 283 us, now
-// 377, 2047 tokens, 8 experts of 768 24 as now).
+// one element of 90 otherwise; 8192 tokens, 256 experts of 7168 then took 283 us, with
+// six 377, 2047 tokens, 8 experts of 768 24 either way).
 //
-// Measured: 8192 tokens, 256 experts of 7168, fp32 dx with dres 235 us: ds 10, dW_g
-// 98 to 110 (90 GFLOP of terms, 0.85 PFLOP/s) and 13 for the sums, dx 123 (470 MB, 3.8
-// TB/s). 2047 tokens, 8 experts of 768 with an auxiliary loss 25 us in four launches.
+// Measured (calls; kernels from a trace of the same, a little longer): 8192 tokens, 256
+// experts of 7168, fp32 dx with dres 236 us: ds 9, dW_g 96 to 99 (90 GFLOP of terms, 0.9
+// PFLOP/s) and 13 for the sums, dx 119 to 125 (470 MB, 3.9 TB/s); bf16 dx of all scores
+// 368, of which its six products 253 (180 GFLOP). 2047 tokens, 8 experts of 768 with an
+// auxiliary loss 24.5 in four launches.
 #include <algorithm>
 #include <type_traits>
 
