@@ -603,8 +603,9 @@ typedef struct {
     int64_t shape[3];
 } moe_q4;
 
-/* Nearest 4-bit weights of W (MOE_F32 or MOE_BF16, finite, the extents of q,
- * 16-byte aligned) into q's buffers, group by group. Without q->zero: scale =
+/* Nearest 4-bit weights of W (MOE_F32 or MOE_BF16, finite, the extents of q, fewer
+ * than 2^35 of them (MOE_ERR_UNSUPPORTED), 16-byte aligned) into q's buffers, group by
+ * group. Without q->zero: scale =
  * max |w| / 7 rounded to bf16, q = 8 + the nearest integer to w / scale in
  * [-8, 7]. With it: the range [min(w, 0), max(w, 0)], scale = its length / 15
  * rounded to bf16, zero = the nearest integer to -min / scale and q = zero +

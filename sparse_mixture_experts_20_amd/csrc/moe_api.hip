@@ -1885,7 +1885,10 @@ int check_q4_full(const moe_tensor *W, const moe_q4 *q) {
     for (int i = 0; i < W->ndim; ++i)
         if (W->shape[i] != q->shape[i])
             return MOE_ERR_SHAPE;
-    if (q4_count(q) / 8 >= ((int64_t)1 << 32) - 256)   // threads of a launch
+    // threads of a launch, 8 weights each (rows first: the product of three extents may
+    // pass 64 bits)
+    const int64_t K = q->shape[W->ndim - 1], rows = q->shape[0] * (W->ndim == 3 ? q->shape[1] : 1);
+    if (rows > (((int64_t)1 << 32) - 257) / (K / 8))
         return MOE_ERR_UNSUPPORTED;
     if (!W->data)
         return MOE_ERR_NULL;

@@ -126,3 +126,13 @@ def test_gates_of_the_backward(L):
     for name in ("dx", "dW", "ws"):
         assert back(a[5], **{name: a[5]}) == ARG
         assert back(a[5] + 4 * N * K - 4, **{name: a[5]}) == ARG
+
+
+def test_extents_whose_product_passes_64_bits(L):
+    """More weights than a conversion takes (2^35), also where E M K wraps to 0 or below."""
+    for E, M, K in ((256, 1 << 28, 1 << 28), (256, 1 << 28, 1 << 27), (1, 1 << 20, 1 << 15),
+                    (256, 1 << 14, 1 << 14)):
+        q = B.MoeQ4(P, 2 * P, None, 32, 3, (ctypes.c_int64 * 3)(E, M, K))
+        W = t(F32, E, M, K, ptr=1 << 50)
+        assert L.moe_quantize(W, ctypes.byref(q), None) == UNSUP, (E, M, K)
+        assert L.moe_dequantize(ctypes.byref(q), W, None) == UNSUP, (E, M, K)
