@@ -23,11 +23,14 @@ bool valid_dtype(int32_t dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// N k assignments or more than 32 bits hold (without forming a product that wraps).
+bool too_many(int64_t N, int k) { return N > INT32_MAX / k; }
+
 int64_t capacity_of(int64_t N, int64_t E, int k, float cf) {
     if (N <= 0)
         return 0;
     // (a factor that stands for "no limit" may pass 64 bits)
-    const double c = ceil((double)cf * (double)((int64_t)k * N) / (double)E);
+    const double c = ceil((double)cf * ((double)k * (double)N) / (double)E);
     return c < 0x1p63 ? (int64_t)c : INT64_MAX;
 }
 
@@ -191,7 +194,7 @@ int check_sizes(Dims &m) {
         return MOE_ERR_ARG;
     if (m.E > MOE_MAX_EXPERTS || m.k > MOE_MAX_TOPK)
         return MOE_ERR_UNSUPPORTED;
-    if (m.d > INT32_MAX || m.d_ff > INT32_MAX || m.N * (int64_t)m.k >= ((int64_t)1 << 31))
+    if (m.d > INT32_MAX || m.d_ff > INT32_MAX || too_many(m.N, m.k))
         return MOE_ERR_UNSUPPORTED;
     if (m.ceff * m.E >= ((int64_t)1 << 31))
         return MOE_ERR_UNSUPPORTED;
@@ -271,7 +274,7 @@ int check_router_args(const moe_tensor *x, const moe_tensor *W_g, const moe_tens
         return MOE_ERR_ARG;
     if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK)
         return MOE_ERR_UNSUPPORTED;
-    if (N * (int64_t)k >= ((int64_t)1 << 31) || d > INT32_MAX)
+    if (too_many(N, k) || d > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
     if (x->dtype == MOE_BF16) {
         if (d % 8 != 0)
@@ -300,7 +303,7 @@ int check_routed_args(const moe_tensor *x, const moe_tensor *W_up, int k, const 
         return MOE_ERR_ARG;
     if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK)
         return MOE_ERR_UNSUPPORTED;
-    if (N * (int64_t)k >= ((int64_t)1 << 31) || d > INT32_MAX)
+    if (too_many(N, k) || d > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
     if (x->dtype == MOE_BF16) {
         if (d % 8 != 0)
@@ -523,7 +526,7 @@ int moe_dispatch_noalloc(int64_t N, int64_t E, int k, int64_t capacity,
                          float *expert_gate_sum, void *stream) {
     if (N < 0 || E <= 0 || k < 1 || k > E || capacity < 0 || (N > 0 && capacity == 0))
         return MOE_ERR_ARG;
-    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || N * (int64_t)k >= ((int64_t)1 << 31))
+    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || too_many(N, k))
         return MOE_ERR_UNSUPPORTED;
     const size_t need = moe::dispatch_workspace_bytes(N, (int)E, k);
     if (need > kNoAllocScratchBytes)
@@ -538,7 +541,7 @@ int moe_dispatch_noalloc(int64_t N, int64_t E, int k, int64_t capacity,
 
 size_t moe_dispatch_workspace_size(int64_t N, int64_t E, int k) {
     if (N < 0 || E <= 0 || E > MOE_MAX_EXPERTS || k < 1 || k > E || k > MOE_MAX_TOPK ||
-        N * (int64_t)k >= ((int64_t)1 << 31))
+        too_many(N, k))
         return 0;
     return moe::dispatch_workspace_bytes(N, (int)E, k);
 }
@@ -562,7 +565,7 @@ int moe_dispatch(int64_t N, int64_t E, int k, int64_t capacity, const int32_t *t
                  void *stream) {
     if (N < 0 || E <= 0 || k < 1 || k > E || capacity < 0 || (N > 0 && capacity == 0))
         return MOE_ERR_ARG;
-    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || N * (int64_t)k >= ((int64_t)1 << 31))
+    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || too_many(N, k))
         return MOE_ERR_UNSUPPORTED;
     const int64_t ceff = capacity < N ? capacity : N;
     if (ceff * E >= ((int64_t)1 << 31))
@@ -2154,7 +2157,7 @@ int moe_router_ex(const moe_tensor *x, const moe_tensor *W_g, const moe_tensor *
 size_t moe_router_backward_workspace_size(int64_t N, int64_t d, int64_t E, int k) {
     if (N <= 0 || N > MOE_ROUTE_MAX_GRAD_ROWS || d <= 0 || d % 8 != 0 || d > MOE_ROUTE_MAX_WIDTH ||
         E <= 0 || E > MOE_MAX_EXPERTS || k < 1 || k > E || k > MOE_MAX_TOPK ||
-        N * (int64_t)k >= ((int64_t)1 << 31))
+        too_many(N, k))
         return 0;
     return moe::route_backward_layout(N, d, (int)E, k, true).total;   // the largest form
 }

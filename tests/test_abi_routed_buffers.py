@@ -136,3 +136,21 @@ def test_extents_whose_product_passes_64_bits(L):
         W = t(F32, E, M, K, ptr=1 << 50)
         assert L.moe_quantize(W, ctypes.byref(q), None) == UNSUP, (E, M, K)
         assert L.moe_dequantize(ctypes.byref(q), W, None) == UNSUP, (E, M, K)
+
+
+def test_rows_whose_assignments_pass_64_bits(L):
+    """N k that wraps to a small number is no small batch."""
+    n = 1 << 62
+    a = [(i + 1) << 50 for i in range(8)]
+    st = B.MoeStats(None, a[4], 1 << 62, a[2], a[3], None, None, -1)
+    for dt in (F32, BF16):
+        x, W = t(dt, n, 16, ptr=a[0]), t(F32, 8, 16, ptr=a[1])
+        assert L.moe_router_ex(x, W, None, None, 4, a[2], a[3], None, a[4], 1 << 62, None) == UNSUP
+        up = t(dt, 8, 32, 16, ptr=a[5])
+        assert L.moe_forward_routed(x, up, t(dt, 8, 16, 32, ptr=a[6]), None, 4, 1.0,
+                                    t(dt, n, 16, ptr=a[7]), ctypes.byref(st)) == UNSUP
+    assert L.moe_router_backward(t(BF16, n, 16, ptr=a[0]), t(F32, 8, 16, ptr=a[1]), None, 4, a[2],
+                                 t(F32, n, 8, ptr=a[3]), t(F32, n, 4, ptr=a[4]), None, None, None,
+                                 t(F32, 8, 16, ptr=a[5]), a[6], 1 << 62, None) == UNSUP
+    assert L.moe_router_backward_workspace_size(n, 16, 8, 4) == 0
+    assert L.moe_workspace_size(n, 16, 8, 32, 4, 1.0, BF16) == 0
