@@ -301,22 +301,23 @@ struct Rows {
 };
 
 // dx = dres + sum_j ds_j W_g[idx_j], choices in order. grid: (blocks of 64 V
-// columns, groups of tokens); W_g's columns of the block in LDS (E x 64 V fp32).
+// columns, groups of tokens); W_g's columns of the block in LDS (E x 64 V fp32, and a
+// row of zeros for ids that are no expert: a branch around them took 256 us, this 236).
 template <bool F32, int V>
 __global__ __launch_bounds__(1024) void route_dx_kernel(
     const float *__restrict__ ds, const int32_t *__restrict__ idx, const float *__restrict__ wg,
     const void *__restrict__ dres, int N, int d, int E, int k, void *__restrict__ dx) {
-    extern __shared__ __attribute__((aligned(16))) float w[];   // [E][64 V]
+    extern __shared__ __attribute__((aligned(16))) float w[];   // [E + 1][64 V]
     typedef Rows<F32, V> R;
     constexpr int C = 64 * V;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c0 = blockIdx.x * C, c = c0 + V * lane;
     const bool ok = c < d;   // (d % 8 == 0)
-    for (int i = threadIdx.x; i < E * (C / 4); i += 1024) {
+    for (int i = threadIdx.x; i < (E + 1) * (C / 4); i += 1024) {
         const int e = i / (C / 4), q = i % (C / 4) * 4;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (c0 + q < d)
+        if (e < E && c0 + q < d)
             v = *reinterpret_cast<const f32x4 *>(wg + (int64_t)e * d + c0 + q);
         *reinterpret_cast<f32x4 *>(w + e * C + q) = v;
     }
@@ -334,13 +335,13 @@ __global__ __launch_bounds__(1024) void route_dx_kernel(
     };
     auto choices = [&](int64_t t0) {
         const int64_t t = t0 + hu * waves;
-        Choice c{0, 0.f};
+        Choice c{E, 0.f};
         if (hj < k && t < N) {
             c.e = idx[t * k + hj];
             c.g = ds[t * k + hj];
         }
-        if (c.e < 0 || c.e >= E)   // no expert: ds is 0
-            c = Choice{0, 0.f};
+        if (c.e < 0 || c.e >= E)
+            c = Choice{E, 0.f};   // no expert: nothing, whatever W_g holds
         return c;
     };
     int64_t t0 = (int64_t)blockIdx.y * 16 + wv;
@@ -541,8 +542,10 @@ hipError_t launch_route_backward(const void *x, const float *wg, const int32_t *
     auto go = [&](auto f32, auto v) {
         constexpr int V = decltype(v)::value;
         const int64_t blocks = (d + 64 * V - 1) / (64 * V);
-        const size_t lds = (size_t)E * 64 * V * 4;
-        const int64_t per_cu = lds <= 40 * 1024 ? 2 : 1;   // (1024 threads each)
+        const size_t lds = (size_t)(E + 1) * 64 * V * 4;
+        // (1024 threads each; one and two with 8 experts of 4096, 8192 tokens 53 and 51 us,
+        // with 64 56 and 53, 32 of 768, 2048 tokens 8.0 and 8.6)
+        const int64_t per_cu = lds <= 80 * 1024 ? 2 : 1;
         const int64_t groups = std::min<int64_t>(std::max<int64_t>(256 * per_cu / blocks, 1),
                                                  (N + 15) / 16);
         moeLaunchKernelGGL((route_dx_kernel<decltype(f32)::value, V>),

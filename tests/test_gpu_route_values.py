@@ -157,3 +157,26 @@ def test_gates_given_to_the_backward(torch_mod):
         a = B.route_backward(x, W, idx, p, dgate, gate=gate, **rule)
         b = B.route_backward(x, W, idx, p, dgate, **rule)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_no_expert_takes_nothing_of_the_weights(torch_mod):
+    """A token whose ids are outside [0, E) has dx = dres, also where rows of W_g are not
+    finite (with k values a token no other expert's row is read)."""
+    torch = torch_mod
+    from sparse_mixture_experts_20_amd import binding as B
+    N, d, E, k = 40, 264, 6, 3
+    g = _gen(torch, 2)
+    x = torch.randn((N, d), generator=g, device="cuda").to(torch.bfloat16)
+    W = torch.randn((E, d), generator=g, device="cuda") / d ** 0.5
+    idx, _, p = B.route(x, W, k, score="sigmoid", export_scores=True)
+    idx = torch.where(idx == 0, torch.full_like(idx, E), idx)
+    idx[3] = torch.tensor([-1, E, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    dgate = torch.randn((N, k), generator=g, device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        dres = torch.randn((N, d), generator=g, device="cuda").to(dt)
+        kw = dict(dres=dres, score="sigmoid", need_dW=False, dx_dtype=dt)
+        want, _ = B.route_backward(x, W, idx, p, dgate, **kw)
+        V = W.clone()
+        V[0, ::2], V[0, 1::2] = float("inf"), float("nan")
+        got, _ = B.route_backward(x, V, idx, p, dgate, **kw)
+        assert torch.equal(got, want) and torch.equal(got[3], dres[3])
